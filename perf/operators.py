@@ -265,7 +265,8 @@ def quantize(fmt, x, tscale):
     amax = b.abs().amax(-1)
     if fmt == "nvfp4":
         t = tscale[:, None]
-        sb = torch.clamp(amax / 6.0 / t, max=448.0).to(torch.float8_e4m3fn)
+        # (a division by a tensor: by a number it may become a product with 1/6)
+        sb = torch.clamp(amax / torch.full_like(amax, 6.0) / t, max=448.0).to(torch.float8_e4m3fn)
         code, d = sb.view(torch.uint8), (sb.float() * t)[..., None]
         q = torch.where(d > 0, b / torch.where(d > 0, d, torch.ones_like(d)), 0.0 * b)
     else:
