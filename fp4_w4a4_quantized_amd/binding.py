@@ -19,6 +19,8 @@ OUT_F32 = 0
 OUT_BF16 = 1
 ROWMAJOR = 0
 TILED = 1
+SOFTMAX = 0
+SIGMOID = 1
 BLOCK = {NVFP4: 16, MXFP4: 32}
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libfp4q.so")
@@ -154,6 +156,31 @@ def lib():
         L.fp4q_quantize_status.argtypes = [P, sz, ctypes.POINTER(i32), P]
         L.fp4q_test_hook.restype = ctypes.c_int
         L.fp4q_test_hook.argtypes = [i32, i64]
+        i, f32 = ctypes.c_int, ctypes.c_float
+        kv = [i, P, i64, i32, i32, i32, P, i32, P, i64, i64, P, i64]  # fmt, cache ... lens, rows
+        L.fp4q_kv_page_bytes.restype = sz
+        L.fp4q_kv_page_bytes.argtypes = [i, i32, i32]
+        L.fp4q_kv_append.restype = i
+        L.fp4q_kv_append.argtypes = kv + [P, i64, P, i64, P, P, P]
+        L.fp4q_kv_read.restype = i
+        L.fp4q_kv_read.argtypes = kv + [P, i64, P, i64, P, P, P]
+        L.fp4q_kv_attention_workspace_bytes.restype = sz
+        L.fp4q_kv_attention_workspace_bytes.argtypes = [i, i64, i32, i32, i32, i32, i64, i64, i32]
+        L.fp4q_kv_attention.restype = i
+        L.fp4q_kv_attention.argtypes = kv + [P, i64, i32, i64, i64, i32, f32, P, P, P, i, i64, P,
+                                             sz, P]
+        L.fp4q_route_workspace_bytes.restype = sz
+        L.fp4q_route_workspace_bytes.argtypes = [i64, i32]
+        L.fp4q_route.restype = i
+        L.fp4q_route.argtypes = [P, i, i64, i32, i64, i32, i, P, i32, i32, i32, P, P, P, P, P, P,
+                                 sz, P]
+        L.fp4q_route_backward.restype = i
+        L.fp4q_route_backward.argtypes = [P, i, i64, i32, i64, i32, i, i32, P, P, P, i64, P]
+        L.fp4q_combine.restype = i
+        L.fp4q_combine.argtypes = [i, P, i64, i64, i64, P, P, i64, i32, P, i64, P]
+        L.fp4q_combine_backward.restype = i
+        L.fp4q_combine_backward.argtypes = [i, P, i64, i64, i64, P, P, i64, i32, P, i64, P, i64, P,
+                                            P]
         L.fp4q_error_decompose_workspace_bytes.restype = sz
         L.fp4q_error_decompose_workspace_bytes.argtypes = [i64, i64]
         L.fp4q_error_decompose.restype = ctypes.c_int
@@ -743,3 +770,276 @@ def error_decompose(fmt, x, stream=None):
         "n_clipped": st.n_clipped,
         "flags": st.flags,
     }
+
+
+# ---- the FP4 key/value cache ----------------------------------------------
+
+def _keep(stream, *tensors):
+    """Memory of torch's current stream that a call on another one uses is not
+    to be given out again before that call is done."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
+def _rows_of(name, t, heads_dim=None):
+    """Row stride of a [rows, heads, dim] tensor whose heads lie one after
+    another."""
+    if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+        raise ValueError(f"{name}: [rows, heads, dim] with contiguous heads is needed")
+    if t.dtype not in (torch.bfloat16, torch.int16):
+        raise ValueError(f"{name}: bf16 is needed")
+    if heads_dim is not None and tuple(t.shape[1:]) != tuple(heads_dim):
+        raise ValueError(f"{name}: {heads_dim[0]} heads of {heads_dim[1]} are needed")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def kv_page_bytes(fmt, page, dim) -> int:
+    """Bytes of one page of one head in the cache (0: not supported)."""
+    return lib().fp4q_kv_page_bytes(fmt, page, dim)
+
+
+def kv_cache(fmt, n_pages, page, kv_heads, dim, device="cuda"):
+    """An empty (uninitialised) cache: u8 [n_pages, kv_heads, page bytes]."""
+    nb = kv_page_bytes(fmt, page, dim)
+    if nb == 0:
+        raise ValueError("no such cache: page is a power of two in 16 .. 1024, dim 64, 128 or 256")
+    return torch.empty((n_pages, kv_heads, nb), dtype=torch.uint8, device=device)
+
+
+def _int32(name, t):
+    if t.dtype != torch.int32 or not t.is_contiguous():
+        raise ValueError(f"{name}: contiguous int32 is needed")
+    return t.data_ptr()
+
+
+def _kv_args(fmt, cache, page, offsets, page_table, lens, rows, dim, k_scale, v_scale):
+    if cache.dtype != torch.uint8 or not cache.is_contiguous() or cache.dim() != 3:
+        raise ValueError("cache: contiguous u8 [n_pages, kv_heads, page bytes] is needed")
+    n_pages, heads, nb = cache.shape
+    if nb != lib().fp4q_kv_page_bytes(fmt, page, dim):
+        raise ValueError("cache: its page bytes are not those of this format, page and dim")
+    if page_table.dtype != torch.int32 or page_table.dim() != 2 or (
+            page_table.shape[1] > 1 and page_table.stride(1) != 1):
+        raise ValueError("page_table: int32 [batch, pages] is needed")
+    batch = lens.numel()
+    if offsets.numel() != batch + 1 or page_table.shape[0] != batch:
+        raise ValueError("offsets, page_table and lens differ in their sequences")
+    for t in (k_scale, v_scale):
+        if t is not None and (t.dtype != torch.float32 or not t.is_contiguous()
+                              or t.numel() != heads):
+            raise ValueError("k_scale, v_scale: contiguous f32, one for each kv head")
+    return (fmt, cache.data_ptr(), n_pages, page, heads, dim, _int32("offsets", offsets), batch,
+            page_table.data_ptr(), page_table.stride(0) if batch > 1 else page_table.shape[1],
+            page_table.shape[1], _int32("lens", lens), rows)
+
+
+def _opt(t):
+    return None if t is None else t.data_ptr()
+
+
+def kv_append(fmt, cache, page, offsets, page_table, lens, k, v, k_scale=None, v_scale=None,
+              stream=None):
+    """Quantize the new tokens' keys and values (bf16 [rows, kv_heads, dim])
+    into the paged cache.  offsets int32 [batch + 1] (rows of each sequence),
+    page_table int32 [batch, pages], lens int32 [batch] (new tokens
+    included), all on the GPU; k_scale, v_scale f32 [kv_heads] (NVFP4)."""
+    ldk = _rows_of("k", k, (cache.shape[1], k.shape[-1]))
+    ldv = _rows_of("v", v, k.shape[1:])
+    if v.shape[0] != k.shape[0]:
+        raise ValueError("k and v differ in their rows")
+    args = _kv_args(fmt, cache, page, offsets, page_table, lens, k.shape[0], k.shape[2],
+                    k_scale, v_scale)
+    _check("fp4q_kv_append",
+           lib().fp4q_kv_append(*args, k.data_ptr(), ldk, v.data_ptr(), ldv, _opt(k_scale),
+                                _opt(v_scale), _stream(stream)))
+
+
+def kv_read(fmt, cache, page, offsets, page_table, lens, rows, dim, k_scale=None, v_scale=None,
+            stream=None):
+    """The values that stand in the cache for the new tokens: (k, v) bf16
+    [rows, kv_heads, dim]."""
+    k, v = torch.empty((2, rows, cache.shape[1], dim), dtype=torch.bfloat16, device=cache.device)
+    args = _kv_args(fmt, cache, page, offsets, page_table, lens, rows, dim, k_scale, v_scale)
+    ld = cache.shape[1] * dim
+    _check("fp4q_kv_read",
+           lib().fp4q_kv_read(*args, k.data_ptr(), ld, v.data_ptr(), ld, _opt(k_scale),
+                              _opt(v_scale), _stream(stream)))
+    _keep(stream, k)
+    return k, v
+
+
+def kv_attention_workspace_bytes(fmt, rows, heads, kv_heads, dim, batch, max_new, max_len,
+                                 window=0) -> int:
+    return lib().fp4q_kv_attention_workspace_bytes(fmt, rows, heads, kv_heads, dim, batch, max_new,
+                                                   max_len, window)
+
+
+def kv_attention_into(fmt, cache, page, offsets, page_table, lens, q, max_new, max_len, k_scale,
+                      v_scale, window, scale, y, workspace, stream=None):
+    """fp4q_kv_attention: y bf16 or f32 [rows, heads, dim]."""
+    ldq = _rows_of("q", q)
+    rows, heads, dim = q.shape
+    if y.shape != q.shape or y.stride(2) != 1 or (heads > 1 and y.stride(1) != dim):
+        raise ValueError("y: q's shape with contiguous heads is needed")
+    if y.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("y: bf16 or f32 is needed")
+    args = _kv_args(fmt, cache, page, offsets, page_table, lens, rows, dim, k_scale, v_scale)
+    nb = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check("fp4q_kv_attention",
+           lib().fp4q_kv_attention(*args, q.data_ptr(), ldq, heads, max_new, max_len, window, scale,
+                                   _opt(k_scale), _opt(v_scale), y.data_ptr(),
+                                   OUT_F32 if y.dtype == torch.float32 else OUT_BF16,
+                                   y.stride(0) if rows > 1 else heads * dim, _opt(workspace), nb,
+                                   _stream(stream)))
+
+
+def kv_attention(fmt, cache, page, offsets, page_table, lens, q, max_new, max_len, k_scale=None,
+                 v_scale=None, window=0, scale=None, y_dtype=OUT_BF16, stream=None):
+    """Attention of the new tokens' q (bf16 [rows, heads, dim]) over the cache
+    (their keys and values appended before).  No sequence has more than
+    max_new new tokens or is longer than max_len.  window > 0: a token sees
+    the last `window` keys only; scale: dim^-0.5 unless given.  Returns
+    [rows, heads, dim]."""
+    rows, heads, dim = q.shape
+    y = torch.empty((rows, heads, dim), device=q.device,
+                    dtype=torch.float32 if y_dtype == OUT_F32 else torch.bfloat16)
+    nb = kv_attention_workspace_bytes(fmt, rows, heads, cache.shape[1], dim, lens.numel(), max_new,
+                                      max_len, window)
+    ws = torch.empty(nb, dtype=torch.uint8, device=q.device) if nb else None
+    kv_attention_into(fmt, cache, page, offsets, page_table, lens, q, max_new, max_len, k_scale,
+                      v_scale, window, dim ** -0.5 if scale is None else scale, y, ws, stream)
+    _keep(stream, y, ws)
+    return y
+
+
+# ---- the router and the combination ---------------------------------------
+
+def _float_type(name, t):
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name}: a matrix with contiguous rows is needed")
+    if t.dtype == torch.float32:
+        return OUT_F32
+    if t.dtype == torch.bfloat16:
+        return OUT_BF16
+    raise ValueError(f"{name}: f32 or bf16 is needed")
+
+
+def _ld(t):
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _f32(name, t, shape):
+    if t.dtype != torch.float32 or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: contiguous f32 {list(shape)} is needed")
+    return t.data_ptr()
+
+
+def route_workspace_bytes(tokens, experts) -> int:
+    return lib().fp4q_route_workspace_bytes(tokens, experts)
+
+
+def route_into(logits, k, score, bias, n_groups, top_groups, renorm, experts, weights, offsets,
+               row_src, row_of, workspace, stream=None):
+    T, E = logits.shape
+    dt = _float_type("logits", logits)
+    nb = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check("fp4q_route",
+           lib().fp4q_route(logits.data_ptr(), dt, T, E, _ld(logits), k, score,
+                            None if bias is None else _f32("bias", bias, (E,)), n_groups,
+                            top_groups, int(renorm), _int32("experts", experts),
+                            _f32("weights", weights, (T, k)), _int32("offsets", offsets),
+                            _int32("row_src", row_src), _int32("row_of", row_of), _opt(workspace),
+                            nb, _stream(stream)))
+
+
+def route(logits, k, score=SOFTMAX, bias=None, n_groups=1, top_groups=1, renorm=True, stream=None):
+    """The k experts of each token from the router's logits (f32 or bf16
+    [tokens, experts]), their weights, and the order by expert.  bias f32
+    [experts] takes part in the choice only; of n_groups runs of experts the
+    top_groups best stay.  Returns dict(experts int32 [tokens, k], weights f32
+    [tokens, k], offsets int32 [experts + 1], row_src int32 [tokens * k],
+    row_of int32 [tokens, k])."""
+    T, E = logits.shape
+    dev = logits.device
+    # one allocation for the five results
+    Tk = T * k
+    buf = torch.empty(4 * Tk + E + 1, dtype=torch.int32, device=dev)
+    r = {"experts": buf[:Tk].view(T, k), "weights": buf[Tk:2 * Tk].view(torch.float32).view(T, k),
+         "offsets": buf[4 * Tk:], "row_src": buf[2 * Tk:3 * Tk],
+         "row_of": buf[3 * Tk:4 * Tk].view(T, k)}
+    nb = route_workspace_bytes(T, E)
+    ws = torch.empty(nb, dtype=torch.uint8, device=dev) if nb else None
+    route_into(logits, k, score, bias, n_groups, top_groups, renorm, r["experts"], r["weights"],
+               r["offsets"], r["row_src"], r["row_of"], ws, stream)
+    _keep(stream, buf, ws)
+    return r
+
+
+def route_backward_into(logits, experts, d_weights, score, renorm, d_logits, stream=None):
+    T, E = logits.shape
+    dt = _float_type("logits", logits)
+    if d_logits.shape != logits.shape or _float_type("d_logits", d_logits) != dt:
+        raise ValueError("d_logits: the logits' shape and type are needed")
+    if experts.shape[0] != T:
+        raise ValueError("experts: one row for each token")
+    _check("fp4q_route_backward",
+           lib().fp4q_route_backward(logits.data_ptr(), dt, T, E, _ld(logits), experts.shape[1],
+                                     score, int(renorm), _int32("experts", experts),
+                                     _f32("d_weights", d_weights, experts.shape),
+                                     d_logits.data_ptr(), _ld(d_logits), _stream(stream)))
+
+
+def route_backward(logits, experts, d_weights, score=SOFTMAX, renorm=True, stream=None):
+    """Gradient of the logits from that of route()'s weights (f32
+    [tokens, k]) and its chosen experts."""
+    d = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    route_backward_into(logits, experts, d_weights, score, renorm, d, stream)
+    _keep(stream, d)
+    return d
+
+
+def combine_into(y, row_of, weights, out, stream=None):
+    T, k = row_of.shape
+    dt = _float_type("y", y)
+    if _float_type("out", out) != dt or tuple(out.shape) != (T, y.shape[1]):
+        raise ValueError("out: [tokens, cols] of y's type is needed")
+    _check("fp4q_combine",
+           lib().fp4q_combine(dt, y.data_ptr(), y.shape[0], y.shape[1], _ld(y),
+                              _int32("row_of", row_of), _f32("weights", weights, (T, k)), T, k,
+                              out.data_ptr(), _ld(out), _stream(stream)))
+
+
+def combine(y, row_of, weights, stream=None):
+    """out[t] = sum_j weights[t, j] y[row_of[t, j]]: the experts' outputs y
+    (f32 or bf16 [rows, cols], in expert order) back to the tokens."""
+    out = torch.empty((row_of.shape[0], y.shape[1]), dtype=y.dtype, device=y.device)
+    combine_into(y, row_of, weights, out, stream)
+    _keep(stream, out)
+    return out
+
+
+def combine_backward_into(y, row_of, weights, d_out, d_y, d_weights, stream=None):
+    T, k = row_of.shape
+    dt = _float_type("y", y)
+    if _float_type("d_out", d_out) != dt or tuple(d_out.shape) != (T, y.shape[1]):
+        raise ValueError("d_out: [tokens, cols] of y's type is needed")
+    if _float_type("d_y", d_y) != dt or d_y.shape != y.shape:
+        raise ValueError("d_y: y's shape and type are needed")
+    _check("fp4q_combine_backward",
+           lib().fp4q_combine_backward(dt, y.data_ptr(), y.shape[0], y.shape[1], _ld(y),
+                                       _int32("row_of", row_of),
+                                       _f32("weights", weights, (T, k)), T, k, d_out.data_ptr(),
+                                       _ld(d_out), d_y.data_ptr(), _ld(d_y),
+                                       _f32("d_weights", d_weights, (T, k)), _stream(stream)))
+
+
+def combine_backward(y, row_of, weights, d_out, stream=None):
+    """(d_y, d_weights) of combine() from d_out.  row_of names every row of y
+    (combine_backward_into leaves the others as they are)."""
+    d_y = torch.empty(y.shape, dtype=y.dtype, device=y.device)
+    d_w = torch.empty(row_of.shape, dtype=torch.float32, device=y.device)
+    combine_backward_into(y, row_of, weights, d_out, d_y, d_w, stream)
+    _keep(stream, d_y, d_w)
+    return d_y, d_w

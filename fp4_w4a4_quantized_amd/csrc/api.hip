@@ -790,3 +790,243 @@ int fp4q_error_decompose(fp4q_format_t fmt, const uint16_t* x, int64_t rows, int
 }
 
 }  // extern "C"
+
+// ---- the key/value cache, the router and the combination -------------------
+
+namespace {
+
+inline bool dtype_ok(int d) { return d == FP4Q_OUT_F32 || d == FP4Q_OUT_BF16; }
+
+inline int page_shift_of(int32_t page) {
+  for (int s = 4; s <= 10; ++s)
+    if (page == (1 << s)) return s;
+  return -1;
+}
+
+// What the cache's calls have in common, short of the packed tensors.
+int kv_checks(int fmt, const uint8_t* cache, int64_t n_pages, int32_t page, int32_t kv_heads,
+              int32_t dim, const int32_t* offsets, int32_t batch, const int32_t* page_table,
+              int64_t ld_table,
+              int64_t table_cols, const int32_t* lens, int64_t rows, const float* k_scale,
+              const float* v_scale) {
+  if (!fmt_ok(fmt)) return FP4Q_ERR_INVALID;
+  if (n_pages < 0 || page < 1 || kv_heads < 1 || dim < 1 || batch < 0 || table_cols < 0 || rows < 0 ||
+      ld_table < (batch > 1 ? table_cols : 0))
+    return FP4Q_ERR_INVALID;
+  if (fmt == FP4Q_NVFP4 ? (!k_scale || !v_scale) : (k_scale || v_scale)) return FP4Q_ERR_INVALID;
+  if (rows > 0 && (n_pages < 1 || batch < 1 || table_cols < 1)) return FP4Q_ERR_INVALID;
+  if (rows > 0 && (!cache || !offsets || !page_table || !lens || !aligned(cache, 16)))
+    return FP4Q_ERR_INVALID;
+  if (page_shift_of(page) < 0 || (dim != 64 && dim != 128 && dim != 256))
+    return FP4Q_ERR_UNSUPPORTED;
+  if (kv_heads >= (1 << 20) || table_cols >= ((int64_t)1 << 31) / page) return FP4Q_ERR_UNSUPPORTED;
+  return FP4Q_OK;
+}
+
+inline bool packed_ok(const void* p, int64_t ld, int64_t cols) {
+  return p && aligned(p, 16) && ld >= cols && ld % 8 == 0;
+}
+
+int kv_copy(bool append, int fmt, uint8_t* cache, int64_t n_pages, int32_t page, int32_t kv_heads,
+            int32_t dim, const int32_t* offsets, int32_t batch, const int32_t* page_table,
+            int64_t ld_table,
+            int64_t table_cols, const int32_t* lens, int64_t rows, uint16_t* k, int64_t ldk,
+            uint16_t* v, int64_t ldv, const float* k_scale, const float* v_scale, void* stream) {
+  const int rc = kv_checks(fmt, cache, n_pages, page, kv_heads, dim, offsets, batch, page_table,
+                           ld_table, table_cols, lens, rows, k_scale, v_scale);
+  if (rc != FP4Q_OK) return rc;
+  if (rows == 0) return FP4Q_OK;
+  const int64_t cols = (int64_t)kv_heads * dim;
+  if (!packed_ok(k, ldk, cols) || !packed_ok(v, ldv, cols)) return FP4Q_ERR_INVALID;
+  if (rows >= ((int64_t)1 << 31) || (rows + 3) / 4 * 4 * (cols / 32) >= ((int64_t)1 << 31))
+    return FP4Q_ERR_UNSUPPORTED;
+  if (injected_failure()) return FP4Q_ERR_HIP;
+  clear_error();
+  fp4q::launch_kv_copy(append, fmt, cache, n_pages, page_shift_of(page), kv_heads, dim, offsets,
+                       batch, page_table, ld_table, table_cols, lens, rows, k, ldk, v, ldv, k_scale, v_scale,
+                       static_cast<hipStream_t>(stream));
+  return check_launch();
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t fp4q_kv_page_bytes(fp4q_format_t fmt, int32_t page, int32_t dim) {
+  if (!fmt_ok(fmt) || page_shift_of(page) < 0 || (dim != 64 && dim != 128 && dim != 256)) return 0;
+  return (size_t)page * (size_t)(dim + 2 * (dim / blk_of(fmt)));
+}
+
+int fp4q_kv_append(fp4q_format_t fmt, uint8_t* cache, int64_t n_pages, int32_t page,
+                   int32_t kv_heads, int32_t dim, const int32_t* offsets, int32_t batch,
+                   const int32_t* page_table, int64_t ld_table,
+                   int64_t table_cols, const int32_t* lens, int64_t rows,
+                   const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ldv,
+                   const float* k_scale, const float* v_scale, void* stream) {
+  return kv_copy(true, fmt, cache, n_pages, page, kv_heads, dim, offsets, batch, page_table,
+                 ld_table, table_cols, lens, rows, const_cast<uint16_t*>(k), ldk, const_cast<uint16_t*>(v),
+                 ldv, k_scale, v_scale, stream);
+}
+
+int fp4q_kv_read(fp4q_format_t fmt, const uint8_t* cache, int64_t n_pages, int32_t page,
+                 int32_t kv_heads, int32_t dim, const int32_t* offsets, int32_t batch,
+                 const int32_t* page_table, int64_t ld_table,
+                 int64_t table_cols, const int32_t* lens, int64_t rows,
+                 uint16_t* k, int64_t ldk, uint16_t* v, int64_t ldv, const float* k_scale,
+                 const float* v_scale, void* stream) {
+  return kv_copy(false, fmt, const_cast<uint8_t*>(cache), n_pages, page, kv_heads, dim, offsets,
+                 batch, page_table, ld_table, table_cols, lens, rows, k, ldk, v, ldv, k_scale, v_scale, stream);
+}
+
+size_t fp4q_kv_attention_workspace_bytes(fp4q_format_t fmt, int64_t rows, int32_t heads,
+                                         int32_t kv_heads, int32_t dim, int32_t batch,
+                                         int64_t max_new, int64_t max_len, int32_t window) {
+  if (!fmt_ok(fmt) || rows <= 0 || heads < 1 || kv_heads < 1 || heads % kv_heads != 0 ||
+      batch < 1 || max_new < 1 || max_len < 0 || window < 0 ||
+      (dim != 64 && dim != 128 && dim != 256))
+    return 0;
+  return fp4q::attention_workspace_bytes(rows, dim, batch, kv_heads, heads / kv_heads, max_new,
+                                         max_len, window);
+}
+
+int fp4q_kv_attention(fp4q_format_t fmt, const uint8_t* cache, int64_t n_pages, int32_t page,
+                      int32_t kv_heads, int32_t dim, const int32_t* offsets, int32_t batch,
+                      const int32_t* page_table, int64_t ld_table,
+                      int64_t table_cols, const int32_t* lens, int64_t rows, const uint16_t* q, int64_t ldq, int32_t heads,
+                      int64_t max_new, int64_t max_len, int32_t window, float scale,
+                      const float* k_scale, const float* v_scale, void* y, fp4q_dtype_t y_dtype,
+                      int64_t ldy, void* workspace, size_t workspace_bytes, void* stream) {
+  const int rc = kv_checks(fmt, cache, n_pages, page, kv_heads, dim, offsets, batch, page_table,
+                           ld_table, table_cols, lens, rows, k_scale, v_scale);
+  if (rc != FP4Q_OK && rc != FP4Q_ERR_UNSUPPORTED) return rc;
+  if (!dtype_ok(y_dtype) || heads < 1 || heads % kv_heads != 0 || max_new < 0 || max_len < 0 ||
+      window < 0 || !(scale > 0.0f) || !(scale <= 3.4e38f))
+    return FP4Q_ERR_INVALID;
+  if (rc != FP4Q_OK) return rc;
+  if (rows == 0) return FP4Q_OK;
+  const int64_t cols = (int64_t)heads * dim;
+  if (max_new < 1 || !packed_ok(q, ldq, cols) || !packed_ok(y, ldy, cols)) return FP4Q_ERR_INVALID;
+  if (heads / kv_heads > 128 || rows >= ((int64_t)1 << 31) / heads ||
+      max_new >= ((int64_t)1 << 31) / heads || max_len >= ((int64_t)1 << 31) ||
+      !fp4q::attention_shape_ok(dim, batch, kv_heads, heads / kv_heads, max_new, max_len, window))
+    return FP4Q_ERR_UNSUPPORTED;
+  const size_t need = fp4q_kv_attention_workspace_bytes(fmt, rows, heads, kv_heads, dim, batch,
+                                                        max_new, max_len, window);
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
+    return FP4Q_ERR_WORKSPACE;
+  if (injected_failure()) return FP4Q_ERR_HIP;
+  clear_error();
+  fp4q::launch_attention(fmt, cache, n_pages, page_shift_of(page), kv_heads, dim, offsets, batch,
+                         page_table, ld_table, table_cols, lens, q, ldq, rows, heads / kv_heads, max_new,
+                         max_len, window, scale, k_scale, v_scale, y, y_dtype == FP4Q_OUT_BF16,
+                         ldy, workspace, static_cast<hipStream_t>(stream));
+  return check_launch();
+}
+
+size_t fp4q_route_workspace_bytes(int64_t tokens, int32_t experts) {
+  if (tokens <= 0 || experts < 1) return 0;
+  return fp4q::route_workspace_bytes(tokens, experts);
+}
+
+int fp4q_route(const void* logits, fp4q_dtype_t dtype, int64_t tokens, int32_t n_experts,
+               int64_t ldx, int32_t k, fp4q_score_t score, const float* bias, int32_t n_groups,
+               int32_t top_groups, int32_t renorm, int32_t* experts, float* weights,
+               int32_t* offsets, int32_t* row_src, int32_t* row_of, void* workspace,
+               size_t workspace_bytes, void* stream) {
+  if (!dtype_ok(dtype) || (score != FP4Q_SCORE_SOFTMAX && score != FP4Q_SCORE_SIGMOID))
+    return FP4Q_ERR_INVALID;
+  if (tokens < 0 || n_experts < 1 || ldx < n_experts || k < 1 || n_groups < 1 ||
+      n_experts % n_groups != 0 || top_groups < 1 || top_groups > n_groups ||
+      k > n_experts / n_groups * top_groups)
+    return FP4Q_ERR_INVALID;
+  if (!offsets || !aligned(offsets, 4) || !aligned(bias, 4)) return FP4Q_ERR_INVALID;
+  if (tokens > 0 && (!logits || !experts || !weights || !row_src || !row_of))
+    return FP4Q_ERR_INVALID;
+  if (!aligned(logits, dtype == FP4Q_OUT_F32 ? 4 : 2) || !aligned(experts, 4) ||
+      !aligned(weights, 4) || !aligned(row_src, 4) || !aligned(row_of, 4))
+    return FP4Q_ERR_INVALID;
+  if (n_experts > FP4Q_ROUTE_MAX_EXPERTS || n_groups > FP4Q_ROUTE_MAX_GROUPS ||
+      k > FP4Q_ROUTE_MAX_K || tokens >= ((int64_t)1 << 31) / k)
+    return FP4Q_ERR_UNSUPPORTED;
+  const size_t need = fp4q_route_workspace_bytes(tokens, n_experts);
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 8)))
+    return FP4Q_ERR_WORKSPACE;
+  if (injected_failure()) return FP4Q_ERR_HIP;
+  clear_error();
+  fp4q::launch_route(logits, dtype == FP4Q_OUT_F32, tokens, ldx, n_experts, k, score, bias,
+                     n_groups, top_groups, renorm != 0, experts, weights, offsets, row_src, row_of,
+                     workspace, static_cast<hipStream_t>(stream));
+  return check_launch();
+}
+
+int fp4q_route_backward(const void* logits, fp4q_dtype_t dtype, int64_t tokens,
+                        int32_t n_experts, int64_t ldx, int32_t k, fp4q_score_t score,
+                        int32_t renorm, const int32_t* experts, const float* d_weights,
+                        void* d_logits, int64_t ldd, void* stream) {
+  if (!dtype_ok(dtype) || (score != FP4Q_SCORE_SOFTMAX && score != FP4Q_SCORE_SIGMOID))
+    return FP4Q_ERR_INVALID;
+  if (tokens < 0 || n_experts < 1 || ldx < n_experts || ldd < n_experts || k < 1 || k > n_experts)
+    return FP4Q_ERR_INVALID;
+  if (tokens > 0 && (!logits || !experts || !d_weights || !d_logits)) return FP4Q_ERR_INVALID;
+  const int el = dtype == FP4Q_OUT_F32 ? 4 : 2;
+  if (!aligned(logits, el) || !aligned(d_logits, el) || !aligned(experts, 4) ||
+      !aligned(d_weights, 4))
+    return FP4Q_ERR_INVALID;
+  if (n_experts > FP4Q_ROUTE_MAX_EXPERTS || k > FP4Q_ROUTE_MAX_K ||
+      tokens >= ((int64_t)1 << 31) / k)
+    return FP4Q_ERR_UNSUPPORTED;
+  if (tokens == 0) return FP4Q_OK;
+  if (injected_failure()) return FP4Q_ERR_HIP;
+  clear_error();
+  fp4q::launch_route_backward(logits, dtype == FP4Q_OUT_F32, tokens, ldx, n_experts, k, score,
+                              renorm != 0, experts, d_weights, d_logits, ldd,
+                              static_cast<hipStream_t>(stream));
+  return check_launch();
+}
+
+int fp4q_combine(fp4q_dtype_t dtype, const void* y, int64_t rows, int64_t cols, int64_t ldy,
+                 const int32_t* row_of, const float* weights, int64_t tokens, int32_t k,
+                 void* out, int64_t ldo, void* stream) {
+  if (!dtype_ok(dtype) || rows < 0 || cols < 1 || ldy < cols || tokens < 0 || k < 1 || ldo < cols)
+    return FP4Q_ERR_INVALID;
+  if (tokens > 0 && (!row_of || !weights || !out || (rows > 0 && !y))) return FP4Q_ERR_INVALID;
+  const int el = dtype == FP4Q_OUT_F32 ? 4 : 2;
+  if (!aligned(y, el) || !aligned(out, el) || !aligned(row_of, 4) || !aligned(weights, 4))
+    return FP4Q_ERR_INVALID;
+  if (k > 128 || tokens >= ((int64_t)1 << 31) / k || cols >= ((int64_t)1 << 31) ||
+      tokens * ((cols + 7) / 8) >= ((int64_t)1 << 31))
+    return FP4Q_ERR_UNSUPPORTED;
+  if (tokens == 0) return FP4Q_OK;
+  if (injected_failure()) return FP4Q_ERR_HIP;
+  clear_error();
+  fp4q::launch_combine(dtype == FP4Q_OUT_F32, y, rows, cols, ldy, row_of, weights, tokens, k, out,
+                       ldo, static_cast<hipStream_t>(stream));
+  return check_launch();
+}
+
+int fp4q_combine_backward(fp4q_dtype_t dtype, const void* y, int64_t rows, int64_t cols,
+                          int64_t ldy, const int32_t* row_of, const float* weights,
+                          int64_t tokens, int32_t k, const void* d_out, int64_t ldo, void* d_y,
+                          int64_t lddy, float* d_weights, void* stream) {
+  if (!dtype_ok(dtype) || rows < 0 || cols < 1 || ldy < cols || tokens < 0 || k < 1 ||
+      ldo < cols || lddy < cols)
+    return FP4Q_ERR_INVALID;
+  if (tokens > 0 && (!row_of || !weights || !d_out || !d_weights || (rows > 0 && (!y || !d_y))))
+    return FP4Q_ERR_INVALID;
+  const int el = dtype == FP4Q_OUT_F32 ? 4 : 2;
+  if (!aligned(y, el) || !aligned(d_out, el) || !aligned(d_y, el) || !aligned(row_of, 4) ||
+      !aligned(weights, 4) || !aligned(d_weights, 4))
+    return FP4Q_ERR_INVALID;
+  if (k > 128 || tokens >= ((int64_t)1 << 31) / k || cols >= ((int64_t)1 << 31) ||
+      tokens * ((cols + 7) / 8) >= ((int64_t)1 << 31))
+    return FP4Q_ERR_UNSUPPORTED;
+  if (tokens == 0) return FP4Q_OK;
+  if (injected_failure()) return FP4Q_ERR_HIP;
+  clear_error();
+  fp4q::launch_combine_backward(dtype == FP4Q_OUT_F32, y, rows, cols, ldy, row_of, weights, tokens,
+                                k, d_out, ldo, d_y, lddy, d_weights,
+                                static_cast<hipStream_t>(stream));
+  return check_launch();
+}
+
+}  // extern "C"

@@ -138,6 +138,39 @@ void launch_permute(int fmt, const uint16_t* x, int64_t ldx, int64_t tokens, int
                     const int32_t* chan, int nS, uint8_t* q_out, uint8_t* s_out, float* ts_out,
                     uint16_t* r_out, hipStream_t stream);
 
+// The paged FP4 key/value cache: append (k, v read) or read (k, v written);
+// attention over it, split over the keys where the plan says so.
+void launch_kv_copy(bool append, int fmt, uint8_t* cache, int64_t n_pages, int page_shift, int H,
+                    int D, const int32_t* off, int B, const int32_t* table, int64_t ldt, int64_t table_cols,
+                    const int32_t* lens, int64_t rows, uint16_t* k, int64_t ldk, uint16_t* v,
+                    int64_t ldv, const float* kts, const float* vts, hipStream_t stream);
+bool attention_shape_ok(int D, int B, int H, int G, int64_t max_new, int64_t max_len, int window);
+size_t attention_workspace_bytes(int64_t rows, int D, int B, int H, int G, int64_t max_new,
+                                 int64_t max_len, int window);
+void launch_attention(int fmt, const uint8_t* cache, int64_t n_pages, int page_shift, int H, int D,
+                      const int32_t* off, int B, const int32_t* table, int64_t ldt, int64_t table_cols,
+                      const int32_t* lens, const uint16_t* q, int64_t ldq, int64_t rows, int G,
+                      int64_t max_new, int64_t max_len, int window, float scale, const float* kts,
+                      const float* vts, void* y, int y_bf16, int64_t ldy, void* ws,
+                      hipStream_t stream);
+
+// The router and the combination of the experts' outputs.
+size_t route_workspace_bytes(int64_t T, int E);
+void launch_route(const void* logits, int f32, int64_t T, int64_t ldx, int E, int k, int score,
+                  const float* bias, int G, int top_groups, int renorm, int32_t* experts,
+                  float* weights, int32_t* offsets, int32_t* row_src, int32_t* row_of, void* ws,
+                  hipStream_t stream);
+void launch_route_backward(const void* logits, int f32, int64_t T, int64_t ldx, int E, int k,
+                           int score, int renorm, const int32_t* experts, const float* d_weights,
+                           void* d_logits, int64_t ldd, hipStream_t stream);
+void launch_combine(int f32, const void* y, int64_t rows, int64_t N, int64_t ldy,
+                    const int32_t* row_of, const float* w, int64_t T, int k, void* out,
+                    int64_t ldo, hipStream_t stream);
+void launch_combine_backward(int f32, const void* y, int64_t rows, int64_t N, int64_t ldy,
+                             const int32_t* row_of, const float* w, int64_t T, int k,
+                             const void* d_out, int64_t ldo, void* d_y, int64_t lddy, float* d_w,
+                             hipStream_t stream);
+
 size_t decompose_workspace_bytes(int64_t rows, int64_t cols);
 int launch_decompose(int fmt, const uint16_t* x, int64_t rows, int64_t cols, int64_t ldx,
                      fp4q_err_stats_t* out, void* ws, hipStream_t stream);

@@ -1,0 +1,572 @@
+// route.hip -- the router of the expert layer (scores, top-k, expert order;
+// gradient of the logits) and the combination of the experts' outputs (and
+// its gradients).  The operations are defined in include/fp4q.h.
+#include "fp4q_device.h"
+#include "fp4q_internal.h"
+
+#include <type_traits>
+
+namespace fp4q {
+
+namespace {
+
+typedef __bf16 bf16x2r __attribute__((ext_vector_type(2)));
+typedef float v2f32r __attribute__((ext_vector_type(2)));
+
+constexpr int RT_TOK = 64;        // tokens of a workgroup: one bit each in the experts' masks
+constexpr int RT_THREADS = 512;  // 8 waves
+constexpr int RT_MAX_E = FP4Q_ROUTE_MAX_EXPERTS;
+constexpr int RT_MAX_K = FP4Q_ROUTE_MAX_K;
+
+struct RouteArgs {
+  const void* logits;
+  int f32;
+  int64_t T, ldx;
+  int E, k, score, G, top_groups, renorm;
+  const float* bias;
+  int32_t* experts;
+  float* weights;
+  int32_t* offsets;
+  int32_t* row_src;
+  int32_t* row_of;
+  uint64_t* masks;  // [blocks][E]: which of the block's tokens chose the expert
+  uint8_t* counts;  // [blocks][E]: how many
+  int blocks;
+};
+
+__device__ __forceinline__ float load_logit(const void* x, int f32, int64_t i) {
+  return f32 ? reinterpret_cast<const float*>(x)[i]
+             : bf16_to_f32(reinterpret_cast<const uint16_t*>(x)[i]);
+}
+
+template <typename T>
+__device__ __forceinline__ T wave_max(T v) {
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) {
+    const T o = __shfl_xor(v, d);
+    v = o > v ? o : v;
+  }
+  return v;
+}
+
+__device__ __forceinline__ double wave_sum(double v) {
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d);
+  return v;
+}
+
+// The expert order of a workgroup's tokens: base[e] is where the block's
+// first row of expert e goes, a token's row among them the number of earlier
+// tokens of the block that chose e too.
+__device__ __forceinline__ void write_rows(const RouteArgs& p, int64_t t0, int nt,
+                                           const int32_t* ex, const uint64_t* mask,
+                                           const int* base) {
+  for (int i = threadIdx.x; i < nt * p.k; i += blockDim.x) {
+    const int t = i / p.k, e = ex[i];
+    const int pos = base[e] + (int)__popcll(mask[e] & ((1ull << t) - 1ull));
+    p.row_src[pos] = (int32_t)(t0 + t);
+    p.row_of[t0 * p.k + i] = pos;
+  }
+}
+
+// Exclusive scan of n values in LDS by the workgroup (n <= RT_THREADS;
+// tmp: one int a wave).
+__device__ __forceinline__ void block_scan(int* v, int n, int* tmp, int* total) {
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  const int own = t < n ? v[t] : 0;
+  int run = own;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(run, d);
+    if (lane >= d) run += o;
+  }
+  if (lane == 63) tmp[wave] = run;
+  __syncthreads();
+  int before = 0, all = 0;
+  for (int w = 0; w < RT_THREADS / 64; ++w) {
+    before += w < wave ? tmp[w] : 0;
+    all += tmp[w];
+  }
+  __syncthreads();
+  if (t < n) v[t] = before + run - own;
+  if (t == 0) *total = all;
+  __syncthreads();
+}
+
+// One wave per token; lane l holds experts l, l + 64, ...  The order of the
+// experts is taken on the logits themselves where they decide it (no bias and
+// no groups: both scores are increasing functions of the logit), else on the
+// scores in 64 bits, so that near ties are told apart as the definition does.
+template <int NS, bool WIDE>
+__global__ __launch_bounds__(RT_THREADS) void k_route_pick(RouteArgs p) {
+  __shared__ uint64_t s_mask[RT_MAX_E];
+  __shared__ int s_base[RT_MAX_E];
+  __shared__ int32_t s_ex[RT_TOK * RT_MAX_K];
+  __shared__ int s_tmp[RT_THREADS / 64], s_total;
+  extern __shared__ double s_rank[];  // WIDE with groups: [8][E]
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int E = p.E, k = p.k;
+  for (int e = threadIdx.x; e < E; e += RT_THREADS) s_mask[e] = 0;
+  __syncthreads();
+  const int64_t t0 = (int64_t)blockIdx.x * RT_TOK;
+  const int nt = (int)min((int64_t)RT_TOK, p.T - t0);
+  for (int tt = wave; tt < nt; tt += RT_THREADS / 64) {
+    const int64_t row = (t0 + tt) * p.ldx;
+    float x[NS];
+    float top = -__builtin_inff();
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+      const int e = lane + 64 * i;
+      x[i] = e < E ? load_logit(p.logits, p.f32, row + e) : -__builtin_inff();
+      top = fmaxf(top, x[i]);
+    }
+    top = wave_max(top);
+    // softmax: scores are exp(x - m) / Z; all scores of a row without a
+    // finite logit are 0
+    const double m = top > -__builtin_inff() ? (double)top : 0.0;
+    const bool soft = p.score == FP4Q_SCORE_SOFTMAX;
+    double z = 1.0, s[WIDE ? NS : 1];
+    if (WIDE) {
+#pragma unroll
+      for (int i = 0; i < NS; ++i)
+        s[i] = soft ? exp((double)x[i] - m) : 1.0 / (1.0 + exp(-(double)x[i]));
+    }
+    if (soft && (WIDE || !p.renorm)) {
+      double part = 0.0;
+#pragma unroll
+      for (int i = 0; i < NS; ++i)
+        if (lane + 64 * i < E) part += WIDE ? s[i] : exp((double)x[i] - m);
+      z = wave_sum(part);
+      if (!(z > 0.0)) z = 1.0;
+      if (WIDE) {
+#pragma unroll
+        for (int i = 0; i < NS; ++i) s[i] /= z;
+      }
+    }
+    typedef typename std::conditional<WIDE, double, float>::type key_t;
+    key_t key[NS];
+    uint32_t avail = 0;
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+      const int e = lane + 64 * i;
+      if (e < E) avail |= 1u << i;
+      key[i] = WIDE ? (key_t)(s[i] + (p.bias && e < E ? (double)p.bias[e] : 0.0)) : (key_t)x[i];
+      if (!(key[i] == key[i])) key[i] = -__builtin_inff();  // NaN comes last
+    }
+    if (WIDE && p.G > 1) {
+      // each group's two best, by 64 / 2^ceil(log2 G) lanes a group
+      double* r = s_rank + wave * E;
+#pragma unroll
+      for (int i = 0; i < NS; ++i)
+        if (lane + 64 * i < E) r[lane + 64 * i] = key[i];
+      __builtin_amdgcn_wave_barrier();
+      const int gs = E / p.G;
+      int P = 64;
+      while (P * p.G > 64) P >>= 1;
+      const int g = lane / P;
+      double a = -__builtin_inf(), b = -__builtin_inf();
+      if (g < p.G)
+        for (int i = lane % P; i < gs; i += P) {
+          const double v = r[g * gs + i];
+          if (v > a) { b = a; a = v; }
+          else if (v > b) b = v;
+        }
+      for (int d = 1; d < P; d <<= 1) {
+        const double a2 = __shfl_xor(a, d), b2 = __shfl_xor(b, d);
+        const double lo = fmin(a, a2);
+        a = fmax(a, a2);
+        b = fmax(lo, fmax(b, b2));
+      }
+      const double sum = gs > 1 ? a + b : a;
+      int rank = 0;
+      for (int o = 0; o < p.G; ++o) {
+        const double other = __shfl(sum, o * P);
+        rank += (other > sum || (other == sum && o < g)) ? 1 : 0;
+      }
+      const uint64_t keep = __ballot(g < p.G && rank < p.top_groups);  // a group's P lanes agree
+#pragma unroll
+      for (int i = 0; i < NS; ++i) {
+        const int e = lane + 64 * i;
+        if (e < E && !((keep >> (e / gs * P)) & 1)) avail &= ~(1u << i);
+      }
+      __builtin_amdgcn_wave_barrier();
+    }
+    // k rounds: the largest key left, the lowest expert that has it; lane j
+    // keeps the round's expert and its score
+    int my_e = 0;
+    double my_s = 0.0;
+    for (int j = 0; j < k; ++j) {
+      key_t best = -__builtin_inff();
+#pragma unroll
+      for (int i = 0; i < NS; ++i)
+        if ((avail >> i) & 1) best = key[i] > best ? key[i] : best;
+      best = wave_max(best);
+      int pick = -1;
+#pragma unroll
+      for (int i = 0; i < NS; ++i) {
+        const uint64_t has = __ballot(((avail >> i) & 1) && key[i] == best);
+        if (pick < 0 && has) pick = 64 * i + (int)__ffsll((unsigned long long)has) - 1;
+      }
+      const int slot = pick >> 6, owner = pick & 63;
+      double sv = 0.0;
+      float xv = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NS; ++i)
+        if (i == slot) {
+          if (WIDE) sv = s[i];
+          else xv = x[i];
+        }
+      if (WIDE) sv = __shfl(sv, owner);
+      else sv = (double)__shfl(xv, owner);
+      if (lane == owner) avail &= ~(1u << slot);
+      if (lane == j) {
+        my_e = pick;
+        my_s = sv;
+      }
+    }
+    if (!WIDE) my_s = soft ? exp(my_s - m) / z : 1.0 / (1.0 + exp(-my_s));
+    if (p.renorm) {
+      const double total = wave_sum(lane < k ? my_s : 0.0);
+      my_s = total > 0.0 ? my_s / total : 0.0;
+    }
+    if (lane < k) {
+      p.experts[(t0 + tt) * k + lane] = my_e;
+      p.weights[(t0 + tt) * k + lane] = (float)my_s;
+      s_ex[tt * k + lane] = my_e;
+      atomicOr(reinterpret_cast<uint32_t*>(&s_mask[my_e]) + (tt >> 5), 1u << (tt & 31));
+    }
+  }
+  __syncthreads();
+  if (p.blocks > 1) {
+    for (int e = threadIdx.x; e < E; e += RT_THREADS) {
+      p.masks[(int64_t)blockIdx.x * E + e] = s_mask[e];
+      p.counts[(int64_t)blockIdx.x * E + e] = (uint8_t)__popcll(s_mask[e]);
+    }
+    return;
+  }
+  for (int e = threadIdx.x; e < E; e += RT_THREADS) s_base[e] = (int)__popcll(s_mask[e]);
+  __syncthreads();
+  block_scan(s_base, E, s_tmp, &s_total);
+  for (int e = threadIdx.x; e < E; e += RT_THREADS) p.offsets[e] = s_base[e];
+  if (threadIdx.x == 0) p.offsets[E] = s_total;
+  write_rows(p, t0, nt, s_ex, s_mask, s_base);
+}
+
+// Expert order over all workgroups' tokens: a workgroup sums every block's
+// counts (all of them for the experts' offsets, the earlier blocks' for its
+// own base) and places its rows.
+__global__ __launch_bounds__(RT_THREADS) void k_route_order(RouteArgs p) {
+  __shared__ int s_base[RT_MAX_E], s_before[RT_MAX_E];
+  __shared__ int s_tmp[RT_THREADS / 64], s_total;
+  __shared__ uint64_t s_mask[RT_MAX_E];
+  const int E = p.E;
+  const int64_t t0 = (int64_t)blockIdx.x * RT_TOK;
+  const int nt = (int)min((int64_t)RT_TOK, p.T - t0);
+  for (int e = threadIdx.x; e < E; e += RT_THREADS) {
+    int all = 0, before = 0;
+    for (int b = 0; b < p.blocks; ++b) {
+      const int c = p.counts[(int64_t)b * E + e];
+      all += c;
+      before += b < (int)blockIdx.x ? c : 0;
+    }
+    s_base[e] = all;
+    s_before[e] = before;
+    s_mask[e] = p.masks[(int64_t)blockIdx.x * E + e];
+  }
+  __syncthreads();
+  block_scan(s_base, E, s_tmp, &s_total);
+  if (blockIdx.x == 0) {
+    for (int e = threadIdx.x; e < E; e += RT_THREADS) p.offsets[e] = s_base[e];
+    if (threadIdx.x == 0) p.offsets[E] = s_total;
+  }
+  for (int e = threadIdx.x; e < E; e += RT_THREADS) s_base[e] += s_before[e];
+  __syncthreads();
+  write_rows(p, t0, nt, p.experts + t0 * p.k, s_mask, s_base);
+}
+
+// Gradient of the logits, one wave per token.  With p the chosen scores and
+// dp their gradient (through the renormalisation w = p / sum p when there is
+// one: dp = (dw - sum(dw w)) / sum p):
+//   softmax: dx_i = -score_i sum(dp p), plus dp_i score_i where chosen
+//   sigmoid: dx_i = dp_i score_i (1 - score_i) where chosen, else 0
+template <int NS>
+__global__ __launch_bounds__(256) void k_route_backward(const void* logits, int f32, int64_t T,
+                                                        int64_t ldx, int E, int k, int score,
+                                                        int renorm, const int32_t* experts,
+                                                        const float* d_weights, void* d_logits,
+                                                        int64_t ldd) {
+  const int lane = threadIdx.x & 63;
+  const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (t >= T) return;
+  const bool soft = score == FP4Q_SCORE_SOFTMAX;
+  float x[NS];
+  float top = -__builtin_inff();
+#pragma unroll
+  for (int i = 0; i < NS; ++i) {
+    const int e = lane + 64 * i;
+    x[i] = e < E ? load_logit(logits, f32, t * ldx + e) : -__builtin_inff();
+    top = fmaxf(top, x[i]);
+  }
+  top = wave_max(top);
+  const double m = top > -__builtin_inff() ? (double)top : 0.0;
+  double s[NS], z = 1.0;
+  if (soft) {
+    double part = 0.0;
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+      s[i] = lane + 64 * i < E ? exp((double)x[i] - m) : 0.0;
+      part += s[i];
+    }
+    z = wave_sum(part);
+    if (!(z > 0.0)) z = 1.0;
+#pragma unroll
+    for (int i = 0; i < NS; ++i) s[i] /= z;
+  }
+  // lane j: the j-th chosen expert (indices outside the experts: no gradient)
+  const int e = lane < k ? experts[t * k + lane] : -1;
+  const bool on = e >= 0 && e < E;
+  double p = 0.0, dw = 0.0;
+  if (on) {
+    const double xe = (double)load_logit(logits, f32, t * ldx + e);
+    p = soft ? exp(xe - m) / z : 1.0 / (1.0 + exp(-xe));
+    dw = (double)d_weights[t * k + lane];
+  }
+  if (renorm) {
+    const double sum = wave_sum(p), dot = wave_sum(dw * p);
+    dw = on && sum > 0.0 ? (dw - dot / sum) / sum : 0.0;
+  }
+  const double dot = soft ? wave_sum(dw * p) : 0.0;
+  const double add = soft ? dw * p : dw * p * (1.0 - p);
+  double dx[NS];
+#pragma unroll
+  for (int i = 0; i < NS; ++i) dx[i] = soft ? -s[i] * dot : 0.0;
+  for (int j = 0; j < k; ++j) {
+    const int ej = __shfl(e, j);
+    const double aj = __shfl(add, j);
+    if (ej >= 0 && (ej & 63) == lane) {
+#pragma unroll
+      for (int i = 0; i < NS; ++i)
+        if (i == ej >> 6) dx[i] += aj;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NS; ++i) {
+    const int c = lane + 64 * i;
+    if (c < E) {
+      if (f32) reinterpret_cast<float*>(d_logits)[t * ldd + c] = (float)dx[i];
+      else reinterpret_cast<__bf16*>(d_logits)[t * ldd + c] = (__bf16)(float)dx[i];
+    }
+  }
+}
+
+// ---- the combination --------------------------------------------------------
+
+// VEC consecutive values as f32: 8 BF16 (16 bytes) or 4 F32, or one of either.
+template <bool F32, int VEC>
+__device__ __forceinline__ void load_vec(const void* x, int64_t i, float (&v)[VEC]) {
+  if (VEC == 1) {
+    v[0] = load_logit(x, F32, i);
+  } else if (F32) {
+#pragma unroll
+    for (int c = 0; c < VEC / 4; ++c) {
+      const u32x4 u = reinterpret_cast<const u32x4*>(reinterpret_cast<const float*>(x) + i)[c];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[4 * c + e] = __uint_as_float(u[e]);
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < VEC / 8; ++c) {
+      const u32x4 u = reinterpret_cast<const u32x4*>(reinterpret_cast<const uint16_t*>(x) + i)[c];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[8 * c + 2 * e] = __uint_as_float(u[e] << 16);
+        v[8 * c + 2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
+      }
+    }
+  }
+}
+
+template <bool F32, int VEC>
+__device__ __forceinline__ void store_vec(void* y, int64_t i, const float (&v)[VEC]) {
+  if (VEC == 1) {
+    if (F32) reinterpret_cast<float*>(y)[i] = v[0];
+    else reinterpret_cast<__bf16*>(y)[i] = (__bf16)v[0];
+  } else if (F32) {
+#pragma unroll
+    for (int c = 0; c < VEC / 4; ++c) {
+      u32x4 u;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) u[e] = __float_as_uint(v[4 * c + e]);
+      reinterpret_cast<u32x4*>(reinterpret_cast<float*>(y) + i)[c] = u;
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < VEC / 8; ++c) {
+      u32x4 u;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const v2f32r f = {v[8 * c + 2 * e], v[8 * c + 2 * e + 1]};
+        u[e] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f, bf16x2r));
+      }
+      reinterpret_cast<u32x4*>(reinterpret_cast<uint16_t*>(y) + i)[c] = u;
+    }
+  }
+}
+
+struct CombineArgs {
+  const void* y;
+  int64_t rows, N, ldy;
+  const int32_t* row_of;
+  const float* w;
+  int64_t T;
+  int k;
+  void* out;
+  int64_t ldo;
+  const void* d_out;
+  void* d_y;
+  int64_t lddy;
+  float* d_w;
+};
+
+// out[t] = sum_j w[t, j] y[row_of[t, j]]: a thread holds VEC columns of one
+// token, the rows added in order j in FP32.
+template <bool F32, int VEC>
+__global__ __launch_bounds__(256) void k_combine(CombineArgs p) {
+  const int64_t per = p.N / VEC;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= p.T * per) return;
+  const int64_t t = i / per, c = (i - t * per) * VEC;
+  float acc[VEC];
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) acc[e] = 0.0f;
+#pragma unroll 8
+  for (int j = 0; j < p.k; ++j) {
+    const int64_t r = p.row_of[t * p.k + j];
+    if (r < 0 || r >= p.rows) continue;
+    const float w = p.w[t * p.k + j];
+    float v[VEC];
+    load_vec<F32, VEC>(p.y, r * p.ldy + c, v);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) acc[e] = __builtin_fmaf(w, v[e], acc[e]);
+  }
+  store_vec<F32, VEC>(p.out, t * p.ldo + c, acc);
+}
+
+// d_y[row_of[t, j]] = w[t, j] d_out[t], d_w[t, j] = y[row_of[t, j]] . d_out[t]:
+// one wave per (token, j), the products summed in FP32.
+template <bool F32, int VEC>
+__global__ __launch_bounds__(256) void k_combine_backward(CombineArgs p) {
+  const int lane = threadIdx.x & 63;
+  const int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (i >= p.T * p.k) return;
+  const int64_t t = i / p.k, r = p.row_of[i];
+  if (r < 0 || r >= p.rows) {
+    if (lane == 0) p.d_w[i] = 0.0f;
+    return;
+  }
+  const float w = p.w[i];
+  float dot = 0.0f;
+  for (int64_t c = (int64_t)lane * VEC; c < p.N; c += 64 * VEC) {
+    float v[VEC], d[VEC];
+    load_vec<F32, VEC>(p.y, r * p.ldy + c, v);
+    load_vec<F32, VEC>(p.d_out, t * p.ldo + c, d);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      dot = __builtin_fmaf(v[e], d[e], dot);
+      d[e] *= w;
+    }
+    store_vec<F32, VEC>(p.d_y, r * p.lddy + c, d);
+  }
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) dot += __shfl_xor(dot, d);
+  if (lane == 0) p.d_w[i] = dot;
+}
+
+inline bool vec_ok(const void* p, int64_t ld, int esz) {
+  return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (ld * esz) % 16 == 0;
+}
+
+}  // namespace
+
+size_t route_workspace_bytes(int64_t T, int E) {
+  const int64_t blocks = (T + RT_TOK - 1) / RT_TOK;
+  return blocks > 1 ? (size_t)(blocks * E * 9) : 0;
+}
+
+void launch_route(const void* logits, int f32, int64_t T, int64_t ldx, int E, int k, int score,
+                  const float* bias, int G, int top_groups, int renorm, int32_t* experts,
+                  float* weights, int32_t* offsets, int32_t* row_src, int32_t* row_of, void* ws,
+                  hipStream_t stream) {
+  const int blocks = (int)((T + RT_TOK - 1) / RT_TOK);
+  RouteArgs p = {logits,  f32,     T,       ldx,     E,      k,  score, G, top_groups, renorm, bias,
+                 experts, weights, offsets, row_src, row_of, nullptr, nullptr, blocks > 0 ? blocks : 1};
+  if (blocks > 1) {
+    p.masks = static_cast<uint64_t*>(ws);
+    p.counts = reinterpret_cast<uint8_t*>(p.masks + (int64_t)blocks * E);
+  }
+  const bool wide = bias != nullptr || G > 1;
+  const dim3 grid((unsigned)p.blocks), thr(RT_THREADS);
+  const size_t lds = G > 1 ? (size_t)(RT_THREADS / 64) * E * sizeof(double) : 0;
+#define FP4Q_ROUTE(N)                                                                    \
+  if (wide) hipLaunchKernelGGL((k_route_pick<N, true>), grid, thr, lds, stream, p);      \
+  else hipLaunchKernelGGL((k_route_pick<N, false>), grid, thr, 0, stream, p)
+  if (E <= 64) { FP4Q_ROUTE(1); }
+  else if (E <= 128) { FP4Q_ROUTE(2); }
+  else if (E <= 256) { FP4Q_ROUTE(4); }
+  else { FP4Q_ROUTE(8); }
+#undef FP4Q_ROUTE
+  if (blocks > 1) hipLaunchKernelGGL(k_route_order, grid, thr, 0, stream, p);
+}
+
+void launch_route_backward(const void* logits, int f32, int64_t T, int64_t ldx, int E, int k,
+                           int score, int renorm, const int32_t* experts, const float* d_weights,
+                           void* d_logits, int64_t ldd, hipStream_t stream) {
+  const dim3 grid((unsigned)((T + 3) / 4)), thr(256);
+#define FP4Q_ROUTE(N)                                                                         \
+  hipLaunchKernelGGL((k_route_backward<N>), grid, thr, 0, stream, logits, f32, T, ldx, E, k,  \
+                     score, renorm, experts, d_weights, d_logits, ldd)
+  if (E <= 64) FP4Q_ROUTE(1);
+  else if (E <= 128) FP4Q_ROUTE(2);
+  else if (E <= 256) FP4Q_ROUTE(4);
+  else FP4Q_ROUTE(8);
+#undef FP4Q_ROUTE
+}
+
+void launch_combine(int f32, const void* y, int64_t rows, int64_t N, int64_t ldy,
+                    const int32_t* row_of, const float* w, int64_t T, int k, void* out,
+                    int64_t ldo, hipStream_t stream) {
+  const CombineArgs p = {y, rows, N, ldy, row_of, w, T, k, out, ldo, nullptr, nullptr, 0, nullptr};
+  const int esz = f32 ? 4 : 2;
+  const bool vec = N % 8 == 0 && vec_ok(y, ldy, esz) && vec_ok(out, ldo, esz);
+  const int64_t items = T * (vec ? N / 8 : N);
+  const dim3 grid((unsigned)((items + 255) / 256)), thr(256);
+  if (f32) {
+    if (vec) hipLaunchKernelGGL((k_combine<true, 8>), grid, thr, 0, stream, p);
+    else hipLaunchKernelGGL((k_combine<true, 1>), grid, thr, 0, stream, p);
+  } else {
+    if (vec) hipLaunchKernelGGL((k_combine<false, 8>), grid, thr, 0, stream, p);
+    else hipLaunchKernelGGL((k_combine<false, 1>), grid, thr, 0, stream, p);
+  }
+}
+
+void launch_combine_backward(int f32, const void* y, int64_t rows, int64_t N, int64_t ldy,
+                             const int32_t* row_of, const float* w, int64_t T, int k,
+                             const void* d_out, int64_t ldo, void* d_y, int64_t lddy, float* d_w,
+                             hipStream_t stream) {
+  const CombineArgs p = {y,       rows, N,     ldy, row_of, w,  T,
+                         k,       nullptr, ldo, d_out, d_y, lddy, d_w};
+  const int esz = f32 ? 4 : 2;
+  const bool vec = N % 8 == 0 && vec_ok(y, ldy, esz) && vec_ok(d_out, ldo, esz) &&
+                   vec_ok(d_y, lddy, esz);
+  const dim3 grid((unsigned)((T * k + 3) / 4)), thr(256);
+  if (f32) {
+    if (vec) hipLaunchKernelGGL((k_combine_backward<true, 8>), grid, thr, 0, stream, p);
+    else hipLaunchKernelGGL((k_combine_backward<true, 1>), grid, thr, 0, stream, p);
+  } else {
+    if (vec) hipLaunchKernelGGL((k_combine_backward<false, 8>), grid, thr, 0, stream, p);
+    else hipLaunchKernelGGL((k_combine_backward<false, 1>), grid, thr, 0, stream, p);
+  }
+}
+
+}  // namespace fp4q

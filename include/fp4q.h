@@ -660,6 +660,178 @@ int fp4q_grouped_gemm_gather(fp4q_format_t fmt, fp4q_layout_t w_layout, int64_t 
                              size_t comp_w_bytes, void* y, fp4q_dtype_t y_dtype, void* stream);
 
 /* ------------------------------------------------------------------------
+ * Between the FP4 linear layers of a rollout decoder layer: the key/value
+ * cache held in FP4, attention over it, the router of the expert layer and
+ * the combination of the experts' outputs.
+ *
+ * The paged FP4 key/value cache.  A cache is u8 [n_pages, kv_heads, B]
+ * (16-byte aligned), B = fp4q_kv_page_bytes(fmt, page, dim) bytes for each
+ * page of `page` tokens (a power of two, 16 .. 1024) and each head of `dim`
+ * elements (64, 128 or 256), in this order:
+ *   K codes   token s of the page at s * dim/2, two neighbouring elements to
+ *             a byte, the even one in the low nibble
+ *   V codes   by groups of four tokens: element d of token s is in byte
+ *             (s/4) * 2 dim + ((d % 16) * 4 + s % 4) * dim/32 + d/32, in
+ *             the low nibble where d % 32 < 16, else in the high one
+ *   K scales  [page, dim/blk] block scale codes
+ *   V scales  [page, dim/blk]
+ * Every byte belongs to one token.  The V order puts the four tokens'
+ * values that one lane of a 16-row matrix instruction needs side by side.
+ * Blocks run along the head's elements and are quantized as by
+ * fp4q_quantize; NVFP4's tensor scale is given, one for each head
+ * (k_scale, v_scale: device f32 [kv_heads], positive, of calibrated keys
+ * and values; values beyond 2688 times it saturate); NULL for MXFP4.
+ *
+ * Sequences: sequence b owns the pages page_table[b, 0 .. table_cols)
+ * (device int32, row stride ld_table), token position p in page p / page.  Its new tokens
+ * are rows offsets[b] .. offsets[b+1] of the packed tensors (device int32
+ * [batch + 1], offsets[0] = 0), its length with them lens[b] (device int32
+ * [batch]), so that the new tokens stand at the end: new token i at position
+ * lens[b] - (offsets[b+1] - offsets[b]) + i.  A page number outside the
+ * cache (-1 for a page that a sliding window has left, say), a position
+ * past the table or below 0 is never read or written: nothing is stored for
+ * such a token, reading gives zeros, and attention does not see it.
+ * Pages that several sequences share are read by all (append to none).
+ *
+ * fp4q_kv_append quantizes k, v (bf16, row strides ldk, ldv elements,
+ * multiples of 8, 16-byte aligned; heads one after another) into the
+ * cache.  fp4q_kv_read writes the values that stand there for the same
+ * rows: bf16 of (e2m1 * scale) * t (NVFP4) or of e2m1 * 2^e (MXFP4).
+ * rows = offsets[batch] (further rows: not stored, read as zeros).
+ * FP4Q_ERR_UNSUPPORTED: another dim or page, or rows * kv_heads * dim / 32
+ * not below 2^31.  No workspace.
+ * ------------------------------------------------------------------------ */
+size_t fp4q_kv_page_bytes(fp4q_format_t fmt, int32_t page, int32_t dim); /* 0: not supported */
+
+int fp4q_kv_append(fp4q_format_t fmt, uint8_t* cache, int64_t n_pages, int32_t page,
+                   int32_t kv_heads, int32_t dim, const int32_t* offsets, int32_t batch,
+                   const int32_t* page_table, int64_t ld_table,
+                   int64_t table_cols, const int32_t* lens, int64_t rows,
+                   const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ldv,
+                   const float* k_scale, const float* v_scale, void* stream);
+
+int fp4q_kv_read(fp4q_format_t fmt, const uint8_t* cache, int64_t n_pages, int32_t page,
+                 int32_t kv_heads, int32_t dim, const int32_t* offsets, int32_t batch,
+                 const int32_t* page_table, int64_t ld_table,
+                 int64_t table_cols, const int32_t* lens, int64_t rows,
+                 uint16_t* k, int64_t ldk, uint16_t* v, int64_t ldv, const float* k_scale,
+                 const float* v_scale, void* stream);
+
+/* Attention of the new tokens over the cache (their own keys and values
+ * stored before):
+ *
+ *   y[r, h] = sum_j softmax_j(scale q[r, h] . K[j, g]) V[j, g]
+ *
+ * over the keys j of the row's sequence with j <= position(r), and, with
+ * window > 0, j > position(r) - window; g = h / (heads / kv_heads).  A row
+ * that sees no key gives 0.  What stands in the cache outside these keys
+ * (NaN scales included) does not reach the result.  One token a sequence
+ * (decode), the few of a speculative step, prompts and chunks of them are
+ * all this call.
+ *
+ *   q              bf16 [rows, heads, dim], row stride ldq (a multiple of 8,
+ *                  16-byte aligned)
+ *   max_new, max_len   host bounds: no sequence has more new tokens, or a
+ *                  greater length (they size the launch; rows or keys past
+ *                  them are left out)
+ *   window         0: none
+ *   scale          of the scores, > 0 (dim^-0.5 as a rule)
+ *   y              out f32 or bf16 [rows, heads, dim], row stride ldy (a
+ *                  multiple of 8, 16-byte aligned)
+ *   workspace      device scratch of fp4q_kv_attention_workspace_bytes()
+ *                  bytes, 16-byte aligned (may be NULL when that is 0): the
+ *                  partial results of keys that are split over workgroups;
+ *                  needs no initialisation
+ *
+ * Keys and values are decoded exactly (f16 for NVFP4, bf16 for MXFP4),
+ * scores, their maximum and sums and the output are FP32, the weights are
+ * rounded once to f16 or bf16 before they meet the values.  For NVFP4 q is
+ * held in f16 relative to its row's largest magnitude (bf16 for MXFP4).
+ * heads % kv_heads == 0; FP4Q_ERR_UNSUPPORTED: another dim or page, more
+ * than 128 heads on one kv head, batch above 65535, or rows * heads not
+ * below 2^31. */
+size_t fp4q_kv_attention_workspace_bytes(fp4q_format_t fmt, int64_t rows, int32_t heads,
+                                         int32_t kv_heads, int32_t dim, int32_t batch,
+                                         int64_t max_new, int64_t max_len, int32_t window);
+
+int fp4q_kv_attention(fp4q_format_t fmt, const uint8_t* cache, int64_t n_pages, int32_t page,
+                      int32_t kv_heads, int32_t dim, const int32_t* offsets, int32_t batch,
+                      const int32_t* page_table, int64_t ld_table, int64_t table_cols,
+                      const int32_t* lens, int64_t rows, const uint16_t* q, int64_t ldq, int32_t heads,
+                      int64_t max_new, int64_t max_len, int32_t window, float scale,
+                      const float* k_scale, const float* v_scale, void* y, fp4q_dtype_t y_dtype,
+                      int64_t ldy, void* workspace, size_t workspace_bytes, void* stream);
+
+/* The router of an expert layer.  Per token t with logits x [experts]:
+ *   score    softmax(x) or sigmoid(x)
+ *   ranked   score + bias (bias: device f32 [experts] or NULL; it chooses,
+ *            and does not enter the weights)
+ *   groups   n_groups equal runs of experts; the top_groups of largest sum
+ *            of their two best ranked scores stay (n_groups 1: no groups)
+ *   experts  the k best ranked of those, best first
+ *   weights  their scores (renorm: divided by their sum)
+ * Ties go to the lower index; NaN ranks last.  A token without a finite
+ * logit has weights 0.  And the order by expert that the grouped calls
+ * above take: row_src (token of each routed row, rows of an expert by
+ * token), group offsets, and row_of (the row of each token's j-th expert).
+ *
+ *   logits     f32 or bf16 (dtype) [tokens, experts], row stride ldx
+ *   experts, row_of   out int32 [tokens, k];  weights out f32 [tokens, k]
+ *   offsets    out int32 [experts + 1];  row_src out int32 [tokens * k]
+ *   workspace  fp4q_route_workspace_bytes() bytes, 8-byte aligned (may be
+ *              NULL when that is 0), no initialisation
+ *
+ * Scores are computed in 64 bits where they decide the order (a bias or
+ * groups).  FP4Q_ERR_UNSUPPORTED: more than 512 experts or 64 groups, k
+ * above 32, or tokens * k not below 2^31.  k may not exceed the experts of
+ * top_groups groups.
+ *
+ * fp4q_route_backward: the gradient of the logits from that of the weights
+ * (d_weights f32 [tokens, k]) and the chosen experts; d_logits has the
+ * logits' type, row stride ldd. */
+#define FP4Q_ROUTE_MAX_EXPERTS 512
+#define FP4Q_ROUTE_MAX_GROUPS 64
+#define FP4Q_ROUTE_MAX_K 32
+typedef enum { FP4Q_SCORE_SOFTMAX = 0, FP4Q_SCORE_SIGMOID = 1 } fp4q_score_t;
+
+size_t fp4q_route_workspace_bytes(int64_t tokens, int32_t experts);
+
+int fp4q_route(const void* logits, fp4q_dtype_t dtype, int64_t tokens, int32_t n_experts,
+               int64_t ldx, int32_t k, fp4q_score_t score, const float* bias, int32_t n_groups,
+               int32_t top_groups, int32_t renorm, int32_t* experts, float* weights,
+               int32_t* offsets, int32_t* row_src, int32_t* row_of, void* workspace,
+               size_t workspace_bytes, void* stream);
+
+int fp4q_route_backward(const void* logits, fp4q_dtype_t dtype, int64_t tokens,
+                        int32_t n_experts, int64_t ldx, int32_t k, fp4q_score_t score,
+                        int32_t renorm, const int32_t* experts, const float* d_weights,
+                        void* d_logits, int64_t ldd, void* stream);
+
+/* The experts' outputs back to the tokens (the last step of the expert
+ * layer):
+ *   out[t] = sum_j weights[t, j] y[row_of[t, j]]
+ * and its gradients, for a row_of that names no row twice:
+ *   d_y[row_of[t, j]] = weights[t, j] d_out[t]
+ *   d_weights[t, j]   = y[row_of[t, j]] . d_out[t]
+ *
+ *   y, out, d_out, d_y   f32 or bf16 (dtype, the same for all), row strides
+ *              ldy, ldo, ldo, lddy; y and d_y have `rows` rows of cols
+ *   row_of     device int32 [tokens, k]; an entry outside the rows adds
+ *              nothing and has d_weights 0
+ *   weights, d_weights   f32 [tokens, k]
+ * Sums are FP32 in the order of j.  d_y's rows that row_of does not name
+ * are not written.  FP4Q_ERR_UNSUPPORTED: k above 128, tokens * k or
+ * tokens * cols / 8 not below 2^31. */
+int fp4q_combine(fp4q_dtype_t dtype, const void* y, int64_t rows, int64_t cols, int64_t ldy,
+                 const int32_t* row_of, const float* weights, int64_t tokens, int32_t k,
+                 void* out, int64_t ldo, void* stream);
+
+int fp4q_combine_backward(fp4q_dtype_t dtype, const void* y, int64_t rows, int64_t cols,
+                          int64_t ldy, const int32_t* row_of, const float* weights,
+                          int64_t tokens, int32_t k, const void* d_out, int64_t ldo, void* d_y,
+                          int64_t lddy, float* d_weights, void* stream);
+
+/* ------------------------------------------------------------------------
  * Exact three-way MXFP4 error decomposition ("Decomposing MXFP4
  * quantization error ...", abstract).  Per 32-block with actual scale
  * s = 2^e and ideal scale s* = amax/6, per element x:
