@@ -26,7 +26,8 @@ namespace {
 
 typedef float v16f __attribute__((ext_vector_type(16)));
 
-constexpr int TILE_KEYS = 64;
+// Keys of a step.
+template <int D> struct TileKeys { static constexpr int N = D <= 128 ? 64 : 32; };
 
 template <int FMT> struct Wide;
 template <> struct Wide<FP4Q_NVFP4> {
@@ -45,31 +46,50 @@ template <> struct Wide<FP4Q_MXFP4> {
 // reads cover all banks.
 template <int D>
 struct TileLds {
-  static constexpr int KROW = D * 2 + 16;
-  static constexpr int VROW = TILE_KEYS * 2 + 16;
-  static constexpr int V0 = TILE_KEYS * KROW;
-  static constexpr int BYTES = V0 + D * VROW;
+  static constexpr int TILE_KEYS = TileKeys<D>::N;
+  static constexpr int KROW = D * 2 + 16, KBYTES = TILE_KEYS * KROW, KBUFS = 3;
+  static constexpr int VROW = TILE_KEYS * 2 + 16, VBYTES = D * VROW;
+  static constexpr int V0 = KBUFS * KBYTES;
+  static constexpr int BYTES = V0 + 2 * VBYTES;
 };
 
-// The cache bytes that a thread decodes for one step.  K: 32 elements of one
-// key; V: the four tokens of a group, elements c, c + 16, ...
-template <int FMT, int D, int TEAM>
+// The cache bytes that a wave decodes for one step: UNITS times 16 keys, which
+// stand in one page (its number and address are scalars).  A lane has of K the
+// 32-element runs lane, lane + 64, ... of the 16 keys (ITEMS of them), of V four
+// tokens' elements lane % 16, lane % 16 + 16, ...
+template <int FMT, int D, int TEAM_WAVES>
 struct Staged {
   typedef KvLayout<FMT, D> L;
-  static constexpr int K_ITEMS = TILE_KEYS * (D / 32);
-  static constexpr int V_ITEMS = TILE_KEYS * 4;
-  static constexpr int NK = (K_ITEMS + TEAM - 1) / TEAM;
-  static constexpr int NV = (V_ITEMS + TEAM - 1) / TEAM;
-  static constexpr int VC = D / 32, VS = L::SB;  // dwords of codes and scales of a V item
-  static constexpr int NK_W = NK * 5, NV_W = NV * (VC + VS);
-  uint32_t w[NK_W > NV_W ? NK_W : NV_W];
-  int id[NK > NV ? NK : NV];  // pages of the step after
+  static constexpr int UNITS = TileKeys<D>::N / 16 / TEAM_WAVES;
+  static constexpr int ITEMS = (16 * L::J + 63) / 64;
+  static constexpr int VC = D / 32, VS = L::SB;  // dwords of codes and scales of a V unit
+  static constexpr int K_W = ITEMS * 5, V_W = VC + VS, W = K_W > V_W ? K_W : V_W;
+  uint32_t w[UNITS][W];
+  int id[UNITS];    // pages of the step after (-1: none)
+  bool good[UNITS]; // are those of the staged step in the cache?
 };
+
+// The page table's entries, which no kernel writes while this one runs, through
+// the scalar cache.
+typedef const __attribute__((address_space(4))) int32_t* TablePtr;
 
 __device__ __forceinline__ float other_half_max(float v) {
   const u32x2 r = __builtin_bit_cast(
       u32x2, __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false));
   return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
+// Asks the scheduler for N products fed by N LDS reads with AHEAD of the reads
+// in flight: left alone, it reads, waits and multiplies by turns.
+template <int N, int AHEAD>
+__device__ __forceinline__ void pipeline_reads() {
+  __builtin_amdgcn_sched_group_barrier(0x100, AHEAD, 0);  // LDS reads
+#pragma unroll
+  for (int i = 0; i < N - AHEAD; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // a product
+    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+  }
+  __builtin_amdgcn_sched_group_barrier(0x008, AHEAD, 0);
 }
 
 template <int FMT, int D, int WAVES>
@@ -78,9 +98,10 @@ __global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void k_attn_tile(Attn
   typedef typename Num<FMT>::pair pair;
   typedef KvLayout<FMT, D> L;
   typedef TileLds<D> S;
-  constexpr int TEAM = 32 * WAVES;  // threads that decode K; as many decode V
-  typedef Staged<FMT, D, TEAM> St;
-  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];  // two steps' K and V
+  constexpr int TILE_KEYS = TileKeys<D>::N, NU = TILE_KEYS / 32;
+  constexpr uint32_t ALL_OK = NU == 2 ? 0x01010101u : 0x0101u;
+  typedef Staged<FMT, D, WAVES / 2> St;
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   // of the last steps, byte u: is the page of keys 16u .. 16u + 15 in the cache?
   __shared__ uint32_t s_ok[4];
 
@@ -91,16 +112,17 @@ __global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void k_attn_tile(Attn
   const uint32_t bh = (blockIdx.x + blockIdx.y) % gridDim.x;
   const int b = bh / p.H, h = bh - b * p.H;
   // the last rows, which see the most keys, first
-  const int row0 = (int)(gridDim.y - 1 - blockIdx.y) * p.tile;
   const int n_rows = (p.off[b + 1] - p.off[b]) * p.G;
-  if (row0 >= n_rows) return;
+  const int tile_id = min((n_rows + p.tile - 1) / p.tile, (int)gridDim.y) - 1 - (int)blockIdx.y;
+  if (tile_id < 0) return;
+  const int row0 = tile_id * p.tile;
   const Range rg = tile_range(p, b, row0);
   const int split = blockIdx.z;
   if (split >= active_splits(p, rg)) return;
   const int k0 = rg.lo + split * p.chunk;
   const int k1 = min(rg.hi, k0 + p.chunk);
   const int page = 1 << p.page_shift;
-  const int32_t* table = p.table + b * p.ldt;
+  const TablePtr table = (TablePtr)(uintptr_t)(p.table + b * p.ldt);
   const uint32_t n_pages = (uint32_t)min(p.n_pages, (int64_t)0x7FFFFFFF);
 
   // ---- this wave's rows -----------------------------------------------------
@@ -148,161 +170,162 @@ __global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void k_attn_tile(Attn
 
   // ---- loading and decoding -------------------------------------------------
   const bool v_team = wave < WAVES / 2;
-  const int tid = threadIdx.x & (TEAM - 1);
+  const int unit0 = wave % (WAVES / 2);  // its units: unit0, unit0 + WAVES / 2, ...
   St st;
-  // page numbers of the step that starts at kt (past the last key: any)
-  auto load_ids = [&](int kt) {
-    if (v_team) {
+  const int64_t page_stride = (int64_t)p.H * L::bytes(page), head0 = h * (int64_t)L::bytes(page);
+  // page numbers of step t
+  auto load_ids = [&](int t) {
 #pragma unroll
-      for (int n = 0; n < St::NV; ++n)
-        st.id[n] = table[min(kt + 4 * ((tid + n * TEAM) >> 4), k1 - 1) >> p.page_shift];
-    } else {
-#pragma unroll
-      for (int n = 0; n < St::NK; ++n)
-        st.id[n] = table[min(kt + (tid + n * TEAM) / (D / 32), k1 - 1) >> p.page_shift];
+    for (int n = 0; n < St::UNITS; ++n) {
+      const int key = k0 + t * TILE_KEYS + 16 * (unit0 + n * (WAVES / 2));
+      st.id[n] = key < k1 ? table[key >> p.page_shift] : -1;
     }
   };
-  // bytes of the step at kt, from st.id; the K team notes which pages are good
-  auto load_bytes = [&](int kt) {
-    if (v_team) {
+  // bytes of step t, from st.id; the K team notes which pages are good
+  auto load_bytes = [&](int t) {
 #pragma unroll
-      for (int n = 0; n < St::NV; ++n) {
-        const int item = tid + n * TEAM, key = kt + 4 * (item >> 4);
-        const bool good = (uint32_t)st.id[n] < n_pages;
-        const int64_t id = good ? st.id[n] : 0;  // (some page's bytes: their scales become 0)
-        const uint8_t* base = p.cache + (id * p.H + h) * (int64_t)L::bytes(page);
-        const int slot = key & (page - 1);
-        uint32_t* w = st.w + n * (St::VC + St::VS);
+    for (int n = 0; n < St::UNITS; ++n) {
+      const int unit = unit0 + n * (WAVES / 2);
+      const bool good = (uint32_t)st.id[n] < n_pages;
+      st.good[n] = good;
+      // (for a page that is not in the cache some page's bytes, all masked)
+      const uint8_t* base = p.cache + (good ? st.id[n] : 0) * page_stride + head0;
+      const int slot = (k0 + t * TILE_KEYS + 16 * unit) & (page - 1);
+      if (v_team) {
         uint32_t c[St::VC], s[St::VS];
-        load_words(base + L::v_codes(page) + slot * (D / 2) + (item & 15) * (D / 8), c);
-        load_words(base + L::v_scales(page) + slot * L::SB, s);
+        load_words(base + L::v_codes(page) + slot * (D / 2) + (uint32_t)(lane * (D / 8)), c);
+        load_words(base + L::v_scales(page) + slot * L::SB + (uint32_t)((lane >> 4) * 4 * L::SB), s);
 #pragma unroll
-        for (int i = 0; i < St::VC; ++i) w[i] = c[i];
+        for (int i = 0; i < St::VC; ++i) st.w[n][i] = c[i];
 #pragma unroll
-        for (int i = 0; i < St::VS; ++i) w[St::VC + i] = s[i];
-      }
-    } else {
+        for (int i = 0; i < St::VS; ++i) st.w[n][St::VC + i] = s[i];
+      } else {
+        const uint8_t *kc = base + slot * (D / 2), *ks = base + L::k_scales(page) + slot * L::SB;
 #pragma unroll
-      for (int n = 0; n < St::NK; ++n) {
-        const int item = tid + n * TEAM, key = kt + item / (D / 32), part = item % (D / 32);
-        if (St::K_ITEMS % TEAM != 0 && item >= St::K_ITEMS) continue;
-        const bool good = (uint32_t)st.id[n] < n_pages;
-        const int64_t id = good ? st.id[n] : 0;
-        const uint8_t* base = p.cache + (id * p.H + h) * (int64_t)L::bytes(page);
-        const int slot = key & (page - 1);
-        const w4 u = *reinterpret_cast<const w4*>(base + slot * (D / 2) + part * 16);
+        for (int i = 0; i < St::ITEMS; ++i) {
+          const uint32_t run = lane + 64 * i;
+          if (16 * L::J < 64 && run >= 16 * L::J) continue;
+          const w4 u = *reinterpret_cast<const w4*>(kc + run * 16);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) st.w[n * 5 + i] = u[i];
-        const uint8_t* ks = base + L::k_scales(page) + slot * L::SB;
-        if (FMT == FP4Q_NVFP4) st.w[n * 5 + 4] = reinterpret_cast<const uint16_t*>(ks)[part];
-        else st.w[n * 5 + 4] = ks[part];
-        if (part == 0 && (key & 15) == 0)
-          reinterpret_cast<uint8_t*>(&s_ok[(key / TILE_KEYS) & 3])[(key >> 4) & 3] = good ? 1 : 0;
+          for (int e = 0; e < 4; ++e) st.w[n][5 * i + e] = u[e];
+          if (FMT == FP4Q_NVFP4) st.w[n][5 * i + 4] = *reinterpret_cast<const uint16_t*>(ks + run * 2);
+          else st.w[n][5 * i + 4] = ks[run];
+        }
+        if (lane == 0) reinterpret_cast<uint8_t*>(&s_ok[t & 3])[unit] = good ? 1 : 0;
       }
     }
   };
   // the staged bytes as values in LDS
-  auto decode = [&](int kt, int buf, uint32_t bad) {
-    uint8_t* base = lds + buf * S::BYTES;
-    if (v_team) {
+  uint8_t* const vdst = lds + S::V0 + (lane & 15) * S::VROW + ((lane >> 4) & 1) * 16 + (lane >> 5) * 8;
+  auto decode = [&](int t) {
 #pragma unroll
-      for (int n = 0; n < St::NV; ++n) {
-        const int item = tid + n * TEAM, grp = item >> 4, c = item & 15;
+    for (int n = 0; n < St::UNITS; ++n) {
+      const int unit = unit0 + n * (WAVES / 2);
+      if (v_team) {
         Sub<FMT, D> s;
-        uint32_t* w = st.w + n * (St::VC + St::VS);
 #pragma unroll
-        for (int i = 0; i < St::VC; ++i) s.v[i] = w[i];
+        for (int i = 0; i < St::VC; ++i) s.v[i] = st.w[n][i];
 #pragma unroll
-        for (int i = 0; i < St::VS; ++i) s.vs[i] = w[St::VC + i];
-        const int key = kt + 4 * grp;
-        if (((bad >> n) & 1) || key < rg.seen || key + 4 > rg.hi)
-          zero_v_scales<FMT, D>(s, key, (bad >> n) & 1, rg.seen, rg.hi);
-        uint8_t* dst = base + S::V0 + c * S::VROW + (grp >> 2) * 32 + (grp & 1) * 16 + ((grp >> 1) & 1) * 8;
+        for (int i = 0; i < St::VS; ++i) s.vs[i] = st.w[n][St::VC + i];
+        const int key = k0 + t * TILE_KEYS + 16 * unit;
+        if (!st.good[n] || key < rg.seen || key + 16 > rg.hi)
+          zero_v_scales<FMT, D>(s, key + 4 * (lane >> 4), !st.good[n], rg.seen, rg.hi);
+        uint8_t* dst = vdst + (t & 1) * S::VBYTES + unit * 32;
         v_rows<FMT, D, 0>(s, [&](int run, u32x2 lo, u32x2 hi) {
           *reinterpret_cast<u32x2*>(dst + (32 * run) * S::VROW) = lo;
           *reinterpret_cast<u32x2*>(dst + (32 * run + 16) * S::VROW) = hi;
         });
-      }
-    } else {
+      } else {
 #pragma unroll
-      for (int n = 0; n < St::NK; ++n) {
-        const int item = tid + n * TEAM, key = item / (D / 32), part = item % (D / 32);
-        if (St::K_ITEMS % TEAM != 0 && item >= St::K_ITEMS) continue;
-        uint8_t* dst = base + key * S::KROW + part * 64;
+        for (int i = 0; i < St::ITEMS; ++i) {
+          const int run = lane + 64 * i;
+          if (16 * L::J < 64 && run >= 16 * L::J) continue;
+          uint8_t* dst = lds + t % S::KBUFS * S::KBYTES + (16 * unit + run / L::J) * S::KROW + run % L::J * 64;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          // NVFP4: two blocks in the run
-          *reinterpret_cast<vec*>(dst + 16 * i) =
-              decode8<FMT>(st.w[n * 5 + i], k_scale<FMT>(st.w[n * 5 + 4], i >> 1));
+          for (int e = 0; e < 4; ++e)  // NVFP4: two blocks in the run
+            *reinterpret_cast<vec*>(dst + 16 * e) =
+                decode8<FMT>(st.w[n][5 * i + e], k_scale<FMT>(st.w[n][5 * i + 4], e >> 1));
         }
       }
     }
   };
-  auto bad_ids = [&]() {
-    uint32_t bad = 0;
-#pragma unroll
-    for (int n = 0; n < St::NV; ++n) bad |= ((uint32_t)st.id[n] < n_pages ? 0u : 1u) << n;
-    return bad;
-  };
 
   // ---- the keys ---------------------------------------------------------------
-  uint32_t bad = 0;  // V items of the staged step whose page is not in the cache
-  int kt = k0, buf = 0;
-  if (k0 < k1) {
-    load_ids(kt);
-    bad = bad_ids();
-    load_bytes(kt);
-    load_ids(kt + TILE_KEYS);
-    decode(kt, 0, bad);
-    bad = bad_ids();
-    load_bytes(kt + TILE_KEYS);
-    load_ids(kt + 2 * TILE_KEYS);
-    __syncthreads();
-  }
-  for (; kt < k1; kt += TILE_KEYS, buf ^= 1) {
-    const uint32_t ok = s_ok[(kt / TILE_KEYS) & 3];
-    if (kt + TILE_KEYS < k1) {
-      // the other buffer's step ended before the last barrier
-      decode(kt + TILE_KEYS, buf ^ 1, bad);
-      bad = bad_ids();
-      load_bytes(kt + 2 * TILE_KEYS);  // (its flags: read two barriers from here, by then
-      load_ids(kt + 3 * TILE_KEYS);    // those of two steps ago are done with)
+  // One barrier a step.  The V team's waves and the K team's (one of each on a
+  // SIMD) go through a step in another order, so that one's products meet the
+  // other's vector work:
+  //   V team: S of t, V of t + 1 into LDS, weights of t, O += P V of t
+  //   K team: K of t + 2 into LDS, weights of t, O += P V of t, S of t + 1
+  // In step t K of t and t + 1 and V of t are read, K of t + 2 and V of t + 1
+  // written: three K buffers and two V buffers do.  Of the page flags, that of t
+  // is read and that of t + 3 written (with the load): four do.
+  const int steps = k0 < k1 ? (k1 - k0 + TILE_KEYS - 1) / TILE_KEYS : 0;
+  // this wave's steps (those that some row of it sees)
+  int t_on = 0, t_off = wave_on ? min(steps, pos_z < k0 ? 0 : (pos_z - k0) / TILE_KEYS + 1) : 0;
+  if (p.window > 0) t_on = max(0, pos_a - p.window + 1 - k0) / TILE_KEYS;
+  v16f x[NU];
+  vec pb[2 * NU];
+  const uint8_t* const kb = lds + col * S::KROW + half * 16;
+  const uint8_t* const vb = lds + S::V0 + col * S::VROW + half * 16;
+  auto score = [&](int t) {  // S of step t
+    const uint8_t* k = kb + t % S::KBUFS * S::KBYTES;
+#pragma unroll
+    for (int u = 0; u < NU; ++u)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) x[u][r] = 0.0f;
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s)
+#pragma unroll
+      for (int u = 0; u < NU; ++u)
+        x[u] = Wide<FMT>::mfma(*reinterpret_cast<const vec*>(k + u * 32 * S::KROW + s * 32), qf[s], x[u]);
+    pipeline_reads<NU * D / 16, (D < 128 ? D : 128) / 16>();
+  };
+  if (steps > 0) {
+    load_ids(0);
+    load_bytes(0);
+    load_ids(1);
+    decode(0);
+    load_bytes(1);
+    load_ids(2);
+    if (!v_team) {
+      decode(1);
+      load_bytes(2);
+      load_ids(3);
     }
-    const bool on = wave_on && kt <= pos_z && (p.window == 0 || kt + TILE_KEYS > pos_a - p.window + 1);
+    __syncthreads();
+    if (!v_team && t_on == 0 && t_off > 0) score(0);
+  }
+  for (int t = 0; t < steps; ++t) {
+    const bool on = t >= t_on && t < t_off;
+    if (v_team && on) score(t);
+    const int ahead = v_team ? t + 1 : t + 2;
+    decode(ahead);
+    load_bytes(ahead + 1);
+    load_ids(ahead + 2);
     if (on) {
-      const uint8_t* kb = lds + buf * S::BYTES + col * S::KROW + half * 16;
-      const uint8_t* vb = lds + buf * S::BYTES + S::V0 + col * S::VROW + half * 16;
-      v16f x[2];
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) x[u][r] = 0.0f;
-#pragma unroll
-      for (int s = 0; s < D / 16; ++s)
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-          x[u] = Wide<FMT>::mfma(*reinterpret_cast<const vec*>(kb + u * 32 * S::KROW + s * 32), qf[s], x[u]);
-      const bool whole = __builtin_amdgcn_readfirstlane(ok) == 0x01010101u && kt + TILE_KEYS <= pos_a + 1 &&
+      const uint32_t ok = s_ok[t & 3];
+      const int kt = k0 + t * TILE_KEYS;
+      const bool whole = __builtin_amdgcn_readfirstlane(ok) == ALL_OK && kt + TILE_KEYS <= pos_a + 1 &&
                          kt + TILE_KEYS <= rg.hi && (p.window == 0 || kt > pos_z - p.window);
       if (!whole) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < NU; ++u)
 #pragma unroll
           for (int r = 0; r < 16; ++r) {
-            const int k = 32 * u + 8 * (r >> 2) + 4 * half + (r & 3), key = kt + k;
+            const int key = kt + 32 * u + 8 * (r >> 2) + 4 * half + (r & 3);
             if (!((ok >> (8 * (2 * u + (r >> 3)))) & 1) || key < see_lo || key >= see_hi)
               x[u][r] = -__builtin_inff();
           }
       }
-      float t = x[0][0];
+      float top = x[0][0];
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+      for (int u = 0; u < NU; ++u)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) t = fmaxf(t, x[u][r]);
-      t = other_half_max(t);
-      if (__any(t > lim)) {
+        for (int r = 0; r < 16; ++r) top = fmaxf(top, x[u][r]);
+      top = other_half_max(top);
+      if (__any(top > lim)) {
         // (columns whose maximum stays keep it)
-        const float mt = t > lim ? t : m;
+        const float mt = top > lim ? top : m;
         const float f = m > -__builtin_inff() ? __builtin_amdgcn_exp2f((m - mt) * cf) : 0.0f;
         m = mt;
         if (m > -__builtin_inff()) {
@@ -323,13 +346,12 @@ __global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void k_attn_tile(Attn
         const float base = m > -__builtin_inff() ? m : 0.0f;
         add = P_BIAS;
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < NU; ++u)
 #pragma unroll
           for (int r = 0; r < 16; ++r) x[u][r] -= base;
       }
-      vec pb[4];
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+      for (int u = 0; u < NU; ++u)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           w4 pk;
@@ -343,12 +365,15 @@ __global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void k_attn_tile(Attn
           }
           pb[2 * u + e] = __builtin_bit_cast(vec, pk);
         }
+      const uint8_t* v = vb + (t & 1) * S::VBYTES;
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
+      for (int e = 0; e < 2 * NU; ++e)
 #pragma unroll
         for (int i = 0; i < D / 32; ++i)
-          o[i] = Wide<FMT>::mfma(*reinterpret_cast<const vec*>(vb + i * 32 * S::VROW + e * 32), pb[e], o[i]);
+          o[i] = Wide<FMT>::mfma(*reinterpret_cast<const vec*>(v + i * 32 * S::VROW + e * 32), pb[e], o[i]);
+      pipeline_reads<NU * D / 16, (D < 128 ? D : 128) / 16>();
     }
+    if (!v_team && t + 1 >= t_on && t + 1 < t_off) score(t + 1);
     __syncthreads();
   }
 
@@ -384,7 +409,7 @@ __global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void k_attn_tile(Attn
 template <int FMT, int D, int WAVES>
 void launch(const AttnArgs& p, int tiles, int B, hipStream_t stream) {
   const dim3 grid((unsigned)(B * p.H), (unsigned)tiles, (unsigned)p.splits);
-  hipLaunchKernelGGL((k_attn_tile<FMT, D, WAVES>), grid, dim3(64 * WAVES), 2 * TileLds<D>::BYTES,
+  hipLaunchKernelGGL((k_attn_tile<FMT, D, WAVES>), grid, dim3(64 * WAVES), TileLds<D>::BYTES,
                      stream, p);
 }
 
