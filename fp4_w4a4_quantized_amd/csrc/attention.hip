@@ -32,86 +32,108 @@ namespace fp4q {
 namespace {
 
 // WAVES waves share the keys of a (sequence, kv head, rows, split): wave w
-// takes steps w, w + WAVES, ...
+// takes steps w, w + WAVES, ...  With few rows the cache's bytes bound it: K of
+// the next step is loaded as soon as this step's is used up, into the same
+// registers (few enough for three waves on a SIMD), then V, and the numbers of
+// their pages one step before that.
 template <int FMT, int D, int NC, int WAVES>
-__global__ __launch_bounds__(64 * WAVES) void k_attn_split(AttnArgs p) {
+__global__ __launch_bounds__(64 * WAVES, D == 64 ? 4 : D == 128 && NC == 1 && WAVES == 4 ? 3 : 2) void k_attn_split(AttnArgs p) {
   typedef typename Num<FMT>::vec vec;
   typedef typename Num<FMT>::pair pair;
   typedef KvLayout<FMT, D> L;
   const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int b = blockIdx.z, h = blockIdx.y % p.H, row0 = (int)(blockIdx.y / p.H) * p.tile;
+  // Workgroups go to the XCDs in turn: the (sequence, kv head) runs fastest,
+  // rotated by the split, so that no XCD has all of the long sequences' last splits.
+  const uint32_t bh = (blockIdx.x + blockIdx.z) % gridDim.x;
+  const int b = bh / p.H, h = bh - b * p.H, row0 = blockIdx.y * p.tile;
   const int n_rows = (p.off[b + 1] - p.off[b]) * p.G;
   if (row0 >= n_rows) return;
   const Range rg = tile_range(p, b, row0);
-  const int split = blockIdx.x;
+  const int split = blockIdx.z;
   if (split >= active_splits(p, rg)) return;
   const int k0 = rg.lo + split * p.chunk;
   const int k1 = min(rg.hi, k0 + p.chunk);
 
+  const int page = 1 << p.page_shift;
+  const int32_t* table = p.table + b * p.ldt;
+  const uint32_t n_pages = (uint32_t)min(p.n_pages, (int64_t)0x7FFFFFFF);
+  const int64_t page_stride = (int64_t)p.H * L::bytes(page);
+  const uint8_t* const head = p.cache + h * (int64_t)L::bytes(page);
+  Sub<FMT, D> st[2];             // the step's two subtiles
+  Buffer buf[2];                 // the pages of the step after
+  bool good[2], next_good[2];    // is the step's page in the cache?
+  int ids[2];                    // page numbers of the step after that
+  auto load_ids = [&](int kt) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+      ids[u] = table[min(kt + 16 * u + (lane & 1), k1 - 1) >> p.page_shift];
+  };
+  auto next_k = [&](int kt) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int id = __builtin_amdgcn_readfirstlane(ids[u]), key = kt + 16 * u;
+      next_good[u] = (uint32_t)id < n_pages && key < k1;
+      // (for a page that is not in the cache some page's bytes, all masked)
+      buf[u] = page_buffer(head + (next_good[u] ? id : 0) * page_stride, L::bytes(page));
+      load_k<FMT, D>(buf[u], page, key & (page - 1), lane, st[u]);
+    }
+  };
+  auto next_v = [&](int kt) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+      load_v<FMT, D>(buf[u], page, (kt + 16 * u) & (page - 1), lane, st[u]);
+  };
+  constexpr int STRIDE = WAVES * KEYS;
+  int kt = k0 + wave * KEYS;
+  if (kt < k1) {
+    load_ids(kt);
+    next_k(kt);
+    next_v(kt);
+    load_ids(kt + STRIDE);
+  }
+
   vec qf[NC][D / 32];
   float cf[NC], m[NC], z[NC];
   int see_lo[NC], see_hi[NC];  // keys the column sees: [see_lo, see_hi)
-  int64_t slot[NC];
   v4f o[NC][D / 16];
-  int all_lo = 0, all_hi = 0x7FFFFFFF;
   const float c0 = p.scale2 * (FMT == FP4Q_NVFP4 ? p.kts[h] : 1.0f);
 #pragma unroll
   for (int n = 0; n < NC; ++n) {
-    const int row = row0 + n * ROWS + c;
-    const int rr = min(row, rg.rows - 1);
+    const int rr = min(row0 + n * ROWS + c, rg.rows - 1);
     const int qi = rr / p.G, hh = h * p.G + (rr - qi * p.G);
     load_q<FMT, D>(p.q + (rg.r0 + qi) * p.ldq + hh * D, g, c0, qf[n], cf[n]);
     see_hi[n] = min(rg.hi, rg.first + qi + 1);
     see_lo[n] = p.window > 0 ? rg.first + qi - p.window + 1 : 0;
-    slot[n] = row < rg.rows ? (rg.r0 + qi) * (int64_t)(p.H * p.G) + hh : -1;
     m[n] = -__builtin_inff();
     z[n] = 0.0f;
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) o[n][i] = {0.0f, 0.0f, 0.0f, 0.0f};
   }
-  {  // a step inside [all_lo, all_hi) needs no mask
-    const int last = min(rg.rows, row0 + p.tile) - 1;
-    all_hi = rg.first + row0 / p.G + 1;
-    all_lo = p.window > 0 ? rg.first + last / p.G - p.window + 1 : 0;
-  }
+  // a step inside [all_lo, all_hi) needs no mask
+  const int last = min(rg.rows, row0 + p.tile) - 1;
+  const int all_hi = min(rg.hi, rg.first + row0 / p.G + 1);
+  const int all_lo = p.window > 0 ? rg.first + last / p.G - p.window + 1 : 0;
 
-  const int page = 1 << p.page_shift;
-  const int32_t* table = p.table + b * p.ldt;
-  for (int kt = k0 + wave * KEYS; kt < k1; kt += WAVES * KEYS) {
-    Sub<FMT, D> s[2];
-    bool good[2];
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int key = kt + 16 * u;
-      int64_t id = -1;
-      if (key < rg.hi) id = table[key >> p.page_shift];
-      good[u] = id >= 0 && id < p.n_pages;
-      if (!good[u]) id = 0;  // some page's bytes, all masked
-      load_sub<FMT, D>(p.cache + (id * p.H + h) * (int64_t)L::bytes(page), page,
-                       key & (page - 1), lane, s[u]);
-    }
-    const bool whole = good[0] && good[1] && kt >= all_lo && kt + KEYS <= all_hi;
-    if (!whole) {
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-        zero_v_scales<FMT, D>(s[u], kt + 16 * u + 4 * g, !good[u], rg.seen, rg.hi);
-    }
-    vec pb[NC];
-    float up = 0.0f;  // does some column's maximum run ahead of its kept one?
+  for (; kt < k1; kt += STRIDE) {
+    good[0] = next_good[0];
+    good[1] = next_good[1];
     v4f x[NC][2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
 #pragma unroll
       for (int n = 0; n < NC; ++n) x[n][u] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int st = 0; st < D / 32; ++st) {
-        const vec a = decode_k<FMT, D>(s[u], st);
+      for (int i = 0; i < D / 32; ++i) {
+        const vec a = decode_k<FMT, D>(st[u], i);
 #pragma unroll
-        for (int n = 0; n < NC; ++n) x[n][u] = Num<FMT>::mfma(a, qf[n][st], x[n][u]);
+        for (int n = 0; n < NC; ++n) x[n][u] = Num<FMT>::mfma(a, qf[n][i], x[n][u]);
+        __builtin_amdgcn_sched_barrier(0);  // (decoding ahead would cost registers, and so waves)
       }
     }
-    float mt[NC];
+    next_k(kt + STRIDE);  // (past the last step: some page's bytes, not used)
+    const bool whole = good[0] && good[1] && kt >= all_lo && kt + KEYS <= all_hi;
+    float mt[NC], up = 0.0f;  // does some column's maximum run ahead of its kept one?
 #pragma unroll
     for (int n = 0; n < NC; ++n) {
       if (!whole) {
@@ -123,11 +145,9 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_split(AttnArgs p) {
             if (!good[u] || key < see_lo[n] || key >= see_hi[n]) x[n][u][r] = -__builtin_inff();
           }
       }
-      float t = fmaxf(fmaxf(fmaxf(x[n][0][0], x[n][0][1]), fmaxf(x[n][0][2], x[n][0][3])),
-                      fmaxf(fmaxf(x[n][1][0], x[n][1][1]), fmaxf(x[n][1][2], x[n][1][3])));
-      t = fmaxf(t, __shfl_xor(t, 16));
-      t = fmaxf(t, __shfl_xor(t, 32));
-      mt[n] = fmaxf(t, m[n]);
+      const float t = fmaxf(fmaxf(fmaxf(x[n][0][0], x[n][0][1]), fmaxf(x[n][0][2], x[n][0][3])),
+                            fmaxf(fmaxf(x[n][1][0], x[n][1][1]), fmaxf(x[n][1][2], x[n][1][3])));
+      mt[n] = fmaxf(other_half_max(other_quarter_max(t)), m[n]);
       if (mt[n] > -__builtin_inff())
         up = fmaxf(up, m[n] > -__builtin_inff() ? (mt[n] - m[n]) * cf[n] : P_SLACK + 1.0f);
     }
@@ -144,6 +164,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_split(AttnArgs p) {
           for (int r = 0; r < 4; ++r) o[n][i][r] *= f;
       }
     }
+    vec pb[NC];
 #pragma unroll
     for (int n = 0; n < NC; ++n) {
       // (the difference first: m c alone may be past what 32 bits hold to 2^8)
@@ -161,12 +182,20 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_split(AttnArgs p) {
         }
       pb[n] = __builtin_bit_cast(vec, pk);
     }
-    pv_all<FMT, D, 0, NC>(s[0], s[1], pb, o);
+    if (!whole) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        zero_v_scales<FMT, D>(st[u], kt + 16 * u + 4 * g, !good[u], rg.seen, rg.hi);
+    }
+    pv_all<FMT, D, 0, NC>(st[0], st[1], pb, o);
+    next_v(kt + STRIDE);
+    load_ids(kt + 2 * STRIDE);
   }
 
-  // the waves' results meet: common maximum, summed sums and outputs
+  // The waves' results meet: common maximum, summed sums, and the outputs added
+  // pairwise, the upper half of the waves to the lower one.
   __shared__ float s_m[WAVES][NC * ROWS], s_z[WAVES][NC * ROWS];
-  __shared__ float s_o[WAVES][ROWS][D + 4];
+  __shared__ v4f s_o[WAVES / 2][D / 16][64];
 #pragma unroll
   for (int n = 0; n < NC; ++n) {
     z[n] += __shfl_xor(z[n], 16);
@@ -181,97 +210,117 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_split(AttnArgs p) {
 #pragma unroll
   for (int n = 0; n < NC; ++n) {
     float mm = -__builtin_inff(), zz = 0.0f;
+#pragma unroll
     for (int w = 0; w < WAVES; ++w) mm = fmaxf(mm, s_m[w][n * ROWS + c]);
     const float base = mm > -__builtin_inff() ? mm : 0.0f;
+#pragma unroll
     for (int w = 0; w < WAVES; ++w)
       zz += s_z[w][n * ROWS + c] * __builtin_amdgcn_exp2f(s_m[w][n * ROWS + c] - base);
     const float mine = __builtin_amdgcn_exp2f(m[n] * cf[n] - base);
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i) {
-      v4f t;
+    for (int i = 0; i < D / 16; ++i)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) t[r] = o[n][i][r] * mine;
-      *reinterpret_cast<v4f*>(&s_o[wave][c][16 * i + 4 * g]) = t;
-    }
-    __syncthreads();
-    // thread: column c2, elements d, d + 4 * STEP, ...
-    for (int i = threadIdx.x; i < ROWS * D / 4; i += 64 * WAVES) {
-      const int col = i / (D / 4), d = (i - col * (D / 4)) * 4;
-      const int row = row0 + n * ROWS + col;
-      if (row >= rg.rows) continue;
-      v4f t = {0.0f, 0.0f, 0.0f, 0.0f};
-      for (int w = 0; w < WAVES; ++w) {
-        const v4f a = *reinterpret_cast<const v4f*>(&s_o[w][col][d]);
+      for (int r = 0; r < 4; ++r) o[n][i][r] *= mine;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) t[r] += a[r];
+    for (int half = WAVES / 2; half > 0; half >>= 1) {
+      if (wave >= half && wave < 2 * half) {
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) s_o[wave - half][i][lane] = o[n][i];
       }
-      const int qi = row / p.G, hh = h * p.G + (row - qi * p.G);
-      if (p.splits == 1) {
-        float zc = 0.0f, mc = -__builtin_inff();
-        for (int w = 0; w < WAVES; ++w) mc = fmaxf(mc, s_m[w][n * ROWS + col]);
-        const float bc = mc > -__builtin_inff() ? mc : 0.0f;
-        for (int w = 0; w < WAVES; ++w)
-          zc += s_z[w][n * ROWS + col] * __builtin_amdgcn_exp2f(s_m[w][n * ROWS + col] - bc);
-        const float f = zc > 0.0f ? vt / zc : 0.0f;
-        const int64_t at = (rg.r0 + qi) * p.ldy + hh * D + d;
+      __syncthreads();
+      if (wave < half) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) t[r] *= f;
-        store_out(p, at, t);
-      } else {
-        const int64_t s = split * p.slots + (rg.r0 + qi) * (int64_t)(p.H * p.G) + hh;
-        *reinterpret_cast<v4f*>(p.part_o + s * D + d) = t;
+        for (int i = 0; i < D / 16; ++i) {
+          const v4f t = s_o[wave][i][lane];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) o[n][i][r] += t[r];
+        }
       }
+      __syncthreads();
     }
-    if (p.splits > 1 && wave == 0 && g == 0 && slot[n] >= 0)
-      p.part_ms[split * p.slots + slot[n]] = make_float2(mm, zz);
-    __syncthreads();
+    const int row = row0 + n * ROWS + c;
+    if (wave > 0 || row >= rg.rows) continue;
+    const int qi = row / p.G, hh = h * p.G + (row - qi * p.G);
+    if (p.splits == 1) {
+      const float f = zz > 0.0f ? vt / zz : 0.0f;
+      const int64_t at = (rg.r0 + qi) * p.ldy + hh * D + 4 * g;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        v4f t;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) t[r] = o[n][i][r] * f;
+        store_out(p, at + 16 * i, t);
+      }
+    } else {
+      const int64_t s = split * p.slots + (rg.r0 + qi) * (int64_t)(p.H * p.G) + hh;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+        *reinterpret_cast<v4f*>(p.part_o + s * D + 16 * i + 4 * g) = o[n][i];
+      if (g == 0) p.part_ms[s] = make_float2(mm, zz);
+    }
   }
 }
 
-// Joins the splits of a row: one wave per (new token, head).
+// Joins the splits of a row: p.join groups of D / 4 lanes for each (new token,
+// head), each over every p.join-th split with a running maximum, joined in LDS.
 template <int FMT, int D>
 __global__ __launch_bounds__(256) void k_attn_join(AttnArgs p) {
-  const int lane = threadIdx.x & 63;
-  const int64_t s = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (s >= p.slots) return;
+  constexpr int LANES = D / 4;
+  __shared__ v4f s_o[256];
+  __shared__ float2 s_ms[256];
+  const int t = threadIdx.x, d = t % LANES;
+  const int grp = t / LANES % p.join;
+  const int64_t s = (int64_t)blockIdx.x * (256 / LANES / p.join) + t / (LANES * p.join);
   const int heads = p.H * p.G;
   const int64_t row = s / heads;
   const int hh = (int)(s - row * heads);
-  if (row < p.off[0] || row >= p.off[p.B]) return;
-  const int b = kv_sequence(p.off, p.B, row);
-  const int r = (int)(row - p.off[b]) * p.G + hh % p.G;
-  const Range rg = tile_range(p, b, r / p.tile * p.tile);
-  const int n = min(active_splits(p, rg), p.splits);
-  float m = -__builtin_inff();
-  for (int i = lane; i < n; i += 64) m = fmaxf(m, p.part_ms[i * p.slots + s].x);
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
-  const float base = m > -__builtin_inff() ? m : 0.0f;
-  float z = 0.0f, o[D / 64];
-#pragma unroll
-  for (int e = 0; e < D / 64; ++e) o[e] = 0.0f;
-  for (int i = 0; i < n; ++i) {
-    const float2 ms = p.part_ms[i * p.slots + s];
-    const float f = __builtin_amdgcn_exp2f(ms.x - base);
-    z += ms.y * f;
-#pragma unroll
-    for (int e = 0; e < D / 64; ++e)
-      o[e] = __builtin_fmaf(p.part_o[(i * p.slots + s) * D + e * 64 + lane], f, o[e]);
+  int n = 0;
+  if (s < p.slots && row >= p.off[0] && row < p.off[p.B]) {
+    const int b = kv_sequence(p.off, p.B, row);
+    const int tile = ((int)(row - p.off[b]) * p.G + hh % p.G) / p.tile;
+    if (tile < p.tiles) n = min(active_splits(p, tile_range(p, b, tile * p.tile)), p.splits);
   }
+  float m = -__builtin_inff(), z = 0.0f;
+  v4f o = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+  for (int i = grp; i < n; i += p.join) {
+    const float2 ms = p.part_ms[i * p.slots + s];
+    const v4f a = *reinterpret_cast<const v4f*>(p.part_o + (i * p.slots + s) * D + 4 * d);
+    const float mn = fmaxf(m, ms.x), base = mn > -__builtin_inff() ? mn : 0.0f;
+    const float f = __builtin_amdgcn_exp2f(m - base), fa = __builtin_amdgcn_exp2f(ms.x - base);
+    m = mn;
+    z = z * f + ms.y * fa;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) o[r] = __builtin_fmaf(a[r], fa, o[r] * f);
+  }
+  if (p.join > 1) {
+    s_o[t] = o;
+    s_ms[t] = make_float2(m, z);
+    __syncthreads();
+    if (grp > 0) return;
+    for (int i = 1; i < p.join; ++i) {
+      const float2 ms = s_ms[t + i * LANES];
+      const v4f a = s_o[t + i * LANES];
+      const float mn = fmaxf(m, ms.x), base = mn > -__builtin_inff() ? mn : 0.0f;
+      const float f = __builtin_amdgcn_exp2f(m - base), fa = __builtin_amdgcn_exp2f(ms.x - base);
+      m = mn;
+      z = z * f + ms.y * fa;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) o[r] = __builtin_fmaf(a[r], fa, o[r] * f);
+    }
+  }
+  if (n == 0) return;
   const float f = z > 0.0f ? (FMT == FP4Q_NVFP4 ? p.vts[hh / p.G] : 1.0f) / z : 0.0f;
 #pragma unroll
-  for (int e = 0; e < D / 64; ++e) {
-    const int64_t at = row * p.ldy + hh * D + e * 64 + lane;
-    if (p.y_bf16) reinterpret_cast<__bf16*>(p.y)[at] = (__bf16)(o[e] * f);
-    else reinterpret_cast<float*>(p.y)[at] = o[e] * f;
-  }
+  for (int r = 0; r < 4; ++r) o[r] *= f;
+  store_out(p, row * p.ldy + hh * D + 4 * d, o);
 }
 
 // How a call is split: a function of host numbers only, so that the workspace
 // query and the launch agree.
 struct Plan {
   bool wide;  // many rows: k_attn_tile
-  int nc, tile, step, tiles, chunk, splits;
+  int nc, waves, tile, step, tiles, chunk, splits, join;
 };
 
 Plan attn_plan(int D, int B, int H, int G, int64_t max_new, int64_t max_len, int window) {
@@ -287,32 +336,40 @@ Plan attn_plan(int D, int B, int H, int G, int64_t max_new, int64_t max_len, int
     const int64_t seen = (int64_t)window + (p.wide ? (p.tile + G - 1) / G + 1 : max_new) + p.step;
     keys = keys < seen ? keys : seen;
   }
-  // enough workgroups to fill the card a few times over, and at least 256 keys each
   const int64_t groups = (int64_t)B * H * p.tiles;
-  const int64_t want = p.wide ? 512 : 2048;
+  // few short (sequence, head)s: eight waves on the keys of each, none to join
+  p.waves = !p.wide && groups <= 256 && keys <= 2048 && p.nc == 1 && D <= 128 ? 8 : 4;
+  const int64_t want = p.wide ? 512 : 4096;
   int64_t chunk = (keys * groups + want - 1) / want;
-  const int64_t least = p.wide ? 512 : 256;
+  const int64_t least = p.wide ? 512 : p.waves == 8 ? 2048 : 256;
   chunk = chunk < least ? least : chunk;
   chunk = (chunk + p.step - 1) / p.step * p.step;
   p.chunk = (int)(chunk < (1 << 30) ? chunk : (1 << 30));
   p.splits = (int)((keys + p.chunk - 1) / p.chunk);
   if (p.splits < 1) p.splits = 1;
+  // about eight splits for each of the join's lane groups
+  p.join = 1;
+  while (p.join * 4 < p.splits && p.join < 1024 / D) p.join *= 2;
   return p;
 }
 
 template <int FMT, int D>
 void launch(const AttnArgs& p, const Plan& pl, int H, int B, hipStream_t stream) {
-  const dim3 grid((unsigned)pl.splits, (unsigned)(H * pl.tiles), (unsigned)B), thr(256);
+  const dim3 grid((unsigned)(B * H), (unsigned)pl.tiles, (unsigned)pl.splits), thr(64 * pl.waves);
   if (pl.wide) {
     launch_attention_tile(FMT, D, p, pl.tiles, B, stream);
   } else if constexpr (D <= 128) {
     if (pl.nc == 2) hipLaunchKernelGGL((k_attn_split<FMT, D, 2, 4>), grid, thr, 0, stream, p);
-    else hipLaunchKernelGGL((k_attn_split<FMT, D, 1, 4>), grid, thr, 0, stream, p);
+    else if (pl.waves == 4) hipLaunchKernelGGL((k_attn_split<FMT, D, 1, 4>), grid, thr, 0, stream, p);
+    else hipLaunchKernelGGL((k_attn_split<FMT, D, 1, 8>), grid, thr, 0, stream, p);
   } else {
     hipLaunchKernelGGL((k_attn_split<FMT, D, 1, 4>), grid, thr, 0, stream, p);
   }
-  if (pl.splits > 1)
-    hipLaunchKernelGGL((k_attn_join<FMT, D>), dim3((unsigned)((p.slots + 3) / 4)), thr, 0, stream, p);
+  if (pl.splits > 1) {
+    const int per = 1024 / D / pl.join;  // rows and heads of a workgroup
+    hipLaunchKernelGGL((k_attn_join<FMT, D>), dim3((unsigned)((p.slots + per - 1) / per)), dim3(256),
+                       0, stream, p);
+  }
 }
 
 }  // namespace
@@ -360,6 +417,8 @@ void launch_attention(int fmt, const uint8_t* cache, int64_t n_pages, int page_s
   p.splits = pl.splits;
   p.tile = pl.tile;
   p.step = pl.step;
+  p.tiles = pl.tiles;
+  p.join = pl.join;
   p.slots = rows * H * G;
   p.part_o = static_cast<float*>(ws);
   p.part_ms = reinterpret_cast<float2*>(p.part_o + (size_t)pl.splits * (size_t)p.slots * D);

@@ -30,6 +30,8 @@ struct AttnArgs {
   int splits;  // splits launched; 1: the kernel writes y itself
   int tile;    // rows of a workgroup
   int step;    // keys of a step of its kernel: splits begin at its multiples
+  int tiles;   // row tiles launched
+  int join;    // groups of lanes that join a row's splits
   int64_t slots;  // rows * heads: partial results of one split
   float2* part_ms;  // [splits][slots] (maximum in log2 units, sum)
   float* part_o;    // [splits][slots][D]
@@ -142,26 +144,49 @@ __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
   }
 }
 
-// Loads of the subtile that starts at `slot` of a page (base: its bytes for
-// this head).
-template <int FMT, int D>
-__device__ __forceinline__ void load_sub(const uint8_t* base, int page, int slot, int lane,
-                                         Sub<FMT, D>& s) {
-  typedef KvLayout<FMT, D> L;
-  const int c = lane & 15, g = lane >> 4;
-  load_words(base + slot * (D / 2) + c * (D / 2) + g * (D / 8), s.k);
-  load_words(base + L::v_codes(page) + slot * (D / 2) + lane * (D / 8), s.v);
-  const uint8_t* ks = base + L::k_scales(page) + (slot + c) * L::SB;
-  if constexpr (FMT == FP4Q_NVFP4) {
-    if constexpr (D == 64) s.ks = ks[g];
-    else if constexpr (D == 128) s.ks = reinterpret_cast<const uint16_t*>(ks)[g];
-    else s.ks = reinterpret_cast<const uint32_t*>(ks)[g];
+// Loads through a buffer descriptor: the address is scalar but for one 32-bit
+// offset a lane, where plain loads would keep 64-bit vector addresses.
+typedef __amdgpu_buffer_rsrc_t Buffer;
+
+__device__ __forceinline__ Buffer page_buffer(const uint8_t* base, int bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0, bytes, 0x00027000);
+}
+
+template <int N>
+__device__ __forceinline__ void buffer_words(Buffer r, uint32_t lane_off, uint32_t off, uint32_t (&w)[N]) {
+  if constexpr (N % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      const w4 u = __builtin_bit_cast(w4, __builtin_amdgcn_raw_buffer_load_b128(r, lane_off + 16 * i, off, 0));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[4 * i + e] = u[e];
+    }
   } else {
-    if constexpr (D == 64) s.ks = ks[g >> 1];
-    else if constexpr (D == 128) s.ks = ks[g];
-    else s.ks = reinterpret_cast<const uint16_t*>(ks)[g];
+    static_assert(N == 2, "");
+    const u32x2 u = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(r, lane_off, off, 0));
+    w[0] = u[0];
+    w[1] = u[1];
   }
-  load_words(base + L::v_scales(page) + (slot + 4 * g) * L::SB, s.vs);
+}
+
+// The subtile that starts at `slot` of a page of one head.
+template <int FMT, int D>
+__device__ __forceinline__ void load_k(Buffer r, int page, int slot, int lane, Sub<FMT, D>& s) {
+  typedef KvLayout<FMT, D> L;
+  const uint32_t c = lane & 15, g = lane >> 4;
+  buffer_words(r, c * (D / 2) + g * (D / 8), slot * (D / 2), s.k);
+  constexpr int KS = L::SB >= 4 ? L::SB / 4 : 1;  // scale bytes of a lane (two lanes: one)
+  const uint32_t at = c * L::SB + (L::SB >= 4 ? g * KS : g >> 1), off = L::k_scales(page) + slot * L::SB;
+  if constexpr (KS == 1) s.ks = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(r, at, off, 0);
+  else if constexpr (KS == 2) s.ks = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, at, off, 0);
+  else s.ks = __builtin_amdgcn_raw_buffer_load_b32(r, at, off, 0);
+}
+
+template <int FMT, int D>
+__device__ __forceinline__ void load_v(Buffer r, int page, int slot, int lane, Sub<FMT, D>& s) {
+  typedef KvLayout<FMT, D> L;
+  buffer_words(r, lane * (D / 8), L::v_codes(page) + slot * (D / 2), s.v);
+  buffer_words(r, (lane >> 4) * 4 * L::SB, L::v_scales(page) + slot * L::SB, s.vs);
 }
 
 // A K block's scale as decode2 takes it: the low byte(s) of s hold its code
@@ -275,7 +300,20 @@ __device__ __forceinline__ void pv_all(const Sub<FMT, D>& s0, const Sub<FMT, D>&
                                        const typename Num<FMT>::vec (&pb)[NC],
                                        v4f (&o)[NC][D / 16]) {
   pv<FMT, D, JJ, NC>(s0, s1, pb, o);
+  __builtin_amdgcn_sched_barrier(0);
   if constexpr (JJ + 1 < D / 32) pv_all<FMT, D, JJ + 1, NC>(s0, s1, pb, o);
+}
+
+// Maxima over the lanes 32 apart, and 16 apart.
+__device__ __forceinline__ float other_half_max(float v) {
+  const u32x2 r = __builtin_bit_cast(
+      u32x2, __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false));
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float other_quarter_max(float v) {
+  const u32x2 r = __builtin_bit_cast(
+      u32x2, __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false));
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
 
 __device__ __forceinline__ uint32_t max_magnitude(w4 u) {  // of 8 BF16, as bits

@@ -73,12 +73,6 @@ struct Staged {
 // the scalar cache.
 typedef const __attribute__((address_space(4))) int32_t* TablePtr;
 
-__device__ __forceinline__ float other_half_max(float v) {
-  const u32x2 r = __builtin_bit_cast(
-      u32x2, __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false));
-  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
-}
-
 // Asks the scheduler for N products fed by N LDS reads with AHEAD of the reads
 // in flight: left alone, it reads, waits and multiplies by turns.
 template <int N, int AHEAD>
