@@ -194,9 +194,9 @@ def _ptr(t):
 
 
 def _stream(stream):
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+    if stream is None:  # the current stream's handle, without a Stream object around it
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream
 
 
 def _check(fn, rc):
@@ -786,13 +786,15 @@ def _keep(stream, *tensors):
 def _rows_of(name, t, heads_dim=None):
     """Row stride of a [rows, heads, dim] tensor whose heads lie one after
     another."""
-    if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or stride[2] != 1 or (shape[1] > 1 and stride[1] != shape[2]):
         raise ValueError(f"{name}: [rows, heads, dim] with contiguous heads is needed")
-    if t.dtype not in (torch.bfloat16, torch.int16):
+    dtype = t.dtype
+    if dtype is not torch.bfloat16 and dtype is not torch.int16:
         raise ValueError(f"{name}: bf16 is needed")
-    if heads_dim is not None and tuple(t.shape[1:]) != tuple(heads_dim):
+    if heads_dim is not None and (shape[1], shape[2]) != heads_dim:
         raise ValueError(f"{name}: {heads_dim[0]} heads of {heads_dim[1]} are needed")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+    return stride[0] if shape[0] > 1 else shape[1] * shape[2]
 
 
 def kv_page_bytes(fmt, page, dim) -> int:
@@ -809,30 +811,37 @@ def kv_cache(fmt, n_pages, page, kv_heads, dim, device="cuda"):
 
 
 def _int32(name, t):
-    if t.dtype != torch.int32 or not t.is_contiguous():
+    if t.dtype is not torch.int32 or not t.is_contiguous():
         raise ValueError(f"{name}: contiguous int32 is needed")
     return t.data_ptr()
 
 
-def _kv_args(fmt, cache, page, offsets, page_table, lens, rows, dim, k_scale, v_scale):
-    if cache.dtype != torch.uint8 or not cache.is_contiguous() or cache.dim() != 3:
+def _head_scale(t, heads):
+    if t is None:
+        return None
+    if t.dtype is not torch.float32 or not t.is_contiguous() or t.numel() != heads:
+        raise ValueError("k_scale, v_scale: contiguous f32, one for each kv head")
+    return t.data_ptr()
+
+
+def _kv_args(fmt, cache, page, offsets, page_table, lens, rows, dim):
+    shape = cache.shape
+    if cache.dtype is not torch.uint8 or len(shape) != 3 or not cache.is_contiguous():
         raise ValueError("cache: contiguous u8 [n_pages, kv_heads, page bytes] is needed")
-    n_pages, heads, nb = cache.shape
+    n_pages, heads, nb = shape
     if nb != lib().fp4q_kv_page_bytes(fmt, page, dim):
         raise ValueError("cache: its page bytes are not those of this format, page and dim")
-    if page_table.dtype != torch.int32 or page_table.dim() != 2 or (
-            page_table.shape[1] > 1 and page_table.stride(1) != 1):
+    tshape = page_table.shape
+    if page_table.dtype is not torch.int32 or len(tshape) != 2:
         raise ValueError("page_table: int32 [batch, pages] is needed")
-    batch = lens.numel()
-    if offsets.numel() != batch + 1 or page_table.shape[0] != batch:
+    batch, cols = tshape
+    ld, unit = page_table.stride()
+    if cols > 1 and unit != 1:
+        raise ValueError("page_table: int32 [batch, pages] is needed")
+    if offsets.numel() != batch + 1 or lens.numel() != batch:
         raise ValueError("offsets, page_table and lens differ in their sequences")
-    for t in (k_scale, v_scale):
-        if t is not None and (t.dtype != torch.float32 or not t.is_contiguous()
-                              or t.numel() != heads):
-            raise ValueError("k_scale, v_scale: contiguous f32, one for each kv head")
     return (fmt, cache.data_ptr(), n_pages, page, heads, dim, _int32("offsets", offsets), batch,
-            page_table.data_ptr(), page_table.stride(0) if batch > 1 else page_table.shape[1],
-            page_table.shape[1], _int32("lens", lens), rows)
+            page_table.data_ptr(), ld if batch > 1 else cols, cols, _int32("lens", lens), rows)
 
 
 def _opt(t):
@@ -845,27 +854,32 @@ def kv_append(fmt, cache, page, offsets, page_table, lens, k, v, k_scale=None, v
     into the paged cache.  offsets int32 [batch + 1] (rows of each sequence),
     page_table int32 [batch, pages], lens int32 [batch] (new tokens
     included), all on the GPU; k_scale, v_scale f32 [kv_heads] (NVFP4)."""
-    ldk = _rows_of("k", k, (cache.shape[1], k.shape[-1]))
-    ldv = _rows_of("v", v, k.shape[1:])
-    if v.shape[0] != k.shape[0]:
+    ldk = _rows_of("k", k)
+    rows, heads, dim = k.shape
+    ldv = _rows_of("v", v, (heads, dim))
+    if v.shape[0] != rows:
         raise ValueError("k and v differ in their rows")
-    args = _kv_args(fmt, cache, page, offsets, page_table, lens, k.shape[0], k.shape[2],
-                    k_scale, v_scale)
+    args = _kv_args(fmt, cache, page, offsets, page_table, lens, rows, dim)
+    if args[4] != heads:
+        raise ValueError(f"k: {args[4]} heads of {dim} are needed")
     _check("fp4q_kv_append",
-           lib().fp4q_kv_append(*args, k.data_ptr(), ldk, v.data_ptr(), ldv, _opt(k_scale),
-                                _opt(v_scale), _stream(stream)))
+           lib().fp4q_kv_append(*args, k.data_ptr(), ldk, v.data_ptr(), ldv,
+                                _head_scale(k_scale, heads), _head_scale(v_scale, heads),
+                                _stream(stream)))
 
 
 def kv_read(fmt, cache, page, offsets, page_table, lens, rows, dim, k_scale=None, v_scale=None,
             stream=None):
     """The values that stand in the cache for the new tokens: (k, v) bf16
     [rows, kv_heads, dim]."""
-    k, v = torch.empty((2, rows, cache.shape[1], dim), dtype=torch.bfloat16, device=cache.device)
-    args = _kv_args(fmt, cache, page, offsets, page_table, lens, rows, dim, k_scale, v_scale)
-    ld = cache.shape[1] * dim
+    args = _kv_args(fmt, cache, page, offsets, page_table, lens, rows, dim)
+    heads = args[4]
+    k, v = torch.empty((2, rows, heads, dim), dtype=torch.bfloat16, device=cache.device).unbind(0)
+    ld = heads * dim
     _check("fp4q_kv_read",
-           lib().fp4q_kv_read(*args, k.data_ptr(), ld, v.data_ptr(), ld, _opt(k_scale),
-                              _opt(v_scale), _stream(stream)))
+           lib().fp4q_kv_read(*args, k.data_ptr(), ld, v.data_ptr(), ld,
+                              _head_scale(k_scale, heads), _head_scale(v_scale, heads),
+                              _stream(stream)))
     _keep(stream, k)
     return k, v
 
@@ -880,18 +894,19 @@ def kv_attention_into(fmt, cache, page, offsets, page_table, lens, q, max_new, m
                       v_scale, window, scale, y, workspace, stream=None):
     """fp4q_kv_attention: y bf16 or f32 [rows, heads, dim]."""
     ldq = _rows_of("q", q)
-    rows, heads, dim = q.shape
-    if y.shape != q.shape or y.stride(2) != 1 or (heads > 1 and y.stride(1) != dim):
+    rows, heads, dim = shape = q.shape
+    stride, dtype = y.stride(), y.dtype
+    if y.shape != shape or stride[2] != 1 or (heads > 1 and stride[1] != dim):
         raise ValueError("y: q's shape with contiguous heads is needed")
-    if y.dtype not in (torch.bfloat16, torch.float32):
+    if dtype is not torch.bfloat16 and dtype is not torch.float32:
         raise ValueError("y: bf16 or f32 is needed")
-    args = _kv_args(fmt, cache, page, offsets, page_table, lens, rows, dim, k_scale, v_scale)
+    args = _kv_args(fmt, cache, page, offsets, page_table, lens, rows, dim)
     nb = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check("fp4q_kv_attention",
            lib().fp4q_kv_attention(*args, q.data_ptr(), ldq, heads, max_new, max_len, window, scale,
-                                   _opt(k_scale), _opt(v_scale), y.data_ptr(),
-                                   OUT_F32 if y.dtype == torch.float32 else OUT_BF16,
-                                   y.stride(0) if rows > 1 else heads * dim, _opt(workspace), nb,
+                                   _head_scale(k_scale, args[4]), _head_scale(v_scale, args[4]),
+                                   y.data_ptr(), OUT_F32 if dtype is torch.float32 else OUT_BF16,
+                                   stride[0] if rows > 1 else heads * dim, _opt(workspace), nb,
                                    _stream(stream)))
 
 
@@ -916,22 +931,21 @@ def kv_attention(fmt, cache, page, offsets, page_table, lens, q, max_new, max_le
 
 # ---- the router and the combination ---------------------------------------
 
-def _float_type(name, t):
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+def _matrix(name, t):
+    """(type, row stride) of a matrix with contiguous rows."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or (shape[1] > 1 and stride[1] != 1):
         raise ValueError(f"{name}: a matrix with contiguous rows is needed")
-    if t.dtype == torch.float32:
-        return OUT_F32
-    if t.dtype == torch.bfloat16:
-        return OUT_BF16
+    ld = stride[0] if shape[0] > 1 else shape[1]
+    if t.dtype is torch.float32:
+        return OUT_F32, ld
+    if t.dtype is torch.bfloat16:
+        return OUT_BF16, ld
     raise ValueError(f"{name}: f32 or bf16 is needed")
 
 
-def _ld(t):
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
-
-
 def _f32(name, t, shape):
-    if t.dtype != torch.float32 or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+    if t.dtype is not torch.float32 or not t.is_contiguous() or t.shape != shape:
         raise ValueError(f"{name}: contiguous f32 {list(shape)} is needed")
     return t.data_ptr()
 
@@ -943,10 +957,10 @@ def route_workspace_bytes(tokens, experts) -> int:
 def route_into(logits, k, score, bias, n_groups, top_groups, renorm, experts, weights, offsets,
                row_src, row_of, workspace, stream=None):
     T, E = logits.shape
-    dt = _float_type("logits", logits)
+    dt, ld = _matrix("logits", logits)
     nb = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check("fp4q_route",
-           lib().fp4q_route(logits.data_ptr(), dt, T, E, _ld(logits), k, score,
+           lib().fp4q_route(logits.data_ptr(), dt, T, E, ld, k, score,
                             None if bias is None else _f32("bias", bias, (E,)), n_groups,
                             top_groups, int(renorm), _int32("experts", experts),
                             _f32("weights", weights, (T, k)), _int32("offsets", offsets),
@@ -962,33 +976,39 @@ def route(logits, k, score=SOFTMAX, bias=None, n_groups=1, top_groups=1, renorm=
     [tokens, k], offsets int32 [experts + 1], row_src int32 [tokens * k],
     row_of int32 [tokens, k])."""
     T, E = logits.shape
-    dev = logits.device
-    # one allocation for the five results
     Tk = T * k
-    buf = torch.empty(4 * Tk + E + 1, dtype=torch.int32, device=dev)
-    r = {"experts": buf[:Tk].view(T, k), "weights": buf[Tk:2 * Tk].view(torch.float32).view(T, k),
-         "offsets": buf[4 * Tk:], "row_src": buf[2 * Tk:3 * Tk],
-         "row_of": buf[3 * Tk:4 * Tk].view(T, k)}
+    # one allocation for the workspace and the five results
     nb = route_workspace_bytes(T, E)
-    ws = torch.empty(nb, dtype=torch.uint8, device=dev) if nb else None
-    route_into(logits, k, score, bias, n_groups, top_groups, renorm, r["experts"], r["weights"],
-               r["offsets"], r["row_src"], r["row_of"], ws, stream)
-    _keep(stream, buf, ws)
+    ws = -(-nb // 8) * 2
+    buf = torch.empty(ws + 4 * Tk + E + 1, dtype=torch.int32, device=logits.device)
+    scratch, experts, weights, row_src, row_of, offsets = buf.split([ws, Tk, Tk, Tk, Tk, E + 1])
+    r = {"experts": experts.view(T, k), "weights": weights.view(torch.float32).view(T, k),
+         "offsets": offsets, "row_src": row_src, "row_of": row_of.view(T, k)}
+    dt, ld = _matrix("logits", logits)
+    at = buf.data_ptr() + 4 * ws
+    _check("fp4q_route",
+           lib().fp4q_route(logits.data_ptr(), dt, T, E, ld, k, score,
+                            None if bias is None else _f32("bias", bias, (E,)), n_groups,
+                            top_groups, int(renorm), at, at + 4 * Tk, at + 16 * Tk, at + 8 * Tk,
+                            at + 12 * Tk, buf.data_ptr() if nb else None, 4 * ws, _stream(stream)))
+    _keep(stream, buf)
     return r
 
 
 def route_backward_into(logits, experts, d_weights, score, renorm, d_logits, stream=None):
-    T, E = logits.shape
-    dt = _float_type("logits", logits)
-    if d_logits.shape != logits.shape or _float_type("d_logits", d_logits) != dt:
+    T, E = shape = logits.shape
+    dt, ld = _matrix("logits", logits)
+    ddt, ldd = _matrix("d_logits", d_logits)
+    if d_logits.shape != shape or ddt != dt:
         raise ValueError("d_logits: the logits' shape and type are needed")
-    if experts.shape[0] != T:
+    chosen = experts.shape
+    if len(chosen) != 2 or chosen[0] != T:
         raise ValueError("experts: one row for each token")
     _check("fp4q_route_backward",
-           lib().fp4q_route_backward(logits.data_ptr(), dt, T, E, _ld(logits), experts.shape[1],
-                                     score, int(renorm), _int32("experts", experts),
-                                     _f32("d_weights", d_weights, experts.shape),
-                                     d_logits.data_ptr(), _ld(d_logits), _stream(stream)))
+           lib().fp4q_route_backward(logits.data_ptr(), dt, T, E, ld, chosen[1], score,
+                                     int(renorm), _int32("experts", experts),
+                                     _f32("d_weights", d_weights, chosen), d_logits.data_ptr(),
+                                     ldd, _stream(stream)))
 
 
 def route_backward(logits, experts, d_weights, score=SOFTMAX, renorm=True, stream=None):
@@ -1001,14 +1021,16 @@ def route_backward(logits, experts, d_weights, score=SOFTMAX, renorm=True, strea
 
 
 def combine_into(y, row_of, weights, out, stream=None):
-    T, k = row_of.shape
-    dt = _float_type("y", y)
-    if _float_type("out", out) != dt or tuple(out.shape) != (T, y.shape[1]):
+    T, k = shape = row_of.shape
+    rows, cols = y.shape
+    dt, ldy = _matrix("y", y)
+    odt, ldo = _matrix("out", out)
+    if odt != dt or out.shape != (T, cols):
         raise ValueError("out: [tokens, cols] of y's type is needed")
     _check("fp4q_combine",
-           lib().fp4q_combine(dt, y.data_ptr(), y.shape[0], y.shape[1], _ld(y),
-                              _int32("row_of", row_of), _f32("weights", weights, (T, k)), T, k,
-                              out.data_ptr(), _ld(out), _stream(stream)))
+           lib().fp4q_combine(dt, y.data_ptr(), rows, cols, ldy, _int32("row_of", row_of),
+                              _f32("weights", weights, shape), T, k, out.data_ptr(), ldo,
+                              _stream(stream)))
 
 
 def combine(y, row_of, weights, stream=None):
@@ -1021,18 +1043,20 @@ def combine(y, row_of, weights, stream=None):
 
 
 def combine_backward_into(y, row_of, weights, d_out, d_y, d_weights, stream=None):
-    T, k = row_of.shape
-    dt = _float_type("y", y)
-    if _float_type("d_out", d_out) != dt or tuple(d_out.shape) != (T, y.shape[1]):
+    T, k = shape = row_of.shape
+    rows, cols = y.shape
+    dt, ldy = _matrix("y", y)
+    odt, ldo = _matrix("d_out", d_out)
+    if odt != dt or d_out.shape != (T, cols):
         raise ValueError("d_out: [tokens, cols] of y's type is needed")
-    if _float_type("d_y", d_y) != dt or d_y.shape != y.shape:
+    ddt, lddy = _matrix("d_y", d_y)
+    if ddt != dt or d_y.shape != (rows, cols):
         raise ValueError("d_y: y's shape and type are needed")
     _check("fp4q_combine_backward",
-           lib().fp4q_combine_backward(dt, y.data_ptr(), y.shape[0], y.shape[1], _ld(y),
-                                       _int32("row_of", row_of),
-                                       _f32("weights", weights, (T, k)), T, k, d_out.data_ptr(),
-                                       _ld(d_out), d_y.data_ptr(), _ld(d_y),
-                                       _f32("d_weights", d_weights, (T, k)), _stream(stream)))
+           lib().fp4q_combine_backward(dt, y.data_ptr(), rows, cols, ldy,
+                                       _int32("row_of", row_of), _f32("weights", weights, shape),
+                                       T, k, d_out.data_ptr(), ldo, d_y.data_ptr(), lddy,
+                                       _f32("d_weights", d_weights, shape), _stream(stream)))
 
 
 def combine_backward(y, row_of, weights, d_out, stream=None):
