@@ -13,8 +13,8 @@ namespace {
 typedef __bf16 bf16x2r __attribute__((ext_vector_type(2)));
 typedef float v2f32r __attribute__((ext_vector_type(2)));
 
-constexpr int RT_TOK = 64;        // tokens of a workgroup: one bit each in the experts' masks
-constexpr int RT_THREADS = 512;  // 8 waves
+constexpr int RT_TOK = 64;         // most tokens of a workgroup: one bit each in the experts' masks
+constexpr int RT_THREADS = 1024;  // 16 waves
 constexpr int RT_MAX_E = FP4Q_ROUTE_MAX_EXPERTS;
 constexpr int RT_MAX_K = FP4Q_ROUTE_MAX_K;
 
@@ -30,8 +30,9 @@ struct RouteArgs {
   int32_t* row_src;
   int32_t* row_of;
   uint64_t* masks;  // [blocks][E]: which of the block's tokens chose the expert
-  uint8_t* counts;  // [blocks][E]: how many
-  int blocks;
+  uint8_t* counts;  // [E][pitch]: how many, of each block
+  int blocks, tok;  // workgroups and their tokens
+  int pitch;        // blocks up to a multiple of 16
 };
 
 __device__ __forceinline__ float load_logit(const void* x, int f32, int64_t i) {
@@ -39,20 +40,74 @@ __device__ __forceinline__ float load_logit(const void* x, int f32, int64_t i) {
              : bf16_to_f32(reinterpret_cast<const uint16_t*>(x)[i]);
 }
 
-template <typename T>
-__device__ __forceinline__ T wave_max(T v) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) {
-    const T o = __shfl_xor(v, d);
-    v = o > v ? o : v;
-  }
-  return v;
+// The value of the lane that differs in bit 0, 1, 2 or 3 of its number (the
+// last two: of the mirrored lane, the same for a reduction), by vector moves: a
+// shuffle would go through LDS at many times the latency.
+template <int BIT>
+__device__ __forceinline__ uint32_t lane_swap(uint32_t v) {
+  constexpr int ctl = BIT == 0 ? 0xB1 : BIT == 1 ? 0x4E : BIT == 2 ? 0x141 : 0x140;
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, ctl, 0xF, 0xF, true);
 }
 
-__device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d);
-  return v;
+__device__ __forceinline__ int pick_max(int a, int b) { return a > b ? a : b; }
+__device__ __forceinline__ double pick_max(double a, double b) { return fmax(a, b); }
+__device__ __forceinline__ double add(double a, double b) { return a + b; }
+
+// All lanes' values joined by f (commutative): every lane has the result.
+template <typename T, T (*F)(T, T)>
+__device__ __forceinline__ T wave_all(T v) {
+  if constexpr (sizeof(T) == 4) {
+    auto bits = [](uint32_t u) { return __builtin_bit_cast(T, u); };
+    auto raw = [](T t) { return __builtin_bit_cast(uint32_t, t); };
+    v = F(v, bits(lane_swap<0>(raw(v))));
+    v = F(v, bits(lane_swap<1>(raw(v))));
+    v = F(v, bits(lane_swap<2>(raw(v))));
+    v = F(v, bits(lane_swap<3>(raw(v))));
+    u32x2 r = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(raw(v), raw(v), false, false));
+    v = F(bits(r[0]), bits(r[1]));
+    r = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(raw(v), raw(v), false, false));
+    return F(bits(r[0]), bits(r[1]));
+  } else {
+    auto bits = [](uint32_t lo, uint32_t hi) { return __builtin_bit_cast(T, u32x2{lo, hi}); };
+    u32x2 u = __builtin_bit_cast(u32x2, v);
+    v = F(v, bits(lane_swap<0>(u[0]), lane_swap<0>(u[1])));
+    u = __builtin_bit_cast(u32x2, v);
+    v = F(v, bits(lane_swap<1>(u[0]), lane_swap<1>(u[1])));
+    u = __builtin_bit_cast(u32x2, v);
+    v = F(v, bits(lane_swap<2>(u[0]), lane_swap<2>(u[1])));
+    u = __builtin_bit_cast(u32x2, v);
+    v = F(v, bits(lane_swap<3>(u[0]), lane_swap<3>(u[1])));
+    u = __builtin_bit_cast(u32x2, v);
+    u32x2 l = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(u[0], u[0], false, false));
+    u32x2 h = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(u[1], u[1], false, false));
+    v = F(bits(l[0], h[0]), bits(l[1], h[1]));
+    u = __builtin_bit_cast(u32x2, v);
+    l = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(u[0], u[0], false, false));
+    h = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(u[1], u[1], false, false));
+    return F(bits(l[0], h[0]), bits(l[1], h[1]));
+  }
+}
+
+__device__ __forceinline__ int wave_max(int v) { return wave_all<int, pick_max>(v); }
+__device__ __forceinline__ double wave_max(double v) { return wave_all<double, pick_max>(v); }
+__device__ __forceinline__ double wave_sum(double v) { return wave_all<double, add>(v); }
+
+// Lane l's value, l the same for all lanes.
+__device__ __forceinline__ int of_lane(int v, int l) { return __builtin_amdgcn_readlane(v, l); }
+__device__ __forceinline__ double of_lane(double v, int l) {
+  const u32x2 u = __builtin_bit_cast(u32x2, v);
+  return __builtin_bit_cast(double, u32x2{(uint32_t)of_lane((int)u[0], l), (uint32_t)of_lane((int)u[1], l)});
+}
+
+// A float as an integer of the same order (both zeros alike; NaN as -inf, so
+// that it comes last), and back.
+constexpr int ORDER_NONE = (int)0x80000000;  // below every float's
+__device__ __forceinline__ int order_of(float x) {
+  const int u = __float_as_int(x == x ? x + 0.0f : -__builtin_inff());
+  return u ^ ((u >> 31) & 0x7FFFFFFF);
+}
+__device__ __forceinline__ float order_value(int o) {
+  return __int_as_float(o ^ ((o >> 31) & 0x7FFFFFFF));
 }
 
 // The expert order of a workgroup's tokens: base[e] is where the block's
@@ -109,19 +164,30 @@ __global__ __launch_bounds__(RT_THREADS) void k_route_pick(RouteArgs p) {
   const int E = p.E, k = p.k;
   for (int e = threadIdx.x; e < E; e += RT_THREADS) s_mask[e] = 0;
   __syncthreads();
-  const int64_t t0 = (int64_t)blockIdx.x * RT_TOK;
-  const int nt = (int)min((int64_t)RT_TOK, p.T - t0);
-  for (int tt = wave; tt < nt; tt += RT_THREADS / 64) {
-    const int64_t row = (t0 + tt) * p.ldx;
-    float x[NS];
-    float top = -__builtin_inff();
+  const int64_t t0 = (int64_t)blockIdx.x * p.tok;
+  const int nt = (int)min((int64_t)p.tok, p.T - t0);
+  float next[NS];  // the wave's next token's logits, loaded while one is picked for
+  auto load_row = [&](int tt) {
+    const int64_t row = (t0 + min(tt, nt - 1)) * p.ldx;
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
       const int e = lane + 64 * i;
-      x[i] = e < E ? load_logit(p.logits, p.f32, row + e) : -__builtin_inff();
-      top = fmaxf(top, x[i]);
+      next[i] = e < E ? load_logit(p.logits, p.f32, row + e) : -__builtin_inff();
     }
-    top = wave_max(top);
+  };
+  if (wave < nt) load_row(wave);
+  for (int tt = wave; tt < nt; tt += RT_THREADS / 64) {
+    float x[NS];
+#pragma unroll
+    for (int i = 0; i < NS; ++i) x[i] = next[i];
+    load_row(tt + RT_THREADS / 64);
+    int ord[NS], top_ord = ORDER_NONE;
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+      ord[i] = order_of(x[i]);
+      top_ord = pick_max(top_ord, ord[i]);
+    }
+    const float top = order_value(wave_max(top_ord));
     // softmax: scores are exp(x - m) / Z; all scores of a row without a
     // finite logit are 0
     const double m = top > -__builtin_inff() ? (double)top : 0.0;
@@ -144,15 +210,21 @@ __global__ __launch_bounds__(RT_THREADS) void k_route_pick(RouteArgs p) {
         for (int i = 0; i < NS; ++i) s[i] /= z;
       }
     }
-    typedef typename std::conditional<WIDE, double, float>::type key_t;
+    typedef typename std::conditional<WIDE, double, int>::type key_t;
+    // what cannot be picked (any more) has a key that no comparison finds: NaN,
+    // or the integer below every float's
+    const key_t gone = WIDE ? (key_t)__builtin_nan("") : (key_t)ORDER_NONE;
     key_t key[NS];
-    uint32_t avail = 0;
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
       const int e = lane + 64 * i;
-      if (e < E) avail |= 1u << i;
-      key[i] = WIDE ? (key_t)(s[i] + (p.bias && e < E ? (double)p.bias[e] : 0.0)) : (key_t)x[i];
-      if (!(key[i] == key[i])) key[i] = -__builtin_inff();  // NaN comes last
+      if constexpr (WIDE) {
+        key[i] = s[i] + (p.bias && e < E ? (double)p.bias[e] : 0.0);
+        if (!(key[i] == key[i])) key[i] = -__builtin_inf();  // NaN comes last
+      } else {
+        key[i] = ord[i];
+      }
+      if (e >= E) key[i] = gone;
     }
     if (WIDE && p.G > 1) {
       // each group's two best, by 64 / 2^ceil(log2 G) lanes a group
@@ -178,7 +250,8 @@ __global__ __launch_bounds__(RT_THREADS) void k_route_pick(RouteArgs p) {
         a = fmax(a, a2);
         b = fmax(lo, fmax(b, b2));
       }
-      const double sum = gs > 1 ? a + b : a;
+      double sum = gs > 1 ? a + b : a;
+      if (!(sum == sum)) sum = -__builtin_inf();
       int rank = 0;
       for (int o = 0; o < p.G; ++o) {
         const double other = __shfl(sum, o * P);
@@ -188,42 +261,36 @@ __global__ __launch_bounds__(RT_THREADS) void k_route_pick(RouteArgs p) {
 #pragma unroll
       for (int i = 0; i < NS; ++i) {
         const int e = lane + 64 * i;
-        if (e < E && !((keep >> (e / gs * P)) & 1)) avail &= ~(1u << i);
+        if (e < E && !((keep >> (e / gs * P)) & 1)) key[i] = gone;
       }
       __builtin_amdgcn_wave_barrier();
     }
     // k rounds: the largest key left, the lowest expert that has it; lane j
     // keeps the round's expert and its score
     int my_e = 0;
-    double my_s = 0.0;
     for (int j = 0; j < k; ++j) {
-      key_t best = -__builtin_inff();
+      key_t best = key[0];
 #pragma unroll
-      for (int i = 0; i < NS; ++i)
-        if ((avail >> i) & 1) best = key[i] > best ? key[i] : best;
+      for (int i = 1; i < NS; ++i) best = pick_max(best, key[i]);
       best = wave_max(best);
       int pick = -1;
 #pragma unroll
       for (int i = 0; i < NS; ++i) {
-        const uint64_t has = __ballot(((avail >> i) & 1) && key[i] == best);
+        const uint64_t has = __ballot(key[i] == best);
         if (pick < 0 && has) pick = 64 * i + (int)__ffsll((unsigned long long)has) - 1;
       }
-      const int slot = pick >> 6, owner = pick & 63;
-      double sv = 0.0;
-      float xv = 0.0f;
 #pragma unroll
       for (int i = 0; i < NS; ++i)
-        if (i == slot) {
-          if (WIDE) sv = s[i];
-          else xv = x[i];
-        }
-      if (WIDE) sv = __shfl(sv, owner);
-      else sv = (double)__shfl(xv, owner);
-      if (lane == owner) avail &= ~(1u << slot);
-      if (lane == j) {
-        my_e = pick;
-        my_s = sv;
-      }
+        if (lane + 64 * i == pick) key[i] = gone;
+      if (lane == j) my_e = pick;
+    }
+    double my_s = 0.0;
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+      double v;
+      if constexpr (WIDE) v = __shfl(s[i], my_e & 63);
+      else v = (double)__shfl(x[i], my_e & 63);
+      if (i == my_e >> 6) my_s = v;
     }
     if (!WIDE) my_s = soft ? exp(my_s - m) / z : 1.0 / (1.0 + exp(-my_s));
     if (p.renorm) {
@@ -241,7 +308,7 @@ __global__ __launch_bounds__(RT_THREADS) void k_route_pick(RouteArgs p) {
   if (p.blocks > 1) {
     for (int e = threadIdx.x; e < E; e += RT_THREADS) {
       p.masks[(int64_t)blockIdx.x * E + e] = s_mask[e];
-      p.counts[(int64_t)blockIdx.x * E + e] = (uint8_t)__popcll(s_mask[e]);
+      p.counts[(int64_t)e * p.pitch + blockIdx.x] = (uint8_t)__popcll(s_mask[e]);
     }
     return;
   }
@@ -255,24 +322,39 @@ __global__ __launch_bounds__(RT_THREADS) void k_route_pick(RouteArgs p) {
 
 // Expert order over all workgroups' tokens: a workgroup sums every block's
 // counts (all of them for the experts' offsets, the earlier blocks' for its
-// own base) and places its rows.
+// own base) and places its rows.  Q neighbouring lanes share an expert's counts,
+// 16 bytes at a time.
 __global__ __launch_bounds__(RT_THREADS) void k_route_order(RouteArgs p) {
   __shared__ int s_base[RT_MAX_E], s_before[RT_MAX_E];
   __shared__ int s_tmp[RT_THREADS / 64], s_total;
   __shared__ uint64_t s_mask[RT_MAX_E];
   const int E = p.E;
-  const int64_t t0 = (int64_t)blockIdx.x * RT_TOK;
-  const int nt = (int)min((int64_t)RT_TOK, p.T - t0);
-  for (int e = threadIdx.x; e < E; e += RT_THREADS) {
-    int all = 0, before = 0;
-    for (int b = 0; b < p.blocks; ++b) {
-      const int c = p.counts[(int64_t)b * E + e];
-      all += c;
-      before += b < (int)blockIdx.x ? c : 0;
+  const int64_t t0 = (int64_t)blockIdx.x * p.tok;
+  const int nt = (int)min((int64_t)p.tok, p.T - t0);
+  int Q = 64;
+  while (Q * E > RT_THREADS && Q > 1) Q >>= 1;
+  const int q = threadIdx.x % Q;
+  for (int e = threadIdx.x / Q; e < E; e += RT_THREADS / Q) {
+    uint32_t all = 0, before = 0;
+    for (int c = q * 16; c < p.blocks; c += Q * 16) {
+      const u32x4 w = *reinterpret_cast<const u32x4*>(p.counts + (int64_t)e * p.pitch + c);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        // the bytes of the first n of these four blocks
+        auto first = [&](int n) { return n >= 4 ? ~0u : n <= 0 ? 0u : (1u << (8 * n)) - 1u; };
+        all = __builtin_amdgcn_sad_u8(w[i] & first(p.blocks - c - 4 * i), 0u, all);
+        before = __builtin_amdgcn_sad_u8(w[i] & first((int)blockIdx.x - c - 4 * i), 0u, before);
+      }
     }
-    s_base[e] = all;
-    s_before[e] = before;
-    s_mask[e] = p.masks[(int64_t)blockIdx.x * E + e];
+    for (int d = 1; d < Q; d <<= 1) {
+      all += __shfl_xor(all, d);
+      before += __shfl_xor(before, d);
+    }
+    if (q == 0) {
+      s_base[e] = (int)all;
+      s_before[e] = (int)before;
+      s_mask[e] = p.masks[(int64_t)blockIdx.x * E + e];
+    }
   }
   __syncthreads();
   block_scan(s_base, E, s_tmp, &s_total);
@@ -286,10 +368,13 @@ __global__ __launch_bounds__(RT_THREADS) void k_route_order(RouteArgs p) {
 }
 
 // Gradient of the logits, one wave per token.  With p the chosen scores and
-// dp their gradient (through the renormalisation w = p / sum p when there is
-// one: dp = (dw - sum(dw w)) / sum p):
+// dp their gradient:
 //   softmax: dx_i = -score_i sum(dp p), plus dp_i score_i where chosen
 //   sigmoid: dx_i = dp_i score_i (1 - score_i) where chosen, else 0
+// Through the renormalisation w = p / sum p it is dp = (dw - sum(dw w)) / sum p,
+// for which sum(dp p) = 0: then the softmax's sum over all experts cancels and
+// the chosen logits' exponentials are all that is needed.  Bound by the 64-bit
+// arithmetic: 16384 x 128 renormalised takes 13.3 us, its 17 MB 3 us.
 template <int NS>
 __global__ __launch_bounds__(256) void k_route_backward(const void* logits, int f32, int64_t T,
                                                         int64_t ldx, int E, int k, int score,
@@ -301,17 +386,22 @@ __global__ __launch_bounds__(256) void k_route_backward(const void* logits, int 
   if (t >= T) return;
   const bool soft = score == FP4Q_SCORE_SOFTMAX;
   float x[NS];
-  float top = -__builtin_inff();
+  int top_ord = ORDER_NONE;
 #pragma unroll
   for (int i = 0; i < NS; ++i) {
     const int e = lane + 64 * i;
     x[i] = e < E ? load_logit(logits, f32, t * ldx + e) : -__builtin_inff();
-    top = fmaxf(top, x[i]);
+    top_ord = pick_max(top_ord, order_of(x[i]));
   }
-  top = wave_max(top);
+  const float top = order_value(wave_max(top_ord));
   const double m = top > -__builtin_inff() ? (double)top : 0.0;
+  // lane j: the j-th chosen expert (indices outside the experts: no gradient)
+  const int e = lane < k ? experts[t * k + lane] : -1;
+  const bool on = e >= 0 && e < E;
+  double dw = on ? (double)d_weights[t * k + lane] : 0.0;
+  const bool all = soft && !renorm;
   double s[NS], z = 1.0;
-  if (soft) {
+  if (all) {
     double part = 0.0;
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
@@ -319,36 +409,35 @@ __global__ __launch_bounds__(256) void k_route_backward(const void* logits, int 
       part += s[i];
     }
     z = wave_sum(part);
-    if (!(z > 0.0)) z = 1.0;
+    z = z > 0.0 ? 1.0 / z : 1.0;
 #pragma unroll
-    for (int i = 0; i < NS; ++i) s[i] /= z;
+    for (int i = 0; i < NS; ++i) s[i] *= z;
   }
-  // lane j: the j-th chosen expert (indices outside the experts: no gradient)
-  const int e = lane < k ? experts[t * k + lane] : -1;
-  const bool on = e >= 0 && e < E;
-  double p = 0.0, dw = 0.0;
-  if (on) {
-    const double xe = (double)load_logit(logits, f32, t * ldx + e);
-    p = soft ? exp(xe - m) / z : 1.0 / (1.0 + exp(-xe));
-    dw = (double)d_weights[t * k + lane];
+  float xe = 0.0f;
+#pragma unroll
+  for (int i = 0; i < NS; ++i) {
+    const float xi = __shfl(x[i], e & 63);
+    if (i == e >> 6) xe = xi;
   }
+  double p = 0.0;
+  if (on) p = soft ? exp((double)xe - m) * z : 1.0 / (1.0 + exp(-(double)xe));
   if (renorm) {
     const double sum = wave_sum(p), dot = wave_sum(dw * p);
-    dw = on && sum > 0.0 ? (dw - dot / sum) / sum : 0.0;
+    const double r = sum > 0.0 ? 1.0 / sum : 0.0;
+    dw = (dw - dot * r) * r;
   }
-  const double dot = soft ? wave_sum(dw * p) : 0.0;
-  const double add = soft ? dw * p : dw * p * (1.0 - p);
+  const double dot = all ? wave_sum(dw * p) : 0.0;
+  const double add_e = soft ? dw * p : dw * p * (1.0 - p);
   double dx[NS];
 #pragma unroll
-  for (int i = 0; i < NS; ++i) dx[i] = soft ? -s[i] * dot : 0.0;
+  for (int i = 0; i < NS; ++i) dx[i] = all ? -s[i] * dot : 0.0;
   for (int j = 0; j < k; ++j) {
-    const int ej = __shfl(e, j);
-    const double aj = __shfl(add, j);
-    if (ej >= 0 && (ej & 63) == lane) {
+    const int ej = of_lane(e, j);
+    const double aj = of_lane(add_e, j);
+    const double mine = (ej & 63) == lane ? aj : 0.0;
 #pragma unroll
-      for (int i = 0; i < NS; ++i)
-        if (i == ej >> 6) dx[i] += aj;
-    }
+    for (int i = 0; i < NS; ++i)
+      if (i == ej >> 6) dx[i] += mine;  // (of ej < 0: none)
   }
 #pragma unroll
   for (int i = 0; i < NS; ++i) {
@@ -430,7 +519,8 @@ struct CombineArgs {
 };
 
 // out[t] = sum_j w[t, j] y[row_of[t, j]]: a thread holds VEC columns of one
-// token, the rows added in order j in FP32.
+// token, the rows added in order j in FP32, eight rows' loads in flight (an
+// entry outside the rows loads row 0 and adds nothing).
 template <bool F32, int VEC>
 __global__ __launch_bounds__(256) void k_combine(CombineArgs p) {
   const int64_t per = p.N / VEC;
@@ -440,15 +530,21 @@ __global__ __launch_bounds__(256) void k_combine(CombineArgs p) {
   float acc[VEC];
 #pragma unroll
   for (int e = 0; e < VEC; ++e) acc[e] = 0.0f;
-#pragma unroll 8
-  for (int j = 0; j < p.k; ++j) {
-    const int64_t r = p.row_of[t * p.k + j];
-    if (r < 0 || r >= p.rows) continue;
-    const float w = p.w[t * p.k + j];
-    float v[VEC];
-    load_vec<F32, VEC>(p.y, r * p.ldy + c, v);
+  for (int j0 = 0; p.rows > 0 && j0 < p.k; j0 += 8) {
+    float v[8][VEC], w[8];
+    bool ok[8];
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) acc[e] = __builtin_fmaf(w, v[e], acc[e]);
+    for (int u = 0; u < 8; ++u) {
+      const int j = min(j0 + u, p.k - 1);
+      const int32_t r = p.row_of[t * p.k + j];
+      ok[u] = j0 + u < p.k && r >= 0 && r < p.rows;
+      w[u] = p.w[t * p.k + j];
+      load_vec<F32, VEC>(p.y, (ok[u] ? r : 0) * p.ldy + c, v[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) acc[e] = ok[u] ? __builtin_fmaf(w[u], v[u][e], acc[e]) : acc[e];
   }
   store_vec<F32, VEC>(p.out, t * p.ldo + c, acc);
 }
@@ -489,21 +585,25 @@ inline bool vec_ok(const void* p, int64_t ld, int esz) {
 
 }  // namespace
 
+// Tokens of a workgroup: few while that leaves CUs without one.
+static int route_tokens(int64_t T) { return T <= 4096 ? 16 : RT_TOK; }
+
 size_t route_workspace_bytes(int64_t T, int E) {
-  const int64_t blocks = (T + RT_TOK - 1) / RT_TOK;
-  return blocks > 1 ? (size_t)(blocks * E * 9) : 0;
+  const int64_t tok = route_tokens(T), blocks = (T + tok - 1) / tok;
+  return blocks > 1 ? (size_t)E * (size_t)((blocks + 15) / 16 * 16 + blocks * 8) : 0;
 }
 
 void launch_route(const void* logits, int f32, int64_t T, int64_t ldx, int E, int k, int score,
                   const float* bias, int G, int top_groups, int renorm, int32_t* experts,
                   float* weights, int32_t* offsets, int32_t* row_src, int32_t* row_of, void* ws,
                   hipStream_t stream) {
-  const int blocks = (int)((T + RT_TOK - 1) / RT_TOK);
+  const int tok = route_tokens(T), blocks = (int)((T + tok - 1) / tok);
   RouteArgs p = {logits,  f32,     T,       ldx,     E,      k,  score, G, top_groups, renorm, bias,
-                 experts, weights, offsets, row_src, row_of, nullptr, nullptr, blocks > 0 ? blocks : 1};
+                 experts, weights, offsets, row_src, row_of, nullptr, nullptr, blocks > 0 ? blocks : 1,
+                 tok,     (blocks + 15) / 16 * 16};
   if (blocks > 1) {
-    p.masks = static_cast<uint64_t*>(ws);
-    p.counts = reinterpret_cast<uint8_t*>(p.masks + (int64_t)blocks * E);
+    p.counts = static_cast<uint8_t*>(ws);
+    p.masks = reinterpret_cast<uint64_t*>(p.counts + (int64_t)E * p.pitch);
   }
   const bool wide = bias != nullptr || G > 1;
   const dim3 grid((unsigned)p.blocks), thr(RT_THREADS);
