@@ -81,25 +81,48 @@ __device__ __forceinline__ KvItem kv_item(const KvArgs& p, int32_t* s_off) {
   return it;
 }
 
-// The 16 bytes of a V run are byte-interleaved; w holds the codes of the run
-// two neighbouring elements to a byte, b the bytes of elements (l, 16 + l).
-__device__ __forceinline__ void v_bytes_from_codes(const uint32_t (&w)[4], uint8_t (&b)[16]) {
+// A V run is stored with its bytes apart: byte l (elements l, 16 + l of the run)
+// of run j of a token at l * 4J + j, so the J lanes that hold a token's runs
+// exchange bytes through LDS, after which a lane has 16 / J stretches of J bytes
+// that lie together in the cache.  w: the run's codes, two neighbouring elements
+// to a byte; b: bytes (16 / J) j .. of the token, each J long.  (A wave's LDS
+// operations keep their order; the fences hold the compiler to it.)
+__device__ __forceinline__ void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+template <int J>
+__device__ __forceinline__ u32x4 v_bytes_from_codes(const uint32_t (&w)[4], int j, uint8_t* token) {
 #pragma unroll
   for (int l = 0; l < 16; ++l) {
     const uint32_t lo = (w[l >> 3] >> (4 * (l & 7))) & 15u;
     const uint32_t hi = (w[2 + (l >> 3)] >> (4 * (l & 7))) & 15u;
-    b[l] = (uint8_t)(lo | (hi << 4));
+    token[l * J + j] = (uint8_t)(lo | (hi << 4));
   }
+  wave_fence();
+  return *reinterpret_cast<const u32x4*>(token + 16 * j);
 }
 
-__device__ __forceinline__ void v_codes_from_bytes(const uint8_t (&b)[16], uint32_t (&w)[4]) {
+template <int J>
+__device__ __forceinline__ void v_codes_from_bytes(u32x4 b, int j, uint8_t* token, uint32_t (&w)[4]) {
+  *reinterpret_cast<u32x4*>(token + 16 * j) = b;
+  wave_fence();
   w[0] = w[1] = w[2] = w[3] = 0;
 #pragma unroll
   for (int l = 0; l < 16; ++l) {
-    w[l >> 3] |= (uint32_t)(b[l] & 15u) << (4 * (l & 7));
-    w[2 + (l >> 3)] |= (uint32_t)(b[l] >> 4) << (4 * (l & 7));
+    const uint32_t c = token[l * J + j];
+    w[l >> 3] |= (c & 15u) << (4 * (l & 7));
+    w[2 + (l >> 3)] |= (c >> 4) << (4 * (l & 7));
   }
 }
+
+// The stretches of lane j: J bytes each, 4J apart in the cache.
+template <int J>
+struct Stretch;
+template <> struct Stretch<2> { typedef uint16_t type; };
+template <> struct Stretch<4> { typedef uint32_t type; };
+template <> struct Stretch<8> { typedef u32x2 type; };
 
 // Codes (w) and scale codes (s: NVFP4 two bytes, MXFP4 one) of 32 elements.
 template <int FMT>
@@ -157,8 +180,9 @@ template <int FMT, int D>
 __global__ __launch_bounds__(KV_THREADS) void k_kv_append(KvArgs p) {
   typedef KvLayout<FMT, D> L;
   __shared__ int32_t s_off[KV_LDS_SEQ + 1];
+  __shared__ __attribute__((aligned(16))) uint8_t s_v[KV_THREADS * 16];
   const KvItem it = kv_item<FMT, D>(p, s_off);
-  if (it.base == nullptr) return;
+  if (it.base == nullptr) return;  // (the lanes of a token together)
   const bool is_v = blockIdx.y != 0;
   const uint16_t* src = is_v ? p.v + it.row * p.ldv : p.k + it.row * p.ldk;
   const u32x4* x4 = reinterpret_cast<const u32x4*>(src + it.h * D + it.j * 32);
@@ -179,68 +203,102 @@ __global__ __launch_bounds__(KV_THREADS) void k_kv_append(KvArgs p) {
     u32x4 o = {w[0], w[1], w[2], w[3]};
     *reinterpret_cast<u32x4*>(it.base + it.slot * (D / 2) + it.j * 16) = o;
   } else {
-    uint8_t b[16];
-    v_bytes_from_codes(w, b);
-    uint8_t* dst = it.base + L::v_codes(page) + (it.slot >> 2) * (2 * D) + (it.slot & 3) * L::J + it.j;
+    typedef typename Stretch<L::J>::type T;
+    const u32x4 b = v_bytes_from_codes<L::J>(w, it.j, s_v + threadIdx.x / L::J * (16 * L::J));
+    uint8_t* dst = it.base + L::v_codes(page) + (it.slot >> 2) * (2 * D) + (it.slot & 3) * L::J +
+                   it.j * (16 / L::J) * 4 * L::J;
 #pragma unroll
-    for (int l = 0; l < 16; ++l) dst[l * 4 * L::J] = b[l];
+    for (int i = 0; i < 16 / L::J; ++i) {
+      T t;
+      if constexpr (L::J == 2) t = (T)(b[i >> 1] >> (16 * (i & 1)));
+      else if constexpr (L::J == 4) t = b[i];
+      else t = T{b[2 * i], b[2 * i + 1]};
+      *reinterpret_cast<T*>(dst + i * 4 * L::J) = t;
+    }
   }
 }
 
+// A thread's 64 bytes leave through LDS, so that four lanes write each of them
+// at once (stored from the registers that hold them they took half as long again).
 template <int FMT, int D>
 __global__ __launch_bounds__(KV_THREADS) void k_kv_read(KvArgs p) {
   typedef KvLayout<FMT, D> L;
   __shared__ int32_t s_off[KV_LDS_SEQ + 1];
+  __shared__ u32x4 s_out[KV_THREADS * 4];
+  __shared__ u32x4* s_dst[KV_THREADS];
+  uint8_t* const s_v = reinterpret_cast<uint8_t*>(s_out + (threadIdx.x & ~63) * 4);  // the wave's part
   const KvItem it = kv_item<FMT, D>(p, s_off);
-  if (it.row >= p.rows) return;
   const bool is_v = blockIdx.y != 0;
-  uint16_t* dst = is_v ? p.v + it.row * p.ldv : p.k + it.row * p.ldk;
-  u32x4* y4 = reinterpret_cast<u32x4*>(dst + it.h * D + it.j * 32);
-  if (it.base == nullptr) {  // nothing stored for this row
-    const u32x4 z = {0, 0, 0, 0};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) y4[i] = z;
-    return;
+  const int lane = threadIdx.x & 63;
+  {
+    uint16_t* dst = is_v ? p.v + it.row * p.ldv : p.k + it.row * p.ldk;
+    s_dst[threadIdx.x] = it.row < p.rows ? reinterpret_cast<u32x4*>(dst + it.h * D + it.j * 32) : nullptr;
   }
-  const int page = 1 << p.page_shift;
-  uint32_t w[4];
-  if (!is_v) {
-    const u32x4 u = *reinterpret_cast<const u32x4*>(it.base + it.slot * (D / 2) + it.j * 16);
+  u32x4 out[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = u[i];
-  } else {
-    uint8_t b[16];
-    const uint8_t* src =
-        it.base + L::v_codes(page) + (it.slot >> 2) * (2 * D) + (it.slot & 3) * L::J + it.j;
+  for (int i = 0; i < 4; ++i) out[i] = u32x4{0, 0, 0, 0};  // nothing stored for this row: zeros
+  if (it.base != nullptr) {
+    const int page = 1 << p.page_shift;
+    uint32_t w[4];
+    if (!is_v) {
+      const u32x4 u = *reinterpret_cast<const u32x4*>(it.base + it.slot * (D / 2) + it.j * 16);
 #pragma unroll
-    for (int l = 0; l < 16; ++l) b[l] = src[l * 4 * L::J];
-    v_codes_from_bytes(b, w);
-  }
-  const uint8_t* sc = it.base + (is_v ? L::v_scales(page) : L::k_scales(page)) + it.slot * L::SB;
-  float s0, s1, t = 1.0f;
-  if (FMT == FP4Q_NVFP4) {
-    const uint32_t s = reinterpret_cast<const uint16_t*>(sc)[it.j];
-    s0 = e4m3_value(s & 0xFFu);
-    s1 = e4m3_value(s >> 8);
-    t = (is_v ? p.vts : p.kts)[it.h];
-  } else {
-    s0 = s1 = exp2i((int)sc[it.j] - 127);
-  }
+      for (int i = 0; i < 4; ++i) w[i] = u[i];
+    } else {
+      typedef typename Stretch<L::J>::type T;
+      const uint8_t* src = it.base + L::v_codes(page) + (it.slot >> 2) * (2 * D) + (it.slot & 3) * L::J +
+                           it.j * (16 / L::J) * 4 * L::J;
+      u32x4 b = {0, 0, 0, 0};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float s = i < 2 ? s0 : s1;
-    u32x4 o;
+      for (int i = 0; i < 16 / L::J; ++i) {
+        const T t = *reinterpret_cast<const T*>(src + i * 4 * L::J);
+        if constexpr (L::J == 2) {
+          b[i >> 1] |= (uint32_t)t << (16 * (i & 1));
+        } else if constexpr (L::J == 4) {
+          b[i] = t;
+        } else {
+          b[2 * i] = t[0];
+          b[2 * i + 1] = t[1];
+        }
+      }
+      v_codes_from_bytes<L::J>(b, it.j, s_v + lane / L::J * (16 * L::J), w);
+    }
+    const uint8_t* sc = it.base + (is_v ? L::v_scales(page) : L::k_scales(page)) + it.slot * L::SB;
+    float s0, s1, t = 1.0f;
+    if (FMT == FP4Q_NVFP4) {
+      const uint32_t s = reinterpret_cast<const uint16_t*>(sc)[it.j];
+      s0 = e4m3_value(s & 0xFFu);
+      s1 = e4m3_value(s >> 8);
+      t = (is_v ? p.vts : p.kts)[it.h];
+    } else {
+      s0 = s1 = exp2i((int)sc[it.j] - 127);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float s = i < 2 ? s0 : s1;
 #define FP4Q_KV_PAIR(N)                                                             \
-  {                                                                                 \
-    const v2f32k e = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[i], 1.0f, N);       \
-    v2f32k f;                                                                       \
-    f[0] = (e[0] * s) * t;                                                          \
-    f[1] = (e[1] * s) * t;                                                          \
-    o[N] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f, bf16x2k));       \
-  }
-    FP4Q_KV_PAIR(0) FP4Q_KV_PAIR(1) FP4Q_KV_PAIR(2) FP4Q_KV_PAIR(3)
+    {                                                                                 \
+      const v2f32k e = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[i], 1.0f, N);       \
+      v2f32k f;                                                                       \
+      f[0] = (e[0] * s) * t;                                                          \
+      f[1] = (e[1] * s) * t;                                                          \
+      out[i][N] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f, bf16x2k));       \
+    }
+      FP4Q_KV_PAIR(0) FP4Q_KV_PAIR(1) FP4Q_KV_PAIR(2) FP4Q_KV_PAIR(3)
 #undef FP4Q_KV_PAIR
-    y4[i] = o;
+    }
+  }
+  wave_fence();
+  // chunk i of a lane's four, turned by its number so that the banks are all used
+  u32x4* const mine = s_out + (threadIdx.x & ~63) * 4;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) mine[lane * 4 + ((i + (lane >> 2)) & 3)] = out[i];
+  wave_fence();
+#pragma unroll
+  for (int m = 0; m < 4; ++m) {
+    const int from = 16 * m + (lane >> 2), i = lane & 3;
+    u32x4* dst = s_dst[(threadIdx.x & ~63) + from];
+    if (dst) dst[i] = mine[from * 4 + ((i + (from >> 2)) & 3)];
   }
 }
 
