@@ -35,9 +35,15 @@ struct RouteArgs {
   int pitch;        // blocks up to a multiple of 16
 };
 
-__device__ __forceinline__ float load_logit(const void* x, int f32, int64_t i) {
+__device__ __forceinline__ float load_value(const void* x, int f32, int64_t i) {
   return f32 ? reinterpret_cast<const float*>(x)[i]
              : bf16_to_f32(reinterpret_cast<const uint16_t*>(x)[i]);
+}
+
+// A logit: NaN counts as -inf.
+__device__ __forceinline__ float load_logit(const void* x, int f32, int64_t i) {
+  const float v = load_value(x, f32, i);
+  return v == v ? v : -__builtin_inff();
 }
 
 // The value of the lane that differs in bit 0, 1, 2 or 3 of its number (the
@@ -99,11 +105,10 @@ __device__ __forceinline__ double of_lane(double v, int l) {
   return __builtin_bit_cast(double, u32x2{(uint32_t)of_lane((int)u[0], l), (uint32_t)of_lane((int)u[1], l)});
 }
 
-// A float as an integer of the same order (both zeros alike; NaN as -inf, so
-// that it comes last), and back.
+// A float as an integer of the same order (both zeros alike; no NaN), and back.
 constexpr int ORDER_NONE = (int)0x80000000;  // below every float's
 __device__ __forceinline__ int order_of(float x) {
-  const int u = __float_as_int(x == x ? x + 0.0f : -__builtin_inff());
+  const int u = __float_as_int(x + 0.0f);
   return u ^ ((u >> 31) & 0x7FFFFFFF);
 }
 __device__ __forceinline__ float order_value(int o) {
@@ -455,7 +460,7 @@ __global__ __launch_bounds__(256) void k_route_backward(const void* logits, int 
 template <bool F32, int VEC>
 __device__ __forceinline__ void load_vec(const void* x, int64_t i, float (&v)[VEC]) {
   if (VEC == 1) {
-    v[0] = load_logit(x, F32, i);
+    v[0] = load_value(x, F32, i);
   } else if (F32) {
 #pragma unroll
     for (int c = 0; c < VEC / 4; ++c) {

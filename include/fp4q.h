@@ -724,10 +724,12 @@ int fp4q_kv_read(fp4q_format_t fmt, const uint8_t* cache, int64_t n_pages, int32
  *
  * over the keys j of the row's sequence with j <= position(r), and, with
  * window > 0, j > position(r) - window; g = h / (heads / kv_heads).  A row
- * that sees no key gives 0.  What stands in the cache outside these keys
- * (NaN scales included) does not reach the result.  One token a sequence
- * (decode), the few of a speculative step, prompts and chunks of them are
- * all this call.
+ * that sees no key gives 0.  What stands in the cache outside the keys that
+ * the new tokens see (NaN scales included) does not reach the result, nor
+ * does a later token's value that fp4q_kv_append stored: of MXFP4 values,
+ * block scales above 2^125 count as 2^125, so that all of them are finite.
+ * One token a sequence (decode), the few of a speculative step, prompts and
+ * chunks of them are all this call.
  *
  *   q              bf16 [rows, heads, dim], row stride ldq (a multiple of 8,
  *                  16-byte aligned)
@@ -770,8 +772,8 @@ int fp4q_kv_attention(fp4q_format_t fmt, const uint8_t* cache, int64_t n_pages, 
  *            of their two best ranked scores stay (n_groups 1: no groups)
  *   experts  the k best ranked of those, best first
  *   weights  their scores (renorm: divided by their sum)
- * Ties go to the lower index; NaN ranks last.  A token without a finite
- * logit has weights 0.  And the order by expert that the grouped calls
+ * Ties go to the lower index; a NaN logit counts as -inf.  A token without
+ * a finite logit has weights 0.  And the order by expert that the grouped calls
  * above take: row_src (token of each routed row, rows of an expert by
  * token), group offsets, and row_of (the row of each token's j-th expert).
  *

@@ -1,0 +1,133 @@
+"""GPU: the paths that attention and the router take by size (row tiles,
+splits of the keys, tokens of a workgroup), at the borders of their rules,
+against the plain 64-bit forms with the tolerances of
+test_gpu_kv_attention.py and test_gpu_route_combine.py."""
+import numpy as np
+import pytest
+import torch
+
+import fp4_w4a4_quantized_amd as fq
+from gpu_helpers import need_gpu, say
+from oracle import layer
+from test_gpu_kv_attention import FMTS, attend, check_close, dev, make
+from test_gpu_route_combine import check_route, host, logits_of
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("n", [16, 17, 32, 33, 63, 64, 65, 128, 129, 257])
+def test_rows_around_the_tiles(fmt, D, n):
+    """One head a kv head: n rows, the first that see the fewest keys included."""
+    need_gpu()
+    say(f"rows fmt {fmt} D {D} n {n}")
+    c = make(fmt, [n, 1], [n, n + 3], G=1, H=1, D=D, seed=n)
+    check_close(c, attend(c))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("page", [16, 32, 64, 1024])
+@pytest.mark.parametrize("window", [0, 63, 500])
+def test_prompt_chunks_over_split_keys(fmt, page, window):
+    """Many rows over keys that are split, in pages smaller and larger than a
+    step of 64 keys."""
+    need_gpu()
+    say(f"chunk fmt {fmt} page {page} window {window}")
+    c = make(fmt, [70, 40], [1500, 2101], G=4, H=1, D=64, page=page, seed=page + window)
+    a = attend(c, window)
+    check_close(c, a, window)
+    assert torch.equal(a, attend(c, window)), "two runs differ"
+    check_close(c, attend(c, window, max_len=30000), window)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D", [64, 128])
+def test_prompts_with_pages_gone(fmt, D):
+    need_gpu()
+    c = make(fmt, [60, 90, 50], [200, 90, 333], G=3, H=2, D=D, page=16, seed=D)
+    c["table"][0, 2] = -1
+    c["table"][0, 12] = 10 ** 6                    # of the newest tokens
+    c["table"][1, :] = -1
+    c["table"][2, 0:20:2] = -2147483648
+    got = attend(c, max_len=333)
+    check_close(c, got)
+    assert torch.all(got[60:150] == 0)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("mult", [2.0 ** 14, 2.0 ** 30])
+def test_prompt_with_huge_scores(fmt, mult):
+    """Scores far past 2^20, where their differences decide alone: the largest
+    takes all."""
+    need_gpu()
+    c = make(fmt, [50], [90], G=2, H=2, D=128, seed=3)
+    c["q"] = layer.bf16_round(c["q"] * mult)
+    o, _, s = layer.attention(fmt, c["cache"], c["page"], c["off"], c["table"], c["lens"], c["q"], c["t"],
+                              c["t"])
+    g = attend(c).float().cpu().numpy()
+    # rows whose two largest scores are further apart than 64 + the scores' own
+    # rounding have one weight of 1 in both
+    k, _ = zip(*[layer.kv_values(fmt, c["cache"], 16, 128, c["table"][0, np.arange(90) // 16].astype(np.int64),
+                                 np.arange(90) % 16, h, c["t"], c["t"]) for h in range(2)])
+    checked = 0
+    for i in range(50):
+        for j in range(4):
+            x = np.sort((k[j // 2][:41 + i] @ c["q"][i, j]) * 128 ** -0.5)
+            if x[-1] - x[-2] > 64 + 2 * 144 * 2.0 ** -24 * s[i, j, 0]:
+                checked += 1
+                assert np.all(np.abs(g[i, j] - o[i, j]) <= 2.0 ** -7 * np.abs(o[i, j]) + 1e-6), (i, j)
+    assert checked > 100
+
+
+def test_infinite_values_of_later_tokens_stay_there():
+    """MXFP4: a later token's largest possible values do not reach the rows
+    before it."""
+    need_gpu()
+    c = make(1, [64], [64], G=1, H=1, D=64, page=16, seed=6, garbage=False)
+    kb, kh, vb, vh, ks, vs = layer.kv_places(1, 16, 64)
+    clean = attend(c)
+    c["cache"][c["table"][0, 3]][:, vs[15]] = 254   # the last token's V scales
+    got = attend(c)
+    assert torch.equal(got[:63], clean[:63])
+
+
+@pytest.mark.parametrize("T", [15, 16, 17, 4095, 4096, 4097, 9000])
+def test_router_blocks(T):
+    need_gpu()
+    say(f"route T {T}")
+    x = logits_of(T, 40, torch.float32, T)
+    check_route(x, 3)
+    check_route(x, 5, 1, torch.linspace(-0.1, 0.1, 40).cuda(), 4, 2)
+
+
+def test_router_nan_logits_count_as_minus_infinity():
+    need_gpu()
+    x = logits_of(50, 70, torch.float32, 2)
+    x[3, 5:60] = float("nan")
+    x[4, :] = float("nan")
+    x[7, 69] = float("nan")
+    y = torch.where(torch.isnan(x), torch.full_like(x, -float("inf")), x)
+    dw = torch.ones(50, 4, device="cuda")
+    for score in (0, 1):
+        for renorm in (False, True):
+            a, b = (fq.route(v, 4, score=score, renorm=renorm) for v in (x, y))
+            for key in a:
+                assert torch.equal(a[key], b[key]), key
+            da, db = (fq.route_backward(v, a["experts"], dw, score=score, renorm=renorm) for v in (x, y))
+            assert torch.equal(da, db) and torch.isfinite(da).all()
+            check_route(y, 4, score, renorm=renorm)
+
+
+def test_combine_without_rows():
+    need_gpu()
+    row_of = torch.zeros(5, 2, dtype=torch.int32, device="cuda")
+    w = torch.ones(5, 2, device="cuda")
+    out = fq.combine(torch.empty(0, 64, device="cuda"), row_of, w)
+    assert torch.all(out == 0)
+    big = torch.full((3, 64), float("nan"), device="cuda")
+    row_of[:] = -1
+    row_of[0, 1] = 2
+    big[2] = 1.0
+    got = host(fq.combine(big, row_of, w))
+    assert np.all(got[0] == 1.0) and np.all(got[1:] == 0.0)
