@@ -773,6 +773,30 @@ def error_decompose(fmt, x, stream=None):
 
 
 # ---- the FP4 key/value cache ----------------------------------------------
+#
+# These calls and those after them check their tensors and allocate their
+# results in the native module _layer (csrc/layer_binding.cpp).
+
+_native = None
+
+
+def _layer():
+    global _native
+    if _native is None:
+        lib()
+        try:
+            from . import _layer as native
+        except ImportError as e:
+            raise ImportError(f"{e}: build it with "
+                              "`python -m fp4_w4a4_quantized_amd.build`") from e
+        native.set_up(_check, lambda: _stream(None))
+        _native = native
+    return _native
+
+
+def _handle(stream):
+    return None if stream is None else stream.cuda_stream
+
 
 def _keep(stream, *tensors):
     """Memory of torch's current stream that a call on another one uses is not
@@ -781,20 +805,6 @@ def _keep(stream, *tensors):
         for t in tensors:
             if t is not None:
                 t.record_stream(stream)
-
-
-def _rows_of(name, t, heads_dim=None):
-    """Row stride of a [rows, heads, dim] tensor whose heads lie one after
-    another."""
-    shape, stride = t.shape, t.stride()
-    if len(shape) != 3 or stride[2] != 1 or (shape[1] > 1 and stride[1] != shape[2]):
-        raise ValueError(f"{name}: [rows, heads, dim] with contiguous heads is needed")
-    dtype = t.dtype
-    if dtype is not torch.bfloat16 and dtype is not torch.int16:
-        raise ValueError(f"{name}: bf16 is needed")
-    if heads_dim is not None and (shape[1], shape[2]) != heads_dim:
-        raise ValueError(f"{name}: {heads_dim[0]} heads of {heads_dim[1]} are needed")
-    return stride[0] if shape[0] > 1 else shape[1] * shape[2]
 
 
 def kv_page_bytes(fmt, page, dim) -> int:
@@ -810,76 +820,22 @@ def kv_cache(fmt, n_pages, page, kv_heads, dim, device="cuda"):
     return torch.empty((n_pages, kv_heads, nb), dtype=torch.uint8, device=device)
 
 
-def _int32(name, t):
-    if t.dtype is not torch.int32 or not t.is_contiguous():
-        raise ValueError(f"{name}: contiguous int32 is needed")
-    return t.data_ptr()
-
-
-def _head_scale(t, heads):
-    if t is None:
-        return None
-    if t.dtype is not torch.float32 or not t.is_contiguous() or t.numel() != heads:
-        raise ValueError("k_scale, v_scale: contiguous f32, one for each kv head")
-    return t.data_ptr()
-
-
-def _kv_args(fmt, cache, page, offsets, page_table, lens, rows, dim):
-    shape = cache.shape
-    if cache.dtype is not torch.uint8 or len(shape) != 3 or not cache.is_contiguous():
-        raise ValueError("cache: contiguous u8 [n_pages, kv_heads, page bytes] is needed")
-    n_pages, heads, nb = shape
-    if nb != lib().fp4q_kv_page_bytes(fmt, page, dim):
-        raise ValueError("cache: its page bytes are not those of this format, page and dim")
-    tshape = page_table.shape
-    if page_table.dtype is not torch.int32 or len(tshape) != 2:
-        raise ValueError("page_table: int32 [batch, pages] is needed")
-    batch, cols = tshape
-    ld, unit = page_table.stride()
-    if cols > 1 and unit != 1:
-        raise ValueError("page_table: int32 [batch, pages] is needed")
-    if offsets.numel() != batch + 1 or lens.numel() != batch:
-        raise ValueError("offsets, page_table and lens differ in their sequences")
-    return (fmt, cache.data_ptr(), n_pages, page, heads, dim, _int32("offsets", offsets), batch,
-            page_table.data_ptr(), ld if batch > 1 else cols, cols, _int32("lens", lens), rows)
-
-
-def _opt(t):
-    return None if t is None else t.data_ptr()
-
-
 def kv_append(fmt, cache, page, offsets, page_table, lens, k, v, k_scale=None, v_scale=None,
               stream=None):
     """Quantize the new tokens' keys and values (bf16 [rows, kv_heads, dim])
     into the paged cache.  offsets int32 [batch + 1] (rows of each sequence),
     page_table int32 [batch, pages], lens int32 [batch] (new tokens
     included), all on the GPU; k_scale, v_scale f32 [kv_heads] (NVFP4)."""
-    ldk = _rows_of("k", k)
-    rows, heads, dim = k.shape
-    ldv = _rows_of("v", v, (heads, dim))
-    if v.shape[0] != rows:
-        raise ValueError("k and v differ in their rows")
-    args = _kv_args(fmt, cache, page, offsets, page_table, lens, rows, dim)
-    if args[4] != heads:
-        raise ValueError(f"k: {args[4]} heads of {dim} are needed")
-    _check("fp4q_kv_append",
-           lib().fp4q_kv_append(*args, k.data_ptr(), ldk, v.data_ptr(), ldv,
-                                _head_scale(k_scale, heads), _head_scale(v_scale, heads),
-                                _stream(stream)))
+    _layer().append(_handle(stream), fmt, cache, page, offsets, page_table, lens, k_scale, v_scale,
+                    k, v)
 
 
 def kv_read(fmt, cache, page, offsets, page_table, lens, rows, dim, k_scale=None, v_scale=None,
             stream=None):
     """The values that stand in the cache for the new tokens: (k, v) bf16
     [rows, kv_heads, dim]."""
-    args = _kv_args(fmt, cache, page, offsets, page_table, lens, rows, dim)
-    heads = args[4]
-    k, v = torch.empty((2, rows, heads, dim), dtype=torch.bfloat16, device=cache.device).unbind(0)
-    ld = heads * dim
-    _check("fp4q_kv_read",
-           lib().fp4q_kv_read(*args, k.data_ptr(), ld, v.data_ptr(), ld,
-                              _head_scale(k_scale, heads), _head_scale(v_scale, heads),
-                              _stream(stream)))
+    k, v = _layer().read(_handle(stream), fmt, cache, page, offsets, page_table, lens, k_scale,
+                         v_scale, rows, dim)
     _keep(stream, k)
     return k, v
 
@@ -893,21 +849,8 @@ def kv_attention_workspace_bytes(fmt, rows, heads, kv_heads, dim, batch, max_new
 def kv_attention_into(fmt, cache, page, offsets, page_table, lens, q, max_new, max_len, k_scale,
                       v_scale, window, scale, y, workspace, stream=None):
     """fp4q_kv_attention: y bf16 or f32 [rows, heads, dim]."""
-    ldq = _rows_of("q", q)
-    rows, heads, dim = shape = q.shape
-    stride, dtype = y.stride(), y.dtype
-    if y.shape != shape or stride[2] != 1 or (heads > 1 and stride[1] != dim):
-        raise ValueError("y: q's shape with contiguous heads is needed")
-    if dtype is not torch.bfloat16 and dtype is not torch.float32:
-        raise ValueError("y: bf16 or f32 is needed")
-    args = _kv_args(fmt, cache, page, offsets, page_table, lens, rows, dim)
-    nb = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check("fp4q_kv_attention",
-           lib().fp4q_kv_attention(*args, q.data_ptr(), ldq, heads, max_new, max_len, window, scale,
-                                   _head_scale(k_scale, args[4]), _head_scale(v_scale, args[4]),
-                                   y.data_ptr(), OUT_F32 if dtype is torch.float32 else OUT_BF16,
-                                   stride[0] if rows > 1 else heads * dim, _opt(workspace), nb,
-                                   _stream(stream)))
+    _layer().attention_into(_handle(stream), fmt, cache, page, offsets, page_table, lens, k_scale,
+                            v_scale, q, max_new, max_len, window, scale, y, workspace)
 
 
 def kv_attention(fmt, cache, page, offsets, page_table, lens, q, max_new, max_len, k_scale=None,
@@ -917,6 +860,9 @@ def kv_attention(fmt, cache, page, offsets, page_table, lens, q, max_new, max_le
     max_new new tokens or is longer than max_len.  window > 0: a token sees
     the last `window` keys only; scale: dim^-0.5 unless given.  Returns
     [rows, heads, dim]."""
+    if stream is None:
+        return _layer().attention(None, fmt, cache, page, offsets, page_table, lens, k_scale,
+                                  v_scale, q, max_new, max_len, window, scale, y_dtype)
     rows, heads, dim = q.shape
     y = torch.empty((rows, heads, dim), device=q.device,
                     dtype=torch.float32 if y_dtype == OUT_F32 else torch.bfloat16)
@@ -931,41 +877,14 @@ def kv_attention(fmt, cache, page, offsets, page_table, lens, q, max_new, max_le
 
 # ---- the router and the combination ---------------------------------------
 
-def _matrix(name, t):
-    """(type, row stride) of a matrix with contiguous rows."""
-    shape, stride = t.shape, t.stride()
-    if len(shape) != 2 or (shape[1] > 1 and stride[1] != 1):
-        raise ValueError(f"{name}: a matrix with contiguous rows is needed")
-    ld = stride[0] if shape[0] > 1 else shape[1]
-    if t.dtype is torch.float32:
-        return OUT_F32, ld
-    if t.dtype is torch.bfloat16:
-        return OUT_BF16, ld
-    raise ValueError(f"{name}: f32 or bf16 is needed")
-
-
-def _f32(name, t, shape):
-    if t.dtype is not torch.float32 or not t.is_contiguous() or t.shape != shape:
-        raise ValueError(f"{name}: contiguous f32 {list(shape)} is needed")
-    return t.data_ptr()
-
-
 def route_workspace_bytes(tokens, experts) -> int:
     return lib().fp4q_route_workspace_bytes(tokens, experts)
 
 
 def route_into(logits, k, score, bias, n_groups, top_groups, renorm, experts, weights, offsets,
                row_src, row_of, workspace, stream=None):
-    T, E = logits.shape
-    dt, ld = _matrix("logits", logits)
-    nb = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check("fp4q_route",
-           lib().fp4q_route(logits.data_ptr(), dt, T, E, ld, k, score,
-                            None if bias is None else _f32("bias", bias, (E,)), n_groups,
-                            top_groups, int(renorm), _int32("experts", experts),
-                            _f32("weights", weights, (T, k)), _int32("offsets", offsets),
-                            _int32("row_src", row_src), _int32("row_of", row_of), _opt(workspace),
-                            nb, _stream(stream)))
+    _layer().route_into(_handle(stream), logits, k, score, bias, n_groups, top_groups, renorm,
+                        experts, weights, offsets, row_src, row_of, workspace)
 
 
 def route(logits, k, score=SOFTMAX, bias=None, n_groups=1, top_groups=1, renorm=True, stream=None):
@@ -975,95 +894,45 @@ def route(logits, k, score=SOFTMAX, bias=None, n_groups=1, top_groups=1, renorm=
     top_groups best stay.  Returns dict(experts int32 [tokens, k], weights f32
     [tokens, k], offsets int32 [experts + 1], row_src int32 [tokens * k],
     row_of int32 [tokens, k])."""
-    T, E = logits.shape
-    Tk = T * k
-    # one allocation for the workspace and the five results
-    nb = route_workspace_bytes(T, E)
-    ws = -(-nb // 8) * 2
-    buf = torch.empty(ws + 4 * Tk + E + 1, dtype=torch.int32, device=logits.device)
-    scratch, experts, weights, row_src, row_of, offsets = buf.split([ws, Tk, Tk, Tk, Tk, E + 1])
-    r = {"experts": experts.view(T, k), "weights": weights.view(torch.float32).view(T, k),
-         "offsets": offsets, "row_src": row_src, "row_of": row_of.view(T, k)}
-    dt, ld = _matrix("logits", logits)
-    at = buf.data_ptr() + 4 * ws
-    _check("fp4q_route",
-           lib().fp4q_route(logits.data_ptr(), dt, T, E, ld, k, score,
-                            None if bias is None else _f32("bias", bias, (E,)), n_groups,
-                            top_groups, int(renorm), at, at + 4 * Tk, at + 16 * Tk, at + 8 * Tk,
-                            at + 12 * Tk, buf.data_ptr() if nb else None, 4 * ws, _stream(stream)))
-    _keep(stream, buf)
-    return r
+    experts, weights, offsets, row_src, row_of = _layer().route(
+        _handle(stream), logits, k, score, bias, n_groups, top_groups, renorm)
+    _keep(stream, experts, weights)
+    return {"experts": experts, "weights": weights, "offsets": offsets, "row_src": row_src,
+            "row_of": row_of}
 
 
 def route_backward_into(logits, experts, d_weights, score, renorm, d_logits, stream=None):
-    T, E = shape = logits.shape
-    dt, ld = _matrix("logits", logits)
-    ddt, ldd = _matrix("d_logits", d_logits)
-    if d_logits.shape != shape or ddt != dt:
-        raise ValueError("d_logits: the logits' shape and type are needed")
-    chosen = experts.shape
-    if len(chosen) != 2 or chosen[0] != T:
-        raise ValueError("experts: one row for each token")
-    _check("fp4q_route_backward",
-           lib().fp4q_route_backward(logits.data_ptr(), dt, T, E, ld, chosen[1], score,
-                                     int(renorm), _int32("experts", experts),
-                                     _f32("d_weights", d_weights, chosen), d_logits.data_ptr(),
-                                     ldd, _stream(stream)))
+    _layer().route_backward_into(_handle(stream), logits, experts, d_weights, score, renorm,
+                                 d_logits)
 
 
 def route_backward(logits, experts, d_weights, score=SOFTMAX, renorm=True, stream=None):
     """Gradient of the logits from that of route()'s weights (f32
     [tokens, k]) and its chosen experts."""
-    d = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
-    route_backward_into(logits, experts, d_weights, score, renorm, d, stream)
+    d = _layer().route_backward(_handle(stream), logits, experts, d_weights, score, renorm)
     _keep(stream, d)
     return d
 
 
 def combine_into(y, row_of, weights, out, stream=None):
-    T, k = shape = row_of.shape
-    rows, cols = y.shape
-    dt, ldy = _matrix("y", y)
-    odt, ldo = _matrix("out", out)
-    if odt != dt or out.shape != (T, cols):
-        raise ValueError("out: [tokens, cols] of y's type is needed")
-    _check("fp4q_combine",
-           lib().fp4q_combine(dt, y.data_ptr(), rows, cols, ldy, _int32("row_of", row_of),
-                              _f32("weights", weights, shape), T, k, out.data_ptr(), ldo,
-                              _stream(stream)))
+    _layer().combine_into(_handle(stream), y, row_of, weights, out)
 
 
 def combine(y, row_of, weights, stream=None):
     """out[t] = sum_j weights[t, j] y[row_of[t, j]]: the experts' outputs y
     (f32 or bf16 [rows, cols], in expert order) back to the tokens."""
-    out = torch.empty((row_of.shape[0], y.shape[1]), dtype=y.dtype, device=y.device)
-    combine_into(y, row_of, weights, out, stream)
+    out = _layer().combine(_handle(stream), y, row_of, weights)
     _keep(stream, out)
     return out
 
 
 def combine_backward_into(y, row_of, weights, d_out, d_y, d_weights, stream=None):
-    T, k = shape = row_of.shape
-    rows, cols = y.shape
-    dt, ldy = _matrix("y", y)
-    odt, ldo = _matrix("d_out", d_out)
-    if odt != dt or d_out.shape != (T, cols):
-        raise ValueError("d_out: [tokens, cols] of y's type is needed")
-    ddt, lddy = _matrix("d_y", d_y)
-    if ddt != dt or d_y.shape != (rows, cols):
-        raise ValueError("d_y: y's shape and type are needed")
-    _check("fp4q_combine_backward",
-           lib().fp4q_combine_backward(dt, y.data_ptr(), rows, cols, ldy,
-                                       _int32("row_of", row_of), _f32("weights", weights, shape),
-                                       T, k, d_out.data_ptr(), ldo, d_y.data_ptr(), lddy,
-                                       _f32("d_weights", d_weights, shape), _stream(stream)))
+    _layer().combine_backward_into(_handle(stream), y, row_of, weights, d_out, d_y, d_weights)
 
 
 def combine_backward(y, row_of, weights, d_out, stream=None):
     """(d_y, d_weights) of combine() from d_out.  row_of names every row of y
     (combine_backward_into leaves the others as they are)."""
-    d_y = torch.empty(y.shape, dtype=y.dtype, device=y.device)
-    d_w = torch.empty(row_of.shape, dtype=torch.float32, device=y.device)
-    combine_backward_into(y, row_of, weights, d_out, d_y, d_w, stream)
+    d_y, d_w = _layer().combine_backward(_handle(stream), y, row_of, weights, d_out)
     _keep(stream, d_y, d_w)
     return d_y, d_w

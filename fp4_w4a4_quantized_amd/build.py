@@ -17,6 +17,9 @@ SOURCES = ["api.hip", "quantize.hip", "gemm.hip", "gemm_big.hip", "gemm_skinny.h
 # the peak microbenchmarks (measurement only) go into a library of their own
 PEAKS_LIB = os.path.join(HERE, "libfp4q_peaks.so")
 PEAKS_SOURCES = ["peaks.hip"]
+# the Python module of the calls between the FP4 linear layers (host code)
+LAYER_LIB = os.path.join(HERE, "_layer.so")
+LAYER_SOURCE = "layer_binding.cpp"
 ARCH = "gfx950"
 
 
@@ -51,11 +54,38 @@ def _link(out: str, sources: list[str], verbose: bool) -> str:
     return out
 
 
+def _link_layer(verbose: bool) -> str:
+    """The module against libfp4q.so (found next to it when loaded) and torch."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    tmp = LAYER_LIB + ".tmp"
+    include = [x for p in cpp_extension.include_paths() + [sysconfig.get_paths()["include"]]
+               for x in ("-isystem", p)]
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *include, "-o", tmp,
+           os.path.join(CSRC, LAYER_SOURCE), f"-L{HERE}", "-l:" + os.path.basename(LIB),
+           "-Wl,-rpath,$ORIGIN", f"-L{os.path.join(os.path.dirname(torch.__file__), 'lib')}", "-lc10",
+           "-ltorch_cpu", "-ltorch_python"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError("g++ failed:\n" + res.stdout + res.stderr)
+    if verbose and res.stderr:
+        print(res.stderr)
+    os.replace(tmp, LAYER_LIB)
+    return LAYER_LIB
+
+
 def build(verbose: bool = False) -> str:
     """Compile every kernel source into libfp4q.so (and the peak
-    microbenchmarks into libfp4q_peaks.so); returns libfp4q.so's path."""
+    microbenchmarks into libfp4q_peaks.so, and the Python module _layer on top
+    of it); returns libfp4q.so's path."""
     _link(PEAKS_LIB, PEAKS_SOURCES, verbose)
-    return _link(LIB, SOURCES, verbose)
+    _link(LIB, SOURCES, verbose)
+    _link_layer(verbose)
+    return LIB
 
 
 if __name__ == "__main__":
