@@ -87,7 +87,8 @@ __device__ __forceinline__ void pipeline_reads() {
 }
 
 template <int FMT, int D, int WAVES>
-__global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void k_attn_tile(AttnArgs p) {
+__global__ __launch_bounds__(64 * WAVES)
+    __attribute__((amdgpu_waves_per_eu(D == 64 ? 4 : D == 128 ? 2 : 1))) void k_attn_tile(AttnArgs p) {
   typedef typename Num<FMT>::vec vec;
   typedef typename Num<FMT>::pair pair;
   typedef KvLayout<FMT, D> L;
@@ -129,29 +130,6 @@ __global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void k_attn_tile(Attn
   const int see_lo = p.window > 0 ? pos - p.window + 1 : 0;
   const int pos_a = rg.first + min(wrow, rg.rows - 1) / p.G;        // the wave's first and
   const int pos_z = rg.first + (min(wrow + 32, rg.rows) - 1) / p.G;  // last position
-  vec qf[D / 16];
-  float cf;
-  {
-    const uint16_t* q = p.q + (rg.r0 + qi) * p.ldq + hh * D + half * 8;
-    w4 u[D / 16];
-#pragma unroll
-    for (int st = 0; st < D / 16; ++st) u[st] = *reinterpret_cast<const w4*>(q + 16 * st);
-    cf = p.scale2 * (FMT == FP4Q_NVFP4 ? p.kts[h] : 1.0f);
-    if constexpr (FMT == FP4Q_MXFP4) {
-#pragma unroll
-      for (int st = 0; st < D / 16; ++st) qf[st] = __builtin_bit_cast(vec, u[st]);
-    } else {
-      uint32_t mq = 0;
-#pragma unroll
-      for (int st = 0; st < D / 16; ++st) mq = max(mq, max_magnitude(u[st]));
-      mq = max(mq, (uint32_t)__shfl_xor((int)mq, 32));
-      const int sh = q_exponent(mq);
-      cf *= __uint_as_float((uint32_t)(127 + sh) << 23);
-#pragma unroll
-      for (int st = 0; st < D / 16; ++st) qf[st] = __builtin_bit_cast(vec, q_to_f16(u[st], sh));
-    }
-    cf = fmaxf(cf, 1e-37f);
-  }
   float m = -__builtin_inff(), z = 0.0f;
   float lim = m;        // a score above it asks for a new maximum
   float nb = P_BIAS;    // P_BIAS - m cf
@@ -244,6 +222,36 @@ __global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void k_attn_tile(Attn
     }
   };
 
+  const int steps = k0 < k1 ? (k1 - k0 + TILE_KEYS - 1) / TILE_KEYS : 0;
+  if (steps > 0) {  // on their way while q is loaded
+    load_ids(0);
+    load_bytes(0);
+    load_ids(1);
+  }
+  vec qf[D / 16];
+  float cf;
+  {
+    const uint16_t* q = p.q + (rg.r0 + qi) * p.ldq + hh * D + half * 8;
+    w4 u[D / 16];
+#pragma unroll
+    for (int st = 0; st < D / 16; ++st) u[st] = *reinterpret_cast<const w4*>(q + 16 * st);
+    cf = p.scale2 * (FMT == FP4Q_NVFP4 ? p.kts[h] : 1.0f);
+    if constexpr (FMT == FP4Q_MXFP4) {
+#pragma unroll
+      for (int st = 0; st < D / 16; ++st) qf[st] = __builtin_bit_cast(vec, u[st]);
+    } else {
+      uint32_t mq = 0;
+#pragma unroll
+      for (int st = 0; st < D / 16; ++st) mq = max(mq, max_magnitude(u[st]));
+      mq = max(mq, (uint32_t)__shfl_xor((int)mq, 32));
+      const int sh = q_exponent(mq);
+      cf *= __uint_as_float((uint32_t)(127 + sh) << 23);
+#pragma unroll
+      for (int st = 0; st < D / 16; ++st) qf[st] = __builtin_bit_cast(vec, q_to_f16(u[st], sh));
+    }
+    cf = fmaxf(cf, 1e-37f);
+  }
+
   // ---- the keys ---------------------------------------------------------------
   // One barrier a step.  The V team's waves and the K team's (one of each on a
   // SIMD) go through a step in another order, so that one's products meet the
@@ -253,7 +261,6 @@ __global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void k_attn_tile(Attn
   // In step t K of t and t + 1 and V of t are read, K of t + 2 and V of t + 1
   // written: three K buffers and two V buffers do.  Of the page flags, that of t
   // is read and that of t + 3 written (with the load): four do.
-  const int steps = k0 < k1 ? (k1 - k0 + TILE_KEYS - 1) / TILE_KEYS : 0;
   // this wave's steps (those that some row of it sees)
   int t_on = 0, t_off = wave_on ? min(steps, pos_z < k0 ? 0 : (pos_z - k0) / TILE_KEYS + 1) : 0;
   if (p.window > 0) t_on = max(0, pos_a - p.window + 1 - k0) / TILE_KEYS;
@@ -272,12 +279,9 @@ __global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void k_attn_tile(Attn
 #pragma unroll
       for (int u = 0; u < NU; ++u)
         x[u] = Wide<FMT>::mfma(*reinterpret_cast<const vec*>(k + u * 32 * S::KROW + s * 32), qf[s], x[u]);
-    pipeline_reads<NU * D / 16, (D < 128 ? D : 128) / 16>();
+    pipeline_reads<NU * D / 16, D == 64 ? 2 : 8>();
   };
   if (steps > 0) {
-    load_ids(0);
-    load_bytes(0);
-    load_ids(1);
     decode(0);
     load_bytes(1);
     load_ids(2);
@@ -365,7 +369,7 @@ __global__ __launch_bounds__(64 * WAVES, D <= 128 ? 2 : 1) void k_attn_tile(Attn
 #pragma unroll
         for (int i = 0; i < D / 32; ++i)
           o[i] = Wide<FMT>::mfma(*reinterpret_cast<const vec*>(v + i * 32 * S::VROW + e * 32), pb[e], o[i]);
-      pipeline_reads<NU * D / 16, (D < 128 ? D : 128) / 16>();
+      pipeline_reads<NU * D / 16, D == 64 ? 2 : 8>();
     }
     if (!v_team && t + 1 >= t_on && t + 1 < t_off) score(t + 1);
     __syncthreads();
