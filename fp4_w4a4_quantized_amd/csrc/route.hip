@@ -1,6 +1,13 @@
 // route.hip -- the router of the expert layer (scores, top-k, expert order;
 // gradient of the logits) and the combination of the experts' outputs (and
 // its gradients).  The operations are defined in include/fp4q.h.
+//
+// The router is bound by vector instructions: 16384 x 128, k 8, takes 15 us for
+// the choice (300 instructions a token), 5 for the order and 13 for the gradient,
+// where its bytes would take 4; 4096 x 256 with groups 13.4 and 5.  The
+// combination is bound by HBM: 4096 x 8 rows of 2048 (BF16) take 39 us, which
+// also writes back what the call before left in the cache, the gradients 48 us
+// (285 MB, 5.9 TB/s).
 #include "fp4q_device.h"
 #include "fp4q_internal.h"
 
