@@ -946,7 +946,7 @@ int fp4q_route(const void* logits, fp4q_dtype_t dtype, int64_t tokens, int32_t n
       !aligned(weights, 4) || !aligned(row_src, 4) || !aligned(row_of, 4))
     return FP4Q_ERR_INVALID;
   if (n_experts > FP4Q_ROUTE_MAX_EXPERTS || n_groups > FP4Q_ROUTE_MAX_GROUPS ||
-      k > FP4Q_ROUTE_MAX_K || tokens >= ((int64_t)1 << 31) / k)
+      k > FP4Q_ROUTE_MAX_K || tokens >= ((int64_t)1 << 27) / k)
     return FP4Q_ERR_UNSUPPORTED;
   const size_t need = fp4q_route_workspace_bytes(tokens, n_experts);
   if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 8)))
@@ -973,7 +973,7 @@ int fp4q_route_backward(const void* logits, fp4q_dtype_t dtype, int64_t tokens,
       !aligned(d_weights, 4))
     return FP4Q_ERR_INVALID;
   if (n_experts > FP4Q_ROUTE_MAX_EXPERTS || k > FP4Q_ROUTE_MAX_K ||
-      tokens >= ((int64_t)1 << 31) / k)
+      tokens >= ((int64_t)1 << 27) / k)
     return FP4Q_ERR_UNSUPPORTED;
   if (tokens == 0) return FP4Q_OK;
   if (injected_failure()) return FP4Q_ERR_HIP;

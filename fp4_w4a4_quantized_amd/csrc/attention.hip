@@ -381,7 +381,7 @@ void launch(const AttnArgs& p, const Plan& pl, int H, int B, hipStream_t stream)
 
 bool attention_shape_ok(int D, int B, int H, int G, int64_t max_new, int64_t max_len, int window) {
   const Plan pl = attn_plan(D, B, H, G, max_new, max_len, window);
-  return B <= 65535 && (int64_t)H * pl.tiles <= 65535 && pl.splits <= 65535;
+  return B <= 65535 && (int64_t)H * pl.tiles <= 65535 && pl.splits <= 65535 && (int64_t)B * H < (1 << 22);
 }
 
 size_t attention_workspace_bytes(int64_t rows, int D, int B, int H, int G, int64_t max_new,

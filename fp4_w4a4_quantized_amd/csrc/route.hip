@@ -40,6 +40,8 @@ struct RouteArgs {
   uint8_t* counts;  // [E][pitch]: how many, of each block
   int blocks, tok;  // workgroups and their tokens
   int pitch;        // blocks up to a multiple of 16
+  int32_t* before;  // [E][pitch]: rows of the expert in earlier blocks; null: not summed up
+  int32_t* total;   // [E]
 };
 
 __device__ __forceinline__ float load_value(const void* x, int f32, int64_t i) {
@@ -332,10 +334,45 @@ __global__ __launch_bounds__(RT_THREADS) void k_route_pick(RouteArgs p) {
   write_rows(p, t0, nt, s_ex, s_mask, s_base);
 }
 
+// Sums up the counts of the blocks before each one, a workgroup an expert: a
+// lane takes 16 blocks at a time.
+__global__ __launch_bounds__(RT_THREADS) void k_route_sums(RouteArgs p) {
+  __shared__ int s_sum[RT_THREADS], s_tmp[RT_THREADS / 64], s_total;
+  const int64_t row = (int64_t)blockIdx.x * p.pitch;
+  int before = 0;
+  for (int c0 = 0; c0 < p.blocks; c0 += RT_THREADS * 16) {
+    const int c = c0 + threadIdx.x * 16;
+    u32x4 w = {0, 0, 0, 0};
+    if (c < p.blocks) w = *reinterpret_cast<const u32x4*>(p.counts + row + c);
+    uint32_t own = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int n = p.blocks - c - 4 * i;
+      w[i] &= n >= 4 ? ~0u : n <= 0 ? 0u : (1u << (8 * n)) - 1u;
+      own = __builtin_amdgcn_sad_u8(w[i], 0u, own);
+    }
+    s_sum[threadIdx.x] = (int)own;
+    __syncthreads();
+    block_scan(s_sum, RT_THREADS, s_tmp, &s_total);
+    int run = before + s_sum[threadIdx.x];
+    if (c < p.blocks) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        p.before[row + c + i] = run;  // (the row's padding included)
+        run += (w[i >> 2] >> (8 * (i & 3))) & 0xFF;
+      }
+    }
+    before += s_total;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) p.total[blockIdx.x] = before;
+}
+
 // Expert order over all workgroups' tokens: a workgroup sums every block's
 // counts (all of them for the experts' offsets, the earlier blocks' for its
 // own base) and places its rows.  Q neighbouring lanes share an expert's counts,
-// 16 bytes at a time.
+// 16 bytes at a time.  With many blocks, where that would grow with their
+// square, k_route_sums has done it.
 __global__ __launch_bounds__(RT_THREADS) void k_route_order(RouteArgs p) {
   __shared__ int s_base[RT_MAX_E], s_before[RT_MAX_E];
   __shared__ int s_tmp[RT_THREADS / 64], s_total;
@@ -346,7 +383,13 @@ __global__ __launch_bounds__(RT_THREADS) void k_route_order(RouteArgs p) {
   int Q = 64;
   while (Q * E > RT_THREADS && Q > 1) Q >>= 1;
   const int q = threadIdx.x % Q;
-  for (int e = threadIdx.x / Q; e < E; e += RT_THREADS / Q) {
+  if (p.before) {
+    for (int e = threadIdx.x; e < E; e += RT_THREADS) {
+      s_base[e] = p.total[e];
+      s_before[e] = p.before[(int64_t)e * p.pitch + blockIdx.x];
+      s_mask[e] = p.masks[(int64_t)blockIdx.x * E + e];
+    }
+  } else for (int e = threadIdx.x / Q; e < E; e += RT_THREADS / Q) {
     uint32_t all = 0, before = 0;
     for (int c = q * 16; c < p.blocks; c += Q * 16) {
       const u32x4 w = *reinterpret_cast<const u32x4*>(p.counts + (int64_t)e * p.pitch + c);
@@ -394,7 +437,7 @@ __global__ __launch_bounds__(256) void k_route_backward(const void* logits, int 
                                                         const float* d_weights, void* d_logits,
                                                         int64_t ldd) {
   const int lane = threadIdx.x & 63;
-  const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int64_t t = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 4 + (threadIdx.x >> 6);
   if (t >= T) return;
   const bool soft = score == FP4Q_SCORE_SOFTMAX;
   float x[NS];
@@ -536,7 +579,7 @@ struct CombineArgs {
 template <bool F32, int VEC>
 __global__ __launch_bounds__(256) void k_combine(CombineArgs p) {
   const int64_t per = p.N / VEC;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t i = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 256 + threadIdx.x;
   if (i >= p.T * per) return;
   const int64_t t = i / per, c = (i - t * per) * VEC;
   float acc[VEC];
@@ -566,7 +609,7 @@ __global__ __launch_bounds__(256) void k_combine(CombineArgs p) {
 template <bool F32, int VEC>
 __global__ __launch_bounds__(256) void k_combine_backward(CombineArgs p) {
   const int lane = threadIdx.x & 63;
-  const int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int64_t i = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 4 + (threadIdx.x >> 6);
   if (i >= p.T * p.k) return;
   const int64_t t = i / p.k, r = p.row_of[i];
   if (r < 0 || r >= p.rows) {
@@ -591,6 +634,12 @@ __global__ __launch_bounds__(256) void k_combine_backward(CombineArgs p) {
   if (lane == 0) p.d_w[i] = dot;
 }
 
+// A grid of n workgroups of 256, in rows: one dimension holds 2^32 threads.
+inline dim3 grid_of(int64_t n) {
+  const int64_t x = n < (1 << 20) ? n : 1 << 20;
+  return dim3((unsigned)x, (unsigned)((n + x - 1) / x));
+}
+
 inline bool vec_ok(const void* p, int64_t ld, int esz) {
   return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (ld * esz) % 16 == 0;
 }
@@ -600,9 +649,15 @@ inline bool vec_ok(const void* p, int64_t ld, int esz) {
 // Tokens of a workgroup: few while that leaves CUs without one.
 static int route_tokens(int64_t T) { return T <= 4096 ? 16 : RT_TOK; }
 
+// Blocks from which on their counts are summed up by a kernel of its own
+// (x 128 experts, k 8: 256 blocks 20.4 us a call without it and 22.5 with it, 512
+// 33.8 and 32.5, 1024 68.8 and 55).
+constexpr int RT_SUMS = 512;
+
 size_t route_workspace_bytes(int64_t T, int E) {
-  const int64_t tok = route_tokens(T), blocks = (T + tok - 1) / tok;
-  return blocks > 1 ? (size_t)E * (size_t)((blocks + 15) / 16 * 16 + blocks * 8) : 0;
+  const int64_t tok = route_tokens(T), blocks = (T + tok - 1) / tok, pitch = (blocks + 15) / 16 * 16;
+  if (blocks <= 1) return 0;
+  return (size_t)E * (size_t)(pitch + blocks * 8 + (blocks >= RT_SUMS ? (pitch + 1) * 4 : 0));
 }
 
 void launch_route(const void* logits, int f32, int64_t T, int64_t ldx, int E, int k, int score,
@@ -612,10 +667,14 @@ void launch_route(const void* logits, int f32, int64_t T, int64_t ldx, int E, in
   const int tok = route_tokens(T), blocks = (int)((T + tok - 1) / tok);
   RouteArgs p = {logits,  f32,     T,       ldx,     E,      k,  score, G, top_groups, renorm, bias,
                  experts, weights, offsets, row_src, row_of, nullptr, nullptr, blocks > 0 ? blocks : 1,
-                 tok,     (blocks + 15) / 16 * 16};
+                 tok,     (blocks + 15) / 16 * 16, nullptr, nullptr};
   if (blocks > 1) {
     p.counts = static_cast<uint8_t*>(ws);
     p.masks = reinterpret_cast<uint64_t*>(p.counts + (int64_t)E * p.pitch);
+    if (blocks >= RT_SUMS) {
+      p.before = reinterpret_cast<int32_t*>(p.masks + (int64_t)blocks * E);
+      p.total = p.before + (int64_t)E * p.pitch;
+    }
   }
   const bool wide = bias != nullptr || G > 1;
   const dim3 grid((unsigned)p.blocks), thr(RT_THREADS);
@@ -628,13 +687,14 @@ void launch_route(const void* logits, int f32, int64_t T, int64_t ldx, int E, in
   else if (E <= 256) { FP4Q_ROUTE(4); }
   else { FP4Q_ROUTE(8); }
 #undef FP4Q_ROUTE
+  if (p.before) hipLaunchKernelGGL(k_route_sums, dim3((unsigned)E), thr, 0, stream, p);
   if (blocks > 1) hipLaunchKernelGGL(k_route_order, grid, thr, 0, stream, p);
 }
 
 void launch_route_backward(const void* logits, int f32, int64_t T, int64_t ldx, int E, int k,
                            int score, int renorm, const int32_t* experts, const float* d_weights,
                            void* d_logits, int64_t ldd, hipStream_t stream) {
-  const dim3 grid((unsigned)((T + 3) / 4)), thr(256);
+  const dim3 grid = grid_of((T + 3) / 4), thr(256);
 #define FP4Q_ROUTE(N)                                                                         \
   hipLaunchKernelGGL((k_route_backward<N>), grid, thr, 0, stream, logits, f32, T, ldx, E, k,  \
                      score, renorm, experts, d_weights, d_logits, ldd)
@@ -652,7 +712,7 @@ void launch_combine(int f32, const void* y, int64_t rows, int64_t N, int64_t ldy
   const int esz = f32 ? 4 : 2;
   const bool vec = N % 8 == 0 && vec_ok(y, ldy, esz) && vec_ok(out, ldo, esz);
   const int64_t items = T * (vec ? N / 8 : N);
-  const dim3 grid((unsigned)((items + 255) / 256)), thr(256);
+  const dim3 grid = grid_of((items + 255) / 256), thr(256);
   if (f32) {
     if (vec) hipLaunchKernelGGL((k_combine<true, 8>), grid, thr, 0, stream, p);
     else hipLaunchKernelGGL((k_combine<true, 1>), grid, thr, 0, stream, p);
@@ -671,7 +731,7 @@ void launch_combine_backward(int f32, const void* y, int64_t rows, int64_t N, in
   const int esz = f32 ? 4 : 2;
   const bool vec = N % 8 == 0 && vec_ok(y, ldy, esz) && vec_ok(d_out, ldo, esz) &&
                    vec_ok(d_y, lddy, esz);
-  const dim3 grid((unsigned)((T * k + 3) / 4)), thr(256);
+  const dim3 grid = grid_of((T * k + 3) / 4), thr(256);
   if (f32) {
     if (vec) hipLaunchKernelGGL((k_combine_backward<true, 8>), grid, thr, 0, stream, p);
     else hipLaunchKernelGGL((k_combine_backward<true, 1>), grid, thr, 0, stream, p);

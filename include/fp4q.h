@@ -750,8 +750,8 @@ int fp4q_kv_read(fp4q_format_t fmt, const uint8_t* cache, int64_t n_pages, int32
  * rounded once to f16 or bf16 before they meet the values.  For NVFP4 q is
  * held in f16 relative to its row's largest magnitude (bf16 for MXFP4).
  * heads % kv_heads == 0; FP4Q_ERR_UNSUPPORTED: another dim or page, more
- * than 128 heads on one kv head, batch above 65535, or rows * heads not
- * below 2^31. */
+ * than 128 heads on one kv head, batch above 65535, batch * kv_heads not
+ * below 2^22, or rows * heads not below 2^31. */
 size_t fp4q_kv_attention_workspace_bytes(fp4q_format_t fmt, int64_t rows, int32_t heads,
                                          int32_t kv_heads, int32_t dim, int32_t batch,
                                          int64_t max_new, int64_t max_len, int32_t window);
@@ -785,7 +785,7 @@ int fp4q_kv_attention(fp4q_format_t fmt, const uint8_t* cache, int64_t n_pages, 
  *
  * Scores are computed in 64 bits where they decide the order (a bias or
  * groups).  FP4Q_ERR_UNSUPPORTED: more than 512 experts or 64 groups, k
- * above 32, or tokens * k not below 2^31.  k may not exceed the experts of
+ * above 32, or tokens * k not below 2^27.  k may not exceed the experts of
  * top_groups groups.
  *
  * fp4q_route_backward: the gradient of the logits from that of the weights

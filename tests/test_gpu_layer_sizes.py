@@ -101,6 +101,25 @@ def test_router_blocks(T):
     check_route(x, 5, 1, torch.linspace(-0.1, 0.1, 40).cuda(), 4, 2)
 
 
+@pytest.mark.parametrize("T", [64 * 511, 64 * 511 + 1, 64 * 1024 * 16 + 1])
+def test_router_orders_many_blocks(T):
+    """Around the number of workgroups from which their counts are summed up
+    apart, and past what one pass of that takes: the order follows from the
+    choice (checked by itself above)."""
+    need_gpu()
+    say(f"route order T {T}")
+    x = torch.randn(T, 6, device="cuda")
+    r = fq.route(x, 2)
+    e = r["experts"].long()
+    assert torch.equal(e, x.sort(dim=1, descending=True, stable=True).indices[:, :2])
+    flat = e.reshape(-1)
+    order = flat.sort(stable=True).indices
+    assert torch.equal(r["row_src"].long(), order // 2)
+    assert torch.equal(r["row_of"].reshape(-1)[order].long(), torch.arange(2 * T, device="cuda"))
+    assert torch.equal(r["offsets"][1:].long(), torch.bincount(flat, minlength=6).cumsum(0))
+    assert int(r["offsets"][0]) == 0
+
+
 def test_router_nan_logits_count_as_minus_infinity():
     need_gpu()
     x = logits_of(50, 70, torch.float32, 2)
@@ -117,6 +136,21 @@ def test_router_nan_logits_count_as_minus_infinity():
             da, db = (fq.route_backward(v, a["experts"], dw, score=score, renorm=renorm) for v in (x, y))
             assert torch.equal(da, db) and torch.isfinite(da).all()
             check_route(y, 4, score, renorm=renorm)
+
+
+def test_combine_in_two_rows_of_workgroups():
+    """More workgroups than one row of the grid holds (single columns)."""
+    need_gpu()
+    T, N = 1 << 16, 4099                           # 2^28 outputs of one value each
+    y = torch.randn(4, N, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).cuda()
+    row_of = (torch.arange(T, device="cuda") % 5 - 1).int().view(T, 1)
+    w = torch.full((T, 1), 0.5, device="cuda")
+    out = fq.combine(y, row_of, w)
+    for t in (0, 1, 2, 4, T // 2, T - 5, T - 1):
+        r = t % 5 - 1
+        want = torch.zeros(N) if r < 0 else 0.5 * host(y[r])
+        assert np.array_equal(host(out[t]), np.asarray(want, dtype=np.float64)), t
+    assert torch.equal(out[:5].repeat(100, 1), out[T // 5 * 5 - 500:T // 5 * 5])
 
 
 def test_combine_without_rows():

@@ -99,3 +99,13 @@ def test_router_and_combination_tensors():
 def test_the_module_names_its_argument_counts():
     with pytest.raises(TypeError, match="11 arguments"):
         binding._layer().append(None)
+
+
+def test_sizes_past_a_launch_are_refused():
+    L, A = binding.lib(), 0x10000
+    kv = [0, A, 4, 16, 1 << 10, 128, A, 1 << 12, A, 3, 3, A, 5]
+    call = lambda heads: L.fp4q_kv_attention(*kv, A, 1 << 20, heads, 1, 40, 0, 0.1, A, A, A, 1, 1 << 20,
+                                             A, 1 << 30, None)
+    assert call(1 << 10) == -2
+    assert L.fp4q_route(A, 0, 1 << 26, 8, 8, 2, 0, None, 1, 1, 1, A, A, A, A, A, A, 1 << 40, None) == -2
+    assert L.fp4q_route_backward(A, 0, 1 << 26, 8, 8, 2, 0, 1, A, A, A, 8, None) == -2
