@@ -798,13 +798,19 @@ def _handle(stream):
     return None if stream is None else stream.cuda_stream
 
 
-def _keep(stream, *tensors):
-    """Memory of torch's current stream that a call on another one uses is not
-    to be given out again before that call is done."""
-    if stream is not None:
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
+def _results(stream, call, *args):
+    """call(None, *args) with its results and workspace in `stream`'s own
+    memory: memory of the current stream could still have work of its last
+    owner pending there.  A result that the current stream reads afterwards is
+    not given away again before it has."""
+    if stream is None:
+        return call(None, *args)
+    here = torch.cuda.current_stream()
+    with torch.cuda.stream(stream):
+        out = call(None, *args)
+    for t in out if isinstance(out, tuple) else (out,):
+        t.record_stream(here)
+    return out
 
 
 def kv_page_bytes(fmt, page, dim) -> int:
@@ -834,10 +840,8 @@ def kv_read(fmt, cache, page, offsets, page_table, lens, rows, dim, k_scale=None
             stream=None):
     """The values that stand in the cache for the new tokens: (k, v) bf16
     [rows, kv_heads, dim]."""
-    k, v = _layer().read(_handle(stream), fmt, cache, page, offsets, page_table, lens, k_scale,
-                         v_scale, rows, dim)
-    _keep(stream, k)
-    return k, v
+    return _results(stream, _layer().read, fmt, cache, page, offsets, page_table, lens, k_scale,
+                    v_scale, rows, dim)
 
 
 def kv_attention_workspace_bytes(fmt, rows, heads, kv_heads, dim, batch, max_new, max_len,
@@ -860,19 +864,8 @@ def kv_attention(fmt, cache, page, offsets, page_table, lens, q, max_new, max_le
     max_new new tokens or is longer than max_len.  window > 0: a token sees
     the last `window` keys only; scale: dim^-0.5 unless given.  Returns
     [rows, heads, dim]."""
-    if stream is None:
-        return _layer().attention(None, fmt, cache, page, offsets, page_table, lens, k_scale,
-                                  v_scale, q, max_new, max_len, window, scale, y_dtype)
-    rows, heads, dim = q.shape
-    y = torch.empty((rows, heads, dim), device=q.device,
-                    dtype=torch.float32 if y_dtype == OUT_F32 else torch.bfloat16)
-    nb = kv_attention_workspace_bytes(fmt, rows, heads, cache.shape[1], dim, lens.numel(), max_new,
-                                      max_len, window)
-    ws = torch.empty(nb, dtype=torch.uint8, device=q.device) if nb else None
-    kv_attention_into(fmt, cache, page, offsets, page_table, lens, q, max_new, max_len, k_scale,
-                      v_scale, window, dim ** -0.5 if scale is None else scale, y, ws, stream)
-    _keep(stream, y, ws)
-    return y
+    return _results(stream, _layer().attention, fmt, cache, page, offsets, page_table, lens,
+                    k_scale, v_scale, q, max_new, max_len, window, scale, y_dtype)
 
 
 # ---- the router and the combination ---------------------------------------
@@ -894,9 +887,8 @@ def route(logits, k, score=SOFTMAX, bias=None, n_groups=1, top_groups=1, renorm=
     top_groups best stay.  Returns dict(experts int32 [tokens, k], weights f32
     [tokens, k], offsets int32 [experts + 1], row_src int32 [tokens * k],
     row_of int32 [tokens, k])."""
-    experts, weights, offsets, row_src, row_of = _layer().route(
-        _handle(stream), logits, k, score, bias, n_groups, top_groups, renorm)
-    _keep(stream, experts, weights)
+    experts, weights, offsets, row_src, row_of = _results(
+        stream, _layer().route, logits, k, score, bias, n_groups, top_groups, renorm)
     return {"experts": experts, "weights": weights, "offsets": offsets, "row_src": row_src,
             "row_of": row_of}
 
@@ -909,9 +901,7 @@ def route_backward_into(logits, experts, d_weights, score, renorm, d_logits, str
 def route_backward(logits, experts, d_weights, score=SOFTMAX, renorm=True, stream=None):
     """Gradient of the logits from that of route()'s weights (f32
     [tokens, k]) and its chosen experts."""
-    d = _layer().route_backward(_handle(stream), logits, experts, d_weights, score, renorm)
-    _keep(stream, d)
-    return d
+    return _results(stream, _layer().route_backward, logits, experts, d_weights, score, renorm)
 
 
 def combine_into(y, row_of, weights, out, stream=None):
@@ -921,9 +911,7 @@ def combine_into(y, row_of, weights, out, stream=None):
 def combine(y, row_of, weights, stream=None):
     """out[t] = sum_j weights[t, j] y[row_of[t, j]]: the experts' outputs y
     (f32 or bf16 [rows, cols], in expert order) back to the tokens."""
-    out = _layer().combine(_handle(stream), y, row_of, weights)
-    _keep(stream, out)
-    return out
+    return _results(stream, _layer().combine, y, row_of, weights)
 
 
 def combine_backward_into(y, row_of, weights, d_out, d_y, d_weights, stream=None):
@@ -933,6 +921,4 @@ def combine_backward_into(y, row_of, weights, d_out, d_y, d_weights, stream=None
 def combine_backward(y, row_of, weights, d_out, stream=None):
     """(d_y, d_weights) of combine() from d_out.  row_of names every row of y
     (combine_backward_into leaves the others as they are)."""
-    d_y, d_w = _layer().combine_backward(_handle(stream), y, row_of, weights, d_out)
-    _keep(stream, d_y, d_w)
-    return d_y, d_w
+    return _results(stream, _layer().combine_backward, y, row_of, weights, d_out)

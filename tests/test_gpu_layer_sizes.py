@@ -165,3 +165,41 @@ def test_combine_without_rows():
     big[2] = 1.0
     got = host(fq.combine(big, row_of, w))
     assert np.all(got[0] == 1.0) and np.all(got[1:] == 0.0)
+
+
+def test_results_on_another_stream_are_of_its_own_memory():
+    """Memory freed on the current stream while its work there is pending is
+    not what a call on another stream writes to."""
+    need_gpu()
+    say("results on another stream")
+    T, k, E, N = 2048, 4, 64, 512
+    x = logits_of(T, E, torch.float32, 3)
+    y = torch.randn(T * k, N, device="cuda")
+    do = torch.randn(T, N, device="cuda")
+    r = fq.route(x, k)
+    dw = torch.randn(T, k, device="cuda")
+    c = make(0, [1] * 16, [800] * 16, G=4, H=2, seed=5)
+    kv = [0, dev(c["cache"]), c["page"], dev(c["off"]), dev(c["table"]), dev(c["lens"])]
+    t, q = dev(c["t"]), dev(c["q"], torch.bfloat16)
+    calls = [
+        lambda s: list(fq.route(x, k, stream=s).values()),
+        lambda s: [fq.route_backward(x, r["experts"], dw, stream=s)],
+        lambda s: [fq.combine(y, r["row_of"], r["weights"], stream=s)],
+        lambda s: list(fq.combine_backward(y, r["row_of"], r["weights"], do, stream=s)),
+        lambda s: [fq.kv_attention(*kv, q, 1, 800, t, t, stream=s)],
+        lambda s: list(fq.kv_read(*kv, 16, 128, t, t, stream=s)),
+    ]
+    s = torch.cuda.Stream()
+    for i, call in enumerate(calls):
+        want = [v.clone() for v in call(None)]
+        torch.cuda.synchronize()
+        torch.cuda._sleep(20_000_000)
+        left = [torch.empty(v.untyped_storage().nbytes(), dtype=torch.uint8, device="cuda")
+                for v in want for _ in range(2)]
+        for b in left:
+            b.fill_(255)
+        del left, b
+        got = call(s)
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b), i
