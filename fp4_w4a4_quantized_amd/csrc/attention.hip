@@ -52,8 +52,10 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 4 : D == 128 && NC == 1 && WA
   // rotated by the split, so that no XCD has all of the long sequences' last splits.
   const uint32_t bh = (blockIdx.x + blockIdx.z) % gridDim.x;
   const int b = bh / p.H, h = bh - b * p.H, row0 = blockIdx.y * p.tile;
-  const int n_rows = (p.off[b + 1] - p.off[b]) * p.G;
-  if (row0 >= n_rows) return;
+  if (row0 >= tile_rows(p, b)) {
+    zero_rest<D, 64 * WAVES>(p, b, h);
+    return;
+  }
   const Range rg = tile_range(p, b, row0);
   const int split = blockIdx.z;
   if (split >= active_splits(p, rg)) return;
@@ -264,6 +266,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 4 : D == 128 && NC == 1 && WA
       if (g == 0) p.part_ms[s] = make_float2(mm, zz);
     }
   }
+  zero_rest<D, 64 * WAVES>(p, b, h);
 }
 
 // Joins the splits of a row: p.join groups of D / 4 lanes for each (new token,
@@ -314,7 +317,8 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs p) {
       for (int r = 0; r < 4; ++r) o[r] = __builtin_fmaf(a[r], fa, o[r] * f);
     }
   }
-  if (n == 0) return;
+  // (a row past the last sequence's gives 0, one past max_new is left out)
+  if (n == 0 && !(s < p.slots && row >= p.off[p.B])) return;
   const float f = z > 0.0f ? (FMT == FP4Q_NVFP4 ? p.vts[hh / p.G] : 1.0f) / z : 0.0f;
 #pragma unroll
   for (int r = 0; r < 4; ++r) o[r] *= f;
@@ -411,6 +415,7 @@ void launch_attention(int fmt, const uint8_t* cache, int64_t n_pages, int page_s
   p.lens = lens;
   p.q = q;
   p.ldq = ldq;
+  p.rows = (int)rows;
   p.window = window;
   p.scale2 = scale * 1.44269504088896340736f;
   p.kts = kts;

@@ -19,6 +19,7 @@ struct AttnArgs {
   const int32_t* lens;
   const uint16_t* q;
   int64_t ldq;
+  int rows;
   int window;
   float scale2;  // softmax scale * log2(e)
   const float* kts;
@@ -60,6 +61,13 @@ struct Range {
   int seen, lo, hi, rows;
 };
 
+// New-token rows of sequence b times the heads of a kv head (none that the
+// packed tensors do not have, whatever the offsets say).
+__device__ __forceinline__ int tile_rows(const AttnArgs& p, int b) {
+  const int r0 = p.off[b], r1 = min(p.off[b + 1], p.rows);
+  return r0 < 0 || r1 <= r0 ? 0 : (r1 - r0) * p.G;
+}
+
 __device__ __forceinline__ Range tile_range(const AttnArgs& p, int b, int row0) {
   Range r;
   r.r0 = p.off[b];
@@ -67,7 +75,7 @@ __device__ __forceinline__ Range tile_range(const AttnArgs& p, int b, int row0) 
   const int64_t cap = p.table_cols << p.page_shift;
   const int len = (int)min((int64_t)max(p.lens[b], 0), cap);
   r.first = p.lens[b] - r.n;
-  r.rows = r.n * p.G;
+  r.rows = tile_rows(p, b);
   const int last_row = min(r.rows, row0 + p.tile) - 1;
   const int q_lo = row0 / p.G, q_hi = last_row / p.G;
   r.hi = min(len, r.first + q_hi + 1);
@@ -383,6 +391,17 @@ __device__ __forceinline__ void store_out(const AttnArgs& p, int64_t at, v4f t) 
   } else {
     *reinterpret_cast<v4f*>(reinterpret_cast<float*>(p.y) + at) = t;
   }
+}
+
+// Rows past the last sequence's give 0 (of one pass; the join does it otherwise):
+// workgroup (b, h) takes every B-th, for the heads of kv head h.
+template <int D, int THREADS>
+__device__ __forceinline__ void zero_rest(const AttnArgs& p, int b, int h) {
+  if (p.splits > 1 || blockIdx.y > 0) return;
+  const int end = max(p.off[p.B], 0);
+  for (int64_t row = (int64_t)end + b; row < p.rows; row += p.B)
+    for (int i = threadIdx.x * 4; i < p.G * D; i += THREADS * 4)
+      store_out(p, row * p.ldy + (int64_t)h * p.G * D + i, v4f{0.0f, 0.0f, 0.0f, 0.0f});
 }
 
 }  // namespace

@@ -111,8 +111,9 @@ __global__ __launch_bounds__(64 * WAVES)
   // the row tile, so that a long sequence is not left to a few of them.
   const uint32_t bh = (blockIdx.x + blockIdx.y) % gridDim.x;
   const int b = bh / p.H, h = bh - b * p.H;
+  zero_rest<D, 64 * WAVES>(p, b, h);
   // the last rows, which see the most keys, first
-  const int n_rows = (p.off[b + 1] - p.off[b]) * p.G;
+  const int n_rows = tile_rows(p, b);
   const int tile_id = min((n_rows + p.tile - 1) / p.tile, (int)gridDim.y) - 1 - (int)blockIdx.y;
   if (tile_id < 0) return;
   const int row0 = tile_id * p.tile;

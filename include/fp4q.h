@@ -724,12 +724,13 @@ int fp4q_kv_read(fp4q_format_t fmt, const uint8_t* cache, int64_t n_pages, int32
  *
  * over the keys j of the row's sequence with j <= position(r), and, with
  * window > 0, j > position(r) - window; g = h / (heads / kv_heads).  A row
- * that sees no key gives 0.  What stands in the cache outside the keys that
- * the new tokens see (NaN scales included) does not reach the result, nor
- * does a later token's value that fp4q_kv_append stored: of MXFP4 values,
- * block scales above 2^125 count as 2^125, so that all of them are finite.
- * One token a sequence (decode), the few of a speculative step, prompts and
- * chunks of them are all this call.
+ * that sees no key gives 0, and so does a row past offsets[batch] (padding).
+ * What stands in the cache outside the keys that the new tokens see (NaN
+ * scales included) does not reach the result, nor does a later token's value
+ * that fp4q_kv_append stored: of MXFP4 values, block scales above 2^125 count
+ * as 2^125, so that all of them are finite.  One token a sequence (decode),
+ * the few of a speculative step, prompts and chunks of them are all this
+ * call.
  *
  *   q              bf16 [rows, heads, dim], row stride ldq (a multiple of 8,
  *                  16-byte aligned)

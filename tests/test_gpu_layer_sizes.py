@@ -203,3 +203,31 @@ def test_results_on_another_stream_are_of_its_own_memory():
         torch.cuda.synchronize()
         for a, b in zip(got, want):
             assert torch.equal(a, b), i
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("n,lens,G,D", [([1, 0, 1], [300, 0, 70], 4, 128),       # one pass, few rows
+                                        ([1, 1, 1], [9000, 4, 900], 5, 64),      # split keys
+                                        ([5, 1, 0], [700, 1, 9], 6, 128),        # 30 rows of a head
+                                        ([40, 3, 2], [40, 3, 2], 3, 256),        # row tiles
+                                        ([70, 0, 0], [1500, 0, 0], 4, 64),       # the same, split keys
+                                        ([0, 0, 0], [5, 0, 2], 2, 128)])         # no new tokens at all
+def test_rows_past_the_offsets(fmt, n, lens, G, D):
+    """Padding rows give 0; rows that the offsets name and the tensors do not
+    have are left out."""
+    need_gpu()
+    say(f"padding fmt {fmt} n {n} lens {lens} G {G} D {D}")
+    c = make(fmt, n, lens, G=G, H=2, D=D, seed=sum(n))
+    rows = len(c["q"])
+    c["q"] = np.concatenate([c["q"], np.full((37, 2 * G, D), np.nan)])
+    for y_dtype in (fq.OUT_BF16, fq.OUT_F32):
+        nb = 37 * 2 * G * D * 4
+        torch.full((4 * nb,), 255, dtype=torch.uint8, device="cuda")  # what freed memory may hold
+        got = attend(c, y_dtype=y_dtype)
+        assert torch.all(got[rows:] == 0)
+        check_close(c, got, bf16=y_dtype == fq.OUT_BF16)
+    c["q"] = c["q"][:rows]
+    if rows > 2:
+        q = dev(c["q"][:rows - 2], torch.bfloat16)
+        got = torch.cat([attend(c, q=q), attend(c)[rows - 2:]])
+        check_close(c, got)
