@@ -50,9 +50,28 @@ __device__ __forceinline__ float load_value(const void* x, int f32, int64_t i) {
 }
 
 // A logit: NaN counts as -inf.
+__device__ __forceinline__ float logit_of(float x) { return x == x ? x : -__builtin_inff(); }
 __device__ __forceinline__ float load_logit(const void* x, int f32, int64_t i) {
-  const float v = load_value(x, f32, i);
-  return v == v ? v : -__builtin_inff();
+  return logit_of(load_value(x, f32, i));
+}
+
+// The logits of experts l, l + STEP, ... of a row that begins at element `row`
+// (-inf past the last).  One branch on the type and none on the expert around
+// the loads, or each would be waited for before the next is issued.
+template <int STEP, int NS>
+__device__ __forceinline__ void load_logits(const void* x, int f32, int64_t row, int l, int E,
+                                            float (&v)[NS]) {
+  if (f32) {
+    const float* r = reinterpret_cast<const float*>(x) + row;
+#pragma unroll
+    for (int i = 0; i < NS; ++i) v[i] = r[min(l + STEP * i, E - 1)];
+  } else {
+    const uint16_t* r = reinterpret_cast<const uint16_t*>(x) + row;
+#pragma unroll
+    for (int i = 0; i < NS; ++i) v[i] = bf16_to_f32(r[min(l + STEP * i, E - 1)]);
+  }
+#pragma unroll
+  for (int i = 0; i < NS; ++i) v[i] = l + STEP * i < E ? logit_of(v[i]) : -__builtin_inff();
 }
 
 // The value of the lane that differs in bit 0, 1, 2 or 3 of its number (the
@@ -65,12 +84,14 @@ __device__ __forceinline__ uint32_t lane_swap(uint32_t v) {
 }
 
 __device__ __forceinline__ int pick_max(int a, int b) { return a > b ? a : b; }
+__device__ __forceinline__ int pick_min(int a, int b) { return a < b ? a : b; }
 __device__ __forceinline__ double pick_max(double a, double b) { return fmax(a, b); }
 __device__ __forceinline__ double add(double a, double b) { return a + b; }
 
-// All lanes' values joined by f (commutative): every lane has the result.
-template <typename T, T (*F)(T, T)>
-__device__ __forceinline__ T wave_all(T v) {
+// The values of each LANES (16, 32 or 64) lanes joined by f (commutative): every
+// lane has the result of its own.
+template <typename T, T (*F)(T, T), int LANES>
+__device__ __forceinline__ T lanes_all(T v) {
   if constexpr (sizeof(T) == 4) {
     auto bits = [](uint32_t u) { return __builtin_bit_cast(T, u); };
     auto raw = [](T t) { return __builtin_bit_cast(uint32_t, t); };
@@ -78,8 +99,10 @@ __device__ __forceinline__ T wave_all(T v) {
     v = F(v, bits(lane_swap<1>(raw(v))));
     v = F(v, bits(lane_swap<2>(raw(v))));
     v = F(v, bits(lane_swap<3>(raw(v))));
+    if constexpr (LANES == 16) return v;
     u32x2 r = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(raw(v), raw(v), false, false));
     v = F(bits(r[0]), bits(r[1]));
+    if constexpr (LANES == 32) return v;
     r = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(raw(v), raw(v), false, false));
     return F(bits(r[0]), bits(r[1]));
   } else {
@@ -92,10 +115,12 @@ __device__ __forceinline__ T wave_all(T v) {
     v = F(v, bits(lane_swap<2>(u[0]), lane_swap<2>(u[1])));
     u = __builtin_bit_cast(u32x2, v);
     v = F(v, bits(lane_swap<3>(u[0]), lane_swap<3>(u[1])));
+    if constexpr (LANES == 16) return v;
     u = __builtin_bit_cast(u32x2, v);
     u32x2 l = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(u[0], u[0], false, false));
     u32x2 h = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(u[1], u[1], false, false));
     v = F(bits(l[0], h[0]), bits(l[1], h[1]));
+    if constexpr (LANES == 32) return v;
     u = __builtin_bit_cast(u32x2, v);
     l = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(u[0], u[0], false, false));
     h = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(u[1], u[1], false, false));
@@ -103,9 +128,12 @@ __device__ __forceinline__ T wave_all(T v) {
   }
 }
 
-__device__ __forceinline__ int wave_max(int v) { return wave_all<int, pick_max>(v); }
-__device__ __forceinline__ double wave_max(double v) { return wave_all<double, pick_max>(v); }
-__device__ __forceinline__ double wave_sum(double v) { return wave_all<double, add>(v); }
+template <int LANES = 64, typename T>
+__device__ __forceinline__ T wave_max(T v) { return lanes_all<T, pick_max, LANES>(v); }
+template <int LANES = 64>
+__device__ __forceinline__ int wave_min(int v) { return lanes_all<int, pick_min, LANES>(v); }
+template <int LANES = 64>
+__device__ __forceinline__ double wave_sum(double v) { return lanes_all<double, add, LANES>(v); }
 
 // Lane l's value, l the same for all lanes.
 __device__ __forceinline__ int of_lane(int v, int l) { return __builtin_amdgcn_readlane(v, l); }
@@ -183,11 +211,7 @@ __global__ __launch_bounds__(RT_THREADS) void k_route_pick(RouteArgs p) {
   float next[NS];  // the wave's next token's logits, loaded while one is picked for
   auto load_row = [&](int tt) {
     const int64_t row = (t0 + min(tt, nt - 1)) * p.ldx;
-#pragma unroll
-    for (int i = 0; i < NS; ++i) {
-      const int e = lane + 64 * i;
-      next[i] = e < E ? load_logit(p.logits, p.f32, row + e) : -__builtin_inff();
-    }
+    load_logits<64>(p.logits, p.f32, row, lane, E, next);
   };
   if (wave < nt) load_row(wave);
   for (int tt = wave; tt < nt; tt += RT_THREADS / 64) {
@@ -334,6 +358,73 @@ __global__ __launch_bounds__(RT_THREADS) void k_route_pick(RouteArgs p) {
   write_rows(p, t0, nt, s_ex, s_mask, s_base);
 }
 
+// The same without bias and groups for k up to 16 and more tokens than one
+// workgroup has: 16 lanes per token, lane l with experts l, l + 16, ..., so that
+// four tokens share each exchange between lanes and each 64-bit exponential.
+template <int NS>
+__global__ __launch_bounds__(RT_THREADS) void k_route_pick16(RouteArgs p) {
+  __shared__ uint64_t s_mask[RT_MAX_E];
+  const int E = p.E, k = p.k, l = threadIdx.x & 15, tt = threadIdx.x >> 4;
+  const int64_t t0 = (int64_t)blockIdx.x * p.tok;
+  const int nt = (int)min((int64_t)p.tok, p.T - t0);
+  float x[NS];
+  load_logits<16>(p.logits, p.f32, (t0 + min(tt, nt - 1)) * p.ldx, l, E, x);
+  for (int e = threadIdx.x; e < E; e += blockDim.x) s_mask[e] = 0;
+  __syncthreads();
+  int key[NS], best = ORDER_NONE;
+#pragma unroll
+  for (int i = 0; i < NS; ++i) {
+    key[i] = l + 16 * i < E ? order_of(x[i]) : ORDER_NONE;
+    best = pick_max(best, key[i]);
+  }
+  const float top = order_value(wave_max<16>(best));
+  const double m = top > -__builtin_inff() ? (double)top : 0.0;
+  const bool soft = p.score == FP4Q_SCORE_SOFTMAX;
+  double z = 1.0;
+  if (soft && !p.renorm) {
+    double part = 0.0;
+#pragma unroll
+    for (int i = 0; i < NS; ++i)
+      if (l + 16 * i < E) part += exp((double)order_value(key[i]) - m);
+    z = wave_sum<16>(part);
+    if (!(z > 0.0)) z = 1.0;
+  }
+  int my_e = 0, my_key = 0;
+  for (int j = 0; j < k; ++j) {
+    best = key[0];
+#pragma unroll
+    for (int i = 1; i < NS; ++i) best = pick_max(best, key[i]);
+    best = wave_max<16>(best);
+    int at = NS;
+#pragma unroll
+    for (int i = NS - 1; i >= 0; --i) at = key[i] == best ? i : at;
+    const int pick = wave_min<16>(16 * at + l);
+#pragma unroll
+    for (int i = 0; i < NS; ++i)
+      if (pick == 16 * i + l) key[i] = ORDER_NONE;
+    if (l == j) {
+      my_e = pick;
+      my_key = best;
+    }
+  }
+  const double my_x = (double)order_value(my_key);
+  double my_s = soft ? exp(my_x - m) / z : 1.0 / (1.0 + exp(-my_x));
+  if (p.renorm) {
+    const double total = wave_sum<16>(l < k ? my_s : 0.0);
+    my_s = total > 0.0 ? my_s / total : 0.0;
+  }
+  if (l < k && tt < nt) {
+    p.experts[(t0 + tt) * k + l] = my_e;
+    p.weights[(t0 + tt) * k + l] = (float)my_s;
+    atomicOr(reinterpret_cast<uint32_t*>(&s_mask[my_e]) + (tt >> 5), 1u << (tt & 31));
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < E; e += blockDim.x) {
+    p.masks[(int64_t)blockIdx.x * E + e] = s_mask[e];
+    p.counts[(int64_t)e * p.pitch + blockIdx.x] = (uint8_t)__popcll(s_mask[e]);
+  }
+}
+
 // Sums up the counts of the blocks before each one, a workgroup an expert: a
 // lane takes 16 blocks at a time.
 __global__ __launch_bounds__(RT_THREADS) void k_route_sums(RouteArgs p) {
@@ -422,86 +513,134 @@ __global__ __launch_bounds__(RT_THREADS) void k_route_order(RouteArgs p) {
   write_rows(p, t0, nt, p.experts + t0 * p.k, s_mask, s_base);
 }
 
-// Gradient of the logits, one wave per token.  With p the chosen scores and
-// dp their gradient:
+struct GradArgs {
+  const void* logits;
+  int f32;
+  int64_t T, ldx;
+  int E, k, score, renorm;
+  const int32_t* experts;
+  const float* dw;
+  void* d;
+  int64_t ldd;
+};
+
+// The gradients of experts l, l + STEP, ... of token t.
+template <int STEP, int NS>
+__device__ __forceinline__ void store_gradient(const GradArgs& p, int64_t t, int l, const float (&v)[NS]) {
+  if (p.f32) {
+    float* r = reinterpret_cast<float*>(p.d) + t * p.ldd;
+#pragma unroll
+    for (int i = 0; i < NS; ++i)
+      if (l + STEP * i < p.E) r[l + STEP * i] = v[i];
+  } else {
+    __bf16* r = reinterpret_cast<__bf16*>(p.d) + t * p.ldd;
+#pragma unroll
+    for (int i = 0; i < NS; ++i)
+      if (l + STEP * i < p.E) r[l + STEP * i] = (__bf16)v[i];
+  }
+}
+
+// Gradient of the logits.  With p the chosen scores and dp their gradient:
 //   softmax: dx_i = -score_i sum(dp p), plus dp_i score_i where chosen
 //   sigmoid: dx_i = dp_i score_i (1 - score_i) where chosen, else 0
 // Through the renormalisation w = p / sum p it is dp = (dw - sum(dw w)) / sum p,
 // for which sum(dp p) = 0: then the softmax's sum over all experts cancels and
-// the chosen logits' exponentials are all that is needed.  Bound by the 64-bit
-// arithmetic: 16384 x 128 renormalised takes 13.3 us, its 17 MB 3 us.
-template <int NS>
-__global__ __launch_bounds__(256) void k_route_backward(const void* logits, int f32, int64_t T,
-                                                        int64_t ldx, int E, int k, int score,
-                                                        int renorm, const int32_t* experts,
-                                                        const float* d_weights, void* d_logits,
-                                                        int64_t ldd) {
-  const int lane = threadIdx.x & 63;
-  const int64_t t = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 4 + (threadIdx.x >> 6);
-  if (t >= T) return;
-  const bool soft = score == FP4Q_SCORE_SOFTMAX;
-  float x[NS];
-  int top_ord = ORDER_NONE;
+// the chosen logits' exponentials (relative to the largest logit, as the scores
+// have them) are all that is needed.  So it is with all but the plain softmax:
+// LANES lanes per token, lane j with the j-th chosen expert, whose gradients
+// meet the zeros of the others in LDS (an expert that is named twice in the
+// order of j).
+template <int LANES, int NS>
+__global__ __launch_bounds__(256) void k_route_backward(GradArgs p) {
+  extern __shared__ float s_dx[];  // [256 / LANES][E]
+  const int l = threadIdx.x % LANES, E = p.E, k = p.k;
+  const int64_t block = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+  const int64_t t = block * (256 / LANES) + threadIdx.x / LANES;
+  if (t >= p.T) return;
+  float* const dx = s_dx + threadIdx.x / LANES * E;
+  const bool soft = p.score == FP4Q_SCORE_SOFTMAX;
+  const int e = l < k ? p.experts[t * k + l] : -1;
+  const bool on = e >= 0 && e < E;  // (an index outside the experts: no gradient)
+  const float given = l < k ? p.dw[t * k + l] : 0.0f;
+  float row[NS];
+  if (soft) load_logits<LANES>(p.logits, p.f32, t * p.ldx, l, E, row);
+  for (int c = l; c < E; c += LANES) dx[c] = 0.0f;
+  const double x = on ? (double)load_logit(p.logits, p.f32, t * p.ldx + e) : 0.0;
+  double dw = on ? (double)given : 0.0, m = 0.0;
+  if (soft) {
+    int top = ORDER_NONE;
 #pragma unroll
-  for (int i = 0; i < NS; ++i) {
-    const int e = lane + 64 * i;
-    x[i] = e < E ? load_logit(logits, f32, t * ldx + e) : -__builtin_inff();
-    top_ord = pick_max(top_ord, order_of(x[i]));
+    for (int i = 0; i < NS; ++i) top = pick_max(top, order_of(row[i]));
+    const float v = order_value(wave_max<LANES>(top));
+    if (v > -__builtin_inff()) m = (double)v;
   }
-  const float top = order_value(wave_max(top_ord));
-  const double m = top > -__builtin_inff() ? (double)top : 0.0;
-  // lane j: the j-th chosen expert (indices outside the experts: no gradient)
-  const int e = lane < k ? experts[t * k + lane] : -1;
-  const bool on = e >= 0 && e < E;
-  double dw = on ? (double)d_weights[t * k + lane] : 0.0;
-  const bool all = soft && !renorm;
-  double s[NS], z = 1.0;
-  if (all) {
-    double part = 0.0;
-#pragma unroll
-    for (int i = 0; i < NS; ++i) {
-      s[i] = lane + 64 * i < E ? exp((double)x[i] - m) : 0.0;
-      part += s[i];
-    }
-    z = wave_sum(part);
-    z = z > 0.0 ? 1.0 / z : 1.0;
-#pragma unroll
-    for (int i = 0; i < NS; ++i) s[i] *= z;
-  }
-  float xe = 0.0f;
-#pragma unroll
-  for (int i = 0; i < NS; ++i) {
-    const float xi = __shfl(x[i], e & 63);
-    if (i == e >> 6) xe = xi;
-  }
-  double p = 0.0;
-  if (on) p = soft ? exp((double)xe - m) * z : 1.0 / (1.0 + exp(-(double)xe));
-  if (renorm) {
-    const double sum = wave_sum(p), dot = wave_sum(dw * p);
+  double s = 0.0;
+  if (on) s = soft ? exp(x - m) : 1.0 / (1.0 + exp(-x));
+  if (p.renorm) {
+    const double sum = wave_sum<LANES>(s), dot = wave_sum<LANES>(dw * s);
     const double r = sum > 0.0 ? 1.0 / sum : 0.0;
     dw = (dw - dot * r) * r;
   }
-  const double dot = all ? wave_sum(dw * p) : 0.0;
-  const double add_e = soft ? dw * p : dw * p * (1.0 - p);
-  double dx[NS];
+  const float mine = (float)(soft ? dw * s : dw * s * (1.0 - s));
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  // (a wave's LDS operations keep their order)
+  for (int j = 0; j < k; ++j)
+    if (l == j && on) __hip_atomic_fetch_add(&dx[e], mine, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WAVEFRONT);
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  float out[NS];
 #pragma unroll
-  for (int i = 0; i < NS; ++i) dx[i] = all ? -s[i] * dot : 0.0;
-  for (int j = 0; j < k; ++j) {
-    const int ej = of_lane(e, j);
-    const double aj = of_lane(add_e, j);
-    const double mine = (ej & 63) == lane ? aj : 0.0;
+  for (int i = 0; i < NS; ++i) out[i] = dx[min(l + LANES * i, E - 1)];
+  store_gradient<LANES>(p, t, l, out);
+}
+
+// The plain softmax's, one wave per token: it needs all scores.
+template <int NS>
+__global__ __launch_bounds__(256) void k_route_backward_softmax(GradArgs p) {
+  const int lane = threadIdx.x & 63, E = p.E, k = p.k;
+  const int64_t t = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 4 + (threadIdx.x >> 6);
+  if (t >= p.T) return;
+  float x[NS];
+  load_logits<64>(p.logits, p.f32, t * p.ldx, lane, E, x);
+  int top_ord = ORDER_NONE;
 #pragma unroll
-    for (int i = 0; i < NS; ++i)
-      if (i == ej >> 6) dx[i] += mine;  // (of ej < 0: none)
-  }
+  for (int i = 0; i < NS; ++i) top_ord = pick_max(top_ord, order_of(x[i]));
+  const float top = order_value(wave_max(top_ord));
+  const double m = top > -__builtin_inff() ? (double)top : 0.0;
+  // lane j: the j-th chosen expert (indices outside the experts: no gradient)
+  const int e = lane < k ? p.experts[t * k + lane] : -1;
+  const bool on = e >= 0 && e < E;
+  const double dw = on ? (double)p.dw[t * k + lane] : 0.0;
+  double s[NS], part = 0.0;
 #pragma unroll
   for (int i = 0; i < NS; ++i) {
-    const int c = lane + 64 * i;
-    if (c < E) {
-      if (f32) reinterpret_cast<float*>(d_logits)[t * ldd + c] = (float)dx[i];
-      else reinterpret_cast<__bf16*>(d_logits)[t * ldd + c] = (__bf16)(float)dx[i];
-    }
+    s[i] = lane + 64 * i < E ? exp((double)x[i] - m) : 0.0;
+    part += s[i];
   }
+  double z = wave_sum(part);
+  z = z > 0.0 ? 1.0 / z : 1.0;
+  double mine = 0.0;  // dw p of lane j's expert
+#pragma unroll
+  for (int i = 0; i < NS; ++i) {
+    s[i] *= z;
+    const double si = __shfl(s[i], e & 63);
+    if (on && i == e >> 6) mine = dw * si;
+  }
+  const double dot = wave_sum(mine);
+  double dx[NS];
+#pragma unroll
+  for (int i = 0; i < NS; ++i) dx[i] = -s[i] * dot;
+  for (int j = 0; j < k; ++j) {
+    const int ej = of_lane(e, j);
+    const double aj = of_lane(mine, j);
+    const double add_e = (ej & 63) == lane ? aj : 0.0;
+#pragma unroll
+    for (int i = 0; i < NS; ++i)
+      if (i == ej >> 6) dx[i] += add_e;  // (of ej < 0: none)
+  }
+  float out[NS];
+#pragma unroll
+  for (int i = 0; i < NS; ++i) out[i] = (float)dx[i];
+  store_gradient<64>(p, t, lane, out);
 }
 
 // ---- the combination --------------------------------------------------------
@@ -682,11 +821,19 @@ void launch_route(const void* logits, int f32, int64_t T, int64_t ldx, int E, in
 #define FP4Q_ROUTE(N)                                                                    \
   if (wide) hipLaunchKernelGGL((k_route_pick<N, true>), grid, thr, lds, stream, p);      \
   else hipLaunchKernelGGL((k_route_pick<N, false>), grid, thr, 0, stream, p)
-  if (E <= 64) { FP4Q_ROUTE(1); }
+#define FP4Q_ROUTE16(N) hipLaunchKernelGGL((k_route_pick16<N>), grid, dim3(16 * tok), 0, stream, p)
+  if (!wide && blocks > 1 && k <= 16) {
+    if (E <= 64) FP4Q_ROUTE16(4);
+    else if (E <= 128) FP4Q_ROUTE16(8);
+    else if (E <= 256) FP4Q_ROUTE16(16);
+    else FP4Q_ROUTE16(32);
+  }
+  else if (E <= 64) { FP4Q_ROUTE(1); }
   else if (E <= 128) { FP4Q_ROUTE(2); }
   else if (E <= 256) { FP4Q_ROUTE(4); }
   else { FP4Q_ROUTE(8); }
 #undef FP4Q_ROUTE
+#undef FP4Q_ROUTE16
   if (p.before) hipLaunchKernelGGL(k_route_sums, dim3((unsigned)E), thr, 0, stream, p);
   if (blocks > 1) hipLaunchKernelGGL(k_route_order, grid, thr, 0, stream, p);
 }
@@ -694,15 +841,28 @@ void launch_route(const void* logits, int f32, int64_t T, int64_t ldx, int E, in
 void launch_route_backward(const void* logits, int f32, int64_t T, int64_t ldx, int E, int k,
                            int score, int renorm, const int32_t* experts, const float* d_weights,
                            void* d_logits, int64_t ldd, hipStream_t stream) {
-  const dim3 grid = grid_of((T + 3) / 4), thr(256);
-#define FP4Q_ROUTE(N)                                                                         \
-  hipLaunchKernelGGL((k_route_backward<N>), grid, thr, 0, stream, logits, f32, T, ldx, E, k,  \
-                     score, renorm, experts, d_weights, d_logits, ldd)
-  if (E <= 64) FP4Q_ROUTE(1);
-  else if (E <= 128) FP4Q_ROUTE(2);
-  else if (E <= 256) FP4Q_ROUTE(4);
-  else FP4Q_ROUTE(8);
-#undef FP4Q_ROUTE
+  const GradArgs p = {logits, f32, T, ldx, E, k, score, renorm, experts, d_weights, d_logits, ldd};
+  const int lanes = score == FP4Q_SCORE_SOFTMAX && !renorm ? 64 : k <= 16 ? 16 : 32;
+  const int per = 256 / lanes;
+  const dim3 grid = grid_of((T + per - 1) / per), thr(256);
+  const size_t lds = (size_t)per * E * sizeof(float);
+#define FP4Q_SOFTMAX(N) hipLaunchKernelGGL((k_route_backward_softmax<N>), grid, thr, 0, stream, p)
+#define FP4Q_GRAD(L, N) hipLaunchKernelGGL((k_route_backward<L, N>), grid, thr, lds, stream, p)
+  if (lanes == 64) {
+    if (E <= 64) FP4Q_SOFTMAX(1);
+    else if (E <= 128) FP4Q_SOFTMAX(2);
+    else if (E <= 256) FP4Q_SOFTMAX(4);
+    else FP4Q_SOFTMAX(8);
+  } else if (lanes == 32) {
+    FP4Q_GRAD(32, RT_MAX_E / 32);
+  } else {
+    if (E <= 64) FP4Q_GRAD(16, 4);
+    else if (E <= 128) FP4Q_GRAD(16, 8);
+    else if (E <= 256) FP4Q_GRAD(16, 16);
+    else FP4Q_GRAD(16, 32);
+  }
+#undef FP4Q_SOFTMAX
+#undef FP4Q_GRAD
 }
 
 void launch_combine(int f32, const void* y, int64_t rows, int64_t N, int64_t ldy,

@@ -231,3 +231,61 @@ def test_rows_past_the_offsets(fmt, n, lens, G, D):
         q = dev(c["q"][:rows - 2], torch.bfloat16)
         got = torch.cat([attend(c, q=q), attend(c)[rows - 2:]])
         check_close(c, got)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("E,k", [(1, 1), (8, 8), (17, 16), (60, 4), (64, 16), (65, 17), (128, 8), (200, 16),
+                                 (512, 3), (384, 32)])
+def test_route_of_many_tokens(dtype, E, k):
+    """More than 4096 tokens, the last workgroup partly filled; ties, NaN and
+    infinities among the logits."""
+    need_gpu()
+    say(f"route many {dtype} E{E} k{k}")
+    for score in (0, 1):
+        x = logits_of(4099, E, dtype, E + k)
+        x[1] = 0.5
+        x[2, ::2] = -float("inf")
+        x[3] = torch.finfo(dtype).min
+        x[4098] = -float("inf")
+        x[5, E // 2] = torch.finfo(dtype).max
+        check_route(x, k, score, renorm=True)
+        check_route(x, k, score, renorm=False)
+        y = x.clone()
+        y[2, ::2] = float("nan")
+        a, b = fq.route(x, k, score=score), fq.route(y, k, score=score)
+        for key in a:
+            assert torch.equal(a[key], b[key]), key
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,E,k", [(1, 8, 8), (15, 17, 16), (33, 64, 17), (18, 128, 5), (9, 256, 32), (7, 300, 2)])
+def test_route_gradient_of_given_experts(dtype, T, E, k):
+    """Any experts, not the best: of far smaller scores, named twice, outside
+    the experts (no gradient)."""
+    need_gpu()
+    say(f"route gradient {dtype} T{T} E{E} k{k}")
+    g = torch.Generator().manual_seed(T + E)
+    x = logits_of(T, E, dtype, T)
+    x[0, 0] = 900.0                                # the others' scores underflow
+    e = torch.randint(0, E, (T, k), generator=g).int()
+    e[0] = 1
+    dw = torch.randn(T, k, generator=g)
+    far = e.clone()
+    far[-1, 0], far[-1, -1] = -1, E
+    far[0, k // 2] = 2 ** 31 - 1
+    for score in (0, 1):
+        for renorm in (False, True):
+            got = fq.route_backward(x, e.cuda(), dw.cuda(), score=score, renorm=renorm)
+            want, size = layer.route_backward(host(x), e.numpy(), dw.numpy(), score, renorm)
+            u = (2.0 ** -24 if dtype == torch.float32 else 2.0 ** -8) + 2.0 ** -24
+            # an expert named k times: that many roundings of the sum
+            tol = u * np.abs(want) + (2.0 ** -40 + k * 2.0 ** -24) * size + 1e-38
+            assert np.all(np.abs(host(got) - want) <= tol), (score, renorm)
+            # left out like weights of 0 without a gradient, where nothing divides by them
+            if not renorm:
+                a = fq.route_backward(x, far.cuda(), dw.cuda(), score=score, renorm=renorm)
+                b = fq.route_backward(x, e.cuda(), torch.where(far == e, dw, 0.0).cuda(), score=score,
+                                      renorm=renorm)
+                assert torch.equal(a, b), score
+            assert torch.isfinite(fq.route_backward(x, far.cuda(), dw.cuda(), score=score,
+                                                    renorm=renorm)).all()
