@@ -11,8 +11,6 @@
 #include "fp4q_device.h"
 #include "fp4q_internal.h"
 
-#include <type_traits>
-
 namespace fp4q {
 
 namespace {
@@ -83,9 +81,14 @@ __device__ __forceinline__ uint32_t lane_swap(uint32_t v) {
   return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, ctl, 0xF, 0xF, true);
 }
 
+template <int BIT>
+__device__ __forceinline__ double lane_swap(double v) {
+  const u32x2 u = __builtin_bit_cast(u32x2, v);
+  return __builtin_bit_cast(double, u32x2{lane_swap<BIT>(u[0]), lane_swap<BIT>(u[1])});
+}
+
 __device__ __forceinline__ int pick_max(int a, int b) { return a > b ? a : b; }
 __device__ __forceinline__ int pick_min(int a, int b) { return a < b ? a : b; }
-__device__ __forceinline__ double pick_max(double a, double b) { return fmax(a, b); }
 __device__ __forceinline__ double add(double a, double b) { return a + b; }
 
 // The values of each LANES (16, 32 or 64) lanes joined by f (commutative): every
@@ -248,28 +251,33 @@ __global__ __launch_bounds__(RT_THREADS) void k_route_pick(RouteArgs p) {
         for (int i = 0; i < NS; ++i) s[i] /= z;
       }
     }
-    typedef typename std::conditional<WIDE, double, int>::type key_t;
-    // what cannot be picked (any more) has a key that no comparison finds: NaN,
-    // or the integer below every float's
-    const key_t gone = WIDE ? (key_t)__builtin_nan("") : (key_t)ORDER_NONE;
-    key_t key[NS];
+    // 64-bit keys are compared as integers of the same order, their upper halves
+    // first (low: the lower ones); what cannot be picked (any more) has ORDER_NONE
+    int key[NS];
+    uint32_t low[WIDE ? NS : 1];
+    double rank_by[WIDE ? NS : 1];
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
       const int e = lane + 64 * i;
       if constexpr (WIDE) {
-        key[i] = s[i] + (p.bias && e < E ? (double)p.bias[e] : 0.0);
-        if (!(key[i] == key[i])) key[i] = -__builtin_inf();  // NaN comes last
+        double r = s[i] + (p.bias ? (double)p.bias[min(e, E - 1)] : 0.0) + 0.0;
+        if (!(r == r)) r = -__builtin_inf();  // NaN comes last
+        rank_by[i] = r;
+        const u32x2 u = __builtin_bit_cast(u32x2, r);
+        const int sign = (int)u[1] >> 31;
+        key[i] = (int)u[1] ^ (sign & 0x7FFFFFFF);
+        low[i] = u[0] ^ (uint32_t)sign;
       } else {
         key[i] = ord[i];
       }
-      if (e >= E) key[i] = gone;
+      if (e >= E) key[i] = ORDER_NONE;
     }
     if (WIDE && p.G > 1) {
       // each group's two best, by 64 / 2^ceil(log2 G) lanes a group
       double* r = s_rank + wave * E;
 #pragma unroll
       for (int i = 0; i < NS; ++i)
-        if (lane + 64 * i < E) r[lane + 64 * i] = key[i];
+        if (lane + 64 * i < E) r[lane + 64 * i] = rank_by[i];
       __builtin_amdgcn_wave_barrier();
       const int gs = E / p.G;
       int P = 64;
@@ -277,29 +285,34 @@ __global__ __launch_bounds__(RT_THREADS) void k_route_pick(RouteArgs p) {
       const int g = lane / P;
       double a = -__builtin_inf(), b = -__builtin_inf();
       if (g < p.G)
+#pragma unroll 4
         for (int i = lane % P; i < gs; i += P) {
           const double v = r[g * gs + i];
           if (v > a) { b = a; a = v; }
           else if (v > b) b = v;
         }
-      for (int d = 1; d < P; d <<= 1) {
-        const double a2 = __shfl_xor(a, d), b2 = __shfl_xor(b, d);
+      auto join = [&](double a2, double b2) {
         const double lo = fmin(a, a2);
         a = fmax(a, a2);
         b = fmax(lo, fmax(b, b2));
-      }
+      };
+      if (P > 1) join(lane_swap<0>(a), lane_swap<0>(b));
+      if (P > 2) join(lane_swap<1>(a), lane_swap<1>(b));
+      if (P > 4) join(lane_swap<2>(a), lane_swap<2>(b));
+      if (P > 8) join(lane_swap<3>(a), lane_swap<3>(b));
+      for (int d = 16; d < P; d <<= 1) join(__shfl_xor(a, d), __shfl_xor(b, d));
       double sum = gs > 1 ? a + b : a;
       if (!(sum == sum)) sum = -__builtin_inf();
       int rank = 0;
       for (int o = 0; o < p.G; ++o) {
-        const double other = __shfl(sum, o * P);
+        const double other = of_lane(sum, o * P);
         rank += (other > sum || (other == sum && o < g)) ? 1 : 0;
       }
       const uint64_t keep = __ballot(g < p.G && rank < p.top_groups);  // a group's P lanes agree
 #pragma unroll
       for (int i = 0; i < NS; ++i) {
         const int e = lane + 64 * i;
-        if (e < E && !((keep >> (e / gs * P)) & 1)) key[i] = gone;
+        if (e < E && !((keep >> (e / gs * P)) & 1)) key[i] = ORDER_NONE;
       }
       __builtin_amdgcn_wave_barrier();
     }
@@ -307,19 +320,33 @@ __global__ __launch_bounds__(RT_THREADS) void k_route_pick(RouteArgs p) {
     // keeps the round's expert and its score
     int my_e = 0;
     for (int j = 0; j < k; ++j) {
-      key_t best = key[0];
+      int best = key[0];
 #pragma unroll
       for (int i = 1; i < NS; ++i) best = pick_max(best, key[i]);
       best = wave_max(best);
-      int pick = -1;
+      uint64_t has[NS];
+      int n = 0;
 #pragma unroll
       for (int i = 0; i < NS; ++i) {
-        const uint64_t has = __ballot(key[i] == best);
-        if (pick < 0 && has) pick = 64 * i + (int)__ffsll((unsigned long long)has) - 1;
+        has[i] = __ballot(key[i] == best);
+        n += (int)__popcll(has[i]);
       }
+      if (WIDE && n > 1) {  // their lower halves decide
+        uint32_t most = 0;
+#pragma unroll
+        for (int i = 0; i < NS; ++i) most = key[i] == best ? max(most, low[i]) : most;
+        // (as signed integers of the same order)
+        most = (uint32_t)wave_max((int)(most ^ 0x80000000u)) ^ 0x80000000u;
+#pragma unroll
+        for (int i = 0; i < NS; ++i) has[i] = __ballot(key[i] == best && low[i] == most);
+      }
+      int pick = 0;
+#pragma unroll
+      for (int i = NS - 1; i >= 0; --i)
+        if (has[i]) pick = 64 * i + (int)__ffsll((unsigned long long)has[i]) - 1;
 #pragma unroll
       for (int i = 0; i < NS; ++i)
-        if (lane + 64 * i == pick) key[i] = gone;
+        if (lane + 64 * i == pick) key[i] = ORDER_NONE;
       if (lane == j) my_e = pick;
     }
     double my_s = 0.0;
