@@ -2,9 +2,10 @@
 // gradient of the logits) and the combination of the experts' outputs (and
 // its gradients).  The operations are defined in include/fp4q.h.
 //
-// The router is bound by vector instructions: 16384 x 128, k 8, takes 15 us for
-// the choice (300 instructions a token), 5 for the order and 13 for the gradient,
-// where its bytes would take 4; 4096 x 256 with groups 13.4 and 5.  The
+// The router is bound by vector instructions and by the chain of its k rounds:
+// 16384 x 128, k 8, takes 7.9 us for the choice, 5.7 for the order and 6.3 for the
+// gradient, where its bytes would take 4 in all; 4096 x 256 with groups 11.7 and
+// 5.8 (about 1000 vector instructions a token, 64-bit scores among them).  The
 // combination is bound by HBM: 4096 x 8 rows of 2048 (BF16) take 39 us, which
 // also writes back what the call before left in the cache, the gradients 48 us
 // (285 MB, 5.9 TB/s).
@@ -387,7 +388,9 @@ __global__ __launch_bounds__(RT_THREADS) void k_route_pick(RouteArgs p) {
 
 // The same without bias and groups for k up to 16 and more tokens than one
 // workgroup has: 16 lanes per token, lane l with experts l, l + 16, ..., so that
-// four tokens share each exchange between lanes and each 64-bit exponential.
+// four tokens share each exchange between lanes and each 64-bit exponential
+// (x 128 experts, k 8, the order included: 4096 tokens 9.3 us, by one wave a token
+// 10.2).
 template <int NS>
 __global__ __launch_bounds__(RT_THREADS) void k_route_pick16(RouteArgs p) {
   __shared__ uint64_t s_mask[RT_MAX_E];
@@ -576,7 +579,8 @@ __device__ __forceinline__ void store_gradient(const GradArgs& p, int64_t t, int
 // have them) are all that is needed.  So it is with all but the plain softmax:
 // LANES lanes per token, lane j with the j-th chosen expert, whose gradients
 // meet the zeros of the others in LDS (an expert that is named twice in the
-// order of j).
+// order of j).  16384 x 128, k 8 take 6.3 us (17 MB, of which 3 us), with one
+// wave per token and one load after another 13.3.
 template <int LANES, int NS>
 __global__ __launch_bounds__(256) void k_route_backward(GradArgs p) {
   extern __shared__ float s_dx[];  // [256 / LANES][E]
@@ -812,12 +816,14 @@ inline bool vec_ok(const void* p, int64_t ld, int esz) {
 
 }  // namespace
 
-// Tokens of a workgroup: few while that leaves CUs without one.
-static int route_tokens(int64_t T) { return T <= 4096 ? 16 : RT_TOK; }
+// Tokens of a workgroup: few while that leaves CUs without one (x 256 experts, k 8:
+// 4096 tokens 11.7 us a call by 16 and 13.6 by 64, in 8 groups 16.7 and 34.8;
+// 16384 tokens 21.4 and 16.5, in groups 49.4 and 38.0).
+static int route_tokens(int64_t T) { return T <= 256 * 16 ? 16 : T <= 256 * 32 ? 32 : RT_TOK; }
 
 // Blocks from which on their counts are summed up by a kernel of its own
-// (x 128 experts, k 8: 256 blocks 20.4 us a call without it and 22.5 with it, 512
-// 33.8 and 32.5, 1024 68.8 and 55).
+// (x 128 experts, k 8: 256 blocks 12.3 us a call without it and 14.1 with it, 512
+// 20.4 and 18.7, 1024 43.9 and 31.0).
 constexpr int RT_SUMS = 512;
 
 size_t route_workspace_bytes(int64_t T, int E) {

@@ -289,3 +289,29 @@ def test_route_gradient_of_given_experts(dtype, T, E, k):
                 assert torch.equal(a, b), score
             assert torch.isfinite(fq.route_backward(x, far.cuda(), dw.cuda(), score=score,
                                                     renorm=renorm)).all()
+
+
+@pytest.mark.parametrize("T", [8192, 8197])
+def test_route_of_full_workgroups(T):
+    need_gpu()
+    say(f"route full workgroups T {T}")
+    x = logits_of(T, 40, torch.bfloat16, T)
+    check_route(x, 5)
+    check_route(x, 17)
+    check_route(x.float(), 5, 1, torch.linspace(-0.1, 0.1, 40).cuda(), 4, 2)
+
+
+def test_router_keys_that_differ_in_their_last_bits():
+    """Scores in 64 bits that agree in their upper halves, and equal ones."""
+    need_gpu()
+    g = torch.Generator().manual_seed(1)
+    x = 1e-7 * torch.randn(300, 96, generator=g)   # sigmoids within 2^-24 of 1/2
+    x[:, ::7] = 0.0
+    x[:, 1::7] = -0.0
+    x = x.cuda()
+    b = torch.zeros(96).cuda()
+    for score in (0, 1):
+        check_route(x, 9, score, b)
+        check_route(x, 9, score, b - 1.0)          # keys below 0
+        check_route(x, 9, score, b, 8, 3)
+        check_route(x, 9, score, b - 1.0, 3, 2, renorm=False)
