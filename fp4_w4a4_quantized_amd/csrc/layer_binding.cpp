@@ -148,6 +148,17 @@ at::Tensor like(const at::Tensor& t, at::IntArrayRef shape, at::ScalarType type)
   return at::empty(shape, t.options().dtype(type));
 }
 
+// A contiguous tensor over a part of buf's memory, from element `at0` on: not a
+// view to autograd (each has its own version), and without the dispatcher's time
+// (four of them in a call for one token: 7.2 us with as_strided, 6.4 with this).
+at::Tensor part(const at::Tensor& buf, at::IntArrayRef shape, int64_t at0) {
+  at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(buf.storage()), buf.key_set(),
+                                                          buf.dtype());
+  t.unsafeGetTensorImpl()->set_storage_offset(at0);
+  t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
+  return t;
+}
+
 // What the cache's calls have in common: (fmt, cache, page, offsets,
 // page_table, lens, k_scale, v_scale) are arguments 1 .. 8, after the stream.
 struct Kv {
@@ -330,9 +341,8 @@ PyObject* route(PyObject* const* a) {
   const at::Tensor weights = like(x, {T, k}, at::kFloat);
   int32_t* p = buf.data_ptr<int32_t>() + w;
   const int64_t at0 = w;
-  const at::Tensor experts = buf.as_strided({T, k}, {k, 1}, at0), row_of = buf.as_strided({T, k}, {k, 1}, at0 + n),
-                   row_src = buf.as_strided({n}, {1}, at0 + 2 * n),
-                   offsets = buf.as_strided({E + 1}, {1}, at0 + 3 * n);
+  const at::Tensor experts = part(buf, {T, k}, at0), row_of = part(buf, {T, k}, at0 + n),
+                   row_src = part(buf, {n}, at0 + 2 * n), offsets = part(buf, {E + 1}, at0 + 3 * n);
   route_call(a, r, p, weights.data_ptr<float>(), p + 3 * n, p + 2 * n, p + n,
              bytes ? buf.data_ptr() : nullptr, bytes);
   PyObject* t[5] = {wrap(experts), wrap(weights), wrap(offsets), wrap(row_src), wrap(row_of)};
