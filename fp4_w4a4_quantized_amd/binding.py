@@ -789,7 +789,7 @@ def _layer():
         except ImportError as e:
             raise ImportError(f"{e}: build it with "
                               "`python -m fp4_w4a4_quantized_amd.build`") from e
-        native.set_up(_check, lambda: _stream(None))
+        native.set_up(_check, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
         _native = native
     return _native
 

@@ -26,7 +26,8 @@ struct Refused : std::runtime_error {
 struct PythonError {};  // a Python exception is set
 
 PyObject* g_fail = nullptr;     // fail(name, code): raises the package's error
-PyObject* g_current = nullptr;  // current(): the current stream's handle
+PyObject* g_device = nullptr;   // device(): the current device
+PyObject* g_current = nullptr;  // current(device): its current stream's handle
 const char* g_host = nullptr;   // a tensor of this call that is not on the GPU
 
 void check(const char* fn, int rc) {
@@ -65,7 +66,10 @@ int32_t small(PyObject* o, const char* name) {
 void* stream_of(PyObject* o) {
   if (g_host) throw Refused(std::string(g_host) + ": a tensor on the GPU is needed");
   if (o != Py_None) return reinterpret_cast<void*>(integer(o));
-  PyObject* r = PyObject_CallNoArgs(g_current);
+  PyObject* d = PyObject_CallNoArgs(g_device);
+  if (!d) throw PythonError();
+  PyObject* r = PyObject_CallOneArg(g_current, d);
+  Py_DECREF(d);
   if (!r) throw PythonError();
   const int64_t v = PyLong_AsLongLong(r);
   Py_DECREF(r);
@@ -462,16 +466,18 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
   return nullptr;
 }
 
-// set_up(fail, current)
+// set_up(fail, device, current)
 PyObject* set_up(PyObject*, PyObject* args) {
-  PyObject *fail, *current;
-  if (!PyArg_ParseTuple(args, "OO", &fail, &current)) return nullptr;
-  Py_INCREF(fail);
-  Py_INCREF(current);
-  Py_XDECREF(g_fail);
-  Py_XDECREF(g_current);
-  g_fail = fail;
-  g_current = current;
+  PyObject *fail, *device, *current;
+  if (!PyArg_ParseTuple(args, "OOO", &fail, &device, &current)) return nullptr;
+  auto keep = [](PyObject*& at, PyObject* o) {
+    Py_INCREF(o);
+    Py_XDECREF(at);
+    at = o;
+  };
+  keep(g_fail, fail);
+  keep(g_device, device);
+  keep(g_current, current);
   Py_RETURN_NONE;
 }
 
