@@ -27,7 +27,7 @@
 // 2^(x - m), so that weights down to 2^-31 of the largest are not lost.
 //
 // Few rows (this file) are bound by reading the cache: 64 x 1 token over up to
-// 8192 keys (249 MB) take 62-69 us, 3.6-4 TB/s where a copy reaches 4.8, and the
+// 8192 keys (249 MB) take 62-71 us, 3.5-4 TB/s where a copy reaches 4.8, and the
 // join of the splits 7.  One token over 777 keys is one wave's chain of four
 // steps: 10.5 us.  Many rows: attention_tile.hip.
 #include "attention_common.h"
