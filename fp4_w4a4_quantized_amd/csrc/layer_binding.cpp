@@ -8,6 +8,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/detail/CUDAHooksInterface.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
@@ -148,8 +149,25 @@ void* scratch(PyObject* o, size_t* bytes) {
 
 PyObject* wrap(const at::Tensor& t) { return THPVariable_Wrap(t); }
 
+// An uninitialised result beside t: at::empty's memory, from the same allocator,
+// without the dispatcher's time (one token's route 6.4 -> 5.7 us, a combination of
+// 64 tokens 5.1 -> 4.6).
 at::Tensor like(const at::Tensor& t, at::IntArrayRef shape, at::ScalarType type) {
-  return at::empty(shape, t.options().dtype(type));
+  const auto& gpu = at::detail::getCUDAHooks();
+  if (!t.is_cuda() || t.get_device() != gpu.getCurrentDevice())
+    return at::empty(shape, t.options().dtype(type));
+  c10::Allocator* const alloc = gpu.getCUDADeviceAllocator();
+  int64_t n = 1;
+  for (int64_t d : shape)
+    if (__builtin_mul_overflow(n, d, &n) || d < 0) throw std::length_error("a result too large");
+  const size_t bytes = (size_t)n * c10::elementSize(type);
+  auto storage = c10::make_intrusive<c10::StorageImpl>(c10::StorageImpl::use_byte_size_t(), bytes,
+                                                       alloc->allocate(bytes), alloc, true);
+  at::Tensor r = at::detail::make_tensor<c10::TensorImpl>(
+      c10::Storage(std::move(storage)), c10::DispatchKeySet(c10::DispatchKey::CUDA),
+      c10::scalarTypeToTypeMeta(type));
+  r.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
+  return r;
 }
 
 // A contiguous tensor over a part of buf's memory, from element `at0` on: not a
