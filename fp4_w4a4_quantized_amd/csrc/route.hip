@@ -195,9 +195,10 @@ __device__ __forceinline__ void block_scan(int* v, int n, int* tmp, int* total) 
 }
 
 // One wave per token; lane l holds experts l, l + 64, ...  The order of the
-// experts is taken on the logits themselves where they decide it (no bias and
-// no groups: both scores are increasing functions of the logit), else on the
-// scores in 64 bits, so that near ties are told apart as the definition does.
+// experts is taken on the logits themselves where they decide it (no bias: both
+// scores are increasing functions of the logit), else on the scores in 64 bits,
+// so that near ties are told apart as the definition does.  The groups' order
+// needs the scores in either case (WIDE: a bias or groups).
 template <int NS, bool WIDE>
 __global__ __launch_bounds__(RT_THREADS) void k_route_pick(RouteArgs p) {
   __shared__ uint64_t s_mask[RT_MAX_E];
@@ -266,8 +267,8 @@ __global__ __launch_bounds__(RT_THREADS) void k_route_pick(RouteArgs p) {
         rank_by[i] = r;
         const u32x2 u = __builtin_bit_cast(u32x2, r);
         const int sign = (int)u[1] >> 31;
-        key[i] = (int)u[1] ^ (sign & 0x7FFFFFFF);
-        low[i] = u[0] ^ (uint32_t)sign;
+        key[i] = p.bias ? (int)u[1] ^ (sign & 0x7FFFFFFF) : ord[i];
+        low[i] = p.bias ? u[0] ^ (uint32_t)sign : 0u;
       } else {
         key[i] = ord[i];
       }

@@ -771,7 +771,9 @@ int fp4q_kv_attention(fp4q_format_t fmt, const uint8_t* cache, int64_t n_pages, 
  *            and does not enter the weights)
  *   groups   n_groups equal runs of experts; the top_groups of largest sum
  *            of their two best ranked scores stay (n_groups 1: no groups)
- *   experts  the k best ranked of those, best first
+ *   experts  the k best ranked of those, best first (without a bias those of
+ *            the largest logits, which tell apart what a score that saturates
+ *            or underflows does not)
  *   weights  their scores (renorm: divided by their sum)
  * Ties go to the lower index; a NaN logit counts as -inf.  A token without
  * a finite logit has weights 0.  And the order by expert that the grouped calls
