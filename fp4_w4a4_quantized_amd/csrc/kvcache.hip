@@ -145,7 +145,7 @@ __device__ __forceinline__ void quant32(const uint32_t (&x)[16], float t, uint32
     float v[8];
     if (FMT == FP4Q_NVFP4) {
       const uint32_t sb = e4m3_encode((amax / 6.0f) / t);
-      s |= sb << (8 * blk);
+      s |= (sb & 0xFFu) << (8 * blk);  // (more than a byte for a NaN, which must not reach the other block)
       const float d = e4m3_value(sb) * t;
       // quot_rn's range; its operands are held within 8 d (beyond it every
       // quotient gives the largest code)

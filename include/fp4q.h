@@ -681,6 +681,9 @@ int fp4q_grouped_gemm_gather(fp4q_format_t fmt, fp4q_layout_t w_layout, int64_t 
  * fp4q_quantize; NVFP4's tensor scale is given, one for each head
  * (k_scale, v_scale: device f32 [kv_heads], positive, of calibrated keys
  * and values; values beyond 2688 times it saturate); NULL for MXFP4.
+ * Keys and values are finite, as fp4q_quantize's inputs are: an infinity or
+ * a NaN makes the values of its own block arbitrary (under a finite scale)
+ * and no others.
  *
  * Sequences: sequence b owns the pages page_table[b, 0 .. table_cols)
  * (device int32, row stride ld_table), token position p in page p / page.  Its new tokens

@@ -7,6 +7,8 @@ import torch
 
 import fp4_w4a4_quantized_amd as fq
 from gpu_helpers import need_gpu, say
+from oracle import layer
+from test_gpu_kv_attention import FMTS, dev, make
 from test_gpu_route_combine import check_route
 
 pytestmark = pytest.mark.gpu
@@ -42,3 +44,70 @@ def test_a_grouped_choice_by_hand():
     x[0, 2], x[0, 5], x[0, 6] = 38.0, 50.0, 45.0
     r = fq.route(x.cuda(), 2, score=fq.SIGMOID, n_groups=4, top_groups=2)
     assert r["experts"].tolist() == [[5, 6]]
+
+
+# ---- the cache --------------------------------------------------------------
+
+def block_bytes(fmt, page, D, slot, blk):
+    """The bytes of a page of one head that hold block blk of K and of V of the
+    token at slot, and V bytes' share of them (they are half another block's)."""
+    kb, _, vb, vh, ks, vs = layer.kv_places(fmt, page, D)
+    n = layer.BLOCK[fmt]
+    el = slice(blk * n, blk * n + n)
+    return kb[slot, el], vb[slot, el], vh[slot, el], ks[slot, blk], vs[slot, blk]
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_what_is_not_finite_stays_in_its_block(fmt, D, bad):
+    """One bad element in each block of a token in turn: every other block's
+    bytes are those of the clean token, and its own scale is a finite one."""
+    need_gpu()
+    say(f"append {bad} fmt {fmt} D {D}")
+    blocks, page, H = D // layer.BLOCK[fmt], 16, 2
+    off, lens = np.array([0, blocks], np.int32), np.array([blocks], np.int32)
+    table = np.array([[1]], np.int32)
+    rng = np.random.default_rng(D)
+    k = torch.from_numpy(rng.standard_normal((blocks, H, D))).to(torch.bfloat16).cuda()
+    t = dev(np.array([0.003, 0.004], np.float32)) if fmt == 0 else None
+    got = []
+    for spoil in (False, True):
+        x = k.clone()
+        if spoil:
+            for b in range(blocks):
+                x[b, 1, b * layer.BLOCK[fmt] + b % 7] = bad
+        cache = torch.zeros(2, H, layer.kv_page_bytes(fmt, page, D), dtype=torch.uint8, device="cuda")
+        fq.kv_append(fmt, cache, page, dev(off), dev(table), dev(lens), x, x, t, t)
+        got.append(cache.cpu().numpy())
+    clean, dirty = got
+    top = 0x7E if fmt == 0 else 0xFE
+    for b in range(blocks):
+        kb, vb, vh, ks, vs = block_bytes(fmt, page, D, b, b)
+        assert dirty[1, 1, ks] <= top and dirty[1, 1, vs] <= top
+        dirty[1, 1, ks], dirty[1, 1, vs] = clean[1, 1, ks], clean[1, 1, vs]
+        dirty[1, 1, kb] = clean[1, 1, kb]
+        for byte, shift in zip(vb, vh):            # (both halves of a byte may be this block's)
+            own = 0xF << int(shift)
+            dirty[1, 1, byte] = (int(dirty[1, 1, byte]) & ~own) | (int(clean[1, 1, byte]) & own)
+    bad_at = np.argwhere(clean != dirty)
+    assert bad_at.size == 0, f"{len(bad_at)} bytes differ, first {bad_at[:4].tolist()}"
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("n", [8, 40])
+def test_a_later_token_that_is_not_finite_does_not_reach_earlier_rows(fmt, n):
+    need_gpu()
+    c = make(fmt, [n], [n], G=2, H=2, D=128, seed=8, garbage=False)
+    t = None if c["t"] is None else dev(c["t"])
+    k = torch.randn(n, 2, 128, generator=torch.Generator().manual_seed(n)).to(torch.bfloat16).cuda()
+    q, got = dev(c["q"], torch.bfloat16), []
+    for bad in (0.0, float("nan"), float("inf")):
+        x = k.clone()
+        x[n - 1, :, ::5] = bad
+        cache = dev(c["cache"])
+        where = (cache, c["page"], dev(c["off"]), dev(c["table"]), dev(c["lens"]))
+        fq.kv_append(fmt, *where, x, x, t, t)
+        got.append(fq.kv_attention(fmt, *where, q, n, n, t, t)[:n - 1])
+    assert torch.isfinite(got[0]).all()
+    assert torch.equal(got[0], got[1]) and torch.equal(got[0], got[2])
