@@ -181,6 +181,11 @@ def lib():
         L.fp4q_combine_backward.restype = i
         L.fp4q_combine_backward.argtypes = [i, P, i64, i64, i64, P, P, i64, i32, P, i64, P, i64, P,
                                             P]
+        L.fp4q_combine_backward_zeroed_workspace_bytes.restype = sz
+        L.fp4q_combine_backward_zeroed_workspace_bytes.argtypes = [i64]
+        L.fp4q_combine_backward_zeroed.restype = i
+        L.fp4q_combine_backward_zeroed.argtypes = [i, P, i64, i64, i64, P, P, i64, i32, P, i64, P,
+                                                   i64, P, P, sz, P]
         L.fp4q_error_decompose_workspace_bytes.restype = sz
         L.fp4q_error_decompose_workspace_bytes.argtypes = [i64, i64]
         L.fp4q_error_decompose.restype = ctypes.c_int
@@ -919,6 +924,6 @@ def combine_backward_into(y, row_of, weights, d_out, d_y, d_weights, stream=None
 
 
 def combine_backward(y, row_of, weights, d_out, stream=None):
-    """(d_y, d_weights) of combine() from d_out.  row_of names every row of y
-    (combine_backward_into leaves the others as they are)."""
+    """(d_y, d_weights) of combine() from d_out.  Rows of y that row_of does not
+    name get 0 (combine_backward_into leaves them as they are)."""
     return _results(stream, _layer().combine_backward, y, row_of, weights, d_out)

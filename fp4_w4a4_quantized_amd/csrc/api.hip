@@ -848,6 +848,25 @@ int kv_copy(bool append, int fmt, uint8_t* cache, int64_t n_pages, int32_t page,
   return check_launch();
 }
 
+int combine_backward_checks(int dtype, const void* y, int64_t rows, int64_t cols, int64_t ldy,
+                            const int32_t* row_of, const float* weights, int64_t tokens, int32_t k,
+                            const void* d_out, int64_t ldo, const void* d_y, int64_t lddy,
+                            const float* d_weights) {
+  if (!dtype_ok(dtype) || rows < 0 || cols < 1 || ldy < cols || tokens < 0 || k < 1 ||
+      ldo < cols || lddy < cols)
+    return FP4Q_ERR_INVALID;
+  if (tokens > 0 && (!row_of || !weights || !d_out || !d_weights || (rows > 0 && (!y || !d_y))))
+    return FP4Q_ERR_INVALID;
+  const int el = dtype == FP4Q_OUT_F32 ? 4 : 2;
+  if (!aligned(y, el) || !aligned(d_out, el) || !aligned(d_y, el) || !aligned(row_of, 4) ||
+      !aligned(weights, 4) || !aligned(d_weights, 4))
+    return FP4Q_ERR_INVALID;
+  if (k > 128 || tokens >= ((int64_t)1 << 31) / k || cols >= ((int64_t)1 << 31) ||
+      tokens * ((cols + 7) / 8) >= ((int64_t)1 << 31))
+    return FP4Q_ERR_UNSUPPORTED;
+  return FP4Q_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1008,23 +1027,40 @@ int fp4q_combine_backward(fp4q_dtype_t dtype, const void* y, int64_t rows, int64
                           int64_t ldy, const int32_t* row_of, const float* weights,
                           int64_t tokens, int32_t k, const void* d_out, int64_t ldo, void* d_y,
                           int64_t lddy, float* d_weights, void* stream) {
-  if (!dtype_ok(dtype) || rows < 0 || cols < 1 || ldy < cols || tokens < 0 || k < 1 ||
-      ldo < cols || lddy < cols)
-    return FP4Q_ERR_INVALID;
-  if (tokens > 0 && (!row_of || !weights || !d_out || !d_weights || (rows > 0 && (!y || !d_y))))
-    return FP4Q_ERR_INVALID;
-  const int el = dtype == FP4Q_OUT_F32 ? 4 : 2;
-  if (!aligned(y, el) || !aligned(d_out, el) || !aligned(d_y, el) || !aligned(row_of, 4) ||
-      !aligned(weights, 4) || !aligned(d_weights, 4))
-    return FP4Q_ERR_INVALID;
-  if (k > 128 || tokens >= ((int64_t)1 << 31) / k || cols >= ((int64_t)1 << 31) ||
-      tokens * ((cols + 7) / 8) >= ((int64_t)1 << 31))
-    return FP4Q_ERR_UNSUPPORTED;
+  const int rc = combine_backward_checks(dtype, y, rows, cols, ldy, row_of, weights, tokens, k, d_out,
+                                         ldo, d_y, lddy, d_weights);
+  if (rc != FP4Q_OK) return rc;
   if (tokens == 0) return FP4Q_OK;
   if (injected_failure()) return FP4Q_ERR_HIP;
   clear_error();
   fp4q::launch_combine_backward(dtype == FP4Q_OUT_F32, y, rows, cols, ldy, row_of, weights, tokens,
-                                k, d_out, ldo, d_y, lddy, d_weights,
+                                k, d_out, ldo, d_y, lddy, d_weights, nullptr,
+                                static_cast<hipStream_t>(stream));
+  return check_launch();
+}
+
+size_t fp4q_combine_backward_zeroed_workspace_bytes(int64_t rows) {
+  return rows > 0 && rows < ((int64_t)1 << 31) ? (size_t)rows * sizeof(int32_t) : 0;
+}
+
+int fp4q_combine_backward_zeroed(fp4q_dtype_t dtype, const void* y, int64_t rows, int64_t cols,
+                                 int64_t ldy, const int32_t* row_of, const float* weights,
+                                 int64_t tokens, int32_t k, const void* d_out, int64_t ldo, void* d_y,
+                                 int64_t lddy, float* d_weights, void* workspace,
+                                 size_t workspace_bytes, void* stream) {
+  const int rc = combine_backward_checks(dtype, y, rows, cols, ldy, row_of, weights, tokens, k, d_out,
+                                         ldo, d_y, lddy, d_weights);
+  if (rc != FP4Q_OK) return rc;
+  if (rows > 0 && !d_y) return FP4Q_ERR_INVALID;
+  if (rows >= ((int64_t)1 << 31)) return FP4Q_ERR_UNSUPPORTED;
+  const size_t need = fp4q_combine_backward_zeroed_workspace_bytes(rows);
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 4)))
+    return FP4Q_ERR_WORKSPACE;
+  if (tokens == 0 && rows == 0) return FP4Q_OK;
+  if (injected_failure()) return FP4Q_ERR_HIP;
+  clear_error();
+  fp4q::launch_combine_backward(dtype == FP4Q_OUT_F32, y, rows, cols, ldy, row_of, weights, tokens,
+                                k, d_out, ldo, d_y, lddy, d_weights, static_cast<int32_t*>(workspace),
                                 static_cast<hipStream_t>(stream));
   return check_launch();
 }

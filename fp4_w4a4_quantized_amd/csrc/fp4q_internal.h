@@ -169,7 +169,7 @@ void launch_combine(int f32, const void* y, int64_t rows, int64_t N, int64_t ldy
 void launch_combine_backward(int f32, const void* y, int64_t rows, int64_t N, int64_t ldy,
                              const int32_t* row_of, const float* w, int64_t T, int k,
                              const void* d_out, int64_t ldo, void* d_y, int64_t lddy, float* d_w,
-                             hipStream_t stream);
+                             int32_t* named, hipStream_t stream);
 
 size_t decompose_workspace_bytes(int64_t rows, int64_t cols);
 int launch_decompose(int fmt, const uint16_t* x, int64_t rows, int64_t cols, int64_t ldx,

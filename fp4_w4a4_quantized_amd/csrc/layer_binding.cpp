@@ -430,23 +430,30 @@ PyObject* combine(PyObject* const* a) {
   return wrap(out);
 }
 
-// combine_backward_into(stream, y, row_of, weights, d_out, d_y, d_weights)
-void combine_gradient(PyObject* const* a, const Matrix& y, const Table& r, void* dy, int64_t lddy, float* dw) {
+// combine_backward_into(stream, y, row_of, weights, d_out, d_y, d_weights);
+// ws: null, or scratch for the rows that row_of does not name, which then become 0
+void combine_gradient(PyObject* const* a, const Matrix& y, const Table& r, void* dy, int64_t lddy, float* dw,
+                      const at::Tensor* ws) {
   const Matrix d = matrix(a[4], "d_out");
   need(d.type == y.type && d.rows == r.tokens && d.cols == y.cols, "d_out",
        "[tokens, cols] of y's type is needed");
   const float* w = floats(a[3], "weights", r.tokens * r.k);
   void* const stream = stream_of(a[0]);
-  check("fp4q_combine_backward",
-        fp4q_combine_backward(y.type, y.p, y.rows, y.cols, y.ld, r.p, w, r.tokens, (int32_t)r.k, d.p, d.ld,
-                              dy, lddy, dw, stream));
+  if (ws)
+    check("fp4q_combine_backward_zeroed",
+          fp4q_combine_backward_zeroed(y.type, y.p, y.rows, y.cols, y.ld, r.p, w, r.tokens, (int32_t)r.k, d.p,
+                                       d.ld, dy, lddy, dw, ws->data_ptr(), ws->nbytes(), stream));
+  else
+    check("fp4q_combine_backward",
+          fp4q_combine_backward(y.type, y.p, y.rows, y.cols, y.ld, r.p, w, r.tokens, (int32_t)r.k, d.p, d.ld,
+                                dy, lddy, dw, stream));
 }
 
 PyObject* combine_backward_into(PyObject* const* a) {
   const Matrix y = matrix(a[1], "y"), dy = matrix(a[5], "d_y");
   const Table r = table(a[2], "row_of");
   need(dy.type == y.type && dy.rows == y.rows && dy.cols == y.cols, "d_y", "y's shape and type are needed");
-  combine_gradient(a, y, r, dy.p, dy.ld, floats(a[6], "d_weights", r.tokens * r.k));
+  combine_gradient(a, y, r, dy.p, dy.ld, floats(a[6], "d_weights", r.tokens * r.k), nullptr);
   Py_RETURN_NONE;
 }
 
@@ -454,8 +461,9 @@ PyObject* combine_backward(PyObject* const* a) {
   const Matrix y = matrix(a[1], "y");
   const Table r = table(a[2], "row_of");
   const at::Tensor& t = THPVariable_Unpack(a[1]);
-  const at::Tensor dy = like(t, {y.rows, y.cols}, t.scalar_type()), dw = like(t, {r.tokens, r.k}, at::kFloat);
-  combine_gradient(a, y, r, dy.data_ptr(), y.cols, dw.data_ptr<float>());
+  const at::Tensor dy = like(t, {y.rows, y.cols}, t.scalar_type()), dw = like(t, {r.tokens, r.k}, at::kFloat),
+                   ws = like(t, {y.rows}, at::kInt);
+  combine_gradient(a, y, r, dy.data_ptr(), y.cols, dw.data_ptr<float>(), &ws);
   PyObject *p0 = wrap(dy), *p1 = wrap(dw);
   PyObject* out = PyTuple_Pack(2, p0, p1);
   Py_XDECREF(p0);

@@ -742,6 +742,7 @@ struct CombineArgs {
   void* d_y;
   int64_t lddy;
   float* d_w;
+  int32_t* named;  // [rows], null: not asked for; the entry of row_of that names the row
 };
 
 // out[t] = sum_j w[t, j] y[row_of[t, j]]: a thread holds VEC columns of one
@@ -787,6 +788,7 @@ __global__ __launch_bounds__(256) void k_combine_backward(CombineArgs p) {
     if (lane == 0) p.d_w[i] = 0.0f;
     return;
   }
+  if (p.named && lane == 0) p.named[r] = (int32_t)i;
   const float w = p.w[i];
   float dot = 0.0f;
   for (int64_t c = (int64_t)lane * VEC; c < p.N; c += 64 * VEC) {
@@ -805,9 +807,33 @@ __global__ __launch_bounds__(256) void k_combine_backward(CombineArgs p) {
   if (lane == 0) p.d_w[i] = dot;
 }
 
+// The rows of d_y that no entry of row_of names become 0, a wave for 64 rows.
+// named[] was not cleared before k_combine_backward wrote it: what it holds for
+// a row counts where row_of bears it out, and then the row is named, whoever
+// wrote it.  (Zeroing all of d_y first would write it twice: 134 MB in the case
+// below, 25 us, where this launch takes 3.)
+template <bool F32, int VEC>
+__global__ __launch_bounds__(256) void k_zero_unnamed(CombineArgs p) {
+  const int lane = threadIdx.x & 63;
+  const int64_t r0 = (((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 4 + (threadIdx.x >> 6)) * 64;
+  const int64_t r = r0 + lane;
+  bool rest = false;
+  if (r < p.rows) {
+    const int64_t i = p.named[r];
+    rest = i < 0 || i >= p.T * p.k || p.row_of[i] != r;
+  }
+  float zero[VEC];
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) zero[e] = 0.0f;
+  for (uint64_t left = __ballot(rest); left; left &= left - 1) {
+    const int64_t at = (r0 + __ffsll((unsigned long long)left) - 1) * p.lddy;
+    for (int64_t c = (int64_t)lane * VEC; c < p.N; c += 64 * VEC) store_vec<F32, VEC>(p.d_y, at + c, zero);
+  }
+}
+
 // A grid of n workgroups of 256, in rows: one dimension holds 2^32 threads.
 inline dim3 grid_of(int64_t n) {
-  const int64_t x = n < (1 << 20) ? n : 1 << 20;
+  const int64_t x = n < 1 ? 1 : n < (1 << 20) ? n : 1 << 20;
   return dim3((unsigned)x, (unsigned)((n + x - 1) / x));
 }
 
@@ -902,7 +928,7 @@ void launch_route_backward(const void* logits, int f32, int64_t T, int64_t ldx, 
 void launch_combine(int f32, const void* y, int64_t rows, int64_t N, int64_t ldy,
                     const int32_t* row_of, const float* w, int64_t T, int k, void* out,
                     int64_t ldo, hipStream_t stream) {
-  const CombineArgs p = {y, rows, N, ldy, row_of, w, T, k, out, ldo, nullptr, nullptr, 0, nullptr};
+  const CombineArgs p = {y, rows, N, ldy, row_of, w, T, k, out, ldo, nullptr, nullptr, 0, nullptr, nullptr};
   const int esz = f32 ? 4 : 2;
   const bool vec = N % 8 == 0 && vec_ok(y, ldy, esz) && vec_ok(out, ldo, esz);
   const int64_t items = T * (vec ? N / 8 : N);
@@ -919,20 +945,26 @@ void launch_combine(int f32, const void* y, int64_t rows, int64_t N, int64_t ldy
 void launch_combine_backward(int f32, const void* y, int64_t rows, int64_t N, int64_t ldy,
                              const int32_t* row_of, const float* w, int64_t T, int k,
                              const void* d_out, int64_t ldo, void* d_y, int64_t lddy, float* d_w,
-                             hipStream_t stream) {
-  const CombineArgs p = {y,       rows, N,     ldy, row_of, w,  T,
-                         k,       nullptr, ldo, d_out, d_y, lddy, d_w};
+                             int32_t* named, hipStream_t stream) {
+  const CombineArgs p = {y,       rows, N,     ldy, row_of, w,    T,
+                         k,       nullptr, ldo, d_out, d_y, lddy, d_w, named};
   const int esz = f32 ? 4 : 2;
   const bool vec = N % 8 == 0 && vec_ok(y, ldy, esz) && vec_ok(d_out, ldo, esz) &&
                    vec_ok(d_y, lddy, esz);
-  const dim3 grid = grid_of((T * k + 3) / 4), thr(256);
+  const dim3 thr(256), grid = grid_of((T * k + 3) / 4), rest = grid_of((rows + 255) / 256);
+#define FP4Q_GRADIENT(F, V)                                                                        \
+  do {                                                                                             \
+    if (T > 0) hipLaunchKernelGGL((k_combine_backward<F, V>), grid, thr, 0, stream, p);            \
+    if (named && rows > 0) hipLaunchKernelGGL((k_zero_unnamed<F, V>), rest, thr, 0, stream, p);    \
+  } while (0)
   if (f32) {
-    if (vec) hipLaunchKernelGGL((k_combine_backward<true, 8>), grid, thr, 0, stream, p);
-    else hipLaunchKernelGGL((k_combine_backward<true, 1>), grid, thr, 0, stream, p);
+    if (vec) FP4Q_GRADIENT(true, 8);
+    else FP4Q_GRADIENT(true, 1);
   } else {
-    if (vec) hipLaunchKernelGGL((k_combine_backward<false, 8>), grid, thr, 0, stream, p);
-    else hipLaunchKernelGGL((k_combine_backward<false, 1>), grid, thr, 0, stream, p);
+    if (vec) FP4Q_GRADIENT(false, 8);
+    else FP4Q_GRADIENT(false, 1);
   }
+#undef FP4Q_GRADIENT
 }
 
 }  // namespace fp4q

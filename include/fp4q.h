@@ -828,8 +828,10 @@ int fp4q_route_backward(const void* logits, fp4q_dtype_t dtype, int64_t tokens,
  *              nothing and has d_weights 0
  *   weights, d_weights   f32 [tokens, k]
  * Sums are FP32 in the order of j.  d_y's rows that row_of does not name
- * are not written.  FP4Q_ERR_UNSUPPORTED: k above 128, tokens * k or
- * tokens * cols / 8 not below 2^31. */
+ * are not written by fp4q_combine_backward; fp4q_combine_backward_zeroed sets
+ * them to 0 (workspace: device scratch of ..._workspace_bytes(rows) bytes,
+ * 4-byte aligned, no initialisation).  FP4Q_ERR_UNSUPPORTED: k above 128, tokens * k or
+ * tokens * cols / 8 not below 2^31, with _zeroed rows not below 2^31 either. */
 int fp4q_combine(fp4q_dtype_t dtype, const void* y, int64_t rows, int64_t cols, int64_t ldy,
                  const int32_t* row_of, const float* weights, int64_t tokens, int32_t k,
                  void* out, int64_t ldo, void* stream);
@@ -838,6 +840,14 @@ int fp4q_combine_backward(fp4q_dtype_t dtype, const void* y, int64_t rows, int64
                           int64_t ldy, const int32_t* row_of, const float* weights,
                           int64_t tokens, int32_t k, const void* d_out, int64_t ldo, void* d_y,
                           int64_t lddy, float* d_weights, void* stream);
+
+size_t fp4q_combine_backward_zeroed_workspace_bytes(int64_t rows);
+
+int fp4q_combine_backward_zeroed(fp4q_dtype_t dtype, const void* y, int64_t rows, int64_t cols,
+                                 int64_t ldy, const int32_t* row_of, const float* weights,
+                                 int64_t tokens, int32_t k, const void* d_out, int64_t ldo, void* d_y,
+                                 int64_t lddy, float* d_weights, void* workspace,
+                                 size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
  * Exact three-way MXFP4 error decomposition ("Decomposing MXFP4

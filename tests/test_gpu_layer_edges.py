@@ -111,3 +111,64 @@ def test_a_later_token_that_is_not_finite_does_not_reach_earlier_rows(fmt, n):
         got.append(fq.kv_attention(fmt, *where, q, n, n, t, t)[:n - 1])
     assert torch.isfinite(got[0]).all()
     assert torch.equal(got[0], got[1]) and torch.equal(got[0], got[2])
+
+
+# ---- the combination ----------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,k,rows,N", [(3, 2, 6, 64), (3, 2, 9, 64), (0, 2, 5, 8), (1, 1, 1, 3), (5, 4, 700, 96),
+                                        (200, 8, 1600, 130), (200, 8, 5000, 128), (70, 3, 100, 1)])
+def test_gradient_rows_that_nothing_names_are_zero(dtype, T, k, rows, N):
+    """Rows of padded expert buffers, and those that an entry outside the rows
+    leaves without a name; what the freed memory held (old indices among it)
+    does not matter."""
+    need_gpu()
+    say(f"unnamed {dtype} T{T} k{k} rows {rows} N{N}")
+    g = torch.Generator().manual_seed(rows + N)
+    y = torch.randn(rows, N, generator=g).to(dtype).cuda()
+    do = torch.randn(T, N, generator=g).to(dtype).cuda()
+    w = torch.rand(T, k, generator=g).cuda()
+    row_of = torch.full((T * k,), -1, dtype=torch.int32)
+    row_of[:min(rows, T * k)] = torch.randperm(rows, generator=g)[:T * k].int()
+    for drop in (0, T * k // 3):
+        r = row_of.clone()
+        r[:drop] = torch.tensor([-1, rows, 2 ** 31 - 1])[torch.arange(drop) % 3].int()
+        r = r.view(T, k).cuda()
+        named = r[(r >= 0) & (r < rows)].long()
+        want = torch.zeros_like(y)
+        t = torch.arange(T * k, device="cuda").view(T, k)[(r >= 0) & (r < rows)] // max(k, 1)
+        want[named] = (w.reshape(-1)[((r >= 0) & (r < rows)).reshape(-1)][:, None] * do[t].float()).to(dtype)
+        for fill in (0xFF, 0, 1):
+            junk = [torch.full((n,), fill, dtype=torch.uint8, device="cuda")
+                    for n in (y.untyped_storage().nbytes(), rows * 4, T * k * 4) for _ in range(2)]
+            torch.cuda.synchronize()
+            del junk
+            d_y, d_w = fq.combine_backward(y, r, w, do)
+            assert torch.equal(d_y, want), fill
+            into = torch.full_like(y, 3.0)
+            fq.combine_backward_into(y, r, w, do, into, torch.empty_like(w))
+            want_into = torch.full_like(y, 3.0)
+            want_into[named] = want[named]
+            assert torch.equal(into, want_into)
+
+
+def test_unnamed_gradient_rows_keep_strides():
+    """The C call on rows with a stride, from an address that is not a vector's."""
+    need_gpu()
+    from fp4_w4a4_quantized_amd import binding
+    L, p = binding.lib(), (lambda t: t.data_ptr())
+    y, do = torch.randn(300, 40, device="cuda"), torch.randn(10, 40, device="cuda")
+    row_of = (29 * torch.arange(10, device="cuda")).int().view(10, 1)
+    w, dw = torch.rand(10, 1, device="cuda"), torch.empty(10, 1, device="cuda")
+    for c0 in (0, 1, 4):
+        big = torch.full((300, 56), 7.0, device="cuda")
+        d = big[:, c0:c0 + 40]
+        ws = torch.full((300,), 5, dtype=torch.int32, device="cuda")
+        torch.cuda.synchronize()
+        assert L.fp4q_combine_backward_zeroed(0, p(y), 300, 40, 40, p(row_of), p(w), 10, 1, p(do), 40, p(d), 56,
+                                              p(dw), p(ws), 1200, None) == 0
+        torch.cuda.synchronize()
+        want = torch.zeros(300, 40, device="cuda")
+        want[row_of[:, 0].long()] = w * do
+        assert torch.equal(d, want)
+        assert torch.all(big[:, :c0] == 7.0) and torch.all(big[:, c0 + 40:] == 7.0)
