@@ -285,8 +285,8 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs p) {
   int n = 0;
   if (s < p.slots && row >= p.off[0] && row < p.off[p.B]) {
     const int b = kv_sequence(p.off, p.B, row);
-    const int tile = ((int)(row - p.off[b]) * p.G + hh % p.G) / p.tile;
-    if (tile < p.tiles) n = min(active_splits(p, tile_range(p, b, tile * p.tile)), p.splits);
+    const int qi = (int)(row - p.off[b]), tile = (qi * p.G + hh % p.G) / p.tile;
+    if (qi < p.max_new) n = min(active_splits(p, tile_range(p, b, tile * p.tile)), p.splits);
   }
   float m = -__builtin_inff(), z = 0.0f;
   v4f o = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -317,8 +317,8 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs p) {
       for (int r = 0; r < 4; ++r) o[r] = __builtin_fmaf(a[r], fa, o[r] * f);
     }
   }
-  // (a row past the last sequence's gives 0, one past max_new is left out)
-  if (n == 0 && !(s < p.slots && row >= p.off[p.B])) return;
+  if (s >= p.slots) return;
+  // (n = 0: a row past the last sequence's or past max_new gives 0)
   const float f = z > 0.0f ? (FMT == FP4Q_NVFP4 ? p.vts[hh / p.G] : 1.0f) / z : 0.0f;
 #pragma unroll
   for (int r = 0; r < 4; ++r) o[r] *= f;
@@ -416,6 +416,7 @@ void launch_attention(int fmt, const uint8_t* cache, int64_t n_pages, int page_s
   p.q = q;
   p.ldq = ldq;
   p.rows = (int)rows;
+  p.max_new = (int)max_new;
   p.window = window;
   p.scale2 = scale * 1.44269504088896340736f;
   p.kts = kts;
@@ -427,7 +428,6 @@ void launch_attention(int fmt, const uint8_t* cache, int64_t n_pages, int page_s
   p.splits = pl.splits;
   p.tile = pl.tile;
   p.step = pl.step;
-  p.tiles = pl.tiles;
   p.join = pl.join;
   p.slots = rows * H * G;
   p.part_o = static_cast<float*>(ws);

@@ -20,6 +20,7 @@ struct AttnArgs {
   const uint16_t* q;
   int64_t ldq;
   int rows;
+  int max_new;  // new tokens of a sequence that are attended for (further ones give 0)
   int window;
   float scale2;  // softmax scale * log2(e)
   const float* kts;
@@ -31,7 +32,6 @@ struct AttnArgs {
   int splits;  // splits launched; 1: the kernel writes y itself
   int tile;    // rows of a workgroup
   int step;    // keys of a step of its kernel: splits begin at its multiples
-  int tiles;   // row tiles launched
   int join;    // groups of lanes that join a row's splits
   int64_t slots;  // rows * heads: partial results of one split
   float2* part_ms;  // [splits][slots] (maximum in log2 units, sum)
@@ -61,11 +61,11 @@ struct Range {
   int seen, lo, hi, rows;
 };
 
-// New-token rows of sequence b times the heads of a kv head (none that the
-// packed tensors do not have, whatever the offsets say).
+// New-token rows of sequence b times the heads of a kv head (none past max_new,
+// and none that the packed tensors do not have, whatever the offsets say).
 __device__ __forceinline__ int tile_rows(const AttnArgs& p, int b) {
   const int r0 = p.off[b], r1 = min(p.off[b + 1], p.rows);
-  return r0 < 0 || r1 <= r0 ? 0 : (r1 - r0) * p.G;
+  return r0 < 0 || r1 <= r0 ? 0 : min(r1 - r0, p.max_new) * p.G;
 }
 
 __device__ __forceinline__ Range tile_range(const AttnArgs& p, int b, int row0) {
@@ -393,15 +393,19 @@ __device__ __forceinline__ void store_out(const AttnArgs& p, int64_t at, v4f t) 
   }
 }
 
-// Rows past the last sequence's give 0 (of one pass; the join does it otherwise):
-// workgroup (b, h) takes every B-th, for the heads of kv head h.
+// Rows past the last sequence's and past max_new of a sequence give 0 (of one
+// pass; the join does it otherwise): workgroup (b, h) takes every B-th of the
+// first kind and b's of the second, for the heads of kv head h.
 template <int D, int THREADS>
 __device__ __forceinline__ void zero_rest(const AttnArgs& p, int b, int h) {
   if (p.splits > 1 || blockIdx.y > 0) return;
-  const int end = max(p.off[p.B], 0);
-  for (int64_t row = (int64_t)end + b; row < p.rows; row += p.B)
+  auto zero = [&](int64_t row) {
     for (int i = threadIdx.x * 4; i < p.G * D; i += THREADS * 4)
       store_out(p, row * p.ldy + (int64_t)h * p.G * D + i, v4f{0.0f, 0.0f, 0.0f, 0.0f});
+  };
+  for (int64_t row = (int64_t)max(p.off[p.B], 0) + b; row < p.rows; row += p.B) zero(row);
+  const int64_t end = min(p.off[b + 1], p.rows);
+  for (int64_t row = (int64_t)max(p.off[b], 0) + p.max_new; row < end; ++row) zero(row);
 }
 
 }  // namespace

@@ -727,7 +727,8 @@ int fp4q_kv_read(fp4q_format_t fmt, const uint8_t* cache, int64_t n_pages, int32
  *
  * over the keys j of the row's sequence with j <= position(r), and, with
  * window > 0, j > position(r) - window; g = h / (heads / kv_heads).  A row
- * that sees no key gives 0, and so does a row past offsets[batch] (padding).
+ * that sees no key gives 0, and so does a row past offsets[batch] (padding)
+ * or past max_new of its sequence.
  * What stands in the cache outside the keys that the new tokens see (NaN
  * scales included) does not reach the result, nor does a later token's value
  * that fp4q_kv_append stored: of MXFP4 values, block scales above 2^125 count
@@ -738,8 +739,7 @@ int fp4q_kv_read(fp4q_format_t fmt, const uint8_t* cache, int64_t n_pages, int32
  *   q              bf16 [rows, heads, dim], row stride ldq (a multiple of 8,
  *                  16-byte aligned)
  *   max_new, max_len   host bounds: no sequence has more new tokens, or a
- *                  greater length (they size the launch; rows or keys past
- *                  them are left out)
+ *                  greater length (they size the launch)
  *   window         0: none
  *   scale          of the scores, > 0 (dim^-0.5 as a rule)
  *   y              out f32 or bf16 [rows, heads, dim], row stride ldy (a

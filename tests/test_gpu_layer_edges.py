@@ -8,7 +8,7 @@ import torch
 import fp4_w4a4_quantized_amd as fq
 from gpu_helpers import need_gpu, say
 from oracle import layer
-from test_gpu_kv_attention import FMTS, dev, make
+from test_gpu_kv_attention import FMTS, attend, check, check_close, dev, make
 from test_gpu_route_combine import check_route
 
 pytestmark = pytest.mark.gpu
@@ -172,3 +172,32 @@ def test_unnamed_gradient_rows_keep_strides():
         want[row_of[:, 0].long()] = w * do
         assert torch.equal(d, want)
         assert torch.all(big[:, :c0] == 7.0) and torch.all(big[:, c0 + 40:] == 7.0)
+
+
+# ---- attention ----------------------------------------------------------------
+
+def attend_up_to(c, max_new, max_len, y_dtype=fq.OUT_BF16, window=0):
+    t = None if c["t"] is None else dev(c["t"])
+    return fq.kv_attention(c["fmt"], dev(c["cache"]), c["page"], dev(c["off"]), dev(c["table"]), dev(c["lens"]),
+                           dev(c["q"], torch.bfloat16), max_new, max_len, t, t, window=window, y_dtype=y_dtype)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("n,lens,G,D,max_new", [([3, 1, 2], [300, 9, 70], 4, 128, 1),       # one pass, few rows
+                                                ([1, 4, 3], [9000, 4, 900], 5, 64, 2),      # split keys
+                                                ([9, 1, 6], [700, 1, 9], 6, 128, 5),        # 30 rows of a head
+                                                ([40, 17, 2], [40, 30, 2], 3, 256, 16),     # row tiles
+                                                ([300, 0, 5], [1500, 0, 7], 4, 64, 100)])   # the same, split keys
+def test_rows_past_max_new_give_zero(fmt, n, lens, G, D, max_new):
+    need_gpu()
+    say(f"max_new fmt {fmt} n {n} lens {lens} G {G} D {D} max_new {max_new}")
+    c = make(fmt, n, lens, G=G, H=2, D=D, seed=sum(n))
+    within = np.concatenate([np.arange(x) < max_new for x in n])
+    for y_dtype in (fq.OUT_BF16, fq.OUT_F32):
+        nb = len(c["q"]) * 2 * G * D * 4
+        torch.full((4 * nb,), 255, dtype=torch.uint8, device="cuda")  # what freed memory may hold
+        got = attend_up_to(c, max_new, max(lens), y_dtype)
+        assert torch.all(got[torch.from_numpy(~within).cuda()] == 0)
+        g, o, tol = check(c, got)
+        tol = tol + (2.0 ** -8 if y_dtype == fq.OUT_BF16 else 2.0 ** -23) * (np.abs(o) + tol) + 1e-30
+        assert np.all((np.abs(g - o) <= tol)[within])
