@@ -411,7 +411,8 @@ void launch_attention(int fmt, const uint8_t* cache, int64_t n_pages, int page_s
   p.B = B;
   p.table = table;
   p.ldt = ldt;
-  p.table_cols = table_cols;
+  const int64_t held = table_cols << page_shift;
+  p.cap = (int)(held < max_len ? held : max_len);
   p.lens = lens;
   p.q = q;
   p.ldq = ldq;

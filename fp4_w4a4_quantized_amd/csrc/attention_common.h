@@ -15,7 +15,8 @@ struct AttnArgs {
   const int32_t* off;
   int B;
   const int32_t* table;
-  int64_t ldt, table_cols;
+  int64_t ldt;
+  int cap;  // keys from here on are not seen: the table's end, or max_len
   const int32_t* lens;
   const uint16_t* q;
   int64_t ldq;
@@ -72,8 +73,7 @@ __device__ __forceinline__ Range tile_range(const AttnArgs& p, int b, int row0) 
   Range r;
   r.r0 = p.off[b];
   r.n = p.off[b + 1] - p.off[b];
-  const int64_t cap = p.table_cols << p.page_shift;
-  const int len = (int)min((int64_t)max(p.lens[b], 0), cap);
+  const int len = min(max(p.lens[b], 0), p.cap);
   r.first = p.lens[b] - r.n;
   r.rows = tile_rows(p, b);
   const int last_row = min(r.rows, row0 + p.tile) - 1;

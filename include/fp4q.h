@@ -739,7 +739,8 @@ int fp4q_kv_read(fp4q_format_t fmt, const uint8_t* cache, int64_t n_pages, int32
  *   q              bf16 [rows, heads, dim], row stride ldq (a multiple of 8,
  *                  16-byte aligned)
  *   max_new, max_len   host bounds: no sequence has more new tokens, or a
- *                  greater length (they size the launch)
+ *                  greater length (they size the launch; keys from
+ *                  position max_len on are not seen)
  *   window         0: none
  *   scale          of the scores, > 0 (dim^-0.5 as a rule)
  *   y              out f32 or bf16 [rows, heads, dim], row stride ldy (a

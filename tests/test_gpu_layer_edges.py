@@ -201,3 +201,17 @@ def test_rows_past_max_new_give_zero(fmt, n, lens, G, D, max_new):
         g, o, tol = check(c, got)
         tol = tol + (2.0 ** -8 if y_dtype == fq.OUT_BF16 else 2.0 ** -23) * (np.abs(o) + tol) + 1e-30
         assert np.all((np.abs(g - o) <= tol)[within])
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("n,lens,G,D,pages", [([1, 1], [300, 40], 4, 128, 6), ([2, 1], [5000, 900], 3, 64, 190),
+                                              ([70, 9], [150, 9], 4, 64, 5), ([90, 3], [1900, 800], 2, 256, 77)])
+@pytest.mark.parametrize("window", [0, 60])
+def test_keys_past_max_len_are_not_seen(fmt, n, lens, G, D, pages, window):
+    """Whatever the split: as if the table ended there."""
+    need_gpu()
+    say(f"max_len fmt {fmt} n {n} lens {lens} G {G} D {D} pages {pages} window {window}")
+    c = make(fmt, n, lens, G=G, H=2, D=D, page=16, seed=pages)
+    got = attend_up_to(c, max(n), 16 * pages, window=window)
+    c["table"] = c["table"][:, :pages]
+    check_close(c, got, window)
