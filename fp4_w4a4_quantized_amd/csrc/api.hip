@@ -902,7 +902,8 @@ size_t fp4q_kv_attention_workspace_bytes(fp4q_format_t fmt, int64_t rows, int32_
                                          int64_t max_new, int64_t max_len, int32_t window) {
   if (!fmt_ok(fmt) || rows <= 0 || heads < 1 || kv_heads < 1 || heads % kv_heads != 0 ||
       batch < 1 || max_new < 1 || max_len < 0 || window < 0 ||
-      (dim != 64 && dim != 128 && dim != 256))
+      (dim != 64 && dim != 128 && dim != 256) ||
+      !fp4q::attention_shape_ok(rows, dim, batch, kv_heads, heads / kv_heads, max_new, max_len, window))
     return 0;
   return fp4q::attention_workspace_bytes(rows, dim, batch, kv_heads, heads / kv_heads, max_new,
                                          max_len, window);
@@ -925,9 +926,7 @@ int fp4q_kv_attention(fp4q_format_t fmt, const uint8_t* cache, int64_t n_pages, 
   if (rows == 0) return FP4Q_OK;
   const int64_t cols = (int64_t)heads * dim;
   if (max_new < 1 || !packed_ok(q, ldq, cols) || !packed_ok(y, ldy, cols)) return FP4Q_ERR_INVALID;
-  if (heads / kv_heads > 128 || rows >= ((int64_t)1 << 31) / heads ||
-      max_new >= ((int64_t)1 << 31) / heads || max_len >= ((int64_t)1 << 31) ||
-      !fp4q::attention_shape_ok(dim, batch, kv_heads, heads / kv_heads, max_new, max_len, window))
+  if (!fp4q::attention_shape_ok(rows, dim, batch, kv_heads, heads / kv_heads, max_new, max_len, window))
     return FP4Q_ERR_UNSUPPORTED;
   const size_t need = fp4q_kv_attention_workspace_bytes(fmt, rows, heads, kv_heads, dim, batch,
                                                         max_new, max_len, window);

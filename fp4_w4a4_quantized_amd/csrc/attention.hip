@@ -60,7 +60,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 4 : D == 128 && NC == 1 && WA
   const int split = blockIdx.z;
   if (split >= active_splits(p, rg)) return;
   const int k0 = rg.lo + split * p.chunk;
-  const int k1 = min(rg.hi, k0 + p.chunk);
+  const int k1 = split_end(p, rg, k0);
 
   const int page = 1 << p.page_shift;
   const int32_t* table = p.table + b * p.ldt;
@@ -345,7 +345,8 @@ Plan attn_plan(int D, int B, int H, int G, int64_t max_new, int64_t max_len, int
     const int64_t seen = (int64_t)window + (p.wide ? (p.tile + G - 1) / G + 1 : max_new) + p.step;
     keys = keys < seen ? keys : seen;
   }
-  const int64_t groups = (int64_t)B * H * p.tiles;
+  int64_t groups = (int64_t)B * H * p.tiles;
+  if (groups > (1 << 30)) groups = 1 << 30;  // (keys * groups stays below 2^63)
   // few short (sequence, head)s: eight waves on the keys of each, none to join
   p.waves = !p.wide && groups <= 256 && keys <= 2048 && p.nc == 1 && D <= 128 ? 8 : 4;
   const int64_t want = p.wide ? 512 : 4096;
@@ -383,9 +384,16 @@ void launch(const AttnArgs& p, const Plan& pl, int H, int B, hipStream_t stream)
 
 }  // namespace
 
-bool attention_shape_ok(int D, int B, int H, int G, int64_t max_new, int64_t max_len, int window) {
+// Sizes that the launch can hold.  (The kernels look up to 2^12 keys past the
+// last in 32 bits.)
+bool attention_shape_ok(int64_t rows, int D, int B, int H, int G, int64_t max_new, int64_t max_len,
+                        int window) {
+  const int64_t heads = (int64_t)H * G, most = (int64_t)1 << 31;
+  if (G > 128 || B > 65535 || (int64_t)B * H >= (1 << 22) || rows >= most / heads ||
+      max_new >= most / heads || max_len > most - 4096)
+    return false;
   const Plan pl = attn_plan(D, B, H, G, max_new, max_len, window);
-  return B <= 65535 && (int64_t)H * pl.tiles <= 65535 && pl.splits <= 65535 && (int64_t)B * H < (1 << 22);
+  return (int64_t)H * pl.tiles <= 65535 && pl.splits <= 65535;
 }
 
 size_t attention_workspace_bytes(int64_t rows, int D, int B, int H, int G, int64_t max_new,

@@ -84,9 +84,14 @@ __device__ __forceinline__ Range tile_range(const AttnArgs& p, int b, int row0) 
   return r;
 }
 
+// Splits of the tile's keys, and where one that begins at k0 ends.
 __device__ __forceinline__ int active_splits(const AttnArgs& p, const Range& r) {
   const int keys = r.hi - r.lo;
-  return keys > 0 ? (keys + p.chunk - 1) / p.chunk : 1;
+  return keys > 0 ? (keys - 1) / p.chunk + 1 : 1;  // (keys + chunk may pass 2^31)
+}
+
+__device__ __forceinline__ int split_end(const AttnArgs& p, const Range& r, int k0) {
+  return r.hi - k0 > p.chunk ? k0 + p.chunk : r.hi;
 }
 
 template <int FMT> struct Num;

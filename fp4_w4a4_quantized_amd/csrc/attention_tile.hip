@@ -121,7 +121,7 @@ __global__ __launch_bounds__(64 * WAVES)
   const int split = blockIdx.z;
   if (split >= active_splits(p, rg)) return;
   const int k0 = rg.lo + split * p.chunk;
-  const int k1 = min(rg.hi, k0 + p.chunk);
+  const int k1 = split_end(p, rg, k0);
   const int page = 1 << p.page_shift;
   const TablePtr table = (TablePtr)(uintptr_t)(p.table + b * p.ldt);
   const uint32_t n_pages = (uint32_t)min(p.n_pages, (int64_t)0x7FFFFFFF);

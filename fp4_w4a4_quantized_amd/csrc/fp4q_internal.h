@@ -144,7 +144,8 @@ void launch_kv_copy(bool append, int fmt, uint8_t* cache, int64_t n_pages, int p
                     int D, const int32_t* off, int B, const int32_t* table, int64_t ldt, int64_t table_cols,
                     const int32_t* lens, int64_t rows, uint16_t* k, int64_t ldk, uint16_t* v,
                     int64_t ldv, const float* kts, const float* vts, hipStream_t stream);
-bool attention_shape_ok(int D, int B, int H, int G, int64_t max_new, int64_t max_len, int window);
+bool attention_shape_ok(int64_t rows, int D, int B, int H, int G, int64_t max_new, int64_t max_len,
+                        int window);
 size_t attention_workspace_bytes(int64_t rows, int D, int B, int H, int G, int64_t max_new,
                                  int64_t max_len, int window);
 void launch_attention(int fmt, const uint8_t* cache, int64_t n_pages, int page_shift, int H, int D,

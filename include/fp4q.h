@@ -756,7 +756,8 @@ int fp4q_kv_read(fp4q_format_t fmt, const uint8_t* cache, int64_t n_pages, int32
  * held in f16 relative to its row's largest magnitude (bf16 for MXFP4).
  * heads % kv_heads == 0; FP4Q_ERR_UNSUPPORTED: another dim or page, more
  * than 128 heads on one kv head, batch above 65535, batch * kv_heads not
- * below 2^22, or rows * heads not below 2^31. */
+ * below 2^22, rows * heads or max_new * heads not below 2^31, or max_len
+ * above 2^31 - 4096 (the workspace query gives 0 for these). */
 size_t fp4q_kv_attention_workspace_bytes(fp4q_format_t fmt, int64_t rows, int32_t heads,
                                          int32_t kv_heads, int32_t dim, int32_t batch,
                                          int64_t max_new, int64_t max_len, int32_t window);

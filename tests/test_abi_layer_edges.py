@@ -41,3 +41,31 @@ def test_zeroed_combination_gradient(L):
         assert f(**over) == WORKSPACE, over
     assert f(T=0, rows=0, dy=None, ws=None, wsb=0) == 0
     assert passes(f) and passes(lambda: f(T=0, y=None, row=None, w=None, do=None, dw=None))
+
+
+def attention(L, rows=5, heads=4, kv_heads=2, dim=128, batch=2, max_new=1, max_len=40, window=0, page=16, cols=3):
+    """The call with enough workspace, and what it asks for."""
+    need = L.fp4q_kv_attention_workspace_bytes(0, rows, heads, kv_heads, dim, batch, max_new, max_len, window)
+    return need, lambda: L.fp4q_kv_attention(0, A, 4, page, kv_heads, dim, A, batch, A, cols, cols, A, rows, A,
+                                             heads * dim, heads, max_new, max_len, window, 0.1, A, A, B, 1,
+                                             heads * dim, A, need, None)
+
+
+def test_lengths_up_to_the_limit(L):
+    """Up to 2^31 - 4096 keys; the kernels' 32-bit key numbers go a little past
+    the last one."""
+    long = (1 << 31) - 4096
+    for over in (dict(), dict(max_new=40, rows=40), dict(batch=1, kv_heads=1, dim=64)):
+        need, call = attention(L, max_len=long, page=1024, cols=(1 << 21) - 1, **over)
+        assert need > 0 and passes(call), over
+        for more in (1, 4095):
+            need, call = attention(L, max_len=long + more, page=1024, cols=(1 << 21) - 1, **over)
+            assert need == 0 and call() == UNSUPPORTED, (over, more)
+
+
+@pytest.mark.parametrize("over", [dict(max_len=1 << 60), dict(max_new=1 << 60), dict(rows=1 << 60),
+                                  dict(batch=65536), dict(batch=1 << 12, kv_heads=1 << 10, heads=1 << 10),
+                                  dict(heads=258)])
+def test_no_workspace_for_what_is_refused(L, over):
+    need, call = attention(L, **over)
+    assert need == 0 and call() == UNSUPPORTED

@@ -215,3 +215,22 @@ def test_keys_past_max_len_are_not_seen(fmt, n, lens, G, D, pages, window):
     got = attend_up_to(c, max(n), 16 * pages, window=window)
     c["table"] = c["table"][:, :pages]
     check_close(c, got, window)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("n,D,G,window", [(1, 128, 4, 0), (1, 64, 4, 700), (6, 128, 4, 0), (40, 64, 2, 64),
+                                          (30, 256, 2, 1000)])
+def test_the_longest_sequence(fmt, n, D, G, window):
+    """The last page of a sequence of 2^31 - 4096 tokens, the others gone: what
+    the page's tokens give by themselves, wherever they stand."""
+    need_gpu()
+    say(f"longest fmt {fmt} n {n} D {D} G {G} window {window}")
+    long, page = 2 ** 31 - 4096, 1024
+    c = make(fmt, [n], [page], G=G, H=1, D=D, page=page, seed=n)
+    t = None if c["t"] is None else dev(c["t"])
+    table = torch.full((1, 2 ** 21 - 1), -1, dtype=torch.int32, device="cuda")
+    table[0, long // page - 1] = int(c["table"][0, 0])
+    got = fq.kv_attention(fmt, dev(c["cache"]), page, dev(c["off"]), table,
+                          torch.tensor([long], dtype=torch.int32, device="cuda"), dev(c["q"], torch.bfloat16), n, long,
+                          t, t, window=window)
+    check_close(c, got, window)
