@@ -329,7 +329,8 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs p) {
 // query and the launch agree.
 struct Plan {
   bool wide;  // many rows: k_attn_tile
-  int nc, waves, tile, step, tiles, chunk, splits, join;
+  int nc, waves, tile, step, chunk, splits, join;
+  int64_t tiles;
 };
 
 Plan attn_plan(int D, int B, int H, int G, int64_t max_new, int64_t max_len, int window) {
@@ -339,13 +340,13 @@ Plan attn_plan(int D, int B, int H, int G, int64_t max_new, int64_t max_len, int
   p.nc = rows > ROWS && D <= 128 ? 2 : 1;
   p.tile = p.wide ? (rows > 128 && D <= 128 ? 256 : 128) : ROWS * p.nc;
   p.step = p.wide ? 64 : KEYS;
-  p.tiles = (int)((rows + p.tile - 1) / p.tile);
+  p.tiles = (rows + p.tile - 1) / p.tile;
   int64_t keys = max_len;
   if (window > 0) {
     const int64_t seen = (int64_t)window + (p.wide ? (p.tile + G - 1) / G + 1 : max_new) + p.step;
     keys = keys < seen ? keys : seen;
   }
-  int64_t groups = (int64_t)B * H * p.tiles;
+  int64_t groups = B * (int64_t)H * p.tiles;
   if (groups > (1 << 30)) groups = 1 << 30;  // (keys * groups stays below 2^63)
   // few short (sequence, head)s: eight waves on the keys of each, none to join
   p.waves = !p.wide && groups <= 256 && keys <= 2048 && p.nc == 1 && D <= 128 ? 8 : 4;
@@ -367,7 +368,7 @@ template <int FMT, int D>
 void launch(const AttnArgs& p, const Plan& pl, int H, int B, hipStream_t stream) {
   const dim3 grid((unsigned)(B * H), (unsigned)pl.tiles, (unsigned)pl.splits), thr(64 * pl.waves);
   if (pl.wide) {
-    launch_attention_tile(FMT, D, p, pl.tiles, B, stream);
+    launch_attention_tile(FMT, D, p, (int)pl.tiles, B, stream);
   } else if constexpr (D <= 128) {
     if (pl.nc == 2) hipLaunchKernelGGL((k_attn_split<FMT, D, 2, 4>), grid, thr, 0, stream, p);
     else if (pl.waves == 4) hipLaunchKernelGGL((k_attn_split<FMT, D, 1, 4>), grid, thr, 0, stream, p);
@@ -393,7 +394,7 @@ bool attention_shape_ok(int64_t rows, int D, int B, int H, int G, int64_t max_ne
       max_new >= most / heads || max_len > most - 4096)
     return false;
   const Plan pl = attn_plan(D, B, H, G, max_new, max_len, window);
-  return (int64_t)H * pl.tiles <= 65535 && pl.splits <= 65535;
+  return pl.tiles <= 65535 && pl.splits <= 65535;  // (the grid's second and third dimension)
 }
 
 size_t attention_workspace_bytes(int64_t rows, int D, int B, int H, int G, int64_t max_new,

@@ -701,8 +701,9 @@ int fp4q_grouped_gemm_gather(fp4q_format_t fmt, fp4q_layout_t w_layout, int64_t 
  * cache.  fp4q_kv_read writes the values that stand there for the same
  * rows: bf16 of (e2m1 * scale) * t (NVFP4) or of e2m1 * 2^e (MXFP4).
  * rows = offsets[batch] (further rows: not stored, read as zeros).
- * FP4Q_ERR_UNSUPPORTED: another dim or page, or rows * kv_heads * dim / 32
- * not below 2^31.  No workspace.
+ * FP4Q_ERR_UNSUPPORTED: another dim or page, kv_heads not below 2^20, a
+ * table of 2^31 tokens or more, or rows * kv_heads * dim / 32 not below 2^31.
+ * No workspace.
  * ------------------------------------------------------------------------ */
 size_t fp4q_kv_page_bytes(fp4q_format_t fmt, int32_t page, int32_t dim); /* 0: not supported */
 
@@ -754,9 +755,10 @@ int fp4q_kv_read(fp4q_format_t fmt, const uint8_t* cache, int64_t n_pages, int32
  * scores, their maximum and sums and the output are FP32, the weights are
  * rounded once to f16 or bf16 before they meet the values.  For NVFP4 q is
  * held in f16 relative to its row's largest magnitude (bf16 for MXFP4).
- * heads % kv_heads == 0; FP4Q_ERR_UNSUPPORTED: another dim or page, more
+ * heads % kv_heads == 0; FP4Q_ERR_UNSUPPORTED: as for the cache, more
  * than 128 heads on one kv head, batch above 65535, batch * kv_heads not
- * below 2^22, rows * heads or max_new * heads not below 2^31, or max_len
+ * below 2^22, rows * heads or max_new * heads not below 2^31, max_new *
+ * heads / kv_heads above 65535 * 256 (dim 256: 65535 * 128), or max_len
  * above 2^31 - 4096 (the workspace query gives 0 for these). */
 size_t fp4q_kv_attention_workspace_bytes(fp4q_format_t fmt, int64_t rows, int32_t heads,
                                          int32_t kv_heads, int32_t dim, int32_t batch,

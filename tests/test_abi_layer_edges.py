@@ -69,3 +69,20 @@ def test_lengths_up_to_the_limit(L):
 def test_no_workspace_for_what_is_refused(L, over):
     need, call = attention(L, **over)
     assert need == 0 and call() == UNSUPPORTED
+
+
+@pytest.mark.parametrize("dim,tile", [(64, 256), (128, 256), (256, 128)])
+def test_long_prompts_of_many_heads(L, dim, tile):
+    """The row tiles of one kv head are what the grid bounds, not times the kv
+    heads: 131072 new tokens of 128 heads on 8, and up to 65535 tiles."""
+    for n in (65536, 131072):
+        _, call = attention(L, rows=n, heads=128, kv_heads=8, dim=dim, batch=1, max_new=n, max_len=n, page=64,
+                            cols=2048)
+        assert passes(call), n
+    for heads, kv_heads in ((16, 1), (32, 2)):
+        last = 65535 * tile // 16
+        _, call = attention(L, rows=8, heads=heads, kv_heads=kv_heads, dim=dim, batch=1, max_new=last, max_len=last)
+        assert passes(call)
+        need, call = attention(L, rows=8, heads=heads, kv_heads=kv_heads, dim=dim, batch=1, max_new=last + 1,
+                               max_len=last + 1)
+        assert need == 0 and call() == UNSUPPORTED

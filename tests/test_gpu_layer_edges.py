@@ -234,3 +234,26 @@ def test_the_longest_sequence(fmt, n, D, G, window):
                           torch.tensor([long], dtype=torch.int32, device="cuda"), dev(c["q"], torch.bfloat16), n, long,
                           t, t, window=window)
     check_close(c, got, window)
+
+
+def test_many_row_tiles_of_many_heads():
+    """16 row tiles of 4096 kv heads (their product is past 65535); rows of the
+    first and last heads and tiles against the plain form."""
+    need_gpu()
+    H, D, page, n, window = 4096, 64, 16, 4081, 20
+    say("row tiles of many heads")
+    g = torch.Generator(device="cuda").manual_seed(1)
+    pages = -(-n // page)
+    k = torch.randn(n, 1, D, generator=g, device="cuda").to(torch.bfloat16).expand(n, H, D)
+    k = k * (1 + torch.arange(H, device="cuda") % 3)[None, :, None].to(torch.bfloat16)
+    cache = fq.kv_cache(1, pages, page, H, D)
+    off = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    lens = off[1:].clone()
+    table = torch.randperm(pages, generator=g, device="cuda").int().view(1, pages)
+    fq.kv_append(1, cache, page, off, table, lens, k, k)
+    q = torch.randn(n, H, D, generator=g, device="cuda").to(torch.bfloat16)
+    got = fq.kv_attention(1, cache, page, off, table, lens, q, n, n, window=window)
+    for h in (0, 1, 2047, 4094, 4095):
+        c = dict(fmt=1, cache=cache[:, h:h + 1].cpu().numpy(), page=page, off=np.array([0, n]), D=D, t=None,
+                 table=table.cpu().numpy(), lens=np.array([n]), q=q[:, h:h + 1].double().cpu().numpy())
+        check_close(c, got[:, h:h + 1], window)
