@@ -111,7 +111,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 4 : D == 128 && NC == 1 && WA
     const int qi = rr / p.G, hh = h * p.G + (rr - qi * p.G);
     load_q<FMT, D>(p.q + (rg.r0 + qi) * p.ldq + hh * D, g, c0, qf[n], cf[n]);
     see_hi[n] = min(rg.hi, rg.first + qi + 1);
-    see_lo[n] = p.window > 0 ? rg.first + qi - p.window + 1 : 0;
+    see_lo[n] = first_key(p, rg.first + qi);
     m[n] = -__builtin_inff();
     z[n] = 0.0f;
 #pragma unroll
@@ -120,7 +120,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 4 : D == 128 && NC == 1 && WA
   // a step inside [all_lo, all_hi) needs no mask
   const int last = min(rg.rows, row0 + p.tile) - 1;
   const int all_hi = min(rg.hi, rg.first + row0 / p.G + 1);
-  const int all_lo = p.window > 0 ? rg.first + last / p.G - p.window + 1 : 0;
+  const int all_lo = first_key(p, rg.first + last / p.G);
 
   for (; kt < k1; kt += STRIDE) {
     good[0] = next_good[0];

@@ -69,6 +69,12 @@ __device__ __forceinline__ int tile_rows(const AttnArgs& p, int b) {
   return r0 < 0 || r1 <= r0 ? 0 : min(r1 - r0, p.max_new) * p.G;
 }
 
+// The first key that the row at position pos sees (pos may be below 0, the
+// window up to 2^31 - 1: their difference would wrap).
+__device__ __forceinline__ int first_key(const AttnArgs& p, int pos) {
+  return p.window > 0 && pos >= p.window ? pos - p.window + 1 : 0;
+}
+
 __device__ __forceinline__ Range tile_range(const AttnArgs& p, int b, int row0) {
   Range r;
   r.r0 = p.off[b];
@@ -79,8 +85,9 @@ __device__ __forceinline__ Range tile_range(const AttnArgs& p, int b, int row0) 
   const int last_row = min(r.rows, row0 + p.tile) - 1;
   const int q_lo = row0 / p.G, q_hi = last_row / p.G;
   r.hi = min(len, r.first + q_hi + 1);
-  r.seen = p.window > 0 ? max(0, r.first + q_lo - p.window + 1) : 0;
-  r.lo = r.seen & ~(p.step - 1);
+  r.seen = first_key(p, r.first + q_lo);
+  // (never past the keys that there are: the waves count on from it)
+  r.lo = min(r.seen, max(r.hi, 0)) & ~(p.step - 1);
   return r;
 }
 

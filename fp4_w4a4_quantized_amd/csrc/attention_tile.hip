@@ -133,7 +133,7 @@ __global__ __launch_bounds__(64 * WAVES)
   const int qi = rr / p.G, hh = h * p.G + (rr - qi * p.G);
   const int pos = rg.first + qi;
   const int see_hi = min(rg.hi, pos + 1);
-  const int see_lo = p.window > 0 ? pos - p.window + 1 : 0;
+  const int see_lo = first_key(p, pos);
   const int pos_a = rg.first + min(wrow, rg.rows - 1) / p.G;        // the wave's first and
   const int pos_z = rg.first + (min(wrow + 32, rg.rows) - 1) / p.G;  // last position
   float m = -__builtin_inff(), z = 0.0f;
@@ -269,7 +269,7 @@ __global__ __launch_bounds__(64 * WAVES)
   // is read and that of t + 3 written (with the load): four do.
   // this wave's steps (those that some row of it sees)
   int t_on = 0, t_off = wave_on ? min(steps, pos_z < k0 ? 0 : (pos_z - k0) / TILE_KEYS + 1) : 0;
-  if (p.window > 0) t_on = max(0, pos_a - p.window + 1 - k0) / TILE_KEYS;
+  if (p.window > 0) t_on = max(0, first_key(p, pos_a) - k0) / TILE_KEYS;
   v16f x[NU];
   vec pb[2 * NU];
   const uint8_t* const kb = lds + col * S::KROW + half * 16;
@@ -310,7 +310,7 @@ __global__ __launch_bounds__(64 * WAVES)
       const uint32_t ok = s_ok[t & 3];
       const int kt = k0 + t * TILE_KEYS;
       const bool whole = __builtin_amdgcn_readfirstlane(ok) == ALL_OK && kt + TILE_KEYS <= pos_a + 1 &&
-                         kt + TILE_KEYS <= rg.hi && (p.window == 0 || kt > pos_z - p.window);
+                         kt + TILE_KEYS <= rg.hi && kt >= first_key(p, pos_z);
       if (!whole) {
 #pragma unroll
         for (int u = 0; u < NU; ++u)

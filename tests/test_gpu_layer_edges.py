@@ -257,3 +257,36 @@ def test_many_row_tiles_of_many_heads():
         c = dict(fmt=1, cache=cache[:, h:h + 1].cpu().numpy(), page=page, off=np.array([0, n]), D=D, t=None,
                  table=table.cpu().numpy(), lens=np.array([n]), q=q[:, h:h + 1].double().cpu().numpy())
         check_close(c, got[:, h:h + 1], window)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("n,lens,G,D", [([9, 1], [3, 5], 2, 128), ([7, 5], [2, 0], 4, 64), ([90, 40], [33, 50], 3, 64),
+                                        ([40, 30], [4, 1], 2, 256), ([50, 3], [700, 1], 4, 128)])
+def test_windows_wider_than_any_length(fmt, n, lens, G, D):
+    """Windows up to 2^31 - 1 are no window, for rows before position 0 too."""
+    need_gpu()
+    say(f"wide window fmt {fmt} n {n} lens {lens} G {G} D {D}")
+    c = make(fmt, n, lens, G=G, H=2, D=D, page=16, seed=sum(n))
+    want = attend(c)
+    check_close(c, want)
+    for window in (max(lens), max(lens) + 1, 2 ** 31 - 2, 2 ** 31 - 1):
+        got = attend(c, window)
+        check_close(c, got, window)
+        assert torch.equal(got, want), window
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("n,G,D", [([1, 2], 4, 128), ([5, 1], 4, 64), ([70, 3], 4, 64), ([33, 40], 2, 256)])
+@pytest.mark.parametrize("window", [0, 7, 2 ** 31 - 1])
+def test_lengths_past_the_table(fmt, n, G, D, window):
+    """Lengths up to the largest 32-bit number over a table of a few pages: what
+    the table holds is seen, unless the window has left it."""
+    need_gpu()
+    say(f"past the table fmt {fmt} n {n} G {G} D {D} window {window}")
+    c = make(fmt, n, [96, 95], G=G, H=2, D=D, page=16, seed=sum(n))
+    for long in (97, 5000, 2 ** 31 - 40, 2 ** 31 - 1):
+        c["lens"] = np.array([long, 95], np.int32)
+        got = attend(c, window, max_len=5000)
+        check_close(c, got, window)
+        if window == 7 and long > 96 + n[0] + 7:
+            assert torch.all(got[:n[0]] == 0)
