@@ -208,7 +208,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 4 : D == 128 && NC == 1 && WA
     z[n] += __shfl_xor(z[n], 16);
     z[n] += __shfl_xor(z[n], 32);
     if (g == 0) {
-      s_m[wave][n * ROWS + c] = m[n] * cf[n];
+      s_m[wave][n * ROWS + c] = m[n];  // (m c, rounded, would weigh the waves apart)
       s_z[wave][n * ROWS + c] = z[n];
     }
   }
@@ -222,8 +222,8 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 4 : D == 128 && NC == 1 && WA
     const float base = mm > -__builtin_inff() ? mm : 0.0f;
 #pragma unroll
     for (int w = 0; w < WAVES; ++w)
-      zz += s_z[w][n * ROWS + c] * __builtin_amdgcn_exp2f(s_m[w][n * ROWS + c] - base);
-    const float mine = __builtin_amdgcn_exp2f(m[n] * cf[n] - base);
+      zz += s_z[w][n * ROWS + c] * __builtin_amdgcn_exp2f((s_m[w][n * ROWS + c] - base) * cf[n]);
+    const float mine = __builtin_amdgcn_exp2f((m[n] - base) * cf[n]);
 #pragma unroll
     for (int i = 0; i < D / 16; ++i)
 #pragma unroll
@@ -260,10 +260,16 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 4 : D == 128 && NC == 1 && WA
       }
     } else {
       const int64_t s = split * p.slots + (rg.r0 + qi) * (int64_t)(p.H * p.G) + hh;
+      float f;
+      const float whole = whole_max(mm, cf[n], f);
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i)
-        *reinterpret_cast<v4f*>(p.part_o + s * D + 16 * i + 4 * g) = o[n][i];
-      if (g == 0) p.part_ms[s] = make_float2(mm, zz);
+      for (int i = 0; i < D / 16; ++i) {
+        v4f t;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) t[r] = o[n][i][r] * f;
+        *reinterpret_cast<v4f*>(p.part_o + s * D + 16 * i + 4 * g) = t;
+      }
+      if (g == 0) p.part_ms[s] = make_float2(whole, zz * f);
     }
   }
   zero_rest<D, 64 * WAVES>(p, b, h);

@@ -35,7 +35,7 @@ struct AttnArgs {
   int step;    // keys of a step of its kernel: splits begin at its multiples
   int join;    // groups of lanes that join a row's splits
   int64_t slots;  // rows * heads: partial results of one split
-  float2* part_ms;  // [splits][slots] (maximum in log2 units, sum)
+  float2* part_ms;  // [splits][slots] (maximum in log2 units, a whole number; sum)
   float* part_o;    // [splits][slots][D]
 };
 
@@ -390,6 +390,17 @@ __device__ __forceinline__ void load_q(const uint16_t* q, int g, float c0,
     for (int st = 0; st < D / 32; ++st) out[st] = __builtin_bit_cast(vec, q_to_f16(u[st], sh));
   }
   c = fmaxf(c, 1e-37f);  // (a masked product, -inf, times c stays -inf)
+}
+
+// What a split leaves the join of its maximum m (c: to log2 units): a whole
+// number near m c, and f = 2^(m c - number) for its sums.  (m c itself, rounded,
+// would weigh the splits by 2^(m c 2^-24) apart.)
+__device__ __forceinline__ float whole_max(float m, float c, float& f) {
+  const float r = rintf(m * c);
+  // (past 2^24 the number's own rounding; beyond 2^29 scores are not known to 2^32)
+  const float e = fminf(fmaxf(__builtin_fmaf(m, c, -r), -32.0f), 32.0f);
+  f = __builtin_amdgcn_exp2f(e);
+  return r;
 }
 
 // Four neighbouring outputs, from element `at` of y.

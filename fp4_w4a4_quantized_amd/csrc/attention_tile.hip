@@ -31,6 +31,11 @@ namespace {
 
 typedef float v16f __attribute__((ext_vector_type(16)));
 
+// Weights are 2^(x cf + nb) up to scores of this many log2 units.  nb is rounded
+// anew with each maximum, which weighs older and newer keys apart by up to 2^-16
+// of them there (a weight's own rounding: 2^-11 or 2^-8), and by percents at 2^19.
+constexpr float FAR = 256.0f;
+
 // Keys of a step.
 template <int D> struct TileKeys { static constexpr int N = D <= 128 ? 64 : 32; };
 
@@ -139,7 +144,7 @@ __global__ __launch_bounds__(64 * WAVES)
   float m = -__builtin_inff(), z = 0.0f;
   float lim = m;        // a score above it asks for a new maximum
   float nb = P_BIAS;    // P_BIAS - m cf
-  bool far = false;     // is some column's m cf so large that nb loses its fraction?
+  bool far = false;     // is some column's m cf past FAR?
   v16f o[D / 32];
 #pragma unroll
   for (int i = 0; i < D / 32; ++i)
@@ -334,17 +339,17 @@ __global__ __launch_bounds__(64 * WAVES)
         m = mt;
         if (m > -__builtin_inff()) {
           lim = m + P_SLACK / cf;
-          nb = P_BIAS - m * cf;
+          nb = __builtin_fmaf(-m, cf, P_BIAS);
         }
-        far = __any(fabsf(m * cf) > 0x1p20f && m > -__builtin_inff());
+        far = __any(fabsf(m * cf) > FAR && m > -__builtin_inff());
         z *= f;
 #pragma unroll
         for (int i = 0; i < D / 32; ++i)
 #pragma unroll
           for (int r = 0; r < 16; ++r) o[i][r] *= f;
       }
-      // 2^(x cf + nb): nb's rounding is a factor that all of a column's weights
-      // share.  Where it could reach 1 the difference is taken first.
+      // 2^(x cf + nb), nb = P_BIAS - m cf rounded (past FAR the difference is taken
+      // first).
       float add = nb;
       if (far) {
         const float base = m > -__builtin_inff() ? m : 0.0f;
@@ -398,15 +403,18 @@ __global__ __launch_bounds__(64 * WAVES)
       }
   } else {
     const int64_t s = split * p.slots + (rg.r0 + qi) * (int64_t)(p.H * p.G) + hh;
+    float f;
+    const float whole = whole_max(m, cf, f);
 #pragma unroll
     for (int i = 0; i < D / 32; ++i)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const v4f t = {o[i][4 * r], o[i][4 * r + 1], o[i][4 * r + 2], o[i][4 * r + 3]};
+        v4f t;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) t[e] = o[i][4 * r + e] * f;
         *reinterpret_cast<v4f*>(p.part_o + s * D + 32 * i + 8 * r + 4 * half) = t;
       }
-    if (half == 0)
-      p.part_ms[s] = make_float2(m * cf, z);
+    if (half == 0) p.part_ms[s] = make_float2(whole, z * f);
   }
 }
 

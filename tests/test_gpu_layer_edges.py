@@ -290,3 +290,47 @@ def test_lengths_past_the_table(fmt, n, G, D, window):
         check_close(c, got, window)
         if window == 7 and long > 96 + n[0] + 7:
             assert torch.all(got[:n[0]] == 0)
+
+
+MAGNITUDES = [6, 20, 22, 24, 46, 90, 200, 752, 1504, 3008, 5696, 11904, 23680, 46592, 87040, 159744]
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("n,length", [(1, 700), (1, 3000), (2, 3000), (40, 700), (9, 4000)])
+@pytest.mark.parametrize("rise", [False, True])
+def test_large_scores_that_differ_little(fmt, D, n, length, rise):
+    """Scores up to 2^21 in log2 units, exact in 32 bits, whose differences are
+    all that counts: of two groups of keys (in different steps, waves and splits)
+    that weigh about the same.  rise: the second group is a few keys late in the
+    sequence, 2^9.4 times as heavy each, so that the running maximum moves.
+
+    Tolerance: a weight's rounding u, and 2 keys 2^-24 for the sums (products
+    and scores are exact, so no other term grows with the scores); 2^-14 for
+    what the kernels round in between."""
+    need_gpu()
+    say(f"large scores fmt {fmt} D {D} n {n} length {length} rise {rise}")
+    heads, scale = len(MAGNITUDES), float(np.float32(1.3))
+    c = make(fmt, [n], [length], G=heads, H=1, D=D, page=16, seed=length + n)
+    c["t"] = None if fmt == 1 else np.ones(1, np.float32)
+    k, v = np.zeros((2, length, 1, D))
+    k[:, 0, 0], k[:, 0, 41] = 6.0, 6.0          # (6 in a block: its scale is 1)
+    second = np.zeros(length, bool)
+    if rise:
+        second[length - n - 1 - 97 * np.arange(max(length // 700, 1))] = True
+        k[second, 0, 40], k[~second, 0, 40] = 4.0, -1.0
+    else:
+        second[(np.arange(length) // 32) % 3 == 1] = True
+        second[length // 2:] ^= True
+        k[second, 0, 40] = c["rng"].choice([0.5, 1.0, 1.5], second.sum())
+    v[:, 0] = np.where(second, -6.0, 6.0)[:, None]
+    v[:, 0, ::3] *= 0.5
+    layer.kv_append(fmt, c["cache"], c["page"], np.array([0, length]), c["table"], c["lens"], k, v, c["t"], c["t"])
+    c["q"] = np.zeros((n, heads, D))
+    c["q"][:, :, 0], c["q"][:, :, 40] = MAGNITUDES, 1.0
+    got = attend(c, scale=scale, y_dtype=fq.OUT_F32).double().cpu().numpy()
+    o, w, _ = layer.attention(fmt, c["cache"], c["page"], c["off"], c["table"], c["lens"], c["q"], c["t"], c["t"], 0,
+                              scale)
+    tol = ((2.0 ** -11 if fmt == 0 else 2.0 ** -8) + 2.0 ** -14 + 2 * length * 2.0 ** -24) * w
+    bad = np.argwhere(~(np.abs(got - o) <= tol))
+    assert bad.size == 0, f"{len(bad)} off, worst {np.max(np.abs(got - o) / tol):.2f} of the bound, first {bad[:3].tolist()}"
