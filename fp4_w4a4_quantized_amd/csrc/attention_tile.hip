@@ -108,6 +108,7 @@ __global__ __launch_bounds__(64 * WAVES)
   typedef Staged<FMT, D, WAVES / 2> St;
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   // of the last steps, byte u: is the page of keys 16u .. 16u + 15 in the cache?
+  // (dim 256 has two units a step: its upper bytes are never written)
   __shared__ uint32_t s_ok[4];
 
   const int lane = threadIdx.x & 63, col = lane & 31, half = lane >> 5;
@@ -314,7 +315,7 @@ __global__ __launch_bounds__(64 * WAVES)
     if (on) {
       const uint32_t ok = s_ok[t & 3];
       const int kt = k0 + t * TILE_KEYS;
-      const bool whole = __builtin_amdgcn_readfirstlane(ok) == ALL_OK && kt + TILE_KEYS <= pos_a + 1 &&
+      const bool whole = (__builtin_amdgcn_readfirstlane(ok) & ALL_OK) == ALL_OK && kt + TILE_KEYS <= pos_a + 1 &&
                          kt + TILE_KEYS <= rg.hi && kt >= first_key(p, pos_z);
       if (!whole) {
 #pragma unroll
