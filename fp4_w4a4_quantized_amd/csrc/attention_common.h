@@ -344,11 +344,10 @@ __device__ __forceinline__ uint32_t max_magnitude(w4 u) {  // of 8 BF16, as bits
 }
 
 // The power of two that a row of q is divided by for f16: the exponent of its
-// largest magnitude (BF16 subnormals and zero, and what has no finite
-// reciprocal power: left as they are).
+// largest magnitude, held to where it and its reciprocal are normal numbers
+// (infinities and NaN stay what they are).
 __device__ __forceinline__ int q_exponent(uint32_t m) {
-  const int ex = (int)(m >> 7);
-  return ex == 0 || ex >= 254 ? 0 : ex - 127;
+  return min(max((int)(m >> 7), 1), 253) - 127;
 }
 
 __device__ __forceinline__ w4 q_to_f16(w4 u, int sh) {

@@ -334,3 +334,33 @@ def test_large_scores_that_differ_little(fmt, D, n, length, rise):
     tol = ((2.0 ** -11 if fmt == 0 else 2.0 ** -8) + 2.0 ** -14 + 2 * length * 2.0 ** -24) * w
     bad = np.argwhere(~(np.abs(got - o) <= tol))
     assert bad.size == 0, f"{len(bad)} off, worst {np.max(np.abs(got - o) / tol):.2f} of the bound, first {bad[:3].tolist()}"
+
+
+@pytest.mark.parametrize("fmt", [0])
+@pytest.mark.parametrize("n", [1, 20])
+@pytest.mark.parametrize("top", [1.0, 1.75])
+@pytest.mark.parametrize("power", [-131, -127, -126, -120, 120, 125, 126, 127])
+def test_queries_at_the_ends_of_bf16(fmt, n, top, power):
+    """Rows of the smallest (subnormal) and largest magnitudes, with a scale that
+    brings their scores to a few units.  A row has one value and keys are
+    small, so that no product overflows and all are exact."""
+    need_gpu()
+    say(f"q of {top} 2^{power} fmt {fmt} n {n}")
+    scale = 2.0 ** min(-power, 126)
+    c = make(fmt, [n], [100], G=4, H=1, D=64, page=16, seed=5)
+    c["t"] = None if fmt == 1 else np.full(1, 2.0 ** -6, np.float32)
+    k, v = np.zeros((2, 100, 1, 64))
+    k[:, 0, 3] = 2.0 ** -5 * c["rng"].choice([-3.0, -1.0, 0.5, 1.0, 2.0, 3.0], 100)
+    k[:, 0, 4] = 6 * 2.0 ** -5                    # (the block's scale; q is 0 there)
+    v[:] = layer.bf16_round(c["rng"].standard_normal(v.shape) / 16)
+    layer.kv_append(fmt, c["cache"], c["page"], np.array([0, 100]), c["table"], c["lens"], k, v, c["t"], c["t"])
+    c["q"] = np.zeros((n, 4, 64))
+    c["q"][:, :, 3] = top * 2.0 ** power
+    assert np.array_equal(c["q"], layer.bf16_round(c["q"]))
+    got = attend(c, scale=scale, y_dtype=fq.OUT_F32).double().cpu().numpy()
+    o, w, _ = layer.attention(fmt, c["cache"], c["page"], c["off"], c["table"], c["lens"], c["q"], c["t"], c["t"], 0,
+                              scale)
+    # weights' rounding, 200 roundings of the sums, 2^-14 for the exponents
+    tol = ((2.0 ** -11 if fmt == 0 else 2.0 ** -8) + 200 * 2.0 ** -24 + 2.0 ** -14) * w
+    bad = np.argwhere(~(np.abs(got - o) <= tol))
+    assert bad.size == 0, f"{len(bad)} off, first {bad[:3].tolist()}, got {got[0, 0, :3]} want {o[0, 0, :3]}"
