@@ -51,6 +51,8 @@ typedef uint32_t w4 __attribute__((ext_vector_type(4)));
 
 constexpr float P_BIAS = 7.0f;   // log2 of p at the running maximum
 constexpr float P_SLACK = 8.0f;  // the maximum may fall behind by 2^8: p <= 2^15
+// Products' factor to log2 units, at least: a masked one, -inf, times it stays -inf.
+constexpr float MIN_FACTOR = 0x1p-149f;
 constexpr int ROWS = 16;         // rows of a wave (columns of its products)
 constexpr int KEYS = 32;         // keys of a step
 
@@ -388,7 +390,7 @@ __device__ __forceinline__ void load_q(const uint16_t* q, int g, float c0,
 #pragma unroll
     for (int st = 0; st < D / 32; ++st) out[st] = __builtin_bit_cast(vec, q_to_f16(u[st], sh));
   }
-  c = fmaxf(c, 1e-37f);  // (a masked product, -inf, times c stays -inf)
+  c = fmaxf(c, MIN_FACTOR);
 }
 
 // What a split leaves the join of its maximum m (c: to log2 units): a whole

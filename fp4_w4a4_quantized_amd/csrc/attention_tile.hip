@@ -261,7 +261,7 @@ __global__ __launch_bounds__(64 * WAVES)
 #pragma unroll
       for (int st = 0; st < D / 16; ++st) qf[st] = __builtin_bit_cast(vec, q_to_f16(u[st], sh));
     }
-    cf = fmaxf(cf, 1e-37f);
+    cf = fmaxf(cf, MIN_FACTOR);
   }
 
   // ---- the keys ---------------------------------------------------------------

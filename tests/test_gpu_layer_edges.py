@@ -336,7 +336,7 @@ def test_large_scores_that_differ_little(fmt, D, n, length, rise):
     assert bad.size == 0, f"{len(bad)} off, worst {np.max(np.abs(got - o) / tol):.2f} of the bound, first {bad[:3].tolist()}"
 
 
-@pytest.mark.parametrize("fmt", [0])
+@pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("n", [1, 20])
 @pytest.mark.parametrize("top", [1.0, 1.75])
 @pytest.mark.parametrize("power", [-131, -127, -126, -120, 120, 125, 126, 127])
