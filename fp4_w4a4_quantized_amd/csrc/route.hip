@@ -48,8 +48,10 @@ __device__ __forceinline__ float load_value(const void* x, int f32, int64_t i) {
              : bf16_to_f32(reinterpret_cast<const uint16_t*>(x)[i]);
 }
 
-// A logit: NaN counts as -inf.
-__device__ __forceinline__ float logit_of(float x) { return x == x ? x : -__builtin_inff(); }
+// A logit: NaN counts as -inf, +inf as the largest finite number.
+__device__ __forceinline__ float logit_of(float x) {
+  return x == x ? fminf(x, 0x1.fffffep127f) : -__builtin_inff();
+}
 __device__ __forceinline__ float load_logit(const void* x, int f32, int64_t i) {
   return logit_of(load_value(x, f32, i));
 }

@@ -782,10 +782,11 @@ int fp4q_kv_attention(fp4q_format_t fmt, const uint8_t* cache, int64_t n_pages, 
  *            the largest logits, which tell apart what a score that saturates
  *            or underflows does not)
  *   weights  their scores (renorm: divided by their sum)
- * Ties go to the lower index; a NaN logit counts as -inf.  A token without
- * a finite logit has weights 0.  And the order by expert that the grouped calls
- * above take: row_src (token of each routed row, rows of an expert by
- * token), group offsets, and row_of (the row of each token's j-th expert).
+ * Ties go to the lower index; a NaN logit counts as -inf, +inf as the largest
+ * finite f32 number.  A token of nothing but -inf has weights 0.  And the order
+ * by expert that the grouped calls above take: row_src (token of each routed
+ * row, rows of an expert by token), group offsets, and row_of (the row of each
+ * token's j-th expert).
  *
  *   logits     f32 or bf16 (dtype) [tokens, experts], row stride ldx
  *   experts, row_of   out int32 [tokens, k];  weights out f32 [tokens, k]

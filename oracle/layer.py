@@ -196,12 +196,13 @@ def attention(fmt, cache, page, offsets, table, lens, q, kt=None, vt=None, windo
 
 def route(logits, k, score=SOFTMAX, bias=None, n_groups=1, top_groups=1, renorm=True):
     """dict as fp4q_route's outputs (weights float64), row by row."""
+    logits = logits_of(logits)
     T, E = logits.shape
     ex, w = np.zeros((T, k), np.int32), np.zeros((T, k))
     for t in range(T):
         s = scores_of(logits[t], score)
         r = s if bias is None else s + np.asarray(bias, np.float64)
-        key = np.asarray(logits[t], np.float64) if bias is None else r
+        key = logits[t] if bias is None else r
         allowed = np.ones(E, bool)
         if n_groups > 1:
             gs = E // n_groups
@@ -218,8 +219,14 @@ def route(logits, k, score=SOFTMAX, bias=None, n_groups=1, top_groups=1, renorm=
     return out
 
 
-def scores_of(x, score):
+def logits_of(x):
+    """NaN as -inf, +inf as the largest finite f32 number."""
     x = np.asarray(x, np.float64)
+    return np.where(np.isnan(x), -np.inf, np.minimum(x, float(np.finfo(np.float32).max)))
+
+
+def scores_of(x, score):
+    x = logits_of(x)
     if score == SIGMOID:
         with np.errstate(over="ignore"):
             return 1.0 / (1.0 + np.exp(-x))

@@ -9,7 +9,7 @@ import fp4_w4a4_quantized_amd as fq
 from gpu_helpers import need_gpu, say
 from oracle import layer
 from test_gpu_kv_attention import FMTS, attend, check, check_close, dev, make
-from test_gpu_route_combine import check_route
+from test_gpu_route_combine import U, check_route, host, logits_of
 
 pytestmark = pytest.mark.gpu
 
@@ -44,6 +44,37 @@ def test_a_grouped_choice_by_hand():
     x[0, 2], x[0, 5], x[0, 6] = 38.0, 50.0, 45.0
     r = fq.route(x.cuda(), 2, score=fq.SIGMOID, n_groups=4, top_groups=2)
     assert r["experts"].tolist() == [[5, 6]]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T", [14, 210])
+@pytest.mark.parametrize("score", [0, 1])
+@pytest.mark.parametrize("E,groups,top,k", [(8, 1, 1, 2), (60, 1, 1, 20), (96, 4, 2, 7)])
+def test_infinite_logits(dtype, T, score, E, groups, top, k):
+    """+inf counts as the largest finite number: it shares a softmax with its
+    like, and neither weights nor gradients become NaN."""
+    need_gpu()
+    say(f"infinite logits {dtype} T{T} E{E} {groups}/{top} k{k} score {score}")
+    inf = float("inf")
+    x = logits_of(T, E, torch.float32, E)
+    x[0, 3] = inf
+    x[1, 1:7:2] = inf
+    x[2] = inf
+    x[3], x[3, 5] = -inf, inf
+    x[4], x[4, 6], x[4, 2] = float("nan"), inf, -inf
+    x[5, ::2] = inf
+    x[6, 7], x[6, 4] = inf, torch.finfo(torch.float32).max
+    x[T - 1, 0] = inf
+    x = x.to(dtype)
+    bias = 0.1 * torch.randn(E, generator=torch.Generator().manual_seed(E)).cuda()
+    dw = torch.randn(T, k, generator=torch.Generator().manual_seed(T)).cuda()
+    for renorm in (True, False):
+        for b in (None, bias):
+            r, _ = check_route(x, k, score, b, groups, top, renorm)
+            d = fq.route_backward(x, r["experts"], dw, score=score, renorm=renorm)
+            want, size = layer.route_backward(host(x), r["experts"].cpu().numpy(), host(dw), score, renorm)
+            u = U[dtype] + (2.0 ** -24 if dtype == torch.bfloat16 else 0.0)
+            assert np.all(np.abs(host(d) - want) <= u * np.abs(want) + 2.0 ** -40 * size + 1e-38)
 
 
 # ---- the cache --------------------------------------------------------------
