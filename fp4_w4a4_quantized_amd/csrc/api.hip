@@ -837,9 +837,9 @@ int kv_copy(bool append, int fmt, uint8_t* cache, int64_t n_pages, int32_t page,
   if (rc != FP4Q_OK) return rc;
   if (rows == 0) return FP4Q_OK;
   const int64_t cols = (int64_t)kv_heads * dim;
-  if (!packed_ok(k, ldk, cols) || !packed_ok(v, ldv, cols)) return FP4Q_ERR_INVALID;
   if (rows >= ((int64_t)1 << 31) || (rows + 3) / 4 * 4 * (cols / 32) >= ((int64_t)1 << 31))
-    return FP4Q_ERR_UNSUPPORTED;
+    return FP4Q_ERR_UNSUPPORTED;  // (before k and v: a caller may not have made them)
+  if (!packed_ok(k, ldk, cols) || !packed_ok(v, ldv, cols)) return FP4Q_ERR_INVALID;
   if (injected_failure()) return FP4Q_ERR_HIP;
   clear_error();
   fp4q::launch_kv_copy(append, fmt, cache, n_pages, page_shift_of(page), kv_heads, dim, offsets,
@@ -957,15 +957,15 @@ int fp4q_route(const void* logits, fp4q_dtype_t dtype, int64_t tokens, int32_t n
       n_experts % n_groups != 0 || top_groups < 1 || top_groups > n_groups ||
       k > n_experts / n_groups * top_groups)
     return FP4Q_ERR_INVALID;
+  if (n_experts > FP4Q_ROUTE_MAX_EXPERTS || n_groups > FP4Q_ROUTE_MAX_GROUPS ||
+      k > FP4Q_ROUTE_MAX_K || tokens >= ((int64_t)1 << 27) / k)
+    return FP4Q_ERR_UNSUPPORTED;  // (before the results: a caller may not have made them)
   if (!offsets || !aligned(offsets, 4) || !aligned(bias, 4)) return FP4Q_ERR_INVALID;
   if (tokens > 0 && (!logits || !experts || !weights || !row_src || !row_of))
     return FP4Q_ERR_INVALID;
   if (!aligned(logits, dtype == FP4Q_OUT_F32 ? 4 : 2) || !aligned(experts, 4) ||
       !aligned(weights, 4) || !aligned(row_src, 4) || !aligned(row_of, 4))
     return FP4Q_ERR_INVALID;
-  if (n_experts > FP4Q_ROUTE_MAX_EXPERTS || n_groups > FP4Q_ROUTE_MAX_GROUPS ||
-      k > FP4Q_ROUTE_MAX_K || tokens >= ((int64_t)1 << 27) / k)
-    return FP4Q_ERR_UNSUPPORTED;
   const size_t need = fp4q_route_workspace_bytes(tokens, n_experts);
   if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 8)))
     return FP4Q_ERR_WORKSPACE;

@@ -243,7 +243,10 @@ PyObject* read(PyObject* const* a) {
   const Kv c = kv(a, dim);
   void* const stream = stream_of(a[0]);
   const at::Tensor& like_t = THPVariable_Unpack(a[2]);
-  const at::Tensor both = like(like_t, {2, rows, c.heads, dim}, at::kBFloat16);
+  // (no memory for a call that will be refused for its size)
+  const int64_t most = (int64_t)1 << 31;
+  const bool fits = rows < most && (c.heads * dim == 0 || (rows + 3) / 4 * 4 <= most * 32 / (c.heads * dim));
+  const at::Tensor both = like(like_t, {2, fits ? rows : 0, c.heads, dim}, at::kBFloat16);
   const at::Tensor k = both.select(0, 0), v = both.select(0, 1);
   const int64_t ld = (int64_t)c.heads * dim;
   check("fp4q_kv_read",
@@ -355,7 +358,10 @@ PyObject* route(PyObject* const* a) {
   const Router r = router(a);
   need(r.k >= 0, "k", "none below 0");
   const at::Tensor& x = THPVariable_Unpack(a[1]);
-  const int64_t T = r.x.rows, k = r.k, n = T * k, E = r.x.cols;
+  const int64_t T = r.x.rows, k = r.k, E = r.x.cols;
+  if (k < 1 || k > FP4Q_ROUTE_MAX_K || T >= ((int64_t)1 << 27) / k)  // refused: no memory for its results
+    route_call(a, r, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, 0);
+  const int64_t n = T * k;
   const size_t bytes = fp4q_route_workspace_bytes(T, (int32_t)E);
   // one allocation for the workspace and four of the results
   const int64_t w = ((int64_t)bytes + 7) / 8 * 2;

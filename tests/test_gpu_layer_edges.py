@@ -395,3 +395,22 @@ def test_queries_at_the_ends_of_bf16(fmt, n, top, power):
     tol = ((2.0 ** -11 if fmt == 0 else 2.0 ** -8) + 200 * 2.0 ** -24 + 2.0 ** -14) * w
     bad = np.argwhere(~(np.abs(got - o) <= tol))
     assert bad.size == 0, f"{len(bad)} off, first {bad[:3].tolist()}, got {got[0, 0, :3]} want {o[0, 0, :3]}"
+
+
+# ---- refusals -------------------------------------------------------------------
+
+def test_sizes_without_room_are_refused():
+    """With the call's own error, not for lack of memory."""
+    need_gpu()
+    x = torch.zeros(1000, 64, device="cuda")
+    for k, code in ((33, "-2"), (2 ** 31 - 1, "-1"), (65, "-1"), (0, "-1")):
+        with pytest.raises(fq.Fp4qError, match=code):
+            fq.route(x, k)
+    c = make(1, [1], [20], D=64)
+    where = (1, dev(c["cache"]), 16, dev(c["off"]), dev(c["table"]), dev(c["lens"]))
+    for rows in (2 ** 31, 2 ** 40, 2 ** 62, 2 ** 29):
+        with pytest.raises(fq.Fp4qError, match="-2"):
+            fq.kv_read(*where, rows, 64)
+    for max_new, max_len in ((1, 2 ** 62), (2 ** 62, 20), (2 ** 40, 2 ** 40)):
+        with pytest.raises(fq.Fp4qError, match="-2"):
+            fq.kv_attention(*where, dev(c["q"], torch.bfloat16), max_new, max_len)
