@@ -11,6 +11,13 @@
 
 namespace fp4q {
 
+// What a wave's lanes exchange through LDS: its operations keep their order, the
+// fence holds the compiler to it.
+__device__ __forceinline__ void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 __device__ __forceinline__ float bf16_to_f32(uint32_t h) { return __uint_as_float(h << 16); }
 
 // Nearest-even float -> bf16 (inputs finite).

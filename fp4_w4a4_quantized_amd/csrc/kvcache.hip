@@ -88,13 +88,7 @@ __device__ __forceinline__ KvItem kv_item(const KvArgs& p, int32_t* s_off) {
 // of run j of a token at l * 4J + j, so the J lanes that hold a token's runs
 // exchange bytes through LDS, after which a lane has 16 / J stretches of J bytes
 // that lie together in the cache.  w: the run's codes, two neighbouring elements
-// to a byte; b: bytes (16 / J) j .. of the token, each J long.  (A wave's LDS
-// operations keep their order; the fences hold the compiler to it.)
-__device__ __forceinline__ void wave_fence() {
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-}
-
+// to a byte; b: bytes (16 / J) j .. of the token, each J long.
 template <int J>
 __device__ __forceinline__ u32x4 v_bytes_from_codes(const uint32_t (&w)[4], int j, uint8_t* token) {
 #pragma unroll

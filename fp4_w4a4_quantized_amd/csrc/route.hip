@@ -282,7 +282,7 @@ __global__ __launch_bounds__(RT_THREADS) void k_route_pick(RouteArgs p) {
 #pragma unroll
       for (int i = 0; i < NS; ++i)
         if (lane + 64 * i < E) r[lane + 64 * i] = rank_by[i];
-      __builtin_amdgcn_wave_barrier();
+      wave_fence();
       const int gs = E / p.G;
       int P = 64;
       while (P * p.G > 64) P >>= 1;
@@ -318,7 +318,7 @@ __global__ __launch_bounds__(RT_THREADS) void k_route_pick(RouteArgs p) {
         const int e = lane + 64 * i;
         if (e < E && !((keep >> (e / gs * P)) & 1)) key[i] = ORDER_NONE;
       }
-      __builtin_amdgcn_wave_barrier();
+      wave_fence();
     }
     // k rounds: the largest key left, the lowest expert that has it; lane j
     // keeps the round's expert and its score
