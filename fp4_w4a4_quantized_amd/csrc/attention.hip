@@ -26,10 +26,11 @@
 // maximum, sum and output are FP32.  With f16, p is held 2^7 above the usual
 // 2^(x - m), so that weights down to 2^-31 of the largest are not lost.
 //
-// Few rows (this file) are bound by reading the cache: 64 x 1 token over up to
-// 8192 keys (249 MB) take 62-71 us, 3.5-4 TB/s where a copy reaches 4.8, and the
-// join of the splits 7.  One token over 777 keys is one wave's chain of four
-// steps: 10.5 us.  Many rows: attention_tile.hip.
+// Few rows (this file): 64 x 1 token over up to 8192 keys (249 MB) take 70-72 us,
+// 3.5 TB/s where a copy reaches 4.8, and the join of the splits 7.  The vector units
+// issue (decoding, for the most part) in 52% of the cycles, the waves wait for the
+// cache's bytes in 47% of theirs.  One token over 777 keys is one wave's chain of
+// four steps: 10.6 us.  Many rows: attention_tile.hip.
 #include "attention_common.h"
 
 namespace fp4q {
@@ -332,7 +333,26 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs p) {
 }
 
 // How a call is split: a function of host numbers only, so that the workspace
-// query and the launch agree.
+// query and the launch agree.  Its rules, with what the other choice takes (us a
+// call; NVFP4, 8 heads of 128 on a kv head where nothing else is said):
+//   wide    more than 32 rows a kv head.  8 x 8 kv heads over 4096 keys: 24 rows 30.6,
+//           wide 46.5; 48 rows 49.6 either way; 64 rows 52.0, not wide 56.5 (dim 64: 35.8
+//           and 31.4, dim 256: 107 and 110, at 48 rows 103 and 82)
+//   nc      17 to 32 rows in one pass: 30.6, in two 31.7 (dim 64 21.2 and 22.8)
+//   tile    256 rows from 129 on: 160 rows 60.5, by 128 84.0; 1024 rows 182 and 262
+//   waves   eight with at most 256 (sequence, kv head)s and 2048 keys.  256 of them: 777
+//           keys 11.6, split over workgroups of four 18.2; 2048 keys 19.2 and 30.4.  The
+//           rule is too wide for few of them (8: 777 keys 10.7 and 9.9, 2048 keys 17.5 and
+//           10.4) and too narrow above (512, 777 keys: 28.3 by four, 21.7 by eight)
+//   want    workgroups asked for.  64 sequences of up to 8192 keys: 84, 80, 77.5, 90 for 1024,
+//           2048, 4096, 8192; 3 of up to 131072: 63, 58, 57, 67; of equal lengths 2048 would do
+//           (64 x 8192: 127, with 4096 142).  wide: 512 + 83 tokens in a window of 4096 keys,
+//           dim 64: 64, 53, 64 for 256, 512, 1024; equal lengths 88 for 256 and 104 for 512
+//   least   keys of a split.  8 (sequence, kv head)s over 16384 keys: 18.2, 14.0, 13.1, 16.1 for
+//           128, 256, 512, 1024; over 4096: 10.0, 10.5, 12.1, 15.4.  wide: 64 tokens over 65536
+//           keys 53.5, 38.8, 47.3 for 256, 512, 1024
+//   join    lane groups on a row's splits, four to eight splits each.  171 splits: 121 by one
+//           group, 115.5 by this rule and by half as many
 struct Plan {
   bool wide;  // many rows: k_attn_tile
   int nc, waves, tile, step, chunk, splits, join;
@@ -354,7 +374,7 @@ Plan attn_plan(int D, int B, int H, int G, int64_t max_new, int64_t max_len, int
   }
   int64_t groups = B * (int64_t)H * p.tiles;
   if (groups > (1 << 30)) groups = 1 << 30;  // (keys * groups stays below 2^63)
-  // few short (sequence, head)s: eight waves on the keys of each, none to join
+  // eight waves on the keys of each (sequence, kv head), none to join
   p.waves = !p.wide && groups <= 256 && keys <= 2048 && p.nc == 1 && D <= 128 ? 8 : 4;
   const int64_t want = p.wide ? 512 : 4096;
   int64_t chunk = (keys * groups + want - 1) / want;
@@ -364,7 +384,6 @@ Plan attn_plan(int D, int B, int H, int G, int64_t max_new, int64_t max_len, int
   p.chunk = (int)(chunk < (1 << 30) ? chunk : (1 << 30));
   p.splits = (int)((keys + p.chunk - 1) / p.chunk);
   if (p.splits < 1) p.splits = 1;
-  // about eight splits for each of the join's lane groups
   p.join = 1;
   while (p.join * 4 < p.splits && p.join < 1024 / D) p.join *= 2;
   return p;

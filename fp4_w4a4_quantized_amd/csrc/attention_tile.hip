@@ -22,7 +22,9 @@
 // 4 prompts of up to 4096 tokens (32 heads of 128 on 4, 217 GFLOP) take 276 us,
 // 787 TFLOP/s; a library product reaches 1225.  A product takes the vector port
 // for 12 of its 32 cycles, and the two waves' vector work and products are about
-// equal, so at best 2700 cycles of the 4500 that 64 keys take are needed.
+// equal, so at best 2700 cycles of the 4600 that 64 keys take are needed.  Dim 256
+// (one wave a SIMD, so that nothing hides its waits): 2 prompts of up to 2048 tokens,
+// 16 heads on 4, 35 GFLOP, 164 us; the vector units issue in a third of the cycles.
 #include "attention_common.h"
 
 namespace fp4q {

@@ -3,12 +3,14 @@
 // its gradients).  The operations are defined in include/fp4q.h.
 //
 // The router is bound by vector instructions and by the chain of its k rounds:
-// 16384 x 128, k 8, takes 7.9 us for the choice, 5.7 for the order and 6.3 for the
-// gradient, where its bytes would take 4 in all; 4096 x 256 with groups 11.7 and
-// 5.8 (about 1000 vector instructions a token, 64-bit scores among them).  The
-// combination is bound by HBM: 4096 x 8 rows of 2048 (BF16) take 39 us, which
-// also writes back what the call before left in the cache, the gradients 48 us
-// (285 MB, 5.9 TB/s).
+// 16384 x 128, k 8, takes 7.8 us for the choice, 5.6 for the order and 6.2 for the
+// gradient (14.0 for the plain softmax's, 370 vector instructions a token of 64-bit
+// arithmetic, which issue all the time), where its bytes would take 4 in all; 4096 x
+// 256 with groups 11.6 to 12.5 and 5.6 (920 vector instructions a token, 64-bit scores
+// among them, which issue in 63% of the cycles).  The combination is bound by HBM:
+// 4096 x 8 rows of 2048 (BF16) take 39 us, which also writes back what the call
+// before left in the cache, the gradients 48 us (285 MB, 5.9 TB/s); 2047 columns, of
+// which a lane takes one at a time, 65 and 94.
 #include "fp4q_device.h"
 #include "fp4q_internal.h"
 
@@ -812,8 +814,8 @@ __global__ __launch_bounds__(256) void k_combine_backward(CombineArgs p) {
 // The rows of d_y that no entry of row_of names become 0, a wave for 64 rows.
 // named[] was not cleared before k_combine_backward wrote it: what it holds for
 // a row counts where row_of bears it out, and then the row is named, whoever
-// wrote it.  (Zeroing all of d_y first would write it twice: 134 MB in the case
-// below, 25 us, where this launch takes 3.)
+// wrote it.  (Zeroing all of d_y first would write it twice: 134 MB for 4096 x 8 rows
+// of 2048 in BF16, at least 27 us, where this launch adds 2.8 to the pass.)
 template <bool F32, int VEC>
 __global__ __launch_bounds__(256) void k_zero_unnamed(CombineArgs p) {
   const int lane = threadIdx.x & 63;

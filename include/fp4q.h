@@ -755,8 +755,8 @@ int fp4q_kv_read(fp4q_format_t fmt, const uint8_t* cache, int64_t n_pages, int32
  * scores, their maximum and sums and the output are FP32, the weights are
  * rounded once to f16 or bf16 before they meet the values.  For NVFP4 q is
  * held in f16 relative to its row's largest magnitude (bf16 for MXFP4).
- * heads % kv_heads == 0; FP4Q_ERR_UNSUPPORTED: as for the cache, more
- * than 128 heads on one kv head, batch above 65535, batch * kv_heads not
+ * heads % kv_heads == 0; FP4Q_ERR_UNSUPPORTED: a dim, page, kv_heads or
+ * table that the cache's calls do not take, more than 128 heads on one kv head, batch above 65535, batch * kv_heads not
  * below 2^22, rows * heads or max_new * heads not below 2^31, max_new *
  * heads / kv_heads above 65535 * 256 (dim 256: 65535 * 128), or max_len
  * above 2^31 - 4096 (the workspace query gives 0 for these). */
