@@ -928,6 +928,9 @@ int fp4q_kv_attention(fp4q_format_t fmt, const uint8_t* cache, int64_t n_pages, 
   if (max_new < 1 || !packed_ok(q, ldq, cols) || !packed_ok(y, ldy, cols)) return FP4Q_ERR_INVALID;
   if (!fp4q::attention_shape_ok(rows, dim, batch, kv_heads, heads / kv_heads, max_new, max_len, window))
     return FP4Q_ERR_UNSUPPORTED;
+  // the kernels look up to 2^12 keys past the last in 32 bits
+  const int64_t far = ((int64_t)1 << 31) - 4096;
+  if (max_len > far && table_cols * page > far) return FP4Q_ERR_UNSUPPORTED;
   const size_t need = fp4q_kv_attention_workspace_bytes(fmt, rows, heads, kv_heads, dim, batch,
                                                         max_new, max_len, window);
   if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))

@@ -410,13 +410,12 @@ void launch(const AttnArgs& p, const Plan& pl, int H, int B, hipStream_t stream)
 
 }  // namespace
 
-// Sizes that the launch can hold.  (The kernels look up to 2^12 keys past the
-// last in 32 bits.)
+// Sizes that the launch can hold.
 bool attention_shape_ok(int64_t rows, int D, int B, int H, int G, int64_t max_new, int64_t max_len,
                         int window) {
   const int64_t heads = (int64_t)H * G, most = (int64_t)1 << 31;
   if (G > 128 || B > 65535 || (int64_t)B * H >= (1 << 22) || rows >= most / heads ||
-      max_new >= most / heads || max_len > most - 4096)
+      max_new >= most / heads || max_len >= most)
     return false;
   const Plan pl = attn_plan(D, B, H, G, max_new, max_len, window);
   return pl.tiles <= 65535 && pl.splits <= 65535;  // (the grid's second and third dimension)

@@ -756,10 +756,12 @@ int fp4q_kv_read(fp4q_format_t fmt, const uint8_t* cache, int64_t n_pages, int32
  * rounded once to f16 or bf16 before they meet the values.  For NVFP4 q is
  * held in f16 relative to its row's largest magnitude (bf16 for MXFP4).
  * heads % kv_heads == 0; FP4Q_ERR_UNSUPPORTED: a dim, page, kv_heads or
- * table that the cache's calls do not take, more than 128 heads on one kv head, batch above 65535, batch * kv_heads not
- * below 2^22, rows * heads or max_new * heads not below 2^31, max_new *
- * heads / kv_heads above 65535 * 256 (dim 256: 65535 * 128), or max_len
- * above 2^31 - 4096 (the workspace query gives 0 for these). */
+ * table that the cache's calls do not take, more than 128 heads on one kv
+ * head, batch above 65535, batch * kv_heads not below 2^22, rows * heads or
+ * max_new * heads not below 2^31, max_new * heads / kv_heads above 65535 *
+ * 256 (dim 256: 65535 * 128), max_len not below 2^31, or both max_len and
+ * the table's tokens above 2^31 - 4096.  The workspace query gives 0 for
+ * what its own arguments show to be refused. */
 size_t fp4q_kv_attention_workspace_bytes(fp4q_format_t fmt, int64_t rows, int32_t heads,
                                          int32_t kv_heads, int32_t dim, int32_t batch,
                                          int64_t max_new, int64_t max_len, int32_t window);

@@ -53,14 +53,18 @@ def attention(L, rows=5, heads=4, kv_heads=2, dim=128, batch=2, max_new=1, max_l
 
 def test_lengths_up_to_the_limit(L):
     """Up to 2^31 - 4096 keys; the kernels' 32-bit key numbers go a little past
-    the last one."""
+    the last one.  A larger max_len is taken where the table ends before."""
     long = (1 << 31) - 4096
+    whole = dict(page=1024, cols=(1 << 21) - 1)
     for over in (dict(), dict(max_new=40, rows=40), dict(batch=1, kv_heads=1, dim=64)):
-        need, call = attention(L, max_len=long, page=1024, cols=(1 << 21) - 1, **over)
+        need, call = attention(L, max_len=long, **whole, **over)
         assert need > 0 and passes(call), over
         for more in (1, 4095):
-            need, call = attention(L, max_len=long + more, page=1024, cols=(1 << 21) - 1, **over)
-            assert need == 0 and call() == UNSUPPORTED, (over, more)
+            assert attention(L, max_len=long + more, **whole, **over)[1]() == UNSUPPORTED, (over, more)
+            assert passes(attention(L, max_len=long + more, page=1024, cols=(1 << 21) - 4, **over)[1]), (over, more)
+            assert passes(attention(L, max_len=long + more, **over)[1]), (over, more)
+        need, call = attention(L, max_len=1 << 31, **over)
+        assert need == 0 and call() == UNSUPPORTED, over
 
 
 @pytest.mark.parametrize("over", [dict(max_len=1 << 60), dict(max_new=1 << 60), dict(rows=1 << 60),

@@ -414,3 +414,13 @@ def test_sizes_without_room_are_refused():
     for max_new, max_len in ((1, 2 ** 62), (2 ** 62, 20), (2 ** 40, 2 ** 40)):
         with pytest.raises(fq.Fp4qError, match="-2"):
             fq.kv_attention(*where, dev(c["q"], torch.bfloat16), max_new, max_len)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("n,G", [(1, 4), (30, 3)])
+def test_the_largest_max_len_over_short_sequences(fmt, n, G):
+    need_gpu()
+    c = make(fmt, [n, 1], [300, 77], G=G, H=2, D=128, page=16, seed=n)
+    for max_len in (2 ** 31 - 4096, 2 ** 31 - 1):
+        check_close(c, attend(c, max_len=max_len))
+        check_close(c, attend(c, 100, max_len=max_len), 100)
