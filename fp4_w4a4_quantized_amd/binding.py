@@ -15,13 +15,14 @@ import torch
 
 NVFP4 = 0
 MXFP4 = 1
+MXFP8 = 2
 OUT_F32 = 0
 OUT_BF16 = 1
 ROWMAJOR = 0
 TILED = 1
 SOFTMAX = 0
 SIGMOID = 1
-BLOCK = {NVFP4: 16, MXFP4: 32}
+BLOCK = {NVFP4: 16, MXFP4: 32, MXFP8: 32}
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libfp4q.so")
 _lib = None
@@ -166,6 +167,35 @@ def lib():
         L.fp4q_kv_read.argtypes = kv + [P, i64, P, i64, P, P, P]
         L.fp4q_kv_attention_workspace_bytes.restype = sz
         L.fp4q_kv_attention_workspace_bytes.argtypes = [i, i64, i32, i32, i32, i32, i64, i64, i32]
+        L.fp4q_kv_attention_sinks_workspace_bytes.restype = sz
+        L.fp4q_kv_attention_sinks_workspace_bytes.argtypes = [i, i64, i32, i32, i32, i32, i64, i64,
+                                                              i32, i32]
+        L.fp4q_kv_attention_sinks.restype = i
+        L.fp4q_kv_attention_sinks.argtypes = kv + [P, i64, i32, i64, i64, i32, i32, f32, P, P, P, i,
+                                                   i64, P, sz, P]
+        L.fp4q_kv_append_rotated.restype = i
+        L.fp4q_kv_append_rotated.argtypes = kv + [P, i64, i32, P, i64, P, i64, P, i64, P, i32, i, P,
+                                                  P, P, P]
+        f64 = ctypes.c_double
+        L.fp4q_rms_norm.restype = i
+        L.fp4q_rms_norm.argtypes = [i, P, i64, P, i64, P, i64, P, i, f64, i64, i64, P, i, i64, P, P]
+        L.fp4q_rms_norm_quantize_workspace_bytes.restype = sz
+        L.fp4q_rms_norm_quantize_workspace_bytes.argtypes = [i, i64, i32]
+        L.fp4q_rms_norm_quantize.restype = i
+        L.fp4q_rms_norm_quantize.argtypes = [i, i, i, P, i64, P, i64, P, i64, P, i, f64, i64, i64, P,
+                                             i32, P, P, P, i32, P, P, i, i64, P, P, sz, P]
+        L.fp4q_rms_norm_backward_workspace_bytes.restype = sz
+        L.fp4q_rms_norm_backward_workspace_bytes.argtypes = [i64, i64]
+        L.fp4q_rms_norm_backward.restype = i
+        L.fp4q_rms_norm_backward.argtypes = [i, P, i64, P, i, P, P, i, i64, P, i64, P, i64, P, i64,
+                                             i64, P, sz, P]
+        L.fp4q_dequantize.restype = i
+        L.fp4q_dequantize.argtypes = [i, i, P, P, P, i64, i64, P, i, i64, P]
+        L.fp4q_lora_workspace_bytes.restype = sz
+        L.fp4q_lora_workspace_bytes.argtypes = [i64, i32, i32, i64, i64]
+        L.fp4q_lora.restype = i
+        L.fp4q_lora.argtypes = [P, i64, P, P, P, i32, i32, P, P, i32, i64, i64, i64, P, i64, P, i,
+                                i64, P, sz, P]
         L.fp4q_kv_attention.restype = i
         L.fp4q_kv_attention.argtypes = kv + [P, i64, i32, i64, i64, i32, f32, P, P, P, i, i64, P,
                                              sz, P]
@@ -814,7 +844,8 @@ def _results(stream, call, *args):
     with torch.cuda.stream(stream):
         out = call(None, *args)
     for t in out if isinstance(out, tuple) else (out,):
-        t.record_stream(here)
+        if t is not None:
+            t.record_stream(here)
     return out
 
 
@@ -849,28 +880,123 @@ def kv_read(fmt, cache, page, offsets, page_table, lens, rows, dim, k_scale=None
                     v_scale, rows, dim)
 
 
+def kv_append_rotated_into(fmt, cache, page, offsets, page_table, lens, q, k, v, freqs, k_scale,
+                           v_scale, q_out, positions=None, interleaved=False, stream=None):
+    """kv_append_rotated() with the rotated queries into q_out, which may be q."""
+    _layer().append_rotated(_handle(stream), fmt, cache, page, offsets, page_table, lens, k_scale,
+                            v_scale, q, k, v, freqs, positions, interleaved, q_out)
+
+
+def kv_append_rotated(fmt, cache, page, offsets, page_table, lens, q, k, v, freqs, k_scale=None,
+                      v_scale=None, positions=None, interleaved=False, stream=None):
+    """kv_append() with the position rotation: each head's first 2 * len(freqs)
+    elements of q (bf16 [rows, heads, dim]) and k turn by position * freqs (f32,
+    on the GPU), pair p being elements p and p + len(freqs), or 2p and 2p + 1
+    (interleaved).  positions int32 [rows]: other ones than the tokens' places in
+    their sequences.  Returns the rotated q; rows of no sequence come as they
+    are."""
+    return _results(stream, _layer().append_rotated, fmt, cache, page, offsets, page_table, lens,
+                    k_scale, v_scale, q, k, v, freqs, positions, interleaved, None)
+
+
 def kv_attention_workspace_bytes(fmt, rows, heads, kv_heads, dim, batch, max_new, max_len,
-                                 window=0) -> int:
-    return lib().fp4q_kv_attention_workspace_bytes(fmt, rows, heads, kv_heads, dim, batch, max_new,
-                                                   max_len, window)
+                                 window=0, sinks=0) -> int:
+    return lib().fp4q_kv_attention_sinks_workspace_bytes(fmt, rows, heads, kv_heads, dim, batch,
+                                                         max_new, max_len, window, sinks)
 
 
 def kv_attention_into(fmt, cache, page, offsets, page_table, lens, q, max_new, max_len, k_scale,
-                      v_scale, window, scale, y, workspace, stream=None):
-    """fp4q_kv_attention: y bf16 or f32 [rows, heads, dim]."""
+                      v_scale, window, scale, y, workspace, stream=None, sinks=0):
+    """fp4q_kv_attention(_sinks): y bf16 or f32 [rows, heads, dim]."""
     _layer().attention_into(_handle(stream), fmt, cache, page, offsets, page_table, lens, k_scale,
-                            v_scale, q, max_new, max_len, window, scale, y, workspace)
+                            v_scale, q, max_new, max_len, window, scale, y, workspace, sinks)
 
 
 def kv_attention(fmt, cache, page, offsets, page_table, lens, q, max_new, max_len, k_scale=None,
-                 v_scale=None, window=0, scale=None, y_dtype=OUT_BF16, stream=None):
+                 v_scale=None, window=0, scale=None, y_dtype=OUT_BF16, stream=None, sinks=0):
     """Attention of the new tokens' q (bf16 [rows, heads, dim]) over the cache
     (their keys and values appended before).  No sequence has more than
     max_new new tokens or is longer than max_len.  window > 0: a token sees
-    the last `window` keys only; scale: dim^-0.5 unless given.  Returns
-    [rows, heads, dim]."""
+    the last `window` keys only, and the sequence's first `sinks` ones; scale:
+    dim^-0.5 unless given.  Returns [rows, heads, dim]."""
     return _results(stream, _layer().attention, fmt, cache, page, offsets, page_table, lens,
-                    k_scale, v_scale, q, max_new, max_len, window, scale, y_dtype)
+                    k_scale, v_scale, q, max_new, max_len, window, scale, y_dtype, sinks)
+
+
+# ---- the norm, an operand's values, the adapters --------------------------
+
+def rms_norm_into(x, weight, eps, residual, h, y, rstd, stream=None):
+    """rms_norm() into y (f32 or bf16), h and rstd: residual and h both None, or of
+    x's type; h may be x or residual, y may be x."""
+    _results(stream, _layer().rms_norm, x, weight, eps, residual, None, y, rstd, h)
+
+
+def rms_norm(x, weight, eps=1e-6, residual=None, y_dtype=None, stream=None):
+    """The root-mean-square norm of h = x + residual (f32 or bf16 [rows, cols]):
+    dict(y: h / sqrt(mean(h^2) + eps) * weight, of x's type unless y_dtype says
+    otherwise; h, x itself without a residual; rstd f32 [rows], for
+    rms_norm_backward)."""
+    y, h, rstd = _results(stream, _layer().rms_norm, x, weight, eps, residual, y_dtype, None, None,
+                          None)
+    return {"y": y, "h": h, "rstd": rstd}
+
+
+def rms_norm_quantize(fmt, x, weight, eps=1e-6, residual=None, tscale=None, chan_idx=None,
+                      layout=ROWMAJOR, y_dtype=None, rstd=False, h=None, stream=None):
+    """rms_norm() into the operand of the product behind it: quantize(fmt, y,
+    chan_idx=chan_idx, layout=layout) of the BF16 y, as its dict, with h (given
+    or new), and y and rstd where they are asked for (y_dtype, rstd=True).
+    tscale f32 [1]: a calibrated tensor scale (NVFP4; one pass instead of two).
+    fmt may be MXFP8 (E4M3 codes u8 [rows, cols], E8M0 scales u8 [rows,
+    cols/32])."""
+    rows, cols = x.shape
+    n_chan = 0 if chan_idx is None else chan_idx.numel()
+    q, scales, ts, resid, y, h, r = _results(stream, _layer().rms_norm_quantize, x, weight, eps,
+                                             residual, fmt, layout, tscale, chan_idx, y_dtype, h,
+                                             n_chan, rstd)
+    return {"q": q, "scales": scales, "tscale": ts, "resid": resid, "layout": layout, "rows": rows,
+            "cols": cols, "h": h, "y": y, "rstd": r}
+
+
+def rms_norm_backward_into(h, weight, rstd, d_y, d_h, d_x, d_weight, stream=None):
+    """rms_norm_backward() into d_x and d_weight; d_x may be d_h, or d_y of h's
+    type."""
+    _results(stream, _layer().rms_norm_backward, h, weight, rstd, d_y, d_h, d_x, d_weight)
+
+
+def rms_norm_backward(h, weight, rstd, d_y, d_h=None, stream=None):
+    """(d_x, d_weight f32) of rms_norm() from its h and rstd, y's gradient and
+    that of h from elsewhere (d_h); d_x is the residual's gradient too."""
+    return _results(stream, _layer().rms_norm_backward, h, weight, rstd, d_y, d_h, None, None)
+
+
+def dequantize(fmt, a, dtype=OUT_BF16, stream=None):
+    """The values [rows, cols] that a quantize() or rms_norm_quantize() operand
+    of one group stands for."""
+    if "rows" in a:
+        rows, cols, layout = a["rows"], a["cols"], a["layout"]
+    else:
+        rows, cols, layout = a["q"].shape[0], a["q"].shape[1] * (1 if fmt == MXFP8 else 2), ROWMAJOR
+    return _results(stream, _layer().dequantize, fmt, layout, a["q"], a["scales"], a["tscale"],
+                    rows, cols, dtype)
+
+
+def lora_workspace_bytes(rows, requests, rank, K, N) -> int:
+    return lib().fp4q_lora_workspace_bytes(rows, requests, rank, K, N)
+
+
+def lora_into(x, a, b, offsets, adapters, scale, y, out, stream=None):
+    """lora() with the result in out, which may be y (y None: 0)."""
+    _results(stream, _layer().lora, x, a, b, offsets, adapters, scale, y, None, out)
+
+
+def lora(x, a, b, offsets, adapters, scale=None, y=None, y_dtype=None, stream=None):
+    """Low-rank adapters of many requests beside a shared projection: y + scale
+    (x a^T) b^T, each request's rows (offsets int32 [requests + 1]) with its
+    adapter (adapters int32 [requests], -1: none) of a (bf16 [n, rank, K]) and b
+    (bf16 [n, N, rank]); scale f32 [n] or None.  y f32 or bf16 [rows, N], the
+    projection's output, or None: the adapters' part alone (bf16, or y_dtype)."""
+    return _results(stream, _layer().lora, x, a, b, offsets, adapters, scale, y, y_dtype, None)
 
 
 # ---- the router and the combination ---------------------------------------

@@ -897,16 +897,94 @@ int fp4q_kv_read(fp4q_format_t fmt, const uint8_t* cache, int64_t n_pages, int32
                  batch, page_table, ld_table, table_cols, lens, rows, k, ldk, v, ldv, k_scale, v_scale, stream);
 }
 
+int fp4q_kv_append_rotated(fp4q_format_t fmt, uint8_t* cache, int64_t n_pages, int32_t page,
+                           int32_t kv_heads, int32_t dim, const int32_t* offsets, int32_t batch,
+                           const int32_t* page_table, int64_t ld_table, int64_t table_cols,
+                           const int32_t* lens, int64_t rows, const uint16_t* q, int64_t ldq,
+                           int32_t heads, uint16_t* q_out, int64_t ldqo, const uint16_t* k, int64_t ldk,
+                           const uint16_t* v, int64_t ldv, const float* freqs, int32_t rot,
+                           fp4q_pairs_t pairs, const int32_t* positions, const float* k_scale,
+                           const float* v_scale, void* stream) {
+  const int rc = kv_checks(fmt, cache, n_pages, page, kv_heads, dim, offsets, batch, page_table,
+                           ld_table, table_cols, lens, rows, k_scale, v_scale);
+  if (rc != FP4Q_OK && rc != FP4Q_ERR_UNSUPPORTED) return rc;
+  if (heads < 1 || rot < 0 || rot > dim || (pairs != FP4Q_PAIRS_HALVES && pairs != FP4Q_PAIRS_NEIGHBOURS) ||
+      !aligned(positions, 4))
+    return FP4Q_ERR_INVALID;
+  if (rc != FP4Q_OK) return rc;
+  if (rot % 16 != 0) return FP4Q_ERR_UNSUPPORTED;
+  if (rows == 0) return FP4Q_OK;
+  const int64_t cols = (int64_t)kv_heads * dim, qcols = (int64_t)heads * dim;
+  if (rows >= ((int64_t)1 << 26) || qcols >= ((int64_t)1 << 31))
+    return FP4Q_ERR_UNSUPPORTED;  // (before the packed tensors: a caller may not have made them)
+  if (!packed_ok(k, ldk, cols) || !packed_ok(v, ldv, cols) || !packed_ok(q, ldq, qcols) ||
+      !packed_ok(q_out, ldqo, qcols) || (rot > 0 && !freqs) || !aligned(freqs, 4))
+    return FP4Q_ERR_INVALID;
+  if (injected_failure()) return FP4Q_ERR_HIP;
+  clear_error();
+  fp4q::launch_kv_append_rotated(fmt, cache, n_pages, page_shift_of(page), kv_heads, dim, offsets, batch,
+                                 page_table, ld_table, table_cols, lens, rows, q, ldq, heads, q_out, ldqo,
+                                 k, ldk, v, ldv, freqs, rot / 2, pairs == FP4Q_PAIRS_HALVES, positions,
+                                 k_scale, v_scale, static_cast<hipStream_t>(stream));
+  return check_launch();
+}
+
+size_t fp4q_kv_attention_sinks_workspace_bytes(fp4q_format_t fmt, int64_t rows, int32_t heads,
+                                               int32_t kv_heads, int32_t dim, int32_t batch,
+                                               int64_t max_new, int64_t max_len, int32_t window,
+                                               int32_t sinks) {
+  if (!fmt_ok(fmt) || rows <= 0 || heads < 1 || kv_heads < 1 || heads % kv_heads != 0 ||
+      batch < 1 || max_new < 1 || max_len < 0 || window < 0 || sinks < 0 ||
+      (dim != 64 && dim != 128 && dim != 256) ||
+      !fp4q::attention_shape_ok(rows, dim, batch, kv_heads, heads / kv_heads, max_new, max_len, window,
+                                sinks))
+    return 0;
+  return fp4q::attention_workspace_bytes(rows, dim, batch, kv_heads, heads / kv_heads, max_new,
+                                         max_len, window, sinks);
+}
+
 size_t fp4q_kv_attention_workspace_bytes(fp4q_format_t fmt, int64_t rows, int32_t heads,
                                          int32_t kv_heads, int32_t dim, int32_t batch,
                                          int64_t max_new, int64_t max_len, int32_t window) {
-  if (!fmt_ok(fmt) || rows <= 0 || heads < 1 || kv_heads < 1 || heads % kv_heads != 0 ||
-      batch < 1 || max_new < 1 || max_len < 0 || window < 0 ||
-      (dim != 64 && dim != 128 && dim != 256) ||
-      !fp4q::attention_shape_ok(rows, dim, batch, kv_heads, heads / kv_heads, max_new, max_len, window))
-    return 0;
-  return fp4q::attention_workspace_bytes(rows, dim, batch, kv_heads, heads / kv_heads, max_new,
-                                         max_len, window);
+  return fp4q_kv_attention_sinks_workspace_bytes(fmt, rows, heads, kv_heads, dim, batch, max_new,
+                                                 max_len, window, 0);
+}
+
+int fp4q_kv_attention_sinks(fp4q_format_t fmt, const uint8_t* cache, int64_t n_pages, int32_t page,
+                            int32_t kv_heads, int32_t dim, const int32_t* offsets, int32_t batch,
+                            const int32_t* page_table, int64_t ld_table, int64_t table_cols,
+                            const int32_t* lens, int64_t rows, const uint16_t* q, int64_t ldq,
+                            int32_t heads, int64_t max_new, int64_t max_len, int32_t window,
+                            int32_t sinks, float scale, const float* k_scale, const float* v_scale,
+                            void* y, fp4q_dtype_t y_dtype, int64_t ldy, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+  const int rc = kv_checks(fmt, cache, n_pages, page, kv_heads, dim, offsets, batch, page_table,
+                           ld_table, table_cols, lens, rows, k_scale, v_scale);
+  if (rc != FP4Q_OK && rc != FP4Q_ERR_UNSUPPORTED) return rc;
+  if (!dtype_ok(y_dtype) || heads < 1 || heads % kv_heads != 0 || max_new < 0 || max_len < 0 ||
+      window < 0 || sinks < 0 || !(scale > 0.0f) || !(scale <= 3.4e38f))
+    return FP4Q_ERR_INVALID;
+  if (rc != FP4Q_OK) return rc;
+  if (rows == 0) return FP4Q_OK;
+  const int64_t cols = (int64_t)heads * dim;
+  if (max_new < 1 || !packed_ok(q, ldq, cols) || !packed_ok(y, ldy, cols)) return FP4Q_ERR_INVALID;
+  if (!fp4q::attention_shape_ok(rows, dim, batch, kv_heads, heads / kv_heads, max_new, max_len, window,
+                                sinks))
+    return FP4Q_ERR_UNSUPPORTED;
+  // the kernels look up to 2^12 keys past the last in 32 bits
+  const int64_t far = ((int64_t)1 << 31) - 4096;
+  if (max_len > far && table_cols * page > far) return FP4Q_ERR_UNSUPPORTED;
+  const size_t need = fp4q_kv_attention_sinks_workspace_bytes(fmt, rows, heads, kv_heads, dim, batch,
+                                                              max_new, max_len, window, sinks);
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
+    return FP4Q_ERR_WORKSPACE;
+  if (injected_failure()) return FP4Q_ERR_HIP;
+  clear_error();
+  fp4q::launch_attention(fmt, cache, n_pages, page_shift_of(page), kv_heads, dim, offsets, batch,
+                         page_table, ld_table, table_cols, lens, q, ldq, rows, heads / kv_heads, max_new,
+                         max_len, window, sinks, scale, k_scale, v_scale, y, y_dtype == FP4Q_OUT_BF16,
+                         ldy, workspace, static_cast<hipStream_t>(stream));
+  return check_launch();
 }
 
 int fp4q_kv_attention(fp4q_format_t fmt, const uint8_t* cache, int64_t n_pages, int32_t page,
@@ -916,32 +994,10 @@ int fp4q_kv_attention(fp4q_format_t fmt, const uint8_t* cache, int64_t n_pages, 
                       int64_t max_new, int64_t max_len, int32_t window, float scale,
                       const float* k_scale, const float* v_scale, void* y, fp4q_dtype_t y_dtype,
                       int64_t ldy, void* workspace, size_t workspace_bytes, void* stream) {
-  const int rc = kv_checks(fmt, cache, n_pages, page, kv_heads, dim, offsets, batch, page_table,
-                           ld_table, table_cols, lens, rows, k_scale, v_scale);
-  if (rc != FP4Q_OK && rc != FP4Q_ERR_UNSUPPORTED) return rc;
-  if (!dtype_ok(y_dtype) || heads < 1 || heads % kv_heads != 0 || max_new < 0 || max_len < 0 ||
-      window < 0 || !(scale > 0.0f) || !(scale <= 3.4e38f))
-    return FP4Q_ERR_INVALID;
-  if (rc != FP4Q_OK) return rc;
-  if (rows == 0) return FP4Q_OK;
-  const int64_t cols = (int64_t)heads * dim;
-  if (max_new < 1 || !packed_ok(q, ldq, cols) || !packed_ok(y, ldy, cols)) return FP4Q_ERR_INVALID;
-  if (!fp4q::attention_shape_ok(rows, dim, batch, kv_heads, heads / kv_heads, max_new, max_len, window))
-    return FP4Q_ERR_UNSUPPORTED;
-  // the kernels look up to 2^12 keys past the last in 32 bits
-  const int64_t far = ((int64_t)1 << 31) - 4096;
-  if (max_len > far && table_cols * page > far) return FP4Q_ERR_UNSUPPORTED;
-  const size_t need = fp4q_kv_attention_workspace_bytes(fmt, rows, heads, kv_heads, dim, batch,
-                                                        max_new, max_len, window);
-  if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
-    return FP4Q_ERR_WORKSPACE;
-  if (injected_failure()) return FP4Q_ERR_HIP;
-  clear_error();
-  fp4q::launch_attention(fmt, cache, n_pages, page_shift_of(page), kv_heads, dim, offsets, batch,
-                         page_table, ld_table, table_cols, lens, q, ldq, rows, heads / kv_heads, max_new,
-                         max_len, window, scale, k_scale, v_scale, y, y_dtype == FP4Q_OUT_BF16,
-                         ldy, workspace, static_cast<hipStream_t>(stream));
-  return check_launch();
+  return fp4q_kv_attention_sinks(fmt, cache, n_pages, page, kv_heads, dim, offsets, batch, page_table,
+                                 ld_table, table_cols, lens, rows, q, ldq, heads, max_new, max_len, window,
+                                 0, scale, k_scale, v_scale, y, y_dtype, ldy, workspace, workspace_bytes,
+                                 stream);
 }
 
 size_t fp4q_route_workspace_bytes(int64_t tokens, int32_t experts) {
@@ -1064,6 +1120,180 @@ int fp4q_combine_backward_zeroed(fp4q_dtype_t dtype, const void* y, int64_t rows
   fp4q::launch_combine_backward(dtype == FP4Q_OUT_F32, y, rows, cols, ldy, row_of, weights, tokens,
                                 k, d_out, ldo, d_y, lddy, d_weights, static_cast<int32_t*>(workspace),
                                 static_cast<hipStream_t>(stream));
+  return check_launch();
+}
+
+}  // extern "C"
+
+// ---- the norm, an operand's values, the adapters ----------------------------
+
+namespace {
+
+// A [rows, cols] tensor of F32 or BF16.
+inline bool matrix_ok(const void* p, int dtype, int64_t ld, int64_t rows, int64_t cols) {
+  return ld >= cols && (rows == 0 || p) && aligned(p, dtype == FP4Q_OUT_F32 ? 4 : 2);
+}
+
+// What the norm's calls have in common.
+int norm_checks(int dtype, const void* weight, int w_dtype, int64_t rows, int64_t cols) {
+  if (!dtype_ok(dtype) || !dtype_ok(w_dtype) || rows < 0 || cols < 1) return FP4Q_ERR_INVALID;
+  if (!weight || !aligned(weight, w_dtype == FP4Q_OUT_F32 ? 4 : 2)) return FP4Q_ERR_INVALID;
+  if (cols > fp4q::norm_max_cols() || rows >= ((int64_t)1 << 31)) return FP4Q_ERR_UNSUPPORTED;
+  return FP4Q_OK;
+}
+
+int norm_forward_checks(int dtype, const void* x, int64_t ldx, const void* residual, int64_t ldr,
+                        const void* h, int64_t ldh, const void* weight, int w_dtype, double eps,
+                        int64_t rows, int64_t cols, const void* y, int y_dtype, int64_t ldy,
+                        const float* rstd) {
+  const int rc = norm_checks(dtype, weight, w_dtype, rows, cols);
+  if (rc != FP4Q_OK && rc != FP4Q_ERR_UNSUPPORTED) return rc;
+  if (!(eps >= 0.0) || !(eps <= 1e300) || !dtype_ok(y_dtype) || (residual != nullptr) != (h != nullptr) ||
+      !matrix_ok(x, dtype, ldx, rows, cols) || !aligned(rstd, 4))
+    return FP4Q_ERR_INVALID;
+  if (residual && (!matrix_ok(residual, dtype, ldr, rows, cols) || !matrix_ok(h, dtype, ldh, rows, cols)))
+    return FP4Q_ERR_INVALID;
+  if (y && !matrix_ok(y, y_dtype, ldy, rows, cols)) return FP4Q_ERR_INVALID;
+  return rc;
+}
+
+bool lora_shape_ok(int64_t rows, int32_t n_groups, int32_t rank, int64_t K, int64_t N) {
+  return rank % 8 == 0 && rank <= 128 && K % 8 == 0 && K < ((int64_t)1 << 31) && N < ((int64_t)1 << 31) &&
+         rows < (1 << 24) && n_groups < (1 << 24);
+}
+
+}  // namespace
+
+extern "C" {
+
+int fp4q_rms_norm(fp4q_dtype_t dtype, const void* x, int64_t ldx, const void* residual, int64_t ldr,
+                  void* h, int64_t ldh, const void* weight, fp4q_dtype_t w_dtype, double eps,
+                  int64_t rows, int64_t cols, void* y, fp4q_dtype_t y_dtype, int64_t ldy, float* rstd,
+                  void* stream) {
+  const int rc = norm_forward_checks(dtype, x, ldx, residual, ldr, h, ldh, weight, w_dtype, eps, rows,
+                                     cols, y, y_dtype, ldy, rstd);
+  if (rc != FP4Q_OK) return rc;
+  if (rows == 0) return FP4Q_OK;
+  if (!y) return FP4Q_ERR_INVALID;
+  if (injected_failure()) return FP4Q_ERR_HIP;
+  clear_error();
+  fp4q::launch_norm(dtype == FP4Q_OUT_F32, x, ldx, residual, ldr, h, ldh, weight, w_dtype == FP4Q_OUT_F32,
+                    eps, rows, (int)cols, y, y_dtype == FP4Q_OUT_F32, ldy, rstd, -1, false, nullptr, nullptr,
+                    nullptr, false, nullptr, 0, nullptr, nullptr, static_cast<hipStream_t>(stream));
+  return check_launch();
+}
+
+size_t fp4q_rms_norm_quantize_workspace_bytes(fp4q_format_t fmt, int64_t rows, int32_t scale_given) {
+  return fmt == FP4Q_NVFP4 && rows > 0 && !scale_given ? fp4q::norm_workspace_bytes(rows) : 0;
+}
+
+int fp4q_rms_norm_quantize(fp4q_format_t fmt, fp4q_layout_t layout, fp4q_dtype_t dtype, const void* x,
+                           int64_t ldx, const void* residual, int64_t ldr, void* h, int64_t ldh,
+                           const void* weight, fp4q_dtype_t w_dtype, double eps, int64_t rows,
+                           int64_t cols, const int32_t* chan_idx, int32_t n_chan, uint8_t* q,
+                           uint8_t* scales, float* tensor_scale, int32_t scale_given, uint16_t* resid,
+                           void* y, fp4q_dtype_t y_dtype, int64_t ldy, float* rstd, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  const int rc = norm_forward_checks(dtype, x, ldx, residual, ldr, h, ldh, weight, w_dtype, eps, rows,
+                                     cols, y, y_dtype, ldy, rstd);
+  if (rc != FP4Q_OK && rc != FP4Q_ERR_UNSUPPORTED) return rc;
+  if ((!fmt_ok(fmt) && fmt != FP4Q_MXFP8) || !layout_ok(layout) || cols % blk_of(fmt) != 0 ||
+      (layout == FP4Q_LAYOUT_TILED && (fmt == FP4Q_MXFP8 || cols % 128 != 0)))
+    return FP4Q_ERR_INVALID;
+  if (n_chan < 0 || n_chan > cols || (n_chan > 0) != (chan_idx != nullptr) ||
+      (n_chan > 0) != (resid != nullptr) || (n_chan > 0 && fmt == FP4Q_MXFP8) || !aligned(chan_idx, 4) ||
+      !aligned(resid, 2))
+    return FP4Q_ERR_INVALID;
+  if ((fmt == FP4Q_NVFP4) != (tensor_scale != nullptr) || !aligned(tensor_scale, 4)) return FP4Q_ERR_INVALID;
+  if (rows > 0 && (!q || !scales || !aligned(q, 16) || !aligned(scales, 4))) return FP4Q_ERR_INVALID;
+  if (rc != FP4Q_OK) return rc;
+  const size_t need = fp4q_rms_norm_quantize_workspace_bytes(fmt, rows, scale_given);
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 8)))
+    return FP4Q_ERR_WORKSPACE;
+  if (injected_failure()) return FP4Q_ERR_HIP;
+  clear_error();
+  fp4q::launch_norm(dtype == FP4Q_OUT_F32, x, ldx, residual, ldr, h, ldh, weight, w_dtype == FP4Q_OUT_F32,
+                    eps, rows, (int)cols, y, y_dtype == FP4Q_OUT_F32, ldy, rstd, fmt,
+                    layout == FP4Q_LAYOUT_TILED, q, scales, tensor_scale, scale_given != 0, chan_idx, n_chan,
+                    resid, workspace, static_cast<hipStream_t>(stream));
+  return check_launch();
+}
+
+size_t fp4q_rms_norm_backward_workspace_bytes(int64_t rows, int64_t cols) {
+  if (rows <= 0 || cols < 1 || cols > fp4q::norm_max_cols()) return 0;
+  return fp4q::norm_backward_workspace_bytes(rows, (int)cols);
+}
+
+int fp4q_rms_norm_backward(fp4q_dtype_t dtype, const void* h, int64_t ldh, const void* weight,
+                           fp4q_dtype_t w_dtype, const float* rstd, const void* d_y,
+                           fp4q_dtype_t dy_dtype, int64_t lddy, const void* d_h, int64_t lddh,
+                           void* d_x, int64_t lddx, float* d_weight, int64_t rows, int64_t cols,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+  const int rc = norm_checks(dtype, weight, w_dtype, rows, cols);
+  if (rc != FP4Q_OK && rc != FP4Q_ERR_UNSUPPORTED) return rc;
+  if (!dtype_ok(dy_dtype) || !matrix_ok(h, dtype, ldh, rows, cols) || !matrix_ok(d_y, dy_dtype, lddy, rows, cols) ||
+      !matrix_ok(d_x, dtype, lddx, rows, cols) || (d_h && !matrix_ok(d_h, dtype, lddh, rows, cols)) ||
+      (rows > 0 && !rstd) || !aligned(rstd, 4) || !d_weight || !aligned(d_weight, 4))
+    return FP4Q_ERR_INVALID;
+  if (rc != FP4Q_OK) return rc;
+  const size_t need = fp4q_rms_norm_backward_workspace_bytes(rows, cols);
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 4)))
+    return FP4Q_ERR_WORKSPACE;
+  if (injected_failure()) return FP4Q_ERR_HIP;
+  clear_error();
+  fp4q::launch_norm_backward(dtype == FP4Q_OUT_F32, h, ldh, weight, w_dtype == FP4Q_OUT_F32, rstd, d_y,
+                             dy_dtype == FP4Q_OUT_F32, lddy, d_h, lddh, d_x, lddx, d_weight, rows,
+                             (int)cols, workspace, static_cast<hipStream_t>(stream));
+  return check_launch();
+}
+
+int fp4q_dequantize(fp4q_format_t fmt, fp4q_layout_t layout, const uint8_t* q, const uint8_t* scales,
+                    const float* tensor_scale, int64_t rows, int64_t cols, void* y, fp4q_dtype_t y_dtype,
+                    int64_t ldy, void* stream) {
+  if ((!fmt_ok(fmt) && fmt != FP4Q_MXFP8) || !layout_ok(layout) || !dtype_ok(y_dtype) || rows < 0 || cols < 1 ||
+      cols % blk_of(fmt) != 0 || (layout == FP4Q_LAYOUT_TILED && (fmt == FP4Q_MXFP8 || cols % 128 != 0)))
+    return FP4Q_ERR_INVALID;
+  if ((fmt == FP4Q_NVFP4) != (tensor_scale != nullptr) || !aligned(tensor_scale, 4)) return FP4Q_ERR_INVALID;
+  if (!matrix_ok(y, y_dtype, ldy, rows, cols) ||
+      (rows > 0 && (!q || !scales || !aligned(q, 16) || !aligned(scales, 4))))
+    return FP4Q_ERR_INVALID;
+  if (rows >= ((int64_t)1 << 31) || cols >= ((int64_t)1 << 31) ||
+      (rows + 15) / 16 * ((cols + 511) / 512) >= (1 << 24))
+    return FP4Q_ERR_UNSUPPORTED;
+  if (rows == 0) return FP4Q_OK;
+  if (injected_failure()) return FP4Q_ERR_HIP;
+  clear_error();
+  fp4q::launch_dequantize(fmt, layout == FP4Q_LAYOUT_TILED, q, scales, tensor_scale, rows, cols, y,
+                          y_dtype == FP4Q_OUT_F32, ldy, static_cast<hipStream_t>(stream));
+  return check_launch();
+}
+
+size_t fp4q_lora_workspace_bytes(int64_t rows, int32_t n_groups, int32_t rank, int64_t K, int64_t N) {
+  if (rows <= 0 || n_groups < 1 || rank < 1 || K < 1 || N < 1 || !lora_shape_ok(rows, n_groups, rank, K, N))
+    return 0;
+  return fp4q::lora_workspace_bytes(rows, n_groups, rank, K, N);
+}
+
+int fp4q_lora(const uint16_t* x, int64_t ldx, const uint16_t* a, const uint16_t* b, const float* scale,
+              int32_t n_adapters, int32_t rank, const int32_t* offsets, const int32_t* adapter,
+              int32_t n_groups, int64_t rows, int64_t K, int64_t N, const void* y, int64_t ldy, void* out,
+              fp4q_dtype_t dtype, int64_t ldo, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!dtype_ok(dtype) || n_adapters < 1 || rank < 1 || n_groups < 1 || rows < 0 || K < 1 || N < 1 || ldx < K ||
+      !matrix_ok(out, dtype, ldo, rows, N) || (y && !matrix_ok(y, dtype, ldy, rows, N)))
+    return FP4Q_ERR_INVALID;
+  if (!a || !b || !offsets || !adapter || !aligned(a, 16) || !aligned(b, 16) || !aligned(scale, 4) ||
+      !aligned(offsets, 4) || !aligned(adapter, 4) || (y == out && ldy != ldo))
+    return FP4Q_ERR_INVALID;
+  if (rows > 0 && (!x || !aligned(x, 16) || ldx % 8 != 0)) return FP4Q_ERR_INVALID;
+  if (!lora_shape_ok(rows, n_groups, rank, K, N)) return FP4Q_ERR_UNSUPPORTED;
+  if (rows == 0) return FP4Q_OK;
+  const size_t need = fp4q_lora_workspace_bytes(rows, n_groups, rank, K, N);
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
+    return FP4Q_ERR_WORKSPACE;
+  if (injected_failure()) return FP4Q_ERR_HIP;
+  clear_error();
+  fp4q::launch_lora(dtype == FP4Q_OUT_F32, x, ldx, a, b, scale, n_adapters, rank, offsets, adapter, n_groups,
+                    rows, K, N, y, ldy, out, ldo, workspace, static_cast<hipStream_t>(stream));
   return check_launch();
 }
 

@@ -2,7 +2,7 @@
 // include/fp4q.h): per new token i and head,
 //   o_i = sum_j p_ij v_j / sum_j p_ij,  p_ij = exp(scale q_i.k_j - m_i),
 // over the keys j of its sequence with j <= position(i) (and j > position(i)
-// - window), in one pass over the keys with a running maximum and sum.
+// - window, or j among the first tokens that stay visible), in one pass over the keys with a running maximum and sum.
 //
 // The heads that share a key/value head are rows of the same product: row r
 // of a sequence's (kv head) is query r / G, head r % G of the group.  A wave
@@ -42,7 +42,7 @@ namespace {
 // the next step is loaded as soon as this step's is used up, into the same
 // registers (few enough for three waves on a SIMD), then V, and the numbers of
 // their pages one step before that.
-template <int FMT, int D, int NC, int WAVES>
+template <int FMT, int D, int NC, int WAVES, bool SINK>
 __global__ __launch_bounds__(64 * WAVES, D == 64 ? 4 : D == 128 && NC == 1 && WAVES == 4 ? 3 : 2) void k_attn_split(AttnArgs p) {
   typedef typename Num<FMT>::vec vec;
   typedef typename Num<FMT>::pair pair;
@@ -57,7 +57,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 4 : D == 128 && NC == 1 && WA
     zero_rest<D, 64 * WAVES>(p, b, h);
     return;
   }
-  const Range rg = tile_range(p, b, row0);
+  const Range rg = tile_range<SINK>(p, b, row0);
   const int split = blockIdx.z;
   if (split >= active_splits(p, rg)) return;
   const int k0 = rg.lo + split * p.chunk;
@@ -75,7 +75,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 4 : D == 128 && NC == 1 && WA
   auto load_ids = [&](int kt) {
 #pragma unroll
     for (int u = 0; u < 2; ++u)
-      ids[u] = table[min(kt + 16 * u + (lane & 1), k1 - 1) >> p.page_shift];
+      ids[u] = table[real_key<SINK>(p, rg, min(kt + 16 * u + (lane & 1), k1 - 1)) >> p.page_shift];
   };
   auto next_k = [&](int kt) {
 #pragma unroll
@@ -84,13 +84,13 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 4 : D == 128 && NC == 1 && WA
       next_good[u] = (uint32_t)id < n_pages && key < k1;
       // (for a page that is not in the cache some page's bytes, all masked)
       buf[u] = page_buffer(head + (next_good[u] ? id : 0) * page_stride, L::bytes(page));
-      load_k<FMT, D>(buf[u], page, key & (page - 1), lane, st[u]);
+      load_k<FMT, D>(buf[u], page, real_key<SINK>(p, rg, key) & (page - 1), lane, st[u]);
     }
   };
   auto next_v = [&](int kt) {
 #pragma unroll
     for (int u = 0; u < 2; ++u)
-      load_v<FMT, D>(buf[u], page, (kt + 16 * u) & (page - 1), lane, st[u]);
+      load_v<FMT, D>(buf[u], page, real_key<SINK>(p, rg, kt + 16 * u) & (page - 1), lane, st[u]);
   };
   constexpr int STRIDE = WAVES * KEYS;
   int kt = k0 + wave * KEYS;
@@ -103,7 +103,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 4 : D == 128 && NC == 1 && WA
 
   vec qf[NC][D / 32];
   float cf[NC], m[NC], z[NC];
-  int see_lo[NC], see_hi[NC];  // keys the column sees: [see_lo, see_hi)
+  int see_lo[NC], see_hi[NC];  // keys the column sees: [see_lo, see_hi), and the first ones
   v4f o[NC][D / 16];
   const float c0 = p.scale2 * (FMT == FP4Q_NVFP4 ? p.kts[h] : 1.0f);
 #pragma unroll
@@ -140,7 +140,9 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 4 : D == 128 && NC == 1 && WA
       }
     }
     next_k(kt + STRIDE);  // (past the last step: some page's bytes, not used)
-    const bool whole = good[0] && good[1] && kt >= all_lo && kt + KEYS <= all_hi;
+    const int key0 = real_key<SINK>(p, rg, kt);
+    const bool whole = good[0] && good[1] && (key0 >= all_lo || (SINK && key0 + KEYS <= p.sinks)) &&
+                       key0 + KEYS <= all_hi;
     float mt[NC], up = 0.0f;  // does some column's maximum run ahead of its kept one?
 #pragma unroll
     for (int n = 0; n < NC; ++n) {
@@ -149,8 +151,9 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 4 : D == 128 && NC == 1 && WA
         for (int u = 0; u < 2; ++u)
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            const int key = kt + 16 * u + 4 * g + r;
-            if (!good[u] || key < see_lo[n] || key >= see_hi[n]) x[n][u][r] = -__builtin_inff();
+            const int key = key0 + 16 * u + 4 * g + r;
+            if (!good[u] || (key < see_lo[n] && !(SINK && key < p.sinks)) || key >= see_hi[n])
+              x[n][u][r] = -__builtin_inff();
           }
       }
       const float t = fmaxf(fmaxf(fmaxf(x[n][0][0], x[n][0][1]), fmaxf(x[n][0][2], x[n][0][3])),
@@ -193,7 +196,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 4 : D == 128 && NC == 1 && WA
     if (!whole) {
 #pragma unroll
       for (int u = 0; u < 2; ++u)
-        zero_v_scales<FMT, D>(st[u], kt + 16 * u + 4 * g, !good[u], rg.seen, rg.hi);
+        zero_v_scales<FMT, D, SINK>(st[u], key0 + 16 * u + 4 * g, !good[u], rg.seen, rg.hi, p.sinks);
     }
     pv_all<FMT, D, 0, NC>(st[0], st[1], pb, o);
     next_v(kt + STRIDE);
@@ -293,7 +296,9 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs p) {
   if (s < p.slots && row >= p.off[0] && row < p.off[p.B]) {
     const int b = kv_sequence(p.off, p.B, row);
     const int qi = (int)(row - p.off[b]), tile = (qi * p.G + hh % p.G) / p.tile;
-    if (qi < p.max_new) n = min(active_splits(p, tile_range(p, b, tile * p.tile)), p.splits);
+    if (qi < p.max_new) n = min(active_splits(p, p.sink_end > 0 ? tile_range<true>(p, b, tile * p.tile)
+                                                          : tile_range<false>(p, b, tile * p.tile)),
+                              p.splits);
   }
   float m = -__builtin_inff(), z = 0.0f;
   v4f o = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -359,7 +364,7 @@ struct Plan {
   int64_t tiles;
 };
 
-Plan attn_plan(int D, int B, int H, int G, int64_t max_new, int64_t max_len, int window) {
+Plan attn_plan(int D, int B, int H, int G, int64_t max_new, int64_t max_len, int window, int sinks) {
   Plan p;
   const int64_t rows = max_new * G;
   p.wide = rows > 2 * ROWS;
@@ -369,7 +374,8 @@ Plan attn_plan(int D, int B, int H, int G, int64_t max_new, int64_t max_len, int
   p.tiles = (rows + p.tile - 1) / p.tile;
   int64_t keys = max_len;
   if (window > 0) {
-    const int64_t seen = (int64_t)window + (p.wide ? (p.tile + G - 1) / G + 1 : max_new) + p.step;
+    int64_t seen = (int64_t)window + (p.wide ? (p.tile + G - 1) / G + 1 : max_new) + p.step;
+    if (sinks > 0) seen += ((int64_t)sinks + p.step - 1) / p.step * p.step;
     keys = keys < seen ? keys : seen;
   }
   int64_t groups = B * (int64_t)H * p.tiles;
@@ -389,18 +395,23 @@ Plan attn_plan(int D, int B, int H, int G, int64_t max_new, int64_t max_len, int
   return p;
 }
 
+template <int FMT, int D, bool SINK>
+void launch_split(const AttnArgs& p, const Plan& pl, int H, int B, hipStream_t stream) {
+  const dim3 grid((unsigned)(B * H), (unsigned)pl.tiles, (unsigned)pl.splits), thr(64 * pl.waves);
+  if constexpr (D <= 128) {
+    if (pl.nc == 2) hipLaunchKernelGGL((k_attn_split<FMT, D, 2, 4, SINK>), grid, thr, 0, stream, p);
+    else if (pl.waves == 4) hipLaunchKernelGGL((k_attn_split<FMT, D, 1, 4, SINK>), grid, thr, 0, stream, p);
+    else hipLaunchKernelGGL((k_attn_split<FMT, D, 1, 8, SINK>), grid, thr, 0, stream, p);
+  } else {
+    hipLaunchKernelGGL((k_attn_split<FMT, D, 1, 4, SINK>), grid, thr, 0, stream, p);
+  }
+}
+
 template <int FMT, int D>
 void launch(const AttnArgs& p, const Plan& pl, int H, int B, hipStream_t stream) {
-  const dim3 grid((unsigned)(B * H), (unsigned)pl.tiles, (unsigned)pl.splits), thr(64 * pl.waves);
-  if (pl.wide) {
-    launch_attention_tile(FMT, D, p, (int)pl.tiles, B, stream);
-  } else if constexpr (D <= 128) {
-    if (pl.nc == 2) hipLaunchKernelGGL((k_attn_split<FMT, D, 2, 4>), grid, thr, 0, stream, p);
-    else if (pl.waves == 4) hipLaunchKernelGGL((k_attn_split<FMT, D, 1, 4>), grid, thr, 0, stream, p);
-    else hipLaunchKernelGGL((k_attn_split<FMT, D, 1, 8>), grid, thr, 0, stream, p);
-  } else {
-    hipLaunchKernelGGL((k_attn_split<FMT, D, 1, 4>), grid, thr, 0, stream, p);
-  }
+  if (pl.wide) launch_attention_tile(FMT, D, p, (int)pl.tiles, B, stream);
+  else if (p.sink_end > 0) launch_split<FMT, D, true>(p, pl, H, B, stream);
+  else launch_split<FMT, D, false>(p, pl, H, B, stream);
   if (pl.splits > 1) {
     const int per = 1024 / D / pl.join;  // rows and heads of a workgroup
     hipLaunchKernelGGL((k_attn_join<FMT, D>), dim3((unsigned)((p.slots + per - 1) / per)), dim3(256),
@@ -412,28 +423,28 @@ void launch(const AttnArgs& p, const Plan& pl, int H, int B, hipStream_t stream)
 
 // Sizes that the launch can hold.
 bool attention_shape_ok(int64_t rows, int D, int B, int H, int G, int64_t max_new, int64_t max_len,
-                        int window) {
+                        int window, int sinks) {
   const int64_t heads = (int64_t)H * G, most = (int64_t)1 << 31;
   if (G > 128 || B > 65535 || (int64_t)B * H >= (1 << 22) || rows >= most / heads ||
       max_new >= most / heads || max_len >= most)
     return false;
-  const Plan pl = attn_plan(D, B, H, G, max_new, max_len, window);
+  const Plan pl = attn_plan(D, B, H, G, max_new, max_len, window, sinks);
   return pl.tiles <= 65535 && pl.splits <= 65535;  // (the grid's second and third dimension)
 }
 
 size_t attention_workspace_bytes(int64_t rows, int D, int B, int H, int G, int64_t max_new,
-                                 int64_t max_len, int window) {
-  const Plan pl = attn_plan(D, B, H, G, max_new, max_len, window);
+                                 int64_t max_len, int window, int sinks) {
+  const Plan pl = attn_plan(D, B, H, G, max_new, max_len, window, sinks);
   return pl.splits > 1 ? (size_t)pl.splits * (size_t)(rows * H * G) * (size_t)(D + 2) * 4 : 0;
 }
 
 void launch_attention(int fmt, const uint8_t* cache, int64_t n_pages, int page_shift, int H, int D,
                       const int32_t* off, int B, const int32_t* table, int64_t ldt, int64_t table_cols,
                       const int32_t* lens, const uint16_t* q, int64_t ldq, int64_t rows, int G,
-                      int64_t max_new, int64_t max_len, int window, float scale, const float* kts,
+                      int64_t max_new, int64_t max_len, int window, int sinks, float scale, const float* kts,
                       const float* vts, void* y, int y_bf16, int64_t ldy, void* ws,
                       hipStream_t stream) {
-  const Plan pl = attn_plan(D, B, H, G, max_new, max_len, window);
+  const Plan pl = attn_plan(D, B, H, G, max_new, max_len, window, sinks);
   AttnArgs p = {};
   p.cache = cache;
   p.n_pages = n_pages;
@@ -452,6 +463,9 @@ void launch_attention(int fmt, const uint8_t* cache, int64_t n_pages, int page_s
   p.rows = (int)rows;
   p.max_new = (int)max_new;
   p.window = window;
+  // (without a window every key stays visible)
+  p.sinks = window > 0 ? (sinks < p.cap ? sinks : p.cap) : 0;
+  p.sink_end = (p.sinks + pl.step - 1) & ~(pl.step - 1);
   p.scale2 = scale * 1.44269504088896340736f;
   p.kts = kts;
   p.vts = vts;

@@ -23,6 +23,8 @@ struct AttnArgs {
   int rows;
   int max_new;  // new tokens of a sequence that are attended for (further ones give 0)
   int window;
+  int sinks;     // first tokens that stay visible behind the window (0: none)
+  int sink_end;  // sinks up to a step's boundary
   float scale2;  // softmax scale * log2(e)
   const float* kts;
   const float* vts;
@@ -57,11 +59,17 @@ constexpr int ROWS = 16;         // rows of a wave (columns of its products)
 constexpr int KEYS = 32;         // keys of a step
 
 // Keys [seen, hi) that some row of the tile sees (none if there are none
-// left), lo: seen brought down to a step's boundary.
+// left), lo: seen brought down to a step's boundary.  The kernels count their
+// steps over [lo, end).  Without first tokens that stay visible (SINK) that is
+// [lo, hi); with them the keys between sink_end and the window's first step are
+// left out of the count: lo is 0, the keys from sink_end on are `skip`
+// further along (real_key), and as sink_end and skip are multiples of a step,
+// no step has keys of both kinds.
 struct Range {
   int64_t r0;       // first new-token row of the sequence
   int n, first;     // new tokens, position of the first (below 0 if there are too many)
   int seen, lo, hi, rows;
+  int end, skip;
 };
 
 // New-token rows of sequence b times the heads of a kv head (none past max_new,
@@ -77,6 +85,7 @@ __device__ __forceinline__ int first_key(const AttnArgs& p, int pos) {
   return p.window > 0 && pos >= p.window ? pos - p.window + 1 : 0;
 }
 
+template <bool SINK>
 __device__ __forceinline__ Range tile_range(const AttnArgs& p, int b, int row0) {
   Range r;
   r.r0 = p.off[b];
@@ -90,17 +99,32 @@ __device__ __forceinline__ Range tile_range(const AttnArgs& p, int b, int row0) 
   r.seen = first_key(p, r.first + q_lo);
   // (never past the keys that there are: the waves count on from it)
   r.lo = min(r.seen, max(r.hi, 0)) & ~(p.step - 1);
+  r.end = r.hi;
+  r.skip = 0;
+  if (SINK) {
+    if (r.lo > p.sink_end) {
+      r.skip = r.lo - p.sink_end;
+      r.end -= r.skip;
+    }
+    r.lo = 0;
+  }
   return r;
+}
+
+// The key that stands at `kt` of the count.
+template <bool SINK>
+__device__ __forceinline__ int real_key(const AttnArgs& p, const Range& r, int kt) {
+  return SINK && kt >= p.sink_end ? kt + r.skip : kt;
 }
 
 // Splits of the tile's keys, and where one that begins at k0 ends.
 __device__ __forceinline__ int active_splits(const AttnArgs& p, const Range& r) {
-  const int keys = r.hi - r.lo;
+  const int keys = r.end - r.lo;
   return keys > 0 ? (keys - 1) / p.chunk + 1 : 1;  // (keys + chunk may pass 2^31)
 }
 
 __device__ __forceinline__ int split_end(const AttnArgs& p, const Range& r, int k0) {
-  return r.hi - k0 > p.chunk ? k0 + p.chunk : r.hi;
+  return r.end - k0 > p.chunk ? k0 + p.chunk : r.end;
 }
 
 template <int FMT> struct Num;
@@ -281,15 +305,16 @@ __device__ __forceinline__ void v_rows(const Sub<FMT, D>& s, F f) {
   if constexpr (JJ + 1 < D / 32) v_rows<FMT, D, JJ + 1>(s, f);
 }
 
-// The V scales of tokens key .. key + 3 outside [seen, hi) become 0 (all of
-// them where the page is not in the cache): what stands there may be
-// anything, and a weight of 0 would not remove a NaN.
-template <int FMT, int D>
-__device__ __forceinline__ void zero_v_scales(Sub<FMT, D>& s, int key, bool all, int seen, int hi) {
+// The V scales of tokens key .. key + 3 that are neither in [seen, hi) nor among
+// the first `sinks` become 0 (all of them where the page is not in the cache):
+// what stands there may be anything, and a weight of 0 would not remove a NaN.
+template <int FMT, int D, bool SINK>
+__device__ __forceinline__ void zero_v_scales(Sub<FMT, D>& s, int key, bool all, int seen, int hi,
+                                              int sinks) {
   constexpr int SB = KvLayout<FMT, D>::SB;
 #pragma unroll
   for (int t = 0; t < 4; ++t) {
-    if (!all && key + t >= seen && key + t < hi) continue;
+    if (!all && (key + t >= seen || (SINK && key + t < sinks)) && key + t < hi) continue;
 #pragma unroll
     for (int i = 0; i < Sub<FMT, D>::VS; ++i) {
       uint32_t keep = 0xFFFFFFFFu;

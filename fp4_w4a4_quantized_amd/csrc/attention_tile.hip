@@ -98,7 +98,7 @@ __device__ __forceinline__ void pipeline_reads() {
   __builtin_amdgcn_sched_group_barrier(0x008, AHEAD, 0);
 }
 
-template <int FMT, int D, int WAVES>
+template <int FMT, int D, int WAVES, bool SINK>
 __global__ __launch_bounds__(64 * WAVES)
     __attribute__((amdgpu_waves_per_eu(D == 64 ? 4 : D == 128 ? 2 : 1))) void k_attn_tile(AttnArgs p) {
   typedef typename Num<FMT>::vec vec;
@@ -125,7 +125,7 @@ __global__ __launch_bounds__(64 * WAVES)
   const int tile_id = min((n_rows + p.tile - 1) / p.tile, (int)gridDim.y) - 1 - (int)blockIdx.y;
   if (tile_id < 0) return;
   const int row0 = tile_id * p.tile;
-  const Range rg = tile_range(p, b, row0);
+  const Range rg = tile_range<SINK>(p, b, row0);
   const int split = blockIdx.z;
   if (split >= active_splits(p, rg)) return;
   const int k0 = rg.lo + split * p.chunk;
@@ -164,7 +164,7 @@ __global__ __launch_bounds__(64 * WAVES)
 #pragma unroll
     for (int n = 0; n < St::UNITS; ++n) {
       const int key = k0 + t * TILE_KEYS + 16 * (unit0 + n * (WAVES / 2));
-      st.id[n] = key < k1 ? table[key >> p.page_shift] : -1;
+      st.id[n] = key < k1 ? table[real_key<SINK>(p, rg, key) >> p.page_shift] : -1;
     }
   };
   // bytes of step t, from st.id; the K team notes which pages are good
@@ -176,7 +176,7 @@ __global__ __launch_bounds__(64 * WAVES)
       st.good[n] = good;
       // (for a page that is not in the cache some page's bytes, all masked)
       const uint8_t* base = p.cache + (good ? st.id[n] : 0) * page_stride + head0;
-      const int slot = (k0 + t * TILE_KEYS + 16 * unit) & (page - 1);
+      const int slot = real_key<SINK>(p, rg, k0 + t * TILE_KEYS + 16 * unit) & (page - 1);
       if (v_team) {
         uint32_t c[St::VC], s[St::VS];
         load_words(base + L::v_codes(page) + slot * (D / 2) + (uint32_t)(lane * (D / 8)), c);
@@ -213,9 +213,9 @@ __global__ __launch_bounds__(64 * WAVES)
         for (int i = 0; i < St::VC; ++i) s.v[i] = st.w[n][i];
 #pragma unroll
         for (int i = 0; i < St::VS; ++i) s.vs[i] = st.w[n][St::VC + i];
-        const int key = k0 + t * TILE_KEYS + 16 * unit;
-        if (!st.good[n] || key < rg.seen || key + 16 > rg.hi)
-          zero_v_scales<FMT, D>(s, key + 4 * (lane >> 4), !st.good[n], rg.seen, rg.hi);
+        const int key = real_key<SINK>(p, rg, k0 + t * TILE_KEYS + 16 * unit);
+        if (!st.good[n] || (key < rg.seen && !(SINK && key + 16 <= p.sinks)) || key + 16 > rg.hi)
+          zero_v_scales<FMT, D, SINK>(s, key + 4 * (lane >> 4), !st.good[n], rg.seen, rg.hi, p.sinks);
         uint8_t* dst = vdst + (t & 1) * S::VBYTES + unit * 32;
         v_rows<FMT, D, 0>(s, [&](int run, u32x2 lo, u32x2 hi) {
           *reinterpret_cast<u32x2*>(dst + (32 * run) * S::VROW) = lo;
@@ -276,8 +276,12 @@ __global__ __launch_bounds__(64 * WAVES)
   // written: three K buffers and two V buffers do.  Of the page flags, that of t
   // is read and that of t + 3 written (with the load): four do.
   // this wave's steps (those that some row of it sees)
-  int t_on = 0, t_off = wave_on ? min(steps, pos_z < k0 ? 0 : (pos_z - k0) / TILE_KEYS + 1) : 0;
-  if (p.window > 0) t_on = max(0, first_key(p, pos_a) - k0) / TILE_KEYS;
+  // (a window that skip is taken from begins after it, and so do the rows' positions)
+  const int last_kt = pos_z - rg.skip;
+  int t_on = 0, t_off = wave_on ? min(steps, last_kt < k0 ? 0 : (last_kt - k0) / TILE_KEYS + 1) : 0;
+  if (p.window > 0) t_on = max(0, first_key(p, pos_a) - rg.skip - k0) / TILE_KEYS;
+  const int t_sink = SINK ? max(0, p.sink_end - k0) / TILE_KEYS : 0;  // steps of the first tokens
+  auto is_on = [&](int t) { return (t >= t_on || (SINK && t < t_sink)) && t < t_off; };
   v16f x[NU];
   vec pb[2 * NU];
   const uint8_t* const kb = lds + col * S::KROW + half * 16;
@@ -305,10 +309,10 @@ __global__ __launch_bounds__(64 * WAVES)
       load_ids(3);
     }
     __syncthreads();
-    if (!v_team && t_on == 0 && t_off > 0) score(0);
+    if (!v_team && is_on(0)) score(0);
   }
   for (int t = 0; t < steps; ++t) {
-    const bool on = t >= t_on && t < t_off;
+    const bool on = is_on(t);
     if (v_team && on) score(t);
     const int ahead = v_team ? t + 1 : t + 2;
     decode(ahead);
@@ -316,16 +320,18 @@ __global__ __launch_bounds__(64 * WAVES)
     load_ids(ahead + 2);
     if (on) {
       const uint32_t ok = s_ok[t & 3];
-      const int kt = k0 + t * TILE_KEYS;
+      const int kt = real_key<SINK>(p, rg, k0 + t * TILE_KEYS);
       const bool whole = (__builtin_amdgcn_readfirstlane(ok) & ALL_OK) == ALL_OK && kt + TILE_KEYS <= pos_a + 1 &&
-                         kt + TILE_KEYS <= rg.hi && kt >= first_key(p, pos_z);
+                         kt + TILE_KEYS <= rg.hi &&
+                         (kt >= first_key(p, pos_z) || (SINK && kt + TILE_KEYS <= p.sinks));
       if (!whole) {
 #pragma unroll
         for (int u = 0; u < NU; ++u)
 #pragma unroll
           for (int r = 0; r < 16; ++r) {
             const int key = kt + 32 * u + 8 * (r >> 2) + 4 * half + (r & 3);
-            if (!((ok >> (8 * (2 * u + (r >> 3)))) & 1) || key < see_lo || key >= see_hi)
+            if (!((ok >> (8 * (2 * u + (r >> 3)))) & 1) || (key < see_lo && !(SINK && key < p.sinks)) ||
+                key >= see_hi)
               x[u][r] = -__builtin_inff();
           }
       }
@@ -385,7 +391,7 @@ __global__ __launch_bounds__(64 * WAVES)
           o[i] = Wide<FMT>::mfma(*reinterpret_cast<const vec*>(v + i * 32 * S::VROW + e * 32), pb[e], o[i]);
       pipeline_reads<NU * D / 16, D == 64 ? 2 : 8>();
     }
-    if (!v_team && t + 1 >= t_on && t + 1 < t_off) score(t + 1);
+    if (!v_team && is_on(t + 1)) score(t + 1);
     __syncthreads();
   }
 
@@ -424,8 +430,12 @@ __global__ __launch_bounds__(64 * WAVES)
 template <int FMT, int D, int WAVES>
 void launch(const AttnArgs& p, int tiles, int B, hipStream_t stream) {
   const dim3 grid((unsigned)(B * p.H), (unsigned)tiles, (unsigned)p.splits);
-  hipLaunchKernelGGL((k_attn_tile<FMT, D, WAVES>), grid, dim3(64 * WAVES), TileLds<D>::BYTES,
-                     stream, p);
+  if (p.sink_end > 0)
+    hipLaunchKernelGGL((k_attn_tile<FMT, D, WAVES, true>), grid, dim3(64 * WAVES), TileLds<D>::BYTES,
+                       stream, p);
+  else
+    hipLaunchKernelGGL((k_attn_tile<FMT, D, WAVES, false>), grid, dim3(64 * WAVES), TileLds<D>::BYTES,
+                       stream, p);
 }
 
 template <int FMT>

@@ -74,6 +74,17 @@ __device__ __forceinline__ int mx_exponent(float amax) {
   return e < -127 ? -127 : e;
 }
 
+// MXFP8 block exponent: smallest e in [-127, 127] with 448 * 2^e >= amax.
+// amax = f * 2^E, f in [1, 2): e = E - 8 when f <= 1.75, else E - 7.
+__device__ __forceinline__ int mx8_exponent(float amax) {
+  uint32_t u = __float_as_uint(amax);
+  int ef = (int)(u >> 23);
+  if (ef == 0) return -127;  // zero or subnormal amax: 448 * 2^-127 covers it
+  int E = ef - 127;
+  int e = ((u & 0x7FFFFFu) <= 0x600000u) ? E - 8 : E - 7;
+  return e < -127 ? -127 : e;
+}
+
 // 2^e as float for e in [-127, 127] (2^-127 is an FP32 subnormal).
 __device__ __forceinline__ float exp2i(int e) {
   return e >= -126 ? __uint_as_float((uint32_t)(e + 127) << 23) : __uint_as_float(0x00400000u);

@@ -144,14 +144,21 @@ void launch_kv_copy(bool append, int fmt, uint8_t* cache, int64_t n_pages, int p
                     int D, const int32_t* off, int B, const int32_t* table, int64_t ldt, int64_t table_cols,
                     const int32_t* lens, int64_t rows, uint16_t* k, int64_t ldk, uint16_t* v,
                     int64_t ldv, const float* kts, const float* vts, hipStream_t stream);
+void launch_kv_append_rotated(int fmt, uint8_t* cache, int64_t n_pages, int page_shift, int H, int D,
+                              const int32_t* off, int B, const int32_t* table, int64_t ldt,
+                              int64_t table_cols, const int32_t* lens, int64_t rows, const uint16_t* q,
+                              int64_t ldq, int heads, uint16_t* qo, int64_t ldqo, const uint16_t* k,
+                              int64_t ldk, const uint16_t* v, int64_t ldv, const float* freqs, int half,
+                              bool halves, const int32_t* positions, const float* kts, const float* vts,
+                              hipStream_t stream);
 bool attention_shape_ok(int64_t rows, int D, int B, int H, int G, int64_t max_new, int64_t max_len,
-                        int window);
+                        int window, int sinks);
 size_t attention_workspace_bytes(int64_t rows, int D, int B, int H, int G, int64_t max_new,
-                                 int64_t max_len, int window);
+                                 int64_t max_len, int window, int sinks);
 void launch_attention(int fmt, const uint8_t* cache, int64_t n_pages, int page_shift, int H, int D,
                       const int32_t* off, int B, const int32_t* table, int64_t ldt, int64_t table_cols,
                       const int32_t* lens, const uint16_t* q, int64_t ldq, int64_t rows, int G,
-                      int64_t max_new, int64_t max_len, int window, float scale, const float* kts,
+                      int64_t max_new, int64_t max_len, int window, int sinks, float scale, const float* kts,
                       const float* vts, void* y, int y_bf16, int64_t ldy, void* ws,
                       hipStream_t stream);
 
@@ -171,6 +178,27 @@ void launch_combine_backward(int f32, const void* y, int64_t rows, int64_t N, in
                              const int32_t* row_of, const float* w, int64_t T, int k,
                              const void* d_out, int64_t ldo, void* d_y, int64_t lddy, float* d_w,
                              int32_t* named, hipStream_t stream);
+
+// The root-mean-square norm (fmt < 0: y only; else the quantized operand too), its
+// gradient, and an operand's values.
+int norm_max_cols();
+size_t norm_workspace_bytes(int64_t rows);
+void launch_norm(int f32, const void* x, int64_t ldx, const void* res, int64_t ldr, void* h, int64_t ldh,
+                 const void* w, int w_f32, double eps, int64_t rows, int cols, void* y, int y_f32, int64_t ldy,
+                 float* rstd, int fmt, bool tiled, uint8_t* q, uint8_t* scales, float* tscale, bool given,
+                 const int32_t* chan, int n_chan, uint16_t* resid, void* ws, hipStream_t stream);
+size_t norm_backward_workspace_bytes(int64_t rows, int cols);
+void launch_norm_backward(int f32, const void* h, int64_t ldh, const void* w, int w_f32, const float* rstd,
+                          const void* dy, int dy_f32, int64_t lddy, const void* dh, int64_t lddh, void* dx,
+                          int64_t lddx, float* dw, int64_t rows, int cols, void* ws, hipStream_t stream);
+void launch_dequantize(int fmt, bool tiled, const uint8_t* q, const uint8_t* scales, const float* tscale,
+                       int64_t rows, int64_t cols, void* y, int y_f32, int64_t ldy, hipStream_t stream);
+
+// Low-rank adapters beside a shared projection.
+size_t lora_workspace_bytes(int64_t rows, int G, int rank, int64_t K, int64_t N);
+void launch_lora(int f32, const uint16_t* x, int64_t ldx, const uint16_t* a, const uint16_t* b, const float* scale,
+                 int adapters, int rank, const int32_t* off, const int32_t* adapter, int G, int64_t rows, int64_t K,
+                 int64_t N, const void* y, int64_t ldy, void* out, int64_t ldo, void* ws, hipStream_t stream);
 
 size_t decompose_workspace_bytes(int64_t rows, int64_t cols);
 int launch_decompose(int fmt, const uint16_t* x, int64_t rows, int64_t cols, int64_t ldx,

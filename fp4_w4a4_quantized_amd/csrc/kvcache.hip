@@ -173,6 +173,37 @@ __device__ __forceinline__ void quant32(const uint32_t (&x)[16], float t, uint32
   }
 }
 
+// Run j of a token's scale codes, K codes and (as v_bytes_from_codes gives them) V
+// bytes into its head's page.
+template <int FMT, int D>
+__device__ __forceinline__ void store_scales(uint8_t* base, bool is_v, int page, int slot, int j, uint32_t s) {
+  typedef KvLayout<FMT, D> L;
+  uint8_t* sc = base + (is_v ? L::v_scales(page) : L::k_scales(page)) + slot * L::SB;
+  if (FMT == FP4Q_NVFP4) reinterpret_cast<uint16_t*>(sc)[j] = (uint16_t)s;
+  else sc[j] = (uint8_t)s;
+}
+
+template <int FMT, int D>
+__device__ __forceinline__ void store_k(uint8_t* base, int slot, int j, const uint32_t (&w)[4]) {
+  const u32x4 o = {w[0], w[1], w[2], w[3]};
+  *reinterpret_cast<u32x4*>(base + slot * (D / 2) + j * 16) = o;
+}
+
+template <int FMT, int D>
+__device__ __forceinline__ void store_v(uint8_t* base, int page, int slot, int j, u32x4 b) {
+  typedef KvLayout<FMT, D> L;
+  typedef typename Stretch<L::J>::type T;
+  uint8_t* dst = base + L::v_codes(page) + (slot >> 2) * (2 * D) + (slot & 3) * L::J + j * (16 / L::J) * 4 * L::J;
+#pragma unroll
+  for (int i = 0; i < 16 / L::J; ++i) {
+    T t;
+    if constexpr (L::J == 2) t = (T)(b[i >> 1] >> (16 * (i & 1)));
+    else if constexpr (L::J == 4) t = b[i];
+    else t = T{b[2 * i], b[2 * i + 1]};
+    *reinterpret_cast<T*>(dst + i * 4 * L::J) = t;
+  }
+}
+
 template <int FMT, int D>
 __global__ __launch_bounds__(KV_THREADS) void k_kv_append(KvArgs p) {
   typedef KvLayout<FMT, D> L;
@@ -193,25 +224,12 @@ __global__ __launch_bounds__(KV_THREADS) void k_kv_append(KvArgs p) {
   const float t = FMT == FP4Q_NVFP4 ? (is_v ? p.vts : p.kts)[it.h] : 1.0f;
   quant32<FMT>(x, t, w, s);
   const int page = 1 << p.page_shift;
-  uint8_t* sc = it.base + (is_v ? L::v_scales(page) : L::k_scales(page)) + it.slot * L::SB;
-  if (FMT == FP4Q_NVFP4) reinterpret_cast<uint16_t*>(sc)[it.j] = (uint16_t)s;
-  else sc[it.j] = (uint8_t)s;
+  store_scales<FMT, D>(it.base, is_v, page, it.slot, it.j, s);
   if (!is_v) {
-    u32x4 o = {w[0], w[1], w[2], w[3]};
-    *reinterpret_cast<u32x4*>(it.base + it.slot * (D / 2) + it.j * 16) = o;
+    store_k<FMT, D>(it.base, it.slot, it.j, w);
   } else {
-    typedef typename Stretch<L::J>::type T;
     const u32x4 b = v_bytes_from_codes<L::J>(w, it.j, s_v + threadIdx.x / L::J * (16 * L::J));
-    uint8_t* dst = it.base + L::v_codes(page) + (it.slot >> 2) * (2 * D) + (it.slot & 3) * L::J +
-                   it.j * (16 / L::J) * 4 * L::J;
-#pragma unroll
-    for (int i = 0; i < 16 / L::J; ++i) {
-      T t;
-      if constexpr (L::J == 2) t = (T)(b[i >> 1] >> (16 * (i & 1)));
-      else if constexpr (L::J == 4) t = b[i];
-      else t = T{b[2 * i], b[2 * i + 1]};
-      *reinterpret_cast<T*>(dst + i * 4 * L::J) = t;
-    }
+    store_v<FMT, D>(it.base, page, it.slot, it.j, b);
   }
 }
 
@@ -299,6 +317,200 @@ __global__ __launch_bounds__(KV_THREADS) void k_kv_read(KvArgs p) {
   }
 }
 
+// ---- append with the position rotation ----------------------------------------
+//
+// Queries and keys turn by their positions on the way: with a = position x
+// frequency, a pair (x1, x2) becomes (x1 cos a - x2 sin a, x2 cos a + x1 sin a),
+// rounded to F32 and then to BF16; keys and values go into the cache by
+// quant32's rule.  Angles, their sines and the products are 64-bit: at position
+// 10^5 a 32-bit angle is off by 2^-7, and a key next to one of the format's
+// borders would take another code than the definition's.
+//
+// A wave takes a token: its frequencies' sines and cosines are computed once,
+// into LDS, for all heads.  A lane then has 16 elements of a head (eight pairs,
+// or two chunks of eight that pass) of every 64 / (D/16)-th head, so that its
+// sines stay in registers and a wave's loads lie together.  The keys of those
+// heads pass through LDS to the lanes that quantize 32 of them.
+
+struct RotArgs {
+  KvArgs kv;
+  const uint16_t* q;
+  uint16_t* qo;
+  int64_t ldq, ldqo;
+  int heads, half;  // half: pairs of a head that turn (a multiple of 8)
+  bool halves;      // pair p: elements p and p + half; else 2p and 2p + 1
+  const float* freqs;
+  const int32_t* positions;  // or null: by the sequences
+  int per;                   // query heads of a part; 0: one part does all
+};
+
+// Sine and cosine for |a| < 2^40: a less the nearest multiple of pi/2 (whose
+// product with the first 53 bits of pi/2 leaves a exactly), then the Taylor
+// series to x^15 and x^16, whose next terms are below 2^-54 on [-pi/4, pi/4].
+__device__ __forceinline__ double2 cos_sin(double a) {
+  const double n = rint(a * 0.636619772367581343);
+  double x = __builtin_fma(-n, 0x1.921fb54442d18p+0, a);
+  x = __builtin_fma(-n, 0x1.1a62633145c07p-54, x);
+  const double z = x * x;
+  double s = -1.0 / 1307674368000.0, c = 1.0 / 20922789888000.0;
+  s = __builtin_fma(s, z, 1.0 / 6227020800.0);
+  c = __builtin_fma(c, z, -1.0 / 87178291200.0);
+  s = __builtin_fma(s, z, -1.0 / 39916800.0);
+  c = __builtin_fma(c, z, 1.0 / 479001600.0);
+  s = __builtin_fma(s, z, 1.0 / 362880.0);
+  c = __builtin_fma(c, z, -1.0 / 3628800.0);
+  s = __builtin_fma(s, z, -1.0 / 5040.0);
+  c = __builtin_fma(c, z, 1.0 / 40320.0);
+  s = __builtin_fma(s, z, 1.0 / 120.0);
+  c = __builtin_fma(c, z, -1.0 / 720.0);
+  s = __builtin_fma(s, z, -1.0 / 6.0);
+  c = __builtin_fma(c, z, 1.0 / 24.0);
+  s = __builtin_fma(s * z, x, x);
+  c = __builtin_fma(c, z, -0.5);
+  c = __builtin_fma(c, z, 1.0);
+  const int k = (int)((int64_t)n & 3);
+  const double cc = k & 1 ? s : c, ss = k & 1 ? c : s;
+  return make_double2(k == 1 || k == 2 ? -cc : cc, k >= 2 ? -ss : ss);
+}
+
+// The sequence of row r, by the whole wave: 64 offsets a step.
+__device__ __forceinline__ int wave_sequence(const int32_t* off, int B, int64_t r, int lane) {
+  int lo = 0, n = B;
+  while (n > 1) {
+    const int step = (n + 63) >> 6;
+    const int64_t at = (int64_t)lane * step;
+    const uint64_t m = __ballot(at < n && off[lo + (at < n ? (int)at : 0)] <= r);
+    const int k = max(__popcll(m), 1) - 1;
+    lo += k * step;
+    n = min(step, n - k * step);
+  }
+  return lo;
+}
+
+// Eight pairs: chunk a with chunk b (HALVES), or the neighbours within each.
+template <bool HALVES>
+__device__ __forceinline__ void turn(u32x4& a, u32x4& b, const double2 (&cs)[8]) {
+  auto one = [](uint32_t lo, uint32_t hi, double2 t) {  // (x1, x2) as BF16 bits -> two of them
+    const double x1 = bf16_to_f32(lo), x2 = bf16_to_f32(hi);
+    v2f32k f;
+    f[0] = (float)__builtin_fma(x1, t.x, -(x2 * t.y));
+    f[1] = (float)__builtin_fma(x2, t.x, x1 * t.y);
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f, bf16x2k));
+  };
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (HALVES) {
+      const uint32_t u = one(a[i] & 0xFFFFu, b[i] & 0xFFFFu, cs[2 * i]);
+      const uint32_t v = one(a[i] >> 16, b[i] >> 16, cs[2 * i + 1]);
+      a[i] = (u & 0xFFFFu) | (v << 16);
+      b[i] = (u >> 16) | (v & 0xFFFF0000u);
+    } else {
+      a[i] = one(a[i] & 0xFFFFu, a[i] >> 16, cs[i]);
+      b[i] = one(b[i] & 0xFFFFu, b[i] >> 16, cs[4 + i]);
+    }
+  }
+}
+
+template <int FMT, int D, bool HALVES>
+__global__ __launch_bounds__(KV_THREADS) void k_kv_append_rotated(RotArgs p) {
+  typedef KvLayout<FMT, D> L;
+  constexpr int ITEMS = D / 16, HEADS = 64 / ITEMS, WAVES = KV_THREADS / 64;
+  __shared__ double2 s_cs[WAVES][D / 2];
+  __shared__ u32x4 s_k[WAVES][HEADS * D / 8];
+  __shared__ u32x4 s_v[WAVES][32];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const KvArgs& c = p.kv;
+  const int64_t row = (int64_t)blockIdx.x * WAVES + wave;
+  if (row >= c.rows) return;
+
+  // where the token stands (of no sequence: its q is copied, nothing is stored)
+  const bool on = row >= c.off[0] && row < c.off[c.B];
+  uint8_t* page_of = nullptr;
+  int slot = 0;
+  int64_t at = 0;
+  if (on) {
+    const int b = __builtin_amdgcn_readfirstlane(wave_sequence(c.off, c.B, row, lane));
+    const int64_t pos = (int64_t)c.lens[b] - c.off[b + 1] + row;
+    const int64_t pg = pos >> c.page_shift;
+    if (pos >= 0 && pg < c.table_cols) {
+      const int64_t id = c.table[b * c.ldt + pg];
+      if (id >= 0 && id < c.n_pages) {
+        const int page = 1 << c.page_shift;
+        slot = (int)(pos & (page - 1));
+        page_of = c.cache + id * c.H * (int64_t)L::bytes(page);
+      }
+    }
+    at = p.positions ? (int64_t)p.positions[row] : pos;
+  }
+  if (on) {
+    for (int i = lane; i < p.half; i += 64) s_cs[wave][i] = cos_sin((double)at * (double)p.freqs[i]);
+  }
+  wave_fence();
+
+  // this lane's chunks of a head, and the pairs' cosines and sines
+  const int item = lane % ITEMS, h0 = lane / ITEMS;
+  const bool turns = on && item < p.half / 8;
+  const int c1 = HALVES && turns ? 8 * item : 16 * item;
+  const int c2 = HALVES && turns ? p.half + 8 * item : 16 * item + 8;
+  double2 cs[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) cs[i] = turns ? s_cs[wave][8 * item + i] : make_double2(1.0, 0.0);
+
+  if (p.per == 0 || blockIdx.y > 0) {
+    const int from = p.per == 0 ? 0 : (blockIdx.y - 1) * p.per;
+    const int to = p.per == 0 ? p.heads : min(p.heads, from + p.per);
+    const uint16_t* src = p.q + row * p.ldq;
+    uint16_t* dst = p.qo + row * p.ldqo;
+    for (int h = from + h0; h < to; h += HEADS) {
+      u32x4 a = *reinterpret_cast<const u32x4*>(src + h * D + c1);
+      u32x4 b = *reinterpret_cast<const u32x4*>(src + h * D + c2);
+      if (turns) turn<HALVES>(a, b, cs);
+      *reinterpret_cast<u32x4*>(dst + h * D + c1) = a;
+      *reinterpret_cast<u32x4*>(dst + h * D + c2) = b;
+    }
+  }
+  if ((p.per != 0 && blockIdx.y > 0) || page_of == nullptr) return;
+
+  // keys: by HEADS heads into LDS, from there 32 elements to each of the lower
+  // lanes; the upper ones quantize the same heads' values
+  const int page = 1 << c.page_shift, run = lane & 31, j = run % L::J;
+  const bool is_v = lane >= 32;
+  for (int hb = 0; hb < c.H; hb += HEADS) {
+    const int h = hb + h0, hq = hb + run / L::J;
+    if (h < c.H) {
+      const uint16_t* src = c.k + row * c.ldk + h * D;
+      u32x4 a = *reinterpret_cast<const u32x4*>(src + c1);
+      u32x4 b = *reinterpret_cast<const u32x4*>(src + c2);
+      if (turns) turn<HALVES>(a, b, cs);
+      s_k[wave][(h0 * D + c1) / 8] = a;
+      s_k[wave][(h0 * D + c2) / 8] = b;
+    }
+    wave_fence();
+    if (hq < c.H) {
+      uint32_t x[16], w[4], s;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const u32x4 u = is_v ? reinterpret_cast<const u32x4*>(c.v + row * c.ldv + hq * D + j * 32)[i]
+                             : s_k[wave][run * 4 + i];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[4 * i + e] = u[e];
+      }
+      const float t = FMT == FP4Q_NVFP4 ? (is_v ? c.vts : c.kts)[hq] : 1.0f;
+      quant32<FMT>(x, t, w, s);
+      uint8_t* base = page_of + hq * (int64_t)L::bytes(page);
+      store_scales<FMT, D>(base, is_v, page, slot, j, s);
+      if (!is_v) {
+        store_k<FMT, D>(base, slot, j, w);
+      } else {
+        const u32x4 b = v_bytes_from_codes<L::J>(w, j, reinterpret_cast<uint8_t*>(s_v[wave]) + run / L::J * (16 * L::J));
+        store_v<FMT, D>(base, page, slot, j, b);
+      }
+    }
+    wave_fence();
+  }
+}
+
 template <int FMT, int D>
 void launch(bool append, const KvArgs& p, hipStream_t stream) {
   const int64_t items = (p.rows + 3) / 4 * 4 * p.H * (D / 32);
@@ -307,7 +519,49 @@ void launch(bool append, const KvArgs& p, hipStream_t stream) {
   else hipLaunchKernelGGL((k_kv_read<FMT, D>), grid, dim3(KV_THREADS), 0, stream, p);
 }
 
+template <int FMT, int D>
+void launch_rotated(const RotArgs& p, hipStream_t stream) {
+  const int64_t blocks = (p.kv.rows + 3) / 4;
+  const dim3 grid((unsigned)blocks, p.per == 0 ? 1u : (unsigned)(1 + (p.heads + p.per - 1) / p.per));
+  if (p.halves) hipLaunchKernelGGL((k_kv_append_rotated<FMT, D, true>), grid, dim3(KV_THREADS), 0, stream, p);
+  else hipLaunchKernelGGL((k_kv_append_rotated<FMT, D, false>), grid, dim3(KV_THREADS), 0, stream, p);
+}
+
 }  // namespace
+
+void launch_kv_append_rotated(int fmt, uint8_t* cache, int64_t n_pages, int page_shift, int H, int D,
+                              const int32_t* off, int B, const int32_t* table, int64_t ldt,
+                              int64_t table_cols, const int32_t* lens, int64_t rows, const uint16_t* q,
+                              int64_t ldq, int heads, uint16_t* qo, int64_t ldqo, const uint16_t* k,
+                              int64_t ldk, const uint16_t* v, int64_t ldv, const float* freqs, int half,
+                              bool halves, const int32_t* positions, const float* kts, const float* vts,
+                              hipStream_t stream) {
+  RotArgs p = {};
+  p.kv = {cache, n_pages, page_shift, H, off, B, table, ldt, table_cols, lens, rows,
+          const_cast<uint16_t*>(k), const_cast<uint16_t*>(v), ldk, ldv, kts, vts};
+  p.q = q;
+  p.qo = qo;
+  p.ldq = ldq;
+  p.ldqo = ldqo;
+  p.heads = heads;
+  p.half = half;
+  p.halves = halves;
+  p.freqs = freqs;
+  p.positions = positions;
+  // Few tokens: their heads over several workgroups, each with its own sines.
+  const int once = 64 / (D / 16);  // heads that a wave has at a time
+  p.per = rows <= 2048 && heads > once ? once : 0;
+  if (p.per > 0 && (heads + p.per - 1) / p.per > 65534) p.per = 0;
+  if (fmt == FP4Q_NVFP4) {
+    if (D == 64) launch_rotated<FP4Q_NVFP4, 64>(p, stream);
+    else if (D == 128) launch_rotated<FP4Q_NVFP4, 128>(p, stream);
+    else launch_rotated<FP4Q_NVFP4, 256>(p, stream);
+  } else {
+    if (D == 64) launch_rotated<FP4Q_MXFP4, 64>(p, stream);
+    else if (D == 128) launch_rotated<FP4Q_MXFP4, 128>(p, stream);
+    else launch_rotated<FP4Q_MXFP4, 256>(p, stream);
+  }
+}
 
 void launch_kv_copy(bool append, int fmt, uint8_t* cache, int64_t n_pages, int page_shift, int H,
                     int D, const int32_t* off, int B, const int32_t* table, int64_t ldt, int64_t table_cols,

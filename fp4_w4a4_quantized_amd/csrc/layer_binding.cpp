@@ -1,5 +1,6 @@
 // layer_binding.cpp -- the Python module _layer: the calls between the FP4
-// linear layers (key/value cache, attention, router, combination) on tensors.
+// linear layers (key/value cache, attention, norm, adapters, router, combination)
+// on tensors.
 // It checks the tensors, allocates results and calls the C ABI of fp4q.h; the
 // package's binding.py gives them their public form.  A serving loop makes
 // these calls for every layer and step, where the checks in Python and ctypes
@@ -30,6 +31,8 @@ PyObject* g_fail = nullptr;     // fail(name, code): raises the package's error
 PyObject* g_device = nullptr;   // device(): the current device
 PyObject* g_current = nullptr;  // current(device): its current stream's handle
 const char* g_host = nullptr;   // a tensor of this call that is not on the GPU
+int g_gpu = -1;                 // the GPU of this call's tensors
+const char* g_apart = nullptr;  // a tensor on another one
 
 void check(const char* fn, int rc) {
   if (rc == FP4Q_OK) return;
@@ -46,7 +49,13 @@ void need(bool ok, const char* name, const char* what) {
 const at::Tensor& tensor(PyObject* o, const char* name) {
   need(THPVariable_Check(o), name, "a tensor is needed");
   const at::Tensor& t = THPVariable_Unpack(o);
-  if (!t.is_cuda()) g_host = name;
+  if (!t.is_cuda()) {
+    g_host = name;
+  } else if (g_gpu < 0) {
+    g_gpu = t.get_device();
+  } else if (g_gpu != t.get_device()) {
+    g_apart = name;
+  }
   return t;
 }
 
@@ -78,6 +87,15 @@ void* stream_of(PyObject* o) {
   return reinterpret_cast<void*>(v);
 }
 
+// The same for calls that take tensors of the current device only (a launch on
+// its stream that reads another device's memory may fault).
+void* stream_here(PyObject* o) {
+  void* const s = stream_of(o);
+  need(!g_apart, g_apart, "on another device than the first tensor");
+  need(g_gpu == at::detail::getCUDAHooks().getCurrentDevice(), "tensors", "not on the current device");
+  return s;
+}
+
 // [rows, heads, dim] of BF16 (or its bits) with the heads one after another.
 struct Packed {
   void* p;
@@ -102,7 +120,7 @@ struct Matrix {
 
 Matrix matrix(PyObject* o, const char* name) {
   const at::Tensor& t = tensor(o, name);
-  need(t.dim() == 2 && (t.size(1) <= 1 || t.stride(1) == 1), name,
+  need(t.dim() == 2 && (t.size(0) == 0 || t.size(1) <= 1 || t.stride(1) == 1), name,
        "a matrix with contiguous rows is needed");
   const auto dt = t.scalar_type();
   need(dt == at::kFloat || dt == at::kBFloat16, name, "f32 or bf16 is needed");
@@ -261,14 +279,53 @@ PyObject* read(PyObject* const* a) {
 }
 
 void attend(PyObject* const* a, const Kv& c, const Packed& q, int64_t max_new, int64_t max_len,
-            int32_t window, double scale, void* y, fp4q_dtype_t type, int64_t ldy, void* ws, size_t bytes) {
+            int32_t window, int32_t sinks, double scale, void* y, fp4q_dtype_t type, int64_t ldy, void* ws,
+            size_t bytes) {
   need(q.heads <= INT32_MAX, "q", "too many heads");
-  void* const stream = stream_of(a[0]);
-  check("fp4q_kv_attention",
-        fp4q_kv_attention(c.fmt, c.cache, c.n_pages, c.page, c.heads, c.dim, c.offsets, c.batch, c.table,
-                          c.ld, c.cols, c.lens, q.rows, (uint16_t*)q.p, q.ld, (int32_t)q.heads, max_new,
-                          max_len, window, (float)scale, c.ks, c.vs, y, type, ldy, ws, bytes,
-                          stream));
+  void* const stream = sinks ? stream_here(a[0]) : stream_of(a[0]);
+  check(sinks ? "fp4q_kv_attention_sinks" : "fp4q_kv_attention",
+        fp4q_kv_attention_sinks(c.fmt, c.cache, c.n_pages, c.page, c.heads, c.dim, c.offsets, c.batch, c.table,
+                                c.ld, c.cols, c.lens, q.rows, (uint16_t*)q.p, q.ld, (int32_t)q.heads, max_new,
+                                max_len, window, sinks, (float)scale, c.ks, c.vs, y, type, ldy, ws, bytes,
+                                stream));
+}
+
+// append_rotated(stream, fmt, cache, page, offsets, page_table, lens, k_scale, v_scale, q, k, v, freqs,
+// positions or None, interleaved, q_out or None) -> q_out
+PyObject* append_rotated(PyObject* const* a) {
+  const Packed q = packed(a[9], "q"), k = packed(a[10], "k"), v = packed(a[11], "v");
+  need(q.rows == k.rows && q.dim == k.dim, "k", "q's rows and dim are needed");
+  need(v.rows == k.rows && v.heads == k.heads && v.dim == k.dim, "v", "k's shape is needed");
+  const Kv c = kv(a, k.dim);
+  need(k.heads == c.heads, "k", "the cache's heads are needed");
+  need(q.heads <= INT32_MAX, "q", "too many heads");
+  const at::Tensor& f = tensor(a[12], "freqs");
+  need(f.scalar_type() == at::kFloat && f.is_contiguous(), "freqs", "contiguous f32 is needed");
+  need(f.numel() * 2 <= q.dim, "freqs", "more pairs than a head has");
+  const int32_t* pos = a[13] == Py_None ? nullptr : ints(a[13], "positions", q.rows);
+  const int pairs = PyObject_IsTrue(a[14]);
+  if (pairs < 0) throw PythonError();
+  Packed o = {};
+  at::Tensor made;
+  if (a[15] != Py_None) {
+    o = packed(a[15], "q_out");
+    need(o.rows == q.rows && o.heads == q.heads && o.dim == q.dim, "q_out", "q's shape is needed");
+  }
+  void* const stream = stream_here(a[0]);
+  if (a[15] == Py_None) {
+    const at::Tensor& qt = THPVariable_Unpack(a[9]);
+    made = like(qt, {q.rows, q.heads, q.dim}, qt.scalar_type());
+    o = {made.data_ptr(), q.rows, q.heads, q.dim, q.heads * q.dim};
+  }
+  check("fp4q_kv_append_rotated",
+        fp4q_kv_append_rotated(c.fmt, c.cache, c.n_pages, c.page, c.heads, c.dim, c.offsets, c.batch, c.table,
+                               c.ld, c.cols, c.lens, q.rows, (uint16_t*)q.p, q.ld, (int32_t)q.heads,
+                               (uint16_t*)o.p, o.ld, (uint16_t*)k.p, k.ld, (uint16_t*)v.p, v.ld,
+                               f.numel() ? f.data_ptr<float>() : nullptr, (int32_t)f.numel() * 2,
+                               pairs ? FP4Q_PAIRS_NEIGHBOURS : FP4Q_PAIRS_HALVES, pos, c.ks, c.vs, stream));
+  if (a[15] == Py_None) return wrap(made);
+  Py_INCREF(a[15]);
+  return a[15];
 }
 
 double number(PyObject* o) {
@@ -277,38 +334,355 @@ double number(PyObject* o) {
   return v;
 }
 
-// attention_into(... , q, max_new, max_len, window, scale, y, workspace)
+// attention_into(... , q, max_new, max_len, window, scale, y, workspace, sinks)
 PyObject* attention_into(PyObject* const* a) {
   const Packed q = packed(a[9], "q"), y = packed(a[14], "y", true);
   need(y.rows == q.rows && y.heads == q.heads && y.dim == q.dim, "y", "q's shape is needed");
   const Kv c = kv(a, q.dim);
   size_t bytes;
   void* ws = scratch(a[15], &bytes);
-  attend(a, c, q, integer(a[10]), integer(a[11]), small(a[12], "window"), number(a[13]), y.p,
+  attend(a, c, q, integer(a[10]), integer(a[11]), small(a[12], "window"), small(a[16], "sinks"), number(a[13]), y.p,
          THPVariable_Unpack(a[14]).scalar_type() == at::kFloat ? FP4Q_OUT_F32 : FP4Q_OUT_BF16, y.ld, ws,
          bytes);
   Py_RETURN_NONE;
 }
 
-// attention(..., q, max_new, max_len, window, scale or None, f32) -> y
+// attention(..., q, max_new, max_len, window, scale or None, f32, sinks) -> y
 PyObject* attention(PyObject* const* a) {
   const Packed q = packed(a[9], "q");
   const Kv c = kv(a, q.dim);
   const int64_t max_new = integer(a[10]), max_len = integer(a[11]);
-  const int32_t window = small(a[12], "window");
+  const int32_t window = small(a[12], "window"), sinks = small(a[15], "sinks");
   const double scale = a[13] == Py_None ? 1.0 / std::sqrt((double)q.dim) : number(a[13]);
   const bool f32 = integer(a[14]) == FP4Q_OUT_F32;
   const at::Tensor& qt = THPVariable_Unpack(a[9]);
   const at::Tensor y = like(qt, {q.rows, q.heads, q.dim}, f32 ? at::kFloat : at::kBFloat16);
   const size_t bytes =
       q.heads > INT32_MAX ? 0
-                          : fp4q_kv_attention_workspace_bytes(c.fmt, q.rows, (int32_t)q.heads, c.heads, c.dim,
-                                                              c.batch, max_new, max_len, window);
+                          : fp4q_kv_attention_sinks_workspace_bytes(c.fmt, q.rows, (int32_t)q.heads, c.heads,
+                                                                    c.dim, c.batch, max_new, max_len, window,
+                                                                    sinks);
   at::Tensor ws;
   if (bytes) ws = like(qt, {(int64_t)bytes}, at::kByte);
-  attend(a, c, q, max_new, max_len, window, scale, y.data_ptr(), f32 ? FP4Q_OUT_F32 : FP4Q_OUT_BF16,
+  attend(a, c, q, max_new, max_len, window, sinks, scale, y.data_ptr(), f32 ? FP4Q_OUT_F32 : FP4Q_OUT_BF16,
          q.heads * q.dim, bytes ? ws.data_ptr() : nullptr, bytes);
   return wrap(y);
+}
+
+// The norm's vector of `cols` weights, and its type.
+void* weights_of(PyObject* o, int64_t cols, fp4q_dtype_t* type) {
+  const at::Tensor& t = tensor(o, "weight");
+  const auto dt = t.scalar_type();
+  need(dt == at::kFloat || dt == at::kBFloat16, "weight", "f32 or bf16 is needed");
+  need(t.dim() == 1 && t.is_contiguous() && t.numel() == cols, "weight", "one for each column is needed");
+  *type = dt == at::kFloat ? FP4Q_OUT_F32 : FP4Q_OUT_BF16;
+  return t.data_ptr();
+}
+
+at::ScalarType scalar_of(int64_t type) { return type == FP4Q_OUT_F32 ? at::kFloat : at::kBFloat16; }
+
+// One call of the norm, its tensors checked: (stream, x, weight, eps, residual or
+// None) are arguments 0 .. 4.  h: the caller's, or None for a new one (x itself
+// where there is no residual).
+struct Norm {
+  Matrix x, res, h;
+  void* w;
+  fp4q_dtype_t w_type;
+  double eps;
+  at::Tensor made_h;
+  PyObject* h_obj;  // of the result, where it is not made_h
+};
+
+Norm norm_of(PyObject* const* a, PyObject* h) {
+  Norm n = {};
+  n.x = matrix(a[1], "x");
+  n.w = weights_of(a[2], n.x.cols, &n.w_type);
+  n.eps = number(a[3]);
+  n.h_obj = h;
+  if (a[4] == Py_None) {
+    need(h == Py_None, "h", "a residual is needed with it");
+    n.h_obj = a[1];
+    return n;
+  }
+  n.res = matrix(a[4], "residual");
+  need(n.res.type == n.x.type && n.res.rows == n.x.rows && n.res.cols == n.x.cols, "residual",
+       "x's shape and type are needed");
+  if (h != Py_None) {
+    n.h = matrix(h, "h");
+    need(n.h.type == n.x.type && n.h.rows == n.x.rows && n.h.cols == n.x.cols, "h",
+         "x's shape and type are needed");
+  }
+  return n;
+}
+
+// The result's h, made where the caller gave none.
+void make_h(PyObject* const* a, Norm& n) {
+  if (a[4] == Py_None || n.h_obj != Py_None) return;
+  n.made_h = like(THPVariable_Unpack(a[1]), {n.x.rows, n.x.cols}, scalar_of(n.x.type));
+  n.h = {n.made_h.data_ptr(), n.x.rows, n.x.cols, n.x.cols, n.x.type};
+}
+
+PyObject* result_h(const Norm& n) {
+  if (n.made_h.defined()) return wrap(n.made_h);
+  Py_INCREF(n.h_obj);
+  return n.h_obj;
+}
+
+PyObject* tuple_of(std::initializer_list<PyObject*> items) {  // takes the references
+  PyObject* t = PyTuple_New((Py_ssize_t)items.size());
+  Py_ssize_t i = 0;
+  for (PyObject* o : items) {
+    if (t) PyTuple_SET_ITEM(t, i++, o);
+    else Py_XDECREF(o);
+  }
+  return t;
+}
+
+PyObject* none() {
+  Py_INCREF(Py_None);
+  return Py_None;
+}
+
+fp4q_dtype_t dtype_of(PyObject* o, const char* name) {
+  const int32_t t = small(o, name);
+  need(t == FP4Q_OUT_F32 || t == FP4Q_OUT_BF16, name, "OUT_F32 or OUT_BF16 is needed");
+  return (fp4q_dtype_t)t;
+}
+
+// rms_norm(stream, x, weight, eps, residual, y_dtype or None (x's), y or None, rstd or None, h or None)
+// -> (y, h, rstd)
+PyObject* rms_norm(PyObject* const* a) {
+  Norm n = norm_of(a, a[8]);
+  const fp4q_dtype_t type = a[5] == Py_None ? n.x.type : dtype_of(a[5], "y_dtype");
+  Matrix y = {};
+  float* rstd = nullptr;
+  if (a[6] != Py_None) {
+    y = matrix(a[6], "y");
+    need(y.rows == n.x.rows && y.cols == n.x.cols, "y", "x's shape is needed");
+  }
+  if (a[7] != Py_None) rstd = floats(a[7], "rstd", n.x.rows);
+  void* const stream = stream_here(a[0]);
+  const at::Tensor& t = THPVariable_Unpack(a[1]);
+  at::Tensor my, mr;
+  make_h(a, n);
+  if (a[6] == Py_None) {
+    my = like(t, {n.x.rows, n.x.cols}, scalar_of(type));
+    y = {my.data_ptr(), n.x.rows, n.x.cols, n.x.cols, type};
+  }
+  if (a[7] == Py_None) {
+    mr = like(t, {n.x.rows}, at::kFloat);
+    rstd = mr.data_ptr<float>();
+  }
+  check("fp4q_rms_norm", fp4q_rms_norm(n.x.type, n.x.p, n.x.ld, n.res.p, n.res.ld, n.h.p, n.h.ld, n.w, n.w_type,
+                                       n.eps, n.x.rows, n.x.cols, y.p, y.type, y.ld, rstd, stream));
+  auto given = [](PyObject* o) {
+    Py_INCREF(o);
+    return o;
+  };
+  return tuple_of({my.defined() ? wrap(my) : given(a[6]), result_h(n), mr.defined() ? wrap(mr) : given(a[7])});
+}
+
+// Shapes of an operand's codes and scales, [bytes] where they are tiled.
+struct Operand {
+  c10::SmallVector<int64_t, 2> q, scales;
+};
+
+Operand operand(int32_t fmt, int32_t layout, int64_t rows, int64_t cols) {
+  if (layout == FP4Q_LAYOUT_TILED) {
+    size_t cb = 0, sb = 0;
+    if (fp4q_packed_bytes((fp4q_format_t)fmt, FP4Q_LAYOUT_TILED, rows, cols, &cb, &sb) != FP4Q_OK) cb = sb = 0;
+    return {{(int64_t)cb}, {(int64_t)sb}};
+  }
+  const int64_t blk = fmt == FP4Q_NVFP4 ? 16 : 32;
+  return {{rows, fmt == FP4Q_MXFP8 ? cols : cols / 2}, {rows, cols / blk}};
+}
+
+// rms_norm_quantize(stream, x, weight, eps, residual, fmt, layout, tscale or None, chan or None,
+// y_dtype or None (no y), h or None, n_chan, rstd wanted) -> (q, scales, tscale, resid, y, h, rstd)
+PyObject* rms_norm_quantize(PyObject* const* a) {
+  Norm n = norm_of(a, a[10]);
+  const int32_t fmt = small(a[5], "fmt"), layout = small(a[6], "layout");
+  need(fmt == FP4Q_NVFP4 || fmt == FP4Q_MXFP4 || fmt == FP4Q_MXFP8, "fmt", "no such format");
+  need(layout == FP4Q_LAYOUT_ROWMAJOR || layout == FP4Q_LAYOUT_TILED, "layout", "no such layout");
+  need(layout == FP4Q_LAYOUT_ROWMAJOR || fmt != FP4Q_MXFP8, "layout", "MXFP8 is row-major");
+  need(n.x.cols > 0 && n.x.cols % (layout == FP4Q_LAYOUT_TILED ? 128 : fmt == FP4Q_NVFP4 ? 16 : 32) == 0, "x",
+       "its columns are not whole blocks of the format and layout");
+  float* ts = nullptr;
+  if (a[7] != Py_None) {
+    need(fmt == FP4Q_NVFP4, "tscale", "NVFP4 only");
+    ts = floats(a[7], "tscale", 1);
+  }
+  const int32_t* chan = nullptr;
+  int32_t n_chan = 0;
+  if (a[8] != Py_None) {
+    n_chan = small(a[11], "chan_idx");
+    need(fmt != FP4Q_MXFP8, "chan_idx", "not for MXFP8");
+    chan = ints(a[8], "chan_idx", n_chan);
+    if (n_chan == 0) chan = nullptr;
+  }
+  const bool with_y = a[9] != Py_None;
+  const fp4q_dtype_t type = with_y ? dtype_of(a[9], "y_dtype") : FP4Q_OUT_BF16;
+  const int want_r = PyObject_IsTrue(a[12]);
+  if (want_r < 0) throw PythonError();
+  void* const stream = stream_here(a[0]);
+  const at::Tensor& t = THPVariable_Unpack(a[1]);
+  const int64_t R = n.x.rows, C = n.x.cols;
+  const Operand s = operand(fmt, layout, R, C);
+  make_h(a, n);
+  const at::Tensor q = like(t, s.q, at::kByte), sc = like(t, s.scales, at::kByte);
+  at::Tensor mts, resid, y, rstd, ws;
+  if (fmt == FP4Q_NVFP4 && !ts) {
+    mts = like(t, {1}, at::kFloat);
+    ts = mts.data_ptr<float>();
+  }
+  if (n_chan > 0) resid = like(t, {R, n_chan}, at::kShort);
+  if (with_y) y = like(t, {R, C}, scalar_of(type));
+  if (want_r) rstd = like(t, {R}, at::kFloat);
+  const size_t bytes = fp4q_rms_norm_quantize_workspace_bytes((fp4q_format_t)fmt, R, !mts.defined());
+  if (bytes) ws = like(t, {(int64_t)bytes}, at::kByte);
+  check("fp4q_rms_norm_quantize",
+        fp4q_rms_norm_quantize((fp4q_format_t)fmt, (fp4q_layout_t)layout, n.x.type, n.x.p, n.x.ld, n.res.p, n.res.ld,
+                               n.h.p, n.h.ld, n.w, n.w_type, n.eps, R, C, chan, n_chan,
+                               (uint8_t*)q.data_ptr(), (uint8_t*)sc.data_ptr(), ts, !mts.defined(),
+                               n_chan > 0 ? (uint16_t*)resid.data_ptr() : nullptr,
+                               with_y ? y.data_ptr() : nullptr, type, C, want_r ? rstd.data_ptr<float>() : nullptr,
+                               bytes ? ws.data_ptr() : nullptr, bytes, stream));
+  PyObject* pts = none();
+  if (fmt == FP4Q_NVFP4) {
+    Py_DECREF(pts);
+    if (mts.defined()) {
+      pts = wrap(mts);
+    } else {
+      pts = a[7];
+      Py_INCREF(pts);
+    }
+  }
+  return tuple_of({wrap(q), wrap(sc), pts, n_chan > 0 ? wrap(resid) : none(), with_y ? wrap(y) : none(), result_h(n),
+                   want_r ? wrap(rstd) : none()});
+}
+
+// rms_norm_backward(stream, h, weight, rstd, d_y, d_h or None, d_x or None, d_weight or None) -> (d_x, d_weight)
+PyObject* rms_norm_backward(PyObject* const* a) {
+  const Matrix h = matrix(a[1], "h"), dy = matrix(a[4], "d_y");
+  fp4q_dtype_t w_type;
+  void* const w = weights_of(a[2], h.cols, &w_type);
+  const float* rstd = floats(a[3], "rstd", h.rows);
+  need(dy.rows == h.rows && dy.cols == h.cols, "d_y", "h's shape is needed");
+  Matrix dh = {}, dx = {};
+  float* dw = nullptr;
+  if (a[5] != Py_None) {
+    dh = matrix(a[5], "d_h");
+    need(dh.type == h.type && dh.rows == h.rows && dh.cols == h.cols, "d_h", "h's shape and type are needed");
+  }
+  if (a[6] != Py_None) {
+    dx = matrix(a[6], "d_x");
+    need(dx.type == h.type && dx.rows == h.rows && dx.cols == h.cols, "d_x", "h's shape and type are needed");
+  }
+  if (a[7] != Py_None) dw = floats(a[7], "d_weight", h.cols);
+  void* const stream = stream_here(a[0]);
+  const at::Tensor& t = THPVariable_Unpack(a[1]);
+  at::Tensor mx, mw, ws;
+  if (a[6] == Py_None) {
+    mx = like(t, {h.rows, h.cols}, scalar_of(h.type));
+    dx = {mx.data_ptr(), h.rows, h.cols, h.cols, h.type};
+  }
+  if (a[7] == Py_None) {
+    mw = like(t, {h.cols}, at::kFloat);
+    dw = mw.data_ptr<float>();
+  }
+  const size_t bytes = fp4q_rms_norm_backward_workspace_bytes(h.rows, h.cols);
+  if (bytes) ws = like(t, {(int64_t)bytes}, at::kByte);
+  check("fp4q_rms_norm_backward",
+        fp4q_rms_norm_backward(h.type, h.p, h.ld, w, w_type, rstd, dy.p, dy.type, dy.ld, dh.p, dh.ld, dx.p, dx.ld,
+                               dw, h.rows, h.cols, bytes ? ws.data_ptr() : nullptr, bytes, stream));
+  auto given = [](PyObject* o) {
+    Py_INCREF(o);
+    return o;
+  };
+  return tuple_of({mx.defined() ? wrap(mx) : given(a[6]), mw.defined() ? wrap(mw) : given(a[7])});
+}
+
+// dequantize(stream, fmt, layout, q, scales, tscale or None, rows, cols, dtype) -> y
+PyObject* dequantize(PyObject* const* a) {
+  const int32_t fmt = small(a[1], "fmt"), layout = small(a[2], "layout");
+  need(fmt == FP4Q_NVFP4 || fmt == FP4Q_MXFP4 || fmt == FP4Q_MXFP8, "fmt", "no such format");
+  need(layout == FP4Q_LAYOUT_ROWMAJOR || layout == FP4Q_LAYOUT_TILED, "layout", "no such layout");
+  need(layout == FP4Q_LAYOUT_ROWMAJOR || fmt != FP4Q_MXFP8, "layout", "MXFP8 is row-major");
+  const int64_t rows = integer(a[6]), cols = integer(a[7]);
+  need(rows >= 0 && rows < ((int64_t)1 << 31), "rows", "out of range");
+  need(cols > 0 && cols < ((int64_t)1 << 31), "cols", "out of range");
+  need(cols % (layout == FP4Q_LAYOUT_TILED ? 128 : fmt == FP4Q_NVFP4 ? 16 : 32) == 0, "cols",
+       "not whole blocks of the format and layout");
+  const Operand s = operand(fmt, layout, rows, cols);
+  auto bytes_of = [](PyObject* o, const char* name, const c10::SmallVector<int64_t, 2>& shape) {
+    const at::Tensor& t = tensor(o, name);
+    int64_t n = 1;
+    for (int64_t d : shape) n *= d;
+    need(t.element_size() == 1 && t.is_contiguous() && t.numel() == n, name,
+         "contiguous bytes of this format, layout and shape are needed");
+    return (uint8_t*)t.data_ptr();
+  };
+  uint8_t *q = bytes_of(a[3], "q", s.q), *sc = bytes_of(a[4], "scales", s.scales);
+  need((a[5] != Py_None) == (fmt == FP4Q_NVFP4), "tscale", "NVFP4 has one, the others none");
+  const float* ts = a[5] == Py_None ? nullptr : floats(a[5], "tscale", 1);
+  const fp4q_dtype_t type = dtype_of(a[8], "dtype");
+  void* const stream = stream_here(a[0]);
+  const at::Tensor y = like(THPVariable_Unpack(a[3]), {rows, cols}, scalar_of(type));
+  check("fp4q_dequantize", fp4q_dequantize((fp4q_format_t)fmt, (fp4q_layout_t)layout, q, sc, ts, rows, cols,
+                                           y.data_ptr(), type, cols, stream));
+  return wrap(y);
+}
+
+// lora(stream, x, a, b, offsets, adapters, scale or None, y or None, dtype or None (y's), out or None) -> out
+PyObject* lora(PyObject* const* a) {
+  const Matrix x = matrix(a[1], "x");
+  need(x.type == FP4Q_OUT_BF16, "x", "bf16 is needed");
+  const at::Tensor &ta = tensor(a[2], "a"), &tb = tensor(a[3], "b");
+  need(ta.dim() == 3 && ta.scalar_type() == at::kBFloat16 && ta.is_contiguous(), "a",
+       "contiguous bf16 [adapters, rank, K] is needed");
+  need(tb.dim() == 3 && tb.scalar_type() == at::kBFloat16 && tb.is_contiguous(), "b",
+       "contiguous bf16 [adapters, N, rank] is needed");
+  need(ta.size(2) == x.cols, "a", "x's columns are needed");
+  need(tb.size(0) == ta.size(0) && tb.size(2) == ta.size(1), "b", "a's adapters and rank are needed");
+  need(ta.size(0) <= INT32_MAX && ta.size(1) <= INT32_MAX, "a", "too large");
+  const at::Tensor& ad = tensor(a[5], "adapters");
+  need(ad.dim() == 1 && ad.numel() < INT32_MAX, "adapters", "one for each request is needed");
+  const int32_t* adapter = ints(a[5], "adapters", ad.numel());
+  const int32_t* off = ints(a[4], "offsets", ad.numel() + 1);
+  const float* scale = a[6] == Py_None ? nullptr : floats(a[6], "scale", ta.size(0));
+  const int64_t N = tb.size(1);
+  Matrix y = {}, out = {};
+  fp4q_dtype_t type = FP4Q_OUT_BF16;
+  if (a[7] != Py_None) {
+    y = matrix(a[7], "y");
+    need(y.rows == x.rows && y.cols == N, "y", "[rows, N] is needed");
+    type = y.type;
+    need(a[8] == Py_None || dtype_of(a[8], "y_dtype") == type, "y_dtype", "y's type is needed");
+  } else if (a[8] != Py_None) {
+    type = dtype_of(a[8], "y_dtype");
+  }
+  if (a[9] != Py_None) {
+    out = matrix(a[9], "out");
+    need(out.rows == x.rows && out.cols == N && (a[7] == Py_None || out.type == type), "out",
+         "[rows, N] of y's type is needed");
+    type = out.type;
+  }
+  void* const stream = stream_here(a[0]);
+  const at::Tensor& t = THPVariable_Unpack(a[1]);
+  at::Tensor made, ws;
+  if (a[9] == Py_None) {
+    made = like(t, {x.rows, N}, scalar_of(type));
+    out = {made.data_ptr(), x.rows, N, N, type};
+  }
+  const size_t bytes = fp4q_lora_workspace_bytes(x.rows, (int32_t)ad.numel(), (int32_t)ta.size(1), x.cols, N);
+  if (bytes) ws = like(t, {(int64_t)bytes}, at::kByte);
+  check("fp4q_lora", fp4q_lora((uint16_t*)x.p, x.ld, (uint16_t*)ta.data_ptr(), (uint16_t*)tb.data_ptr(), scale,
+                               (int32_t)ta.size(0), (int32_t)ta.size(1), off, adapter, (int32_t)ad.numel(), x.rows,
+                               x.cols, N, y.p, y.ld, out.p, type, out.ld, bytes ? ws.data_ptr() : nullptr, bytes,
+                               stream));
+  if (made.defined()) return wrap(made);
+  Py_INCREF(a[9]);
+  return a[9];
 }
 
 // (logits, k, score, bias, n_groups, top_groups, renorm) are arguments 1 .. 7
@@ -484,7 +858,8 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
     PyErr_Format(PyExc_TypeError, "%d arguments are needed, not %zd", N, n);
     return nullptr;
   }
-  g_host = nullptr;
+  g_host = g_apart = nullptr;
+  g_gpu = -1;
   try {
     return F(args);
   } catch (const PythonError&) {
@@ -516,8 +891,14 @@ PyObject* set_up(PyObject*, PyObject* args) {
 #define FP4Q_ENTRY(name, n) {#name, (PyCFunction)(void (*)(void))entry<name, n>, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FP4Q_ENTRY(append, 11),
                          FP4Q_ENTRY(read, 11),
-                         FP4Q_ENTRY(attention_into, 16),
-                         FP4Q_ENTRY(attention, 15),
+                         FP4Q_ENTRY(append_rotated, 16),
+                         FP4Q_ENTRY(attention_into, 17),
+                         FP4Q_ENTRY(attention, 16),
+                         FP4Q_ENTRY(rms_norm, 9),
+                         FP4Q_ENTRY(rms_norm_quantize, 13),
+                         FP4Q_ENTRY(rms_norm_backward, 8),
+                         FP4Q_ENTRY(dequantize, 9),
+                         FP4Q_ENTRY(lora, 10),
                          FP4Q_ENTRY(route_into, 14),
                          FP4Q_ENTRY(route, 8),
                          FP4Q_ENTRY(route_backward_into, 7),

@@ -1,0 +1,736 @@
+// norm.hip -- the root-mean-square norm of a residual stream (defined in
+// include/fp4q.h): per row
+//   h = x + residual,  r = 1 / sqrt(mean(h^2) + eps),  y = h r weight,
+// with y written, or quantized into the operand of the product behind it
+// (NVFP4, MXFP4, MXFP8) with the residual of selected channels, its gradient,
+// and the values that an operand stands for.
+//
+// All of it is bound by HBM: x and the residual are read once, h, y or the codes
+// written once, with a row in the registers of one, four or eight waves in
+// between.  NVFP4's own tensor scale needs every row's y before the first code: a
+// first pass writes h, each row's r and the workgroups' maxima, a second reads h
+// again.
+//
+// The sum of squares, r and y are 64-bit: y then is the definition's F32 value
+// but in 2^-28 of the cases, and the BF16 value and code made of it with it; a y
+// of 32-bit steps lies an ulp apart often enough that codes next to a border
+// differ.  It costs one conversion each way and one product an element.
+#include "fp4q_device.h"
+#include "fp4q_internal.h"
+
+namespace fp4q {
+
+namespace {
+
+typedef float f32x2n __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2n __attribute__((ext_vector_type(2)));
+// Sixteen bytes at any element's address (rows of odd strides).
+typedef uint32_t u32x4_2 __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x4_4 __attribute__((ext_vector_type(4), aligned(4)));
+
+struct NormArgs {
+  const void* x;
+  int64_t ldx;
+  const void* res;  // or null
+  int64_t ldr;
+  void* h;          // null: no residual (h is x)
+  int64_t ldh;
+  const void* w;
+  int w_f32;
+  double eps;
+  int64_t rows;
+  int cols;
+  void* y;          // or null
+  int64_t ldy;
+  int y_f32;
+  float* rstd;      // or null
+  // quantized output
+  uint8_t* q;
+  uint8_t* scales;
+  float* tscale;    // NVFP4: given, or written from the maxima
+  int n_max;        // maxima of the first pass (0: tscale is given)
+  float* maxima;
+  double* r64;      // the rows' r, first pass to second
+  bool tiled;
+  const int32_t* chan;
+  int n_chan;
+  uint16_t* resid;
+  int64_t groups;   // groups of rows: one to a workgroup at a time
+};
+
+enum { EMIT_Y, EMIT_MAX, EMIT_NVFP4, EMIT_MXFP4, EMIT_MXFP8 };
+
+constexpr int CH = 8;  // elements of a lane's chunk
+
+// Eight elements as they stand in memory.
+template <typename T> struct Raw;
+template <> struct Raw<uint16_t> {
+  u32x4 v;
+  __device__ __forceinline__ float at(int i) const {
+    return __uint_as_float((i & 1) ? v[i >> 1] & 0xFFFF0000u : v[i >> 1] << 16);
+  }
+  __device__ __forceinline__ void load(const uint16_t* p, int n) {
+    if (n >= CH) {
+      v = *reinterpret_cast<const u32x4_2*>(p);
+    } else {
+      v = u32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int i = 0; i < CH; ++i)
+        if (i < n) v[i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
+    }
+  }
+  __device__ __forceinline__ void store(uint16_t* p, int n) const {
+    if (n >= CH) {
+      *reinterpret_cast<u32x4_2*>(p) = v;
+    } else {
+#pragma unroll
+      for (int i = 0; i < CH; ++i)
+        if (i < n) p[i] = (uint16_t)(v[i >> 1] >> (16 * (i & 1)));
+    }
+  }
+  __device__ __forceinline__ void set(const float (&f)[CH]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const f32x2n t = {f[2 * i], f[2 * i + 1]};
+      v[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(t, bf16x2n));
+    }
+  }
+};
+template <> struct Raw<float> {
+  u32x4 v[2];
+  __device__ __forceinline__ float at(int i) const { return __uint_as_float(v[i >> 2][i & 3]); }
+  __device__ __forceinline__ void load(const float* p, int n) {
+    if (n >= CH) {
+      v[0] = *reinterpret_cast<const u32x4_4*>(p);
+      v[1] = *reinterpret_cast<const u32x4_4*>(p + 4);
+    } else {
+      v[0] = v[1] = u32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int i = 0; i < CH; ++i)
+        if (i < n) v[i >> 2][i & 3] = __float_as_uint(p[i]);
+    }
+  }
+  __device__ __forceinline__ void store(float* p, int n) const {
+    if (n >= CH) {
+      *reinterpret_cast<u32x4_4*>(p) = v[0];
+      *reinterpret_cast<u32x4_4*>(p + 4) = v[1];
+    } else {
+#pragma unroll
+      for (int i = 0; i < CH; ++i)
+        if (i < n) p[i] = at(i);
+    }
+  }
+  __device__ __forceinline__ void set(const float (&f)[CH]) {
+#pragma unroll
+    for (int i = 0; i < CH; ++i) v[i >> 2][i & 3] = __float_as_uint(f[i]);
+  }
+};
+
+// Chunks of a row that a lane holds, and elements that a row of WPR waves has then.
+template <typename T, int WPR>
+struct Held {
+  static constexpr int N = sizeof(T) == 2 || WPR == 8 ? 8 : 4, CAP = WPR * 64 * CH * N;
+};
+
+__device__ __forceinline__ void load_any(const void* p, int64_t at, int f32, int n, float (&f)[CH]) {
+  if (f32) {
+    Raw<float> r;
+    r.load(static_cast<const float*>(p) + at, n);
+#pragma unroll
+    for (int i = 0; i < CH; ++i) f[i] = r.at(i);
+  } else {
+    Raw<uint16_t> r;
+    r.load(static_cast<const uint16_t*>(p) + at, n);
+#pragma unroll
+    for (int i = 0; i < CH; ++i) f[i] = r.at(i);
+  }
+}
+
+__device__ __forceinline__ void store_any(void* p, int64_t at, int f32, int n, const float (&f)[CH]) {
+  if (f32) {
+    Raw<float> r;
+    r.set(f);
+    r.store(static_cast<float*>(p) + at, n);
+  } else {
+    Raw<uint16_t> r;
+    r.set(f);
+    r.store(static_cast<uint16_t*>(p) + at, n);
+  }
+}
+
+__device__ __forceinline__ uint32_t max_bits(const Raw<uint16_t>& r) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = max(m, max(r.v[i] & 0x7FFFu, (r.v[i] >> 16) & 0x7FFFu));
+  return m;
+}
+
+// The largest of v over the N (2 or 4) lanes whose chunks make up a block.
+template <int N>
+__device__ __forceinline__ uint32_t block_max(uint32_t v) {
+  v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, true));
+  if (N == 4) v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xF, 0xF, true));
+  return v;
+}
+
+// A chunk of y (BF16) as codes: FP4's in w[0], MXFP8's in w[0], w[1]; the block's
+// scale code; and the values they stand for, where asked for.
+template <int EMIT>
+__device__ __forceinline__ uint32_t encode(const Raw<uint16_t>& y, uint32_t amax_bits, float t,
+                                           uint32_t (&w)[2], bool want, float (&val)[CH]) {
+  const float amax = bf16_to_f32(amax_bits);
+  float v[CH];
+  if constexpr (EMIT == EMIT_NVFP4) {
+    const uint32_t sb = e4m3_encode((amax / 6.0f) / t);
+    const float s = e4m3_value(sb), d = s * t;
+    // quot_rn's range; its operands are held within 8 d (beyond it every
+    // quotient gives the largest code)
+    const bool fast = d >= 0x1p-96f && d <= 0x1p96f;
+    const float rd = fast ? 1.0f / d : 0.0f;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const float e = y.at(i);
+      if (fast) v[i] = quot_rn(fminf(fmaxf(e, -8.0f * d), 8.0f * d), d, rd);
+      else v[i] = d > 0.0f ? e / d : 0.0f * e;
+    }
+    w[0] = e2m1_pack8(v);
+    if (want) {
+#define FP4Q_PAIR(N)                                                                     \
+  {                                                                                      \
+    const f32x2n e = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[0], 1.0f, N);            \
+    val[2 * N] = (e[0] * s) * t;                                                         \
+    val[2 * N + 1] = (e[1] * s) * t;                                                     \
+  }
+      FP4Q_PAIR(0) FP4Q_PAIR(1) FP4Q_PAIR(2) FP4Q_PAIR(3)
+#undef FP4Q_PAIR
+    }
+    return sb & 0xFFu;
+  } else if constexpr (EMIT == EMIT_MXFP4) {
+    const int e8 = mx_exponent(amax);
+#pragma unroll
+    for (int i = 0; i < CH; ++i) v[i] = y.at(i);
+    w[0] = e2m1_pack8(v, __uint_as_float((uint32_t)(e8 + 127) << 23));
+    if (want) {
+      const float s = exp2i(e8);
+#define FP4Q_PAIR(N)                                                                     \
+  {                                                                                      \
+    const f32x2n e = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[0], 1.0f, N);            \
+    val[2 * N] = e[0] * s;                                                               \
+    val[2 * N + 1] = e[1] * s;                                                           \
+  }
+      FP4Q_PAIR(0) FP4Q_PAIR(1) FP4Q_PAIR(2) FP4Q_PAIR(3)
+#undef FP4Q_PAIR
+    }
+    return (uint32_t)(e8 + 127);
+  } else {
+    const int e8 = mx8_exponent(amax);
+    // times 2^-e, exact where it matters (what underflows is below half the
+    // smallest step)
+    const float s = exp2i(-e8);
+#pragma unroll
+    for (int i = 0; i < CH; ++i) v[i] = y.at(i) * s;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      uint32_t u = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i], v[4 * i + 1], 0, false);
+      w[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i + 2], v[4 * i + 3], (int)u, true);
+    }
+    return (uint32_t)(e8 + 127);
+  }
+}
+
+__device__ __forceinline__ double wave_sum(double v) {
+#pragma unroll
+  for (int s = 32; s > 0; s >>= 1) v += __shfl_xor(v, s);
+  return v;
+}
+
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+#pragma unroll
+  for (int s = 32; s > 0; s >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, s));
+  return v;
+}
+
+// The group of rows that workgroup g takes.  Workgroups go to the eight XCDs in
+// turn; the 16 rows of a tiled block of codes are written by one of them (each
+// writes 16 bytes of a line, which meet in its cache).
+__device__ __forceinline__ int64_t row_group(int64_t g, int64_t groups, int per16, bool tiled) {
+  const int64_t all = 8 * per16, base = g / all * all;
+  if (!tiled || base + all > groups) return g;
+  const int i = (int)(g - base);
+  return base + (i & 7) * per16 + (i >> 3);
+}
+
+// WPR: waves of a row (a workgroup of four rows, or one).  SECOND: r and h are
+// given (the second pass of NVFP4's own tensor scale).
+template <typename T, int WPR, int EMIT, bool SECOND>
+__global__ __launch_bounds__(WPR == 8 ? 512 : 256) void k_norm(NormArgs p) {
+  constexpr int HELD = Held<T, WPR>::N, ROWS = WPR == 1 ? 4 : 1, WAVES = WPR * ROWS;
+  constexpr bool QUANT = EMIT >= EMIT_NVFP4;
+  extern __shared__ __attribute__((aligned(16))) uint8_t s_rows[];  // the rows' quantization errors
+  __shared__ double s_sum[WAVES];
+  __shared__ uint32_t s_max[WAVES];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int sub = WPR == 1 ? 0 : wave;
+  const int nc = (p.cols + WPR * 64 * CH - 1) / (WPR * 64 * CH);
+  const int col0 = (sub * 64 + lane) * CH;  // of chunk 0; chunk c: WPR * 512 c further
+  uint16_t* const errs = reinterpret_cast<uint16_t*>(s_rows) + (WPR == 1 ? wave * p.cols : 0);
+  uint32_t most = 0;
+  float t = 1.0f;
+  if constexpr (EMIT == EMIT_NVFP4) {
+    if (p.n_max > 0) {
+      uint32_t m = 0;
+      for (int i = threadIdx.x; i < p.n_max; i += WAVES * 64) m = max(m, __float_as_uint(p.maxima[i]));
+      m = wave_max(m);
+      if (lane == 0) s_max[wave] = m;
+      __syncthreads();
+      m = 0;
+#pragma unroll
+      for (int i = 0; i < WAVES; ++i) m = max(m, s_max[i]);
+      t = nv_tensor_scale(__uint_as_float(m));
+      if (blockIdx.x == 0 && threadIdx.x == 0) *p.tscale = t;
+    } else {
+      t = *p.tscale;
+    }
+  }
+  for (int64_t gi = blockIdx.x; gi < p.groups; gi += gridDim.x) {
+    const int64_t row = row_group(gi, p.groups, 16 / ROWS, p.tiled) * ROWS + (WPR == 1 ? wave : 0);
+    if (WPR == 1 && row >= p.rows) continue;
+    Raw<T> h[HELD];
+    double ss = 0.0;
+    {
+      const T* x = static_cast<const T*>(SECOND && p.h ? p.h : p.x) + row * (SECOND && p.h ? p.ldh : p.ldx);
+      const T* res = static_cast<const T*>(p.res) + row * p.ldr;
+      constexpr int BATCH = HELD < 16 / (int)sizeof(T) ? HELD : 16 / (int)sizeof(T);  // loads in flight
+#pragma unroll
+      for (int c0 = 0; c0 < HELD; c0 += BATCH) {
+        if (c0 >= nc) break;
+        Raw<T> a[BATCH];
+#pragma unroll
+        for (int c = c0; c < c0 + BATCH; ++c) {
+          if (c >= nc) break;
+          const int col = col0 + c * WPR * 64 * CH;
+          if (col < p.cols) h[c].load(x + col, p.cols - col);
+        }
+        if (SECOND) continue;
+        if (p.res) {
+#pragma unroll
+          for (int c = c0; c < c0 + BATCH; ++c) {
+            if (c >= nc) break;
+            const int col = col0 + c * WPR * 64 * CH;
+            if (col < p.cols) a[c - c0].load(res + col, p.cols - col);
+          }
+        }
+#pragma unroll
+        for (int c = c0; c < c0 + BATCH; ++c) {
+          if (c >= nc) break;
+          const int col = col0 + c * WPR * 64 * CH;
+          if (col >= p.cols) continue;
+          if (p.res) {
+            float f[CH];
+#pragma unroll
+            for (int i = 0; i < CH; ++i) f[i] = h[c].at(i) + a[c - c0].at(i);
+            h[c].set(f);
+            h[c].store(static_cast<T*>(p.h) + row * p.ldh + col, p.cols - col);
+          }
+#pragma unroll
+          for (int i = 0; i < CH; ++i) {
+            const double v = h[c].at(i);
+            ss = __builtin_fma(v, v, ss);
+          }
+        }
+      }
+    }
+    double r;
+    if (SECOND) {
+      r = p.r64[row];
+    } else {
+      ss = wave_sum(ss);
+      if (WPR > 1) {
+        __syncthreads();  // (the sums of the row before have been read)
+        if (lane == 0) s_sum[wave] = ss;
+        __syncthreads();
+        ss = 0.0;
+#pragma unroll
+        for (int i = 0; i < WPR; ++i) ss += s_sum[i];
+      }
+      r = 1.0 / sqrt(ss / (double)p.cols + p.eps);
+      if (lane == 0 && sub == 0) {
+        if (EMIT == EMIT_MAX) p.r64[row] = r;
+        if (p.rstd) p.rstd[row] = (float)r;
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < HELD; ++c) {
+      if (c >= nc) break;
+      const int col = col0 + c * WPR * 64 * CH, n = p.cols - col;
+      if (n <= 0) continue;
+      float w[CH], f[CH];
+      load_any(p.w, col, p.w_f32, n, w);
+      if (sizeof(T) == 2 && !p.w_f32) {
+#pragma unroll
+        for (int i = 0; i < CH; ++i) f[i] = (float)((double)(h[c].at(i) * w[i]) * r);  // (the first product is exact)
+      } else {
+#pragma unroll
+        for (int i = 0; i < CH; ++i) f[i] = (float)(((double)h[c].at(i) * (double)w[i]) * r);
+      }
+      if (EMIT != EMIT_MAX && p.y) store_any(p.y, row * p.ldy + col, p.y_f32, n, f);
+      if constexpr (EMIT != EMIT_Y) {
+        Raw<uint16_t> y;
+        y.set(f);
+        const uint32_t m = max_bits(y);
+        if constexpr (EMIT == EMIT_MAX) {
+          most = max(most, m);
+        } else {
+          uint32_t code[2];
+          float val[CH];
+          const uint32_t s = encode<EMIT>(y, block_max<EMIT == EMIT_NVFP4 ? 2 : 4>(m), t, code,
+                                          p.n_chan > 0, val);
+          if constexpr (EMIT == EMIT_MXFP8) {
+            *reinterpret_cast<u32x2*>(p.q + row * p.cols + col) = u32x2{code[0], code[1]};
+            if ((lane & 3) == 0) p.scales[row * (p.cols / 32) + col / 32] = (uint8_t)s;
+          } else {
+            constexpr int FMT = EMIT == EMIT_NVFP4 ? FP4Q_NVFP4 : FP4Q_MXFP4, BLK = FMT == FP4Q_NVFP4 ? 16 : 32;
+            *reinterpret_cast<uint32_t*>(p.q + code_off(p.tiled, row, col >> 1, p.cols)) = code[0];
+            if (col % BLK == 0) p.scales[scale_off<FMT>(p.tiled, row, col / BLK, p.cols)] = (uint8_t)s;
+            if (p.n_chan > 0) {
+              float e[CH];
+#pragma unroll
+              for (int i = 0; i < CH; ++i) e[i] = y.at(i) - val[i];
+              Raw<uint16_t> b;
+              b.set(e);
+              *reinterpret_cast<u32x4*>(errs + col) = b.v;
+            }
+          }
+        }
+      }
+    }
+    if (QUANT && p.n_chan > 0) {
+      if (WPR > 1) __syncthreads();
+      else wave_fence();
+      for (int j = sub * 64 + lane; j < p.n_chan; j += WPR * 64) {
+        const int ch = p.chan[j];
+        p.resid[row * p.n_chan + j] = (uint32_t)ch < (uint32_t)p.cols ? errs[ch] : 0;
+      }
+      if (WPR > 1) __syncthreads();
+      else wave_fence();
+    }
+  }
+  if constexpr (EMIT == EMIT_MAX) {
+    most = wave_max(most);
+    if (lane == 0) s_max[wave] = most;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      for (int i = 1; i < WAVES; ++i) most = max(most, s_max[i]);
+      p.maxima[blockIdx.x] = bf16_to_f32(most);
+    }
+  }
+}
+
+// ---- the gradient -----------------------------------------------------------
+//
+// With u = h r and g = weight d_y:  d_x = r (g - u mean(g u)) + d_h,
+// d_weight = sum over the rows of d_y u.  Four or eight waves take a row at a time; a
+// lane adds up its columns' d_weight over the workgroup's rows, and a second
+// kernel adds the workgroups' sums, always in the same order.
+struct NormGradArgs {
+  const void* h;
+  int64_t ldh;
+  const void* w;
+  int w_f32;
+  const float* rstd;
+  const void* dy;
+  int64_t lddy;
+  int dy_f32;
+  const void* dh;  // or null
+  int64_t lddh;
+  void* dx;
+  int64_t lddx;
+  float* part;     // [gridDim.x][cols]
+  int64_t rows;
+  int cols;
+};
+
+template <typename T, int WPR, int N>
+__global__ __launch_bounds__(64 * WPR) void k_norm_backward(NormGradArgs p) {
+  __shared__ float s_sum[2][WPR];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int col0 = (wave * 64 + lane) * CH;
+  const int nc = (p.cols + WPR * 64 * CH - 1) / (WPR * 64 * CH);
+  float dw[N][CH];
+#pragma unroll
+  for (int c = 0; c < N; ++c)
+#pragma unroll
+    for (int i = 0; i < CH; ++i) dw[c][i] = 0.0f;
+  int turn = 0;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, turn ^= 1) {
+    const T* h = static_cast<const T*>(p.h) + row * p.ldh;
+    const float r = p.rstd[row];
+    Raw<T> hr[N];
+    float g[N][CH];
+#pragma unroll
+    for (int c = 0; c < N; ++c) {
+      if (c >= nc) break;
+      const int col = col0 + c * WPR * 64 * CH, n = p.cols - col;
+      if (n <= 0) continue;
+      hr[c].load(h + col, n);
+      load_any(p.dy, row * p.lddy + col, p.dy_f32, n, g[c]);
+    }
+    float sum = 0.0f;
+#pragma unroll
+    for (int c = 0; c < N; ++c) {
+      if (c >= nc) break;
+      const int col = col0 + c * WPR * 64 * CH, n = p.cols - col;
+      if (n <= 0) continue;
+      float w[CH];
+      load_any(p.w, col, p.w_f32, n, w);
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        const float u = hr[c].at(i) * r;
+        dw[c][i] = __builtin_fmaf(g[c][i], u, dw[c][i]);
+        g[c][i] *= w[i];
+        sum = __builtin_fmaf(g[c][i], u, sum);
+      }
+    }
+#pragma unroll
+    for (int s = 32; s > 0; s >>= 1) sum += __shfl_xor(sum, s);
+    if (lane == 0) s_sum[turn][wave] = sum;
+    __syncthreads();
+    sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < WPR; ++i) sum += s_sum[turn][i];
+    sum /= (float)p.cols;
+    T* dx = static_cast<T*>(p.dx) + row * p.lddx;
+#pragma unroll
+    for (int c = 0; c < N; ++c) {
+      if (c >= nc) break;
+      const int col = col0 + c * WPR * 64 * CH, n = p.cols - col;
+      if (n <= 0) continue;
+      float f[CH];
+#pragma unroll
+      for (int i = 0; i < CH; ++i) f[i] = r * __builtin_fmaf(-(hr[c].at(i) * r), sum, g[c][i]);
+      if (p.dh) {
+        Raw<T> d;
+        d.load(static_cast<const T*>(p.dh) + row * p.lddh + col, n);
+#pragma unroll
+        for (int i = 0; i < CH; ++i) f[i] += d.at(i);
+      }
+      Raw<T> o;
+      o.set(f);
+      o.store(dx + col, n);
+    }
+  }
+  float* part = p.part + (int64_t)blockIdx.x * p.cols;
+#pragma unroll
+  for (int c = 0; c < N; ++c) {
+    if (c >= nc) break;
+    const int col = col0 + c * WPR * 64 * CH, n = p.cols - col;
+    if (n <= 0) continue;
+    Raw<float> o;
+    o.set(dw[c]);
+    o.store(part + col, n);
+  }
+}
+
+// d_weight from the workgroups' sums: 64 columns a workgroup, 16 threads on each.
+__global__ __launch_bounds__(1024) void k_norm_dweight(const float* __restrict__ part, int n, int cols,
+                                                       float* __restrict__ dw) {
+  __shared__ float s[16][64];
+  const int c = threadIdx.x & 63, k = threadIdx.x >> 6, col = blockIdx.x * 64 + c;
+  float sum = 0.0f;
+  if (col < cols)
+    for (int i = k; i < n; i += 16) sum += part[(int64_t)i * cols + col];
+  s[k][c] = sum;
+  __syncthreads();
+  if (k > 0 || col >= cols) return;
+#pragma unroll
+  for (int i = 1; i < 16; ++i) sum += s[i][c];
+  dw[col] = sum;
+}
+
+// ---- the values of an operand -------------------------------------------------
+//
+// A lane takes eight codes; a workgroup 16 rows of 512 columns, so that a tiled
+// block's lines are read by one.
+template <int EMIT>
+__global__ __launch_bounds__(256) void k_dequantize(const uint8_t* __restrict__ q, const uint8_t* __restrict__ scales,
+                                                    const float* __restrict__ tscale, bool tiled, int64_t rows,
+                                                    int64_t cols, void* __restrict__ y, int y_f32, int64_t ldy,
+                                                    uint32_t col_blocks) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t col = (int64_t)(blockIdx.x % col_blocks) * 512 + lane * CH;
+  const int64_t row0 = (int64_t)(blockIdx.x / col_blocks) * 16 + wave * 4;
+  if (col >= cols) return;
+  const float t = EMIT == EMIT_NVFP4 ? *tscale : 1.0f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t row = row0 + i;
+    if (row >= rows) break;
+    float f[CH];
+    if constexpr (EMIT == EMIT_MXFP8) {
+      const u32x2 w = *reinterpret_cast<const u32x2*>(q + row * cols + col);
+      const float s = exp2i((int)scales[row * (cols / 32) + col / 32] - 127);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const f32x2n a = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[k], false);
+        const f32x2n b = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[k], true);
+        f[4 * k] = a[0] * s;
+        f[4 * k + 1] = a[1] * s;
+        f[4 * k + 2] = b[0] * s;
+        f[4 * k + 3] = b[1] * s;
+      }
+    } else {
+      constexpr int FMT = EMIT == EMIT_NVFP4 ? FP4Q_NVFP4 : FP4Q_MXFP4, BLK = FMT == FP4Q_NVFP4 ? 16 : 32;
+      const uint32_t w = *reinterpret_cast<const uint32_t*>(q + code_off(tiled, row, col >> 1, cols));
+      const uint32_t sc = scales[scale_off<FMT>(tiled, row, col / BLK, cols)];
+      const float s = EMIT == EMIT_NVFP4 ? e4m3_value(sc) : exp2i((int)sc - 127);
+#define FP4Q_PAIR(N)                                                                  \
+  {                                                                                   \
+    const f32x2n e = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, N);            \
+    f[2 * N] = (e[0] * s) * t;                                                        \
+    f[2 * N + 1] = (e[1] * s) * t;                                                    \
+  }
+      FP4Q_PAIR(0) FP4Q_PAIR(1) FP4Q_PAIR(2) FP4Q_PAIR(3)
+#undef FP4Q_PAIR
+    }
+    store_any(y, row * ldy + col, y_f32, CH, f);
+  }
+}
+
+// The tensor scale of no rows.
+__global__ void k_scale_one(float* tscale) { *tscale = 1.0f; }
+
+constexpr int MAX_WGS = 2048;   // workgroups of a pass; further rows in turn
+constexpr int MAX_FIRST = 1024; // of the first of two passes: its maxima are read by all of the second
+
+// Waves of a row: one where the row fits and there are rows enough for all CUs,
+// else four, eight for the longest.
+template <typename T>
+int norm_waves(int64_t rows, int cols) {
+  if (rows >= 2048 && cols <= Held<T, 1>::CAP) return 1;
+  return cols <= Held<T, 4>::CAP ? 4 : 8;
+}
+
+template <typename T, int WPR, int EMIT, bool SECOND>
+int launch_pass(NormArgs p, int most, hipStream_t stream) {
+  constexpr int ROWS = WPR == 1 ? 4 : 1;
+  p.groups = (p.rows + ROWS - 1) / ROWS;
+  const int grid = (int)(p.groups < most ? p.groups : most);
+  const size_t lds = EMIT >= EMIT_NVFP4 && p.n_chan > 0 ? (size_t)ROWS * p.cols * 2 : 0;
+  hipLaunchKernelGGL((k_norm<T, WPR, EMIT, SECOND>), dim3(grid), dim3(WPR == 8 ? 512 : 256), lds, stream, p);
+  return grid;
+}
+
+template <typename T, int WPR>
+void launch_emit(NormArgs p, int emit, bool given, hipStream_t stream) {
+  if (emit == EMIT_Y) {
+    launch_pass<T, WPR, EMIT_Y, false>(p, MAX_WGS, stream);
+  } else if (emit == EMIT_MXFP4) {
+    launch_pass<T, WPR, EMIT_MXFP4, false>(p, MAX_WGS, stream);
+  } else if (emit == EMIT_MXFP8) {
+    launch_pass<T, WPR, EMIT_MXFP8, false>(p, MAX_WGS, stream);
+  } else if (given) {
+    launch_pass<T, WPR, EMIT_NVFP4, false>(p, MAX_WGS, stream);
+  } else {
+    p.n_max = launch_pass<T, WPR, EMIT_MAX, false>(p, MAX_FIRST, stream);
+    p.rstd = nullptr;
+    launch_pass<T, WPR, EMIT_NVFP4, true>(p, MAX_WGS, stream);
+  }
+}
+
+template <typename T>
+void launch_type(const NormArgs& p, int emit, bool given, hipStream_t stream) {
+  const int w = norm_waves<T>(p.rows, p.cols);
+  if (w == 1) launch_emit<T, 1>(p, emit, given, stream);
+  else if (w == 4) launch_emit<T, 4>(p, emit, given, stream);
+  else launch_emit<T, 8>(p, emit, given, stream);
+}
+
+int backward_blocks(int64_t rows) { return (int)(rows < 512 ? rows : 512); }
+
+template <typename T>
+void launch_backward_type(const NormGradArgs& p, hipStream_t stream) {
+  const dim3 grid(backward_blocks(p.rows));
+  if (p.cols <= 4096) hipLaunchKernelGGL((k_norm_backward<T, 4, 2>), grid, dim3(256), 0, stream, p);
+  else if (p.cols <= 8192) hipLaunchKernelGGL((k_norm_backward<T, 4, 4>), grid, dim3(256), 0, stream, p);
+  else if (p.cols <= 16384) hipLaunchKernelGGL((k_norm_backward<T, 8, 4>), grid, dim3(512), 0, stream, p);
+  else hipLaunchKernelGGL((k_norm_backward<T, 8, 8>), grid, dim3(512), 0, stream, p);
+}
+
+}  // namespace
+
+int norm_max_cols() { return Held<float, 8>::CAP; }
+
+// First of the second pass's inputs: the rows' r; then the maxima.
+size_t norm_workspace_bytes(int64_t rows) { return (size_t)rows * 8 + MAX_FIRST * 4; }
+
+void launch_norm(int f32, const void* x, int64_t ldx, const void* res, int64_t ldr, void* h, int64_t ldh,
+                 const void* w, int w_f32, double eps, int64_t rows, int cols, void* y, int y_f32, int64_t ldy,
+                 float* rstd, int fmt, bool tiled, uint8_t* q, uint8_t* scales, float* tscale, bool given,
+                 const int32_t* chan, int n_chan, uint16_t* resid, void* ws, hipStream_t stream) {
+  NormArgs p = {};
+  p.x = x;
+  p.ldx = ldx;
+  p.res = res;
+  p.ldr = ldr;
+  p.h = h;
+  p.ldh = ldh;
+  p.w = w;
+  p.w_f32 = w_f32;
+  p.eps = eps;
+  p.rows = rows;
+  p.cols = cols;
+  p.y = y;
+  p.ldy = ldy;
+  p.y_f32 = y_f32;
+  p.rstd = rstd;
+  p.q = q;
+  p.scales = scales;
+  p.tscale = tscale;
+  p.tiled = tiled;
+  p.chan = chan;
+  p.n_chan = n_chan;
+  p.resid = resid;
+  p.r64 = static_cast<double*>(ws);
+  p.maxima = reinterpret_cast<float*>(p.r64 + rows);
+  if (rows == 0) {
+    if (fmt == FP4Q_NVFP4 && !given) hipLaunchKernelGGL(k_scale_one, dim3(1), dim3(1), 0, stream, tscale);
+    return;
+  }
+  const int emit = fmt < 0 ? EMIT_Y : fmt == FP4Q_NVFP4 ? EMIT_NVFP4 : fmt == FP4Q_MXFP4 ? EMIT_MXFP4 : EMIT_MXFP8;
+  if (f32) launch_type<float>(p, emit, given, stream);
+  else launch_type<uint16_t>(p, emit, given, stream);
+}
+
+size_t norm_backward_workspace_bytes(int64_t rows, int cols) {
+  return (size_t)backward_blocks(rows) * (size_t)cols * 4;
+}
+
+void launch_norm_backward(int f32, const void* h, int64_t ldh, const void* w, int w_f32, const float* rstd,
+                          const void* dy, int dy_f32, int64_t lddy, const void* dh, int64_t lddh, void* dx,
+                          int64_t lddx, float* dw, int64_t rows, int cols, void* ws, hipStream_t stream) {
+  const NormGradArgs p = {h, ldh, w, w_f32, rstd, dy, lddy, dy_f32, dh, lddh, dx, lddx, static_cast<float*>(ws),
+                          rows, cols};
+  const int n = backward_blocks(rows);
+  if (n > 0) {
+    if (f32) launch_backward_type<float>(p, stream);
+    else launch_backward_type<uint16_t>(p, stream);
+  }
+  hipLaunchKernelGGL(k_norm_dweight, dim3((cols + 63) / 64), dim3(1024), 0, stream, p.part, n, cols, dw);
+}
+
+void launch_dequantize(int fmt, bool tiled, const uint8_t* q, const uint8_t* scales, const float* tscale,
+                       int64_t rows, int64_t cols, void* y, int y_f32, int64_t ldy, hipStream_t stream) {
+  const uint32_t cb = (uint32_t)((cols + 511) / 512);
+  const dim3 grid((unsigned)((rows + 15) / 16 * cb));
+  if (fmt == FP4Q_NVFP4)
+    hipLaunchKernelGGL(k_dequantize<EMIT_NVFP4>, grid, dim3(256), 0, stream, q, scales, tscale, tiled, rows, cols,
+                       y, y_f32, ldy, cb);
+  else if (fmt == FP4Q_MXFP4)
+    hipLaunchKernelGGL(k_dequantize<EMIT_MXFP4>, grid, dim3(256), 0, stream, q, scales, tscale, tiled, rows, cols,
+                       y, y_f32, ldy, cb);
+  else
+    hipLaunchKernelGGL(k_dequantize<EMIT_MXFP8>, grid, dim3(256), 0, stream, q, scales, tscale, tiled, rows, cols,
+                       y, y_f32, ldy, cb);
+}
+
+}  // namespace fp4q

@@ -33,6 +33,11 @@
  *    such that 6 * 2^e >= block_amax, stored as E8M0 code e + 127;
  *    element = e2m1(x * 2^-e).  No tensor scale.
  *  - packing: two codes per byte, even element in the low nibble.
+ *  - MXFP8 (an output of the norm, for layers kept in 8 bits): elements E4M3,
+ *    32-element blocks; scale 2^e with the smallest e in [-127, 127] such
+ *    that 448 * 2^e >= block_amax, stored as E8M0 code e + 127; element =
+ *    e4m3(x * 2^-e), nearest-even.  Row-major only: codes u8 [rows, cols],
+ *    scales u8 [rows, cols/32].
  *
  * Packed operand layouts (codes and block scales; chosen per call):
  *  - FP4Q_LAYOUT_ROWMAJOR: codes u8 [rows, cols/2], scales u8 [rows, cols/blk].
@@ -81,7 +86,8 @@
 extern "C" {
 #endif
 
-typedef enum { FP4Q_NVFP4 = 0, FP4Q_MXFP4 = 1 } fp4q_format_t;
+/* (FP4Q_MXFP8: fp4q_rms_norm_quantize and fp4q_dequantize only) */
+typedef enum { FP4Q_NVFP4 = 0, FP4Q_MXFP4 = 1, FP4Q_MXFP8 = 2 } fp4q_format_t;
 typedef enum { FP4Q_OUT_F32 = 0, FP4Q_OUT_BF16 = 1 } fp4q_dtype_t;
 typedef enum { FP4Q_LAYOUT_ROWMAJOR = 0, FP4Q_LAYOUT_TILED = 1 } fp4q_layout_t;
 
@@ -721,6 +727,44 @@ int fp4q_kv_read(fp4q_format_t fmt, const uint8_t* cache, int64_t n_pages, int32
                  uint16_t* k, int64_t ldk, uint16_t* v, int64_t ldv, const float* k_scale,
                  const float* v_scale, void* stream);
 
+/* fp4q_kv_append with the position rotation on the way, and the queries'.
+ * Each head's first `rot` elements are rot/2 pairs (x1, x2), which turn by the
+ * angle a = position * freqs[pair]:
+ *
+ *   x1' = x1 cos a - x2 sin a,   x2' = x2 cos a + x1 sin a
+ *
+ * computed in 64 bits (a the product rounded to them), rounded to F32 and then
+ * to BF16.  The keys so rotated are what fp4q_kv_append would be given; values
+ * are stored as they are.
+ *
+ *   q, q_out   bf16 [rows, heads, dim], row strides ldq, ldqo (multiples of 8,
+ *              16-byte aligned); q_out may be q itself, and overlaps it in no
+ *              other way
+ *   freqs      device f32 [rot/2], finite, with angles below 2^40 (they hold
+ *              whatever scaling of positions a model has)
+ *   rot        a multiple of 16 up to dim; further elements pass unchanged
+ *   pairs      FP4Q_PAIRS_HALVES: pair p is elements p and p + rot/2;
+ *              FP4Q_PAIRS_NEIGHBOURS: elements 2p and 2p + 1
+ *   positions  device int32 [rows], or NULL: the tokens' places in their
+ *              sequences (lens[b] - (offsets[b+1] - offsets[b]) + i); where
+ *              a key is stored goes by its place either way
+ *
+ * Rows past offsets[batch] are copied from q to q_out.  A token whose place is
+ * not in the cache (see above) is rotated too, and not stored.
+ * FP4Q_ERR_UNSUPPORTED: what fp4q_kv_append does not take of dim, page,
+ * kv_heads and table, rot not a multiple of 16, rows not below 2^26, heads *
+ * dim not below 2^31. */
+typedef enum { FP4Q_PAIRS_HALVES = 0, FP4Q_PAIRS_NEIGHBOURS = 1 } fp4q_pairs_t;
+
+int fp4q_kv_append_rotated(fp4q_format_t fmt, uint8_t* cache, int64_t n_pages, int32_t page,
+                           int32_t kv_heads, int32_t dim, const int32_t* offsets, int32_t batch,
+                           const int32_t* page_table, int64_t ld_table, int64_t table_cols,
+                           const int32_t* lens, int64_t rows, const uint16_t* q, int64_t ldq,
+                           int32_t heads, uint16_t* q_out, int64_t ldqo, const uint16_t* k,
+                           int64_t ldk, const uint16_t* v, int64_t ldv, const float* freqs,
+                           int32_t rot, fp4q_pairs_t pairs, const int32_t* positions,
+                           const float* k_scale, const float* v_scale, void* stream);
+
 /* Attention of the new tokens over the cache (their own keys and values
  * stored before):
  *
@@ -773,6 +817,132 @@ int fp4q_kv_attention(fp4q_format_t fmt, const uint8_t* cache, int64_t n_pages, 
                       int64_t max_new, int64_t max_len, int32_t window, float scale,
                       const float* k_scale, const float* v_scale, void* y, fp4q_dtype_t y_dtype,
                       int64_t ldy, void* workspace, size_t workspace_bytes, void* stream);
+
+/* fp4q_kv_attention with first tokens that stay visible behind the window: the
+ * keys with j <= position(r) and (j > position(r) - window or j < sinks).  The
+ * pages between the two are not read.  sinks 0, or no window: as
+ * fp4q_kv_attention.  The workspace is the size that its own query gives. */
+size_t fp4q_kv_attention_sinks_workspace_bytes(fp4q_format_t fmt, int64_t rows, int32_t heads,
+                                               int32_t kv_heads, int32_t dim, int32_t batch,
+                                               int64_t max_new, int64_t max_len, int32_t window,
+                                               int32_t sinks);
+
+int fp4q_kv_attention_sinks(fp4q_format_t fmt, const uint8_t* cache, int64_t n_pages, int32_t page,
+                            int32_t kv_heads, int32_t dim, const int32_t* offsets, int32_t batch,
+                            const int32_t* page_table, int64_t ld_table, int64_t table_cols,
+                            const int32_t* lens, int64_t rows, const uint16_t* q, int64_t ldq,
+                            int32_t heads, int64_t max_new, int64_t max_len, int32_t window,
+                            int32_t sinks, float scale, const float* k_scale, const float* v_scale,
+                            void* y, fp4q_dtype_t y_dtype, int64_t ldy, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/* The root-mean-square norm of a residual stream.  Per row:
+ *
+ *   h = x + residual (rounded to dtype; without a residual h is x)
+ *   r = 1 / sqrt(mean(h^2) + eps)
+ *   y = h r weight
+ *
+ * r and y are computed in 64 bits; y is rounded to F32, and from that to BF16
+ * where y_dtype is BF16 or it is quantized.
+ *
+ *   x, residual, h   f32 or bf16 (dtype) [rows, cols], row strides ldx, ldr,
+ *                    ldh of any size from cols on, aligned to their elements
+ *                    (16-byte aligned rows are faster); residual and h both
+ *                    NULL: none.  h may be x or residual (of its stride)
+ *   weight           f32 or bf16 (w_dtype) [cols]
+ *   eps              >= 0
+ *   y                out f32 or bf16 (y_dtype) [rows, cols], row stride ldy;
+ *                    may be x of the same type and stride
+ *   rstd             out f32 [rows]: r, for the gradient (or NULL)
+ *
+ * fp4q_rms_norm_quantize gives the operand of the product behind the norm:
+ * bit for bit what fp4q_quantize (one group) makes of the BF16 y, without y
+ * passing through memory (y: NULL, or written too).
+ *   fmt, layout, chan_idx, n_chan, q, scales, resid   as fp4q_quantize's;
+ *                    FP4Q_MXFP8: row-major, no channels
+ *   tensor_scale     device f32 [1] (NVFP4, else NULL): with scale_given
+ *                    read (positive; a calibrated one, and the whole is one
+ *                    pass: values beyond 2688 times it saturate), else written
+ *                    as fp4q_quantize's
+ *   workspace        fp4q_rms_norm_quantize_workspace_bytes() bytes, 8-byte
+ *                    aligned (may be NULL when that is 0), no initialisation
+ *
+ * fp4q_rms_norm_backward: with u = h r, g = weight d_y,
+ *   d_x = r (g - u mean(g u)) + d_h,   d_weight = sum over the rows of d_y u
+ * in F32; d_x is the gradient of x and of the residual.
+ *   h, rstd     of the forward call (x where there is no residual)
+ *   d_y         f32 or bf16 (dy_dtype);  d_h: of h's type, or NULL;  d_x out,
+ *               of h's type (may be d_h, or d_y of the same type and stride)
+ *   d_weight    out f32 [cols] (zeros when rows is 0)
+ *   workspace   fp4q_rms_norm_backward_workspace_bytes() bytes, 4-byte
+ *               aligned, no initialisation
+ * Sums are taken in the same order in every call.
+ *
+ * fp4q_dequantize writes the values that an operand of one group stands for
+ * (what a weight's gradient takes): (e2m1 * scale) * t, or element * 2^e, in
+ * F32, rounded to y_dtype.
+ *
+ * FP4Q_ERR_UNSUPPORTED: cols above 32768 (the norm's calls), rows not below
+ * 2^31; dequantize: rows or cols not below 2^31, or rows/16 * cols/512 (each
+ * rounded up) not below 2^24. */
+int fp4q_rms_norm(fp4q_dtype_t dtype, const void* x, int64_t ldx, const void* residual, int64_t ldr,
+                  void* h, int64_t ldh, const void* weight, fp4q_dtype_t w_dtype, double eps,
+                  int64_t rows, int64_t cols, void* y, fp4q_dtype_t y_dtype, int64_t ldy, float* rstd,
+                  void* stream);
+
+size_t fp4q_rms_norm_quantize_workspace_bytes(fp4q_format_t fmt, int64_t rows, int32_t scale_given);
+
+int fp4q_rms_norm_quantize(fp4q_format_t fmt, fp4q_layout_t layout, fp4q_dtype_t dtype, const void* x,
+                           int64_t ldx, const void* residual, int64_t ldr, void* h, int64_t ldh,
+                           const void* weight, fp4q_dtype_t w_dtype, double eps, int64_t rows,
+                           int64_t cols, const int32_t* chan_idx, int32_t n_chan, uint8_t* q,
+                           uint8_t* scales, float* tensor_scale, int32_t scale_given, uint16_t* resid,
+                           void* y, fp4q_dtype_t y_dtype, int64_t ldy, float* rstd, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+size_t fp4q_rms_norm_backward_workspace_bytes(int64_t rows, int64_t cols);
+
+int fp4q_rms_norm_backward(fp4q_dtype_t dtype, const void* h, int64_t ldh, const void* weight,
+                           fp4q_dtype_t w_dtype, const float* rstd, const void* d_y,
+                           fp4q_dtype_t dy_dtype, int64_t lddy, const void* d_h, int64_t lddh,
+                           void* d_x, int64_t lddx, float* d_weight, int64_t rows, int64_t cols,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+int fp4q_dequantize(fp4q_format_t fmt, fp4q_layout_t layout, const uint8_t* q, const uint8_t* scales,
+                    const float* tensor_scale, int64_t rows, int64_t cols, void* y, fp4q_dtype_t y_dtype,
+                    int64_t ldy, void* stream);
+
+/* Low-rank adapters of many requests beside a shared projection: for the rows
+ * r of request g (offsets[g] .. offsets[g+1]) and its adapter a = adapter[g],
+ *
+ *   out[r] = y[r] + scale[a] (x[r] A[a]^T) B[a]^T
+ *
+ *   x          bf16 [rows, K], row stride ldx (a multiple of 8, 16-byte
+ *              aligned): the projection's input
+ *   a, b       bf16 [n_adapters, rank, K], [n_adapters, N, rank], 16-byte
+ *              aligned; adapters of lower rank are padded with zeros
+ *   scale      device f32 [n_adapters], or NULL: 1
+ *   offsets    device int32 [n_groups + 1], non-decreasing, offsets[0] = 0
+ *   adapter    device int32 [n_groups]; outside 0 .. n_adapters - 1 (-1,
+ *              say): none
+ *   y, out     f32 or bf16 (dtype) [rows, N], row strides ldy, ldo of any size
+ *              from N on, aligned to their elements; y NULL: 0.  out may be y
+ *              (of its stride), and overlaps it in no other way
+ *   workspace  fp4q_lora_workspace_bytes() bytes, 16-byte aligned, no
+ *              initialisation
+ *
+ * Rows of a request without an adapter, and rows past the last request, are
+ * y's (zeros where y is NULL; untouched where out is y).  Products are BF16
+ * with F32 sums; x A^T is scaled in F32 and enters the second product as two
+ * BF16 terms (three for F32 out).  Sums are taken in the same order in every call.
+ * FP4Q_ERR_UNSUPPORTED: rank not a multiple of 8 or above 128, K not a multiple
+ * of 8, K or N not below 2^31, rows or n_groups not below 2^24. */
+size_t fp4q_lora_workspace_bytes(int64_t rows, int32_t n_groups, int32_t rank, int64_t K, int64_t N);
+
+int fp4q_lora(const uint16_t* x, int64_t ldx, const uint16_t* a, const uint16_t* b, const float* scale,
+              int32_t n_adapters, int32_t rank, const int32_t* offsets, const int32_t* adapter,
+              int32_t n_groups, int64_t rows, int64_t K, int64_t N, const void* y, int64_t ldy, void* out,
+              fp4q_dtype_t dtype, int64_t ldo, void* workspace, size_t workspace_bytes, void* stream);
 
 /* The router of an expert layer.  Per token t with logits x [experts]:
  *   score    softmax(x) or sigmoid(x)

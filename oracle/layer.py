@@ -1,8 +1,9 @@
 """Plain 64-bit forms of the operators between the FP4 linear layers: the
-paged FP4 key/value cache, attention over it, the router and the combination
-of the experts' outputs.  numpy only, written from the definitions that
-include/fp4q.h states: nearest-value searches over the enumerated grids for
-the formats, loops over sequences, heads and tokens for the rest.
+paged FP4 key/value cache (with the position rotation), attention over it, the
+norm, low-rank adapters, the router and the combination of the experts' outputs.
+numpy only, written from the definitions that include/fp4q.h states:
+nearest-value searches over the enumerated grids for the formats, loops over
+sequences, heads and tokens for the rest.
 """
 from __future__ import annotations
 
@@ -149,7 +150,8 @@ def kv_read(fmt, cache, page, offsets, table, lens, rows, dim, kt=None, vt=None)
     return k, v
 
 
-def attention(fmt, cache, page, offsets, table, lens, q, kt=None, vt=None, window=0, scale=None):
+def attention(fmt, cache, page, offsets, table, lens, q, kt=None, vt=None, window=0, scale=None,
+              sinks=0):
     """(o, bound): the outputs [rows, heads, D] in 64 bits and, beside them,
     what an implementation may be off by, short of the rounding of its result:
     `weights` = sum p |v| / z and `scores` = the largest sum |q k| scale of a
@@ -174,7 +176,7 @@ def attention(fmt, cache, page, offsets, table, lens, q, kt=None, vt=None, windo
         at = first + np.arange(n)[:, None]
         see = pos[None, :] <= at
         if window > 0:
-            see &= pos[None, :] > at - window
+            see &= (pos[None, :] > at - window) | (pos[None, :] < sinks)
         any_ = see.any(0)                        # keys that no row sees may hold anything
         pos, pid, see = pos[any_], pid[any_], see[:, any_]
         if pos.size == 0:
@@ -296,3 +298,83 @@ def combine_backward(y, row_of, weights, d_out):
                 d_w[t, j] = math.fsum(y[r] * d_out[t])
                 mag[t, j] = np.abs(y[r] * d_out[t]).sum()
     return d_y, d_w, mag
+
+
+# ---- rotation, norm, operands' values, adapters -----------------------------
+
+def rotate(x, positions, freqs, interleaved=False):
+    """x [rows, heads, D] with each head's first 2 len(freqs) elements turned by
+    positions [rows] times freqs, 64 bits, rounded as fp4q_kv_append_rotated
+    says: to f32, then to bf16."""
+    n = len(freqs)
+    a = (np.asarray(positions, np.float64)[:, None] * np.asarray(freqs, np.float32).astype(np.float64))[:, None]
+    c, s = np.cos(a), np.sin(a)
+    one = slice(0, 2 * n, 2) if interleaved else slice(0, n)
+    two = slice(1, 2 * n, 2) if interleaved else slice(n, 2 * n)
+    out = np.array(x, np.float64)
+    x1, x2 = out[..., one].copy(), out[..., two].copy()
+    out[..., one], out[..., two] = bf16_round(x1 * c - x2 * s), bf16_round(x2 * c + x1 * s)
+    return out
+
+
+def token_positions(offsets, lens, rows):
+    """Each new token's place in its sequence (0 for rows of none)."""
+    pos = np.zeros(rows, np.int64)
+    for b in range(len(lens)):
+        n = int(offsets[b + 1]) - int(offsets[b])
+        pos[offsets[b]:offsets[b + 1]] = int(lens[b]) - n + np.arange(n)
+    return pos
+
+
+def rms_norm(x, weight, eps, residual=None, bf16=True):
+    """(h, r, y) of fp4q_rms_norm: h rounded to bf16 (or f32), r and y not."""
+    h = np.asarray(x, np.float64)
+    if residual is not None:
+        h = h + residual
+        h = bf16_round(h) if bf16 else h.astype(np.float32).astype(np.float64)
+    r = 1.0 / np.sqrt((h * h).mean(1, keepdims=True) + eps)
+    return h, r, h * r * weight
+
+
+def rms_norm_backward(h, weight, r, d_y, d_h=None):
+    """(d_x, d_weight), and for the tolerances the sums of absolute terms beside
+    them: of a row's mean of g u, and of d_weight."""
+    u, g = h * r, weight * d_y
+    d_x = r * (g - u * (g * u).mean(1, keepdims=True))
+    if d_h is not None:
+        d_x = d_x + d_h
+    return d_x, (d_y * u).sum(0), np.abs(g * u).mean(1, keepdims=True), np.abs(d_y * u).sum(0)
+
+
+def mxfp8_quantize(x):
+    """x [rows, cols] (bf16 values) -> (codes u8, scale codes u8, values)."""
+    b = np.asarray(x, np.float64).reshape(x.shape[0], -1, 32)
+    amax = np.abs(b).max(-1)
+    e = np.full(amax.shape, -127)
+    for k in range(-127, 128):                              # the smallest e with 448 2^e >= amax
+        e = np.where(448.0 * 2.0 ** (k - 1) < amax, k, e)
+    f = 2.0 ** e.astype(np.float64)[..., None]
+    mag = _nearest(E4M3, np.abs(b) / f)
+    neg = np.signbit(b)
+    val = np.where(neg, -1.0, 1.0) * E4M3[mag] * f
+    return ((mag + 128 * neg).astype(np.uint8).reshape(x.shape), (e + 127).astype(np.uint8),
+            val.reshape(x.shape))
+
+
+def lora(x, a, b, offsets, adapters, scale=None, y=None):
+    """(out, inner, outer): out as fp4q_lora's, not rounded, and the sums of
+    absolute terms that bound its error: |scale| (|x| |A|^T) |B|^T and |scale|
+    |x A^T| |B|^T."""
+    rows, N = x.shape[0], b.shape[1]
+    out = np.zeros((rows, N)) if y is None else np.array(y, np.float64)
+    inner, outer = np.zeros((rows, N)), np.zeros((rows, N))
+    for g, j in enumerate(adapters):
+        if not 0 <= j < len(a):
+            continue
+        r = slice(int(offsets[g]), int(offsets[g + 1]))
+        s = 1.0 if scale is None else float(scale[j])
+        u = s * (x[r] @ a[j].T)
+        out[r] += u @ b[j].T
+        inner[r] = abs(s) * (np.abs(x[r]) @ np.abs(a[j]).T) @ np.abs(b[j]).T
+        outer[r] = np.abs(u) @ np.abs(b[j]).T
+    return out, inner, outer
