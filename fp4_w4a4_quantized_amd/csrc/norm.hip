@@ -48,7 +48,7 @@ struct NormArgs {
   uint8_t* q;
   uint8_t* scales;
   float* tscale;    // NVFP4: given, or written from the maxima
-  int n_max;        // maxima of the first pass (0: tscale is given)
+  int n_max;        // maxima of the first pass
   float* maxima;
   double* r64;      // the rows' r, first pass to second
   bool tiled;
@@ -126,11 +126,8 @@ template <> struct Raw<float> {
   }
 };
 
-// Chunks of a row that a lane holds, and elements that a row of WPR waves has then.
-template <typename T, int WPR>
-struct Held {
-  static constexpr int N = sizeof(T) == 2 || WPR == 8 ? 8 : 4, CAP = WPR * 64 * CH * N;
-};
+// Elements that a row of WPR waves with N chunks a lane has room for.
+constexpr int room(int wpr, int n) { return wpr * 64 * CH * n; }
 
 __device__ __forceinline__ void load_any(const void* p, int64_t at, int f32, int n, float (&f)[CH]) {
   if (f32) {
@@ -173,54 +170,48 @@ __device__ __forceinline__ uint32_t block_max(uint32_t v) {
   return v;
 }
 
-// A chunk of y (BF16) as codes: FP4's in w[0], MXFP8's in w[0], w[1]; the block's
-// scale code; and the values they stand for, where asked for.
-template <int EMIT>
-__device__ __forceinline__ uint32_t encode(const Raw<uint16_t>& y, uint32_t amax_bits, float t,
-                                           uint32_t (&w)[2], bool want, float (&val)[CH]) {
+// The tensor scale t as the NVFP4 encoder takes it.  Where it and every divisor
+// scale * t lie within quot_rn's range (all but the most extreme t), reciprocals
+// stand in a table by scale code and no division is left; else rt is 0.
+struct TensorScale {
+  float t, rt;
+  const float* reciprocal;  // LDS: RN(1 / (scale t)) by code, 0 for code 0
+};
+
+// A chunk of y (BF16) as codes: FP4's in w[0], MXFP8's in w[0], w[1]; returns the
+// block's scale code.  FAR: a given tensor scale, whose blocks may lie far past
+// what it can hold (their operands are held within 8 divisors: beyond that every
+// quotient gives the largest code).
+template <int EMIT, bool FAR>
+__device__ __forceinline__ uint32_t encode(const Raw<uint16_t>& y, uint32_t amax_bits, const TensorScale& ts,
+                                           uint32_t (&w)[2]) {
   const float amax = bf16_to_f32(amax_bits);
   float v[CH];
   if constexpr (EMIT == EMIT_NVFP4) {
-    const uint32_t sb = e4m3_encode((amax / 6.0f) / t);
-    const float s = e4m3_value(sb), d = s * t;
-    // quot_rn's range; its operands are held within 8 d (beyond it every
-    // quotient gives the largest code)
-    const bool fast = d >= 0x1p-96f && d <= 0x1p96f;
-    const float rd = fast ? 1.0f / d : 0.0f;
+    if (ts.rt != 0.0f) {
+      // amax / 6: one correction of amax RN(1/6) is the IEEE quotient for every BF16 amax
+      const float q = amax * (1.0f / 6.0f);
+      const float a6 = __builtin_fmaf(__builtin_fmaf(-q, 6.0f, amax), 1.0f / 6.0f, q);
+      const uint32_t sb = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(fminf(quot_rn(a6, ts.t, ts.rt), 448.0f), 0.0f,
+                                                                    0, false) & 0x7Fu;
+      const float d = e4m3_value(sb) * ts.t, rd = ts.reciprocal[sb];
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      const float e = y.at(i);
-      if (fast) v[i] = quot_rn(fminf(fmaxf(e, -8.0f * d), 8.0f * d), d, rd);
-      else v[i] = d > 0.0f ? e / d : 0.0f * e;
+      for (int i = 0; i < CH; ++i)
+        v[i] = quot_rn(FAR ? __builtin_amdgcn_fmed3f(y.at(i), -8.0f * d, 8.0f * d) : y.at(i), d, rd);
+      w[0] = e2m1_pack8(v);
+      return sb;
     }
+    const uint32_t sb = e4m3_encode((amax / 6.0f) / ts.t);
+    const float d = e4m3_value(sb) * ts.t;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) v[i] = d > 0.0f ? y.at(i) / d : 0.0f * y.at(i);
     w[0] = e2m1_pack8(v);
-    if (want) {
-#define FP4Q_PAIR(N)                                                                     \
-  {                                                                                      \
-    const f32x2n e = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[0], 1.0f, N);            \
-    val[2 * N] = (e[0] * s) * t;                                                         \
-    val[2 * N + 1] = (e[1] * s) * t;                                                     \
-  }
-      FP4Q_PAIR(0) FP4Q_PAIR(1) FP4Q_PAIR(2) FP4Q_PAIR(3)
-#undef FP4Q_PAIR
-    }
     return sb & 0xFFu;
   } else if constexpr (EMIT == EMIT_MXFP4) {
     const int e8 = mx_exponent(amax);
 #pragma unroll
     for (int i = 0; i < CH; ++i) v[i] = y.at(i);
     w[0] = e2m1_pack8(v, __uint_as_float((uint32_t)(e8 + 127) << 23));
-    if (want) {
-      const float s = exp2i(e8);
-#define FP4Q_PAIR(N)                                                                     \
-  {                                                                                      \
-    const f32x2n e = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[0], 1.0f, N);            \
-    val[2 * N] = e[0] * s;                                                               \
-    val[2 * N + 1] = e[1] * s;                                                           \
-  }
-      FP4Q_PAIR(0) FP4Q_PAIR(1) FP4Q_PAIR(2) FP4Q_PAIR(3)
-#undef FP4Q_PAIR
-    }
     return (uint32_t)(e8 + 127);
   } else {
     const int e8 = mx8_exponent(amax);
@@ -238,16 +229,55 @@ __device__ __forceinline__ uint32_t encode(const Raw<uint16_t>& y, uint32_t amax
   }
 }
 
-__device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-  for (int s = 32; s > 0; s >>= 1) v += __shfl_xor(v, s);
+// Sums and maxima over a wave by vector moves: within four lanes, eight, sixteen
+// (whose lanes then hold the same), and the lanes 16 and 32 apart.
+template <int CTRL>
+__device__ __forceinline__ uint32_t moved(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, true);
+}
+
+template <typename T, typename F>
+__device__ __forceinline__ T over_wave(T v, F join) {
+  constexpr int N = sizeof(T) / 4;
+  union U {
+    T t;
+    uint32_t w[N];
+  };
+#define FP4Q_STEP(MOVE)                                    \
+  {                                                        \
+    U a, b;                                                \
+    a.t = v;                                               \
+    _Pragma("unroll") for (int i = 0; i < N; ++i) b.w[i] = MOVE(a.w[i]); \
+    v = join(a.t, b.t);                                    \
+  }
+  FP4Q_STEP(moved<0xB1>)
+  FP4Q_STEP(moved<0x4E>)
+  FP4Q_STEP(moved<0x141>)
+  FP4Q_STEP(moved<0x140>)
+#undef FP4Q_STEP
+#define FP4Q_SWAP(SWAP)                                                                        \
+  {                                                                                            \
+    U a, p, q;                                                                                 \
+    a.t = v;                                                                                   \
+    _Pragma("unroll") for (int i = 0; i < N; ++i) {                                            \
+      const u32x2 r = __builtin_bit_cast(u32x2, SWAP(a.w[i], a.w[i], false, false));           \
+      p.w[i] = r[0];                                                                           \
+      q.w[i] = r[1];                                                                           \
+    }                                                                                          \
+    v = join(p.t, q.t);                                                                        \
+  }
+  FP4Q_SWAP(__builtin_amdgcn_permlane16_swap)
+  FP4Q_SWAP(__builtin_amdgcn_permlane32_swap)
+#undef FP4Q_SWAP
   return v;
 }
 
+template <typename T>
+__device__ __forceinline__ T wave_sum(T v) {
+  return over_wave(v, [](T a, T b) { return a + b; });
+}
 __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-#pragma unroll
-  for (int s = 32; s > 0; s >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, s));
-  return v;
+  return over_wave(v, [](uint32_t a, uint32_t b) { return max(a, b); });
 }
 
 // The group of rows that workgroup g takes.  Workgroups go to the eight XCDs in
@@ -260,24 +290,29 @@ __device__ __forceinline__ int64_t row_group(int64_t g, int64_t groups, int per1
   return base + (i & 7) * per16 + (i >> 3);
 }
 
-// WPR: waves of a row (a workgroup of four rows, or one).  SECOND: r and h are
-// given (the second pass of NVFP4's own tensor scale).
-template <typename T, int WPR, int EMIT, bool SECOND>
+// WPR: waves of a row (a workgroup of four rows, or one); N: chunks of a lane at
+// most.  SECOND: r and h are given (the second pass of NVFP4's own tensor scale).
+template <typename T, int WPR, int N, int EMIT, bool SECOND>
 __global__ __launch_bounds__(WPR == 8 ? 512 : 256) void k_norm(NormArgs p) {
-  constexpr int HELD = Held<T, WPR>::N, ROWS = WPR == 1 ? 4 : 1, WAVES = WPR * ROWS;
+  constexpr int ROWS = WPR == 1 ? 4 : 1, WAVES = WPR * ROWS;
   constexpr bool QUANT = EMIT >= EMIT_NVFP4;
-  extern __shared__ __attribute__((aligned(16))) uint8_t s_rows[];  // the rows' quantization errors
-  __shared__ double s_sum[WAVES];
+  // per row, for the selected channels: y, codes and scale codes
+  extern __shared__ __attribute__((aligned(16))) uint8_t s_rows[];
+  __shared__ double s_sum[2][WAVES];
   __shared__ uint32_t s_max[WAVES];
+  __shared__ float s_rec[EMIT == EMIT_NVFP4 ? 128 : 1];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int sub = WPR == 1 ? 0 : wave;
   const int nc = (p.cols + WPR * 64 * CH - 1) / (WPR * 64 * CH);
   const int col0 = (sub * 64 + lane) * CH;  // of chunk 0; chunk c: WPR * 512 c further
-  uint16_t* const errs = reinterpret_cast<uint16_t*>(s_rows) + (WPR == 1 ? wave * p.cols : 0);
+  uint8_t* const mine = s_rows + (WPR == 1 ? wave * 4 * p.cols : 0);
+  uint16_t* const ys = reinterpret_cast<uint16_t*>(mine);
+  uint32_t* const codes = reinterpret_cast<uint32_t*>(mine + 2 * p.cols);
+  uint8_t* const scs = mine + 2 * p.cols + p.cols / 2;
   uint32_t most = 0;
-  float t = 1.0f;
+  TensorScale ts = {1.0f, 0.0f, s_rec};
   if constexpr (EMIT == EMIT_NVFP4) {
-    if (p.n_max > 0) {
+    if (SECOND) {
       uint32_t m = 0;
       for (int i = threadIdx.x; i < p.n_max; i += WAVES * 64) m = max(m, __float_as_uint(p.maxima[i]));
       m = wave_max(m);
@@ -286,72 +321,80 @@ __global__ __launch_bounds__(WPR == 8 ? 512 : 256) void k_norm(NormArgs p) {
       m = 0;
 #pragma unroll
       for (int i = 0; i < WAVES; ++i) m = max(m, s_max[i]);
-      t = nv_tensor_scale(__uint_as_float(m));
-      if (blockIdx.x == 0 && threadIdx.x == 0) *p.tscale = t;
+      ts.t = nv_tensor_scale(__uint_as_float(m));
+      if (blockIdx.x == 0 && threadIdx.x == 0) *p.tscale = ts.t;
     } else {
-      t = *p.tscale;
+      ts.t = *p.tscale;
     }
-  }
-  for (int64_t gi = blockIdx.x; gi < p.groups; gi += gridDim.x) {
-    const int64_t row = row_group(gi, p.groups, 16 / ROWS, p.tiled) * ROWS + (WPR == 1 ? wave : 0);
-    if (WPR == 1 && row >= p.rows) continue;
-    Raw<T> h[HELD];
-    double ss = 0.0;
-    {
-      const T* x = static_cast<const T*>(SECOND && p.h ? p.h : p.x) + row * (SECOND && p.h ? p.ldh : p.ldx);
-      const T* res = static_cast<const T*>(p.res) + row * p.ldr;
-      constexpr int BATCH = HELD < 16 / (int)sizeof(T) ? HELD : 16 / (int)sizeof(T);  // loads in flight
-#pragma unroll
-      for (int c0 = 0; c0 < HELD; c0 += BATCH) {
-        if (c0 >= nc) break;
-        Raw<T> a[BATCH];
-#pragma unroll
-        for (int c = c0; c < c0 + BATCH; ++c) {
-          if (c >= nc) break;
-          const int col = col0 + c * WPR * 64 * CH;
-          if (col < p.cols) h[c].load(x + col, p.cols - col);
-        }
-        if (SECOND) continue;
-        if (p.res) {
-#pragma unroll
-          for (int c = c0; c < c0 + BATCH; ++c) {
-            if (c >= nc) break;
-            const int col = col0 + c * WPR * 64 * CH;
-            if (col < p.cols) a[c - c0].load(res + col, p.cols - col);
-          }
-        }
-#pragma unroll
-        for (int c = c0; c < c0 + BATCH; ++c) {
-          if (c >= nc) break;
-          const int col = col0 + c * WPR * 64 * CH;
-          if (col >= p.cols) continue;
-          if (p.res) {
-            float f[CH];
-#pragma unroll
-            for (int i = 0; i < CH; ++i) f[i] = h[c].at(i) + a[c - c0].at(i);
-            h[c].set(f);
-            h[c].store(static_cast<T*>(p.h) + row * p.ldh + col, p.cols - col);
-          }
-#pragma unroll
-          for (int i = 0; i < CH; ++i) {
-            const double v = h[c].at(i);
-            ss = __builtin_fma(v, v, ss);
-          }
-        }
+    if (ts.t >= 0x1p-80f && ts.t <= 0x1p80f) {
+      ts.rt = 1.0f / ts.t;
+      if (threadIdx.x < 128) {
+        const float d = e4m3_value(threadIdx.x) * ts.t;
+        s_rec[threadIdx.x] = d > 0.0f ? 1.0f / d : 0.0f;
       }
     }
+    __syncthreads();
+  }
+  int turn = 0;
+  for (int64_t gi = blockIdx.x; gi < p.groups; gi += gridDim.x, turn ^= 1) {
+    const int64_t row = row_group(gi, p.groups, 16 / ROWS, p.tiled) * ROWS + (WPR == 1 ? wave : 0);
+    if (WPR == 1 && row >= p.rows) continue;
+    // whole chunks where the columns are a multiple of 8
+    auto left = [&](int col) { return EMIT == EMIT_Y ? p.cols - col : CH; };
+    Raw<T> h[N];
     double r;
+    {
+      const T* x = static_cast<const T*>(SECOND && p.h ? p.h : p.x) + row * (SECOND && p.h ? p.ldh : p.ldx);
+#pragma unroll
+      for (int c = 0; c < N; ++c) {
+        if (c >= nc) break;
+        const int col = col0 + c * WPR * 64 * CH;
+        if (col < p.cols) h[c].load(x + col, left(col));
+      }
+    }
     if (SECOND) {
       r = p.r64[row];
     } else {
+      double ss = 0.0;
+      if (p.res) {
+        const T* res = static_cast<const T*>(p.res) + row * p.ldr;
+        T* out = static_cast<T*>(p.h) + row * p.ldh;
+        Raw<T> a[N];
+#pragma unroll
+        for (int c = 0; c < N; ++c) {
+          if (c >= nc) break;
+          const int col = col0 + c * WPR * 64 * CH;
+          if (col < p.cols) a[c].load(res + col, left(col));
+        }
+#pragma unroll
+        for (int c = 0; c < N; ++c) {
+          if (c >= nc) break;
+          const int col = col0 + c * WPR * 64 * CH;
+          if (col >= p.cols) continue;
+          float f[CH];
+#pragma unroll
+          for (int i = 0; i < CH; ++i) f[i] = h[c].at(i) + a[c].at(i);
+          h[c].set(f);
+          h[c].store(out + col, left(col));
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < N; ++c) {
+        if (c >= nc) break;
+        if (col0 + c * WPR * 64 * CH >= p.cols) continue;
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+          const double v = h[c].at(i);
+          ss = __builtin_fma(v, v, ss);
+        }
+      }
       ss = wave_sum(ss);
       if (WPR > 1) {
-        __syncthreads();  // (the sums of the row before have been read)
-        if (lane == 0) s_sum[wave] = ss;
+        if (lane == 0) s_sum[turn][wave] = ss;
         __syncthreads();
         ss = 0.0;
 #pragma unroll
-        for (int i = 0; i < WPR; ++i) ss += s_sum[i];
+        for (int i = 0; i < WPR; ++i) ss += s_sum[turn][i];
       }
       r = 1.0 / sqrt(ss / (double)p.cols + p.eps);
       if (lane == 0 && sub == 0) {
@@ -360,10 +403,10 @@ __global__ __launch_bounds__(WPR == 8 ? 512 : 256) void k_norm(NormArgs p) {
       }
     }
 #pragma unroll
-    for (int c = 0; c < HELD; ++c) {
+    for (int c = 0; c < N; ++c) {
       if (c >= nc) break;
-      const int col = col0 + c * WPR * 64 * CH, n = p.cols - col;
-      if (n <= 0) continue;
+      const int col = col0 + c * WPR * 64 * CH, n = left(col);
+      if (col >= p.cols) continue;
       float w[CH], f[CH];
       load_any(p.w, col, p.w_f32, n, w);
       if (sizeof(T) == 2 && !p.w_f32) {
@@ -382,9 +425,7 @@ __global__ __launch_bounds__(WPR == 8 ? 512 : 256) void k_norm(NormArgs p) {
           most = max(most, m);
         } else {
           uint32_t code[2];
-          float val[CH];
-          const uint32_t s = encode<EMIT>(y, block_max<EMIT == EMIT_NVFP4 ? 2 : 4>(m), t, code,
-                                          p.n_chan > 0, val);
+          const uint32_t s = encode<EMIT, !SECOND>(y, block_max<EMIT == EMIT_NVFP4 ? 2 : 4>(m), ts, code);
           if constexpr (EMIT == EMIT_MXFP8) {
             *reinterpret_cast<u32x2*>(p.q + row * p.cols + col) = u32x2{code[0], code[1]};
             if ((lane & 3) == 0) p.scales[row * (p.cols / 32) + col / 32] = (uint8_t)s;
@@ -393,23 +434,23 @@ __global__ __launch_bounds__(WPR == 8 ? 512 : 256) void k_norm(NormArgs p) {
             *reinterpret_cast<uint32_t*>(p.q + code_off(p.tiled, row, col >> 1, p.cols)) = code[0];
             if (col % BLK == 0) p.scales[scale_off<FMT>(p.tiled, row, col / BLK, p.cols)] = (uint8_t)s;
             if (p.n_chan > 0) {
-              float e[CH];
-#pragma unroll
-              for (int i = 0; i < CH; ++i) e[i] = y.at(i) - val[i];
-              Raw<uint16_t> b;
-              b.set(e);
-              *reinterpret_cast<u32x4*>(errs + col) = b.v;
+              *reinterpret_cast<u32x4*>(ys + col) = y.v;
+              codes[col / CH] = code[0];
+              scs[col / CH] = (uint8_t)s;
             }
           }
         }
       }
     }
-    if (QUANT && p.n_chan > 0) {
+    if (QUANT && EMIT != EMIT_MXFP8 && p.n_chan > 0) {
       if (WPR > 1) __syncthreads();
       else wave_fence();
       for (int j = sub * 64 + lane; j < p.n_chan; j += WPR * 64) {
-        const int ch = p.chan[j];
-        p.resid[row * p.n_chan + j] = (uint32_t)ch < (uint32_t)p.cols ? errs[ch] : 0;
+        const uint32_t ch = min((uint32_t)p.chan[j], (uint32_t)p.cols - 1);
+        const uint32_t e = codes[ch / CH] >> (4 * (ch % CH)) & 15u, s = scs[ch / CH];
+        const float mag = e2m1_mag_value(e & 7u) * (EMIT == EMIT_NVFP4 ? e4m3_value(s) : exp2i((int)s - 127)) * ts.t;
+        const f32x2n d = {bf16_to_f32(ys[ch]) - (e & 8u ? -mag : mag), 0.0f};
+        p.resid[row * p.n_chan + j] = (uint16_t)__builtin_bit_cast(uint32_t, __builtin_convertvector(d, bf16x2n));
       }
       if (WPR > 1) __syncthreads();
       else wave_fence();
@@ -491,8 +532,7 @@ __global__ __launch_bounds__(64 * WPR) void k_norm_backward(NormGradArgs p) {
         sum = __builtin_fmaf(g[c][i], u, sum);
       }
     }
-#pragma unroll
-    for (int s = 32; s > 0; s >>= 1) sum += __shfl_xor(sum, s);
+    sum = wave_sum(sum);
     if (lane == 0) s_sum[turn][wave] = sum;
     __syncthreads();
     sum = 0.0f;
@@ -531,14 +571,16 @@ __global__ __launch_bounds__(64 * WPR) void k_norm_backward(NormGradArgs p) {
   }
 }
 
-// d_weight from the workgroups' sums: 64 columns a workgroup, 16 threads on each.
-__global__ __launch_bounds__(1024) void k_norm_dweight(const float* __restrict__ part, int n, int cols,
-                                                       float* __restrict__ dw) {
-  __shared__ float s[16][64];
-  const int c = threadIdx.x & 63, k = threadIdx.x >> 6, col = blockIdx.x * 64 + c;
+// d_weight from the workgroups' sums: 16 columns a workgroup, 16 threads on each.
+__global__ __launch_bounds__(256) void k_norm_dweight(const float* __restrict__ part, int n, int cols,
+                                                      float* __restrict__ dw) {
+  __shared__ float s[16][16];
+  const int c = threadIdx.x & 15, k = threadIdx.x >> 4, col = blockIdx.x * 16 + c;
   float sum = 0.0f;
-  if (col < cols)
+  if (col < cols) {
+#pragma unroll 8
     for (int i = k; i < n; i += 16) sum += part[(int64_t)i * cols + col];
+  }
   s[k][c] = sum;
   __syncthreads();
   if (k > 0 || col >= cols) return;
@@ -599,50 +641,43 @@ __global__ __launch_bounds__(256) void k_dequantize(const uint8_t* __restrict__ 
 // The tensor scale of no rows.
 __global__ void k_scale_one(float* tscale) { *tscale = 1.0f; }
 
-constexpr int MAX_WGS = 2048;   // workgroups of a pass; further rows in turn
-constexpr int MAX_FIRST = 1024; // of the first of two passes: its maxima are read by all of the second
+constexpr int MAX_WGS = 2048;  // workgroups of a pass; further rows in turn
 
-// Waves of a row: one where the row fits and there are rows enough for all CUs,
-// else four, eight for the longest.
-template <typename T>
-int norm_waves(int64_t rows, int cols) {
-  if (rows >= 2048 && cols <= Held<T, 1>::CAP) return 1;
-  return cols <= Held<T, 4>::CAP ? 4 : 8;
-}
-
-template <typename T, int WPR, int EMIT, bool SECOND>
-int launch_pass(NormArgs p, int most, hipStream_t stream) {
+// Waves of a row and chunks of a lane: a wave for rows of up to 1024 columns where
+// there are enough of them for all CUs, else four or eight.
+template <typename T, int WPR, int N, int EMIT, bool SECOND>
+int launch_pass(NormArgs p, hipStream_t stream) {
   constexpr int ROWS = WPR == 1 ? 4 : 1;
   p.groups = (p.rows + ROWS - 1) / ROWS;
-  const int grid = (int)(p.groups < most ? p.groups : most);
-  const size_t lds = EMIT >= EMIT_NVFP4 && p.n_chan > 0 ? (size_t)ROWS * p.cols * 2 : 0;
-  hipLaunchKernelGGL((k_norm<T, WPR, EMIT, SECOND>), dim3(grid), dim3(WPR == 8 ? 512 : 256), lds, stream, p);
+  const int grid = (int)(p.groups < MAX_WGS ? p.groups : MAX_WGS);
+  const size_t lds = EMIT >= EMIT_NVFP4 && p.n_chan > 0 ? (size_t)ROWS * p.cols * 4 : 0;
+  hipLaunchKernelGGL((k_norm<T, WPR, N, EMIT, SECOND>), dim3(grid), dim3(WPR == 8 ? 512 : 256), lds, stream, p);
   return grid;
 }
 
-template <typename T, int WPR>
+template <typename T, int WPR, int N>
 void launch_emit(NormArgs p, int emit, bool given, hipStream_t stream) {
   if (emit == EMIT_Y) {
-    launch_pass<T, WPR, EMIT_Y, false>(p, MAX_WGS, stream);
+    launch_pass<T, WPR, N, EMIT_Y, false>(p, stream);
   } else if (emit == EMIT_MXFP4) {
-    launch_pass<T, WPR, EMIT_MXFP4, false>(p, MAX_WGS, stream);
+    launch_pass<T, WPR, N, EMIT_MXFP4, false>(p, stream);
   } else if (emit == EMIT_MXFP8) {
-    launch_pass<T, WPR, EMIT_MXFP8, false>(p, MAX_WGS, stream);
+    launch_pass<T, WPR, N, EMIT_MXFP8, false>(p, stream);
   } else if (given) {
-    launch_pass<T, WPR, EMIT_NVFP4, false>(p, MAX_WGS, stream);
+    launch_pass<T, WPR, N, EMIT_NVFP4, false>(p, stream);
   } else {
-    p.n_max = launch_pass<T, WPR, EMIT_MAX, false>(p, MAX_FIRST, stream);
+    p.n_max = launch_pass<T, WPR, N, EMIT_MAX, false>(p, stream);
     p.rstd = nullptr;
-    launch_pass<T, WPR, EMIT_NVFP4, true>(p, MAX_WGS, stream);
+    launch_pass<T, WPR, N, EMIT_NVFP4, true>(p, stream);
   }
 }
 
 template <typename T>
 void launch_type(const NormArgs& p, int emit, bool given, hipStream_t stream) {
-  const int w = norm_waves<T>(p.rows, p.cols);
-  if (w == 1) launch_emit<T, 1>(p, emit, given, stream);
-  else if (w == 4) launch_emit<T, 4>(p, emit, given, stream);
-  else launch_emit<T, 8>(p, emit, given, stream);
+  if (p.rows >= 2048 && p.cols <= room(1, 2)) launch_emit<T, 1, 2>(p, emit, given, stream);
+  else if (p.cols <= room(4, 2)) launch_emit<T, 4, 2>(p, emit, given, stream);
+  else if (p.cols <= room(4, 4)) launch_emit<T, 4, 4>(p, emit, given, stream);
+  else launch_emit<T, 8, 8>(p, emit, given, stream);
 }
 
 int backward_blocks(int64_t rows) { return (int)(rows < 512 ? rows : 512); }
@@ -650,18 +685,18 @@ int backward_blocks(int64_t rows) { return (int)(rows < 512 ? rows : 512); }
 template <typename T>
 void launch_backward_type(const NormGradArgs& p, hipStream_t stream) {
   const dim3 grid(backward_blocks(p.rows));
-  if (p.cols <= 4096) hipLaunchKernelGGL((k_norm_backward<T, 4, 2>), grid, dim3(256), 0, stream, p);
-  else if (p.cols <= 8192) hipLaunchKernelGGL((k_norm_backward<T, 4, 4>), grid, dim3(256), 0, stream, p);
-  else if (p.cols <= 16384) hipLaunchKernelGGL((k_norm_backward<T, 8, 4>), grid, dim3(512), 0, stream, p);
+  if (p.cols <= room(4, 2)) hipLaunchKernelGGL((k_norm_backward<T, 4, 2>), grid, dim3(256), 0, stream, p);
+  else if (p.cols <= room(4, 4)) hipLaunchKernelGGL((k_norm_backward<T, 4, 4>), grid, dim3(256), 0, stream, p);
+  else if (p.cols <= room(8, 4)) hipLaunchKernelGGL((k_norm_backward<T, 8, 4>), grid, dim3(512), 0, stream, p);
   else hipLaunchKernelGGL((k_norm_backward<T, 8, 8>), grid, dim3(512), 0, stream, p);
 }
 
 }  // namespace
 
-int norm_max_cols() { return Held<float, 8>::CAP; }
+int norm_max_cols() { return room(8, 8); }
 
 // First of the second pass's inputs: the rows' r; then the maxima.
-size_t norm_workspace_bytes(int64_t rows) { return (size_t)rows * 8 + MAX_FIRST * 4; }
+size_t norm_workspace_bytes(int64_t rows) { return (size_t)rows * 8 + MAX_WGS * 4; }
 
 void launch_norm(int f32, const void* x, int64_t ldx, const void* res, int64_t ldr, void* h, int64_t ldh,
                  const void* w, int w_f32, double eps, int64_t rows, int cols, void* y, int y_f32, int64_t ldy,
@@ -715,7 +750,7 @@ void launch_norm_backward(int f32, const void* h, int64_t ldh, const void* w, in
     if (f32) launch_backward_type<float>(p, stream);
     else launch_backward_type<uint16_t>(p, stream);
   }
-  hipLaunchKernelGGL(k_norm_dweight, dim3((cols + 63) / 64), dim3(1024), 0, stream, p.part, n, cols, dw);
+  hipLaunchKernelGGL(k_norm_dweight, dim3((cols + 15) / 16), dim3(256), 0, stream, p.part, n, cols, dw);
 }
 
 void launch_dequantize(int fmt, bool tiled, const uint8_t* q, const uint8_t* scales, const float* tscale,
