@@ -335,6 +335,20 @@ __global__ __launch_bounds__(WPR == 8 ? 512 : 256) void k_norm(NormArgs p) {
     }
     __syncthreads();
   }
+  // What does not change from row to row: the weights of few chunks, and where a
+  // chunk's codes and scale stand in row 0 of a block of rows.
+  constexpr bool KEEP = N <= 2;
+  constexpr int FMT = EMIT == EMIT_NVFP4 ? FP4Q_NVFP4 : FP4Q_MXFP4, BLK = FMT == FP4Q_NVFP4 ? 16 : 32;
+  float kept[KEEP ? N : 1][CH];
+  int64_t code0[N], scale0[N];
+#pragma unroll
+  for (int c = 0; c < N; ++c) {
+    const int col = col0 + c * WPR * 64 * CH;
+    if (c >= nc || col >= p.cols) continue;
+    if (KEEP) load_any(p.w, col, p.w_f32, EMIT == EMIT_Y ? p.cols - col : CH, kept[KEEP ? c : 0]);
+    code0[c] = code_off(p.tiled, 0, col >> 1, p.cols);
+    scale0[c] = scale_off<FMT>(p.tiled, 0, col / BLK, p.cols);
+  }
   int turn = 0;
   for (int64_t gi = blockIdx.x; gi < p.groups; gi += gridDim.x, turn ^= 1) {
     const int64_t row = row_group(gi, p.groups, 16 / ROWS, p.tiled) * ROWS + (WPR == 1 ? wave : 0);
@@ -402,13 +416,19 @@ __global__ __launch_bounds__(WPR == 8 ? 512 : 256) void k_norm(NormArgs p) {
         if (p.rstd) p.rstd[row] = (float)r;
       }
     }
+    const int64_t code_row = code_off(p.tiled, row, 0, p.cols), scale_row = scale_off<FMT>(p.tiled, row, 0, p.cols);
 #pragma unroll
     for (int c = 0; c < N; ++c) {
       if (c >= nc) break;
       const int col = col0 + c * WPR * 64 * CH, n = left(col);
       if (col >= p.cols) continue;
       float w[CH], f[CH];
-      load_any(p.w, col, p.w_f32, n, w);
+      if (KEEP) {
+#pragma unroll
+        for (int i = 0; i < CH; ++i) w[i] = kept[KEEP ? c : 0][i];
+      } else {
+        load_any(p.w, col, p.w_f32, n, w);
+      }
       if (sizeof(T) == 2 && !p.w_f32) {
 #pragma unroll
         for (int i = 0; i < CH; ++i) f[i] = (float)((double)(h[c].at(i) * w[i]) * r);  // (the first product is exact)
@@ -430,9 +450,8 @@ __global__ __launch_bounds__(WPR == 8 ? 512 : 256) void k_norm(NormArgs p) {
             *reinterpret_cast<u32x2*>(p.q + row * p.cols + col) = u32x2{code[0], code[1]};
             if ((lane & 3) == 0) p.scales[row * (p.cols / 32) + col / 32] = (uint8_t)s;
           } else {
-            constexpr int FMT = EMIT == EMIT_NVFP4 ? FP4Q_NVFP4 : FP4Q_MXFP4, BLK = FMT == FP4Q_NVFP4 ? 16 : 32;
-            *reinterpret_cast<uint32_t*>(p.q + code_off(p.tiled, row, col >> 1, p.cols)) = code[0];
-            if (col % BLK == 0) p.scales[scale_off<FMT>(p.tiled, row, col / BLK, p.cols)] = (uint8_t)s;
+            *reinterpret_cast<uint32_t*>(p.q + code_row + code0[c]) = code[0];
+            if (col % BLK == 0) p.scales[scale_row + scale0[c]] = (uint8_t)s;
             if (p.n_chan > 0) {
               *reinterpret_cast<u32x4*>(ys + col) = y.v;
               codes[col / CH] = code[0];
@@ -506,7 +525,7 @@ __global__ __launch_bounds__(64 * WPR) void k_norm_backward(NormGradArgs p) {
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, turn ^= 1) {
     const T* h = static_cast<const T*>(p.h) + row * p.ldh;
     const float r = p.rstd[row];
-    Raw<T> hr[N];
+    Raw<T> hr[N], dh[N];
     float g[N][CH];
 #pragma unroll
     for (int c = 0; c < N; ++c) {
@@ -515,6 +534,7 @@ __global__ __launch_bounds__(64 * WPR) void k_norm_backward(NormGradArgs p) {
       if (n <= 0) continue;
       hr[c].load(h + col, n);
       load_any(p.dy, row * p.lddy + col, p.dy_f32, n, g[c]);
+      if (p.dh) dh[c].load(static_cast<const T*>(p.dh) + row * p.lddh + col, n);
     }
     float sum = 0.0f;
 #pragma unroll
@@ -549,10 +569,8 @@ __global__ __launch_bounds__(64 * WPR) void k_norm_backward(NormGradArgs p) {
 #pragma unroll
       for (int i = 0; i < CH; ++i) f[i] = r * __builtin_fmaf(-(hr[c].at(i) * r), sum, g[c][i]);
       if (p.dh) {
-        Raw<T> d;
-        d.load(static_cast<const T*>(p.dh) + row * p.lddh + col, n);
 #pragma unroll
-        for (int i = 0; i < CH; ++i) f[i] += d.at(i);
+        for (int i = 0; i < CH; ++i) f[i] += dh[c].at(i);
       }
       Raw<T> o;
       o.set(f);
@@ -680,7 +698,7 @@ void launch_type(const NormArgs& p, int emit, bool given, hipStream_t stream) {
   else launch_emit<T, 8, 8>(p, emit, given, stream);
 }
 
-int backward_blocks(int64_t rows) { return (int)(rows < 512 ? rows : 512); }
+int backward_blocks(int64_t rows) { return (int)(rows < 1024 ? rows : 1024); }
 
 template <typename T>
 void launch_backward_type(const NormGradArgs& p, hipStream_t stream) {
