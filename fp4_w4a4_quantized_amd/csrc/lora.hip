@@ -26,8 +26,6 @@ typedef __bf16 bf16x8l __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x4_2l __attribute__((ext_vector_type(4), aligned(2)));
 typedef uint32_t u32x4_4l __attribute__((ext_vector_type(4), aligned(4)));
 
-constexpr int LORA_STEPS = 4;  // steps of 32 along K that a wave loads together
-
 struct LoraArgs {
   const uint16_t* x;
   int64_t ldx;
@@ -57,39 +55,49 @@ struct LoraTile {
   int n, a;
 };
 
+// Sum of v over the lanes up to this one, by vector moves: within 16 lanes, then
+// the last of each 16 added to the next, and of the lower 32 to the upper.
+__device__ __forceinline__ int sum_to_lane(int v) {
+#define FP4Q_SHIFT(CTRL, ROWS) v += __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
+  FP4Q_SHIFT(0x111, 0xF)  // one lane up
+  FP4Q_SHIFT(0x112, 0xF)
+  FP4Q_SHIFT(0x114, 0xF)
+  FP4Q_SHIFT(0x118, 0xF)
+  FP4Q_SHIFT(0x142, 0xA)  // lane 15 of a row to the next row
+  FP4Q_SHIFT(0x143, 0xC)  // lane 31 to the upper half
+#undef FP4Q_SHIFT
+  return v;
+}
+
 // Tile number `tile` when each request's rows are cut into tiles of TM; after
 // the last request come the rows of none.  By a whole wave, 64 requests a step.
 template <int TM>
-__device__ __forceinline__ LoraTile lora_tile(const LoraArgs& p, int64_t tile) {
-  const int lane = threadIdx.x & 63;
+__device__ __forceinline__ LoraTile lora_tile(const LoraArgs& p, int tile) {
+  const int lane = threadIdx.x & 63, rows = (int)p.rows;
   LoraTile t = {0, 0, -1};
-  int64_t before = 0;
+  int before = 0;
   for (int g0 = 0; g0 <= p.G; g0 += 64) {
     const int g = g0 + lane;
-    int64_t r0 = 0, r1 = 0;
+    int r0 = 0, r1 = 0, id = -1;
     if (g <= p.G) {
-      r0 = min(max((int64_t)p.off[g], (int64_t)0), p.rows);
-      r1 = g < p.G ? min(max((int64_t)p.off[g + 1], r0), p.rows) : p.rows;
+      r0 = min(max(p.off[g], 0), rows);
+      r1 = g < p.G ? min(max(p.off[g + 1], r0), rows) : rows;
+      if (g < p.G) id = p.adapter[g];
     }
-    int64_t sum = (r1 - r0 + TM - 1) / TM;
-    const int64_t mine = sum;
-#pragma unroll
-    for (int s = 1; s < 64; s <<= 1) {
-      const int64_t o = __shfl_up(sum, s);
-      if (lane >= s) sum += o;
-    }
-    const int64_t first = before + sum - mine;  // of this request's tiles
-    const uint64_t hit = __ballot(tile >= first && tile < first + mine);
+    const int mine = (r1 - r0 + TM - 1) / TM;
+    const int to = before + sum_to_lane(mine), first = to - mine;  // of this request's tiles
+    const uint64_t hit = __ballot(tile >= first && tile < to);
     if (hit) {
       const int at = __ffsll((unsigned long long)hit) - 1;
-      const int64_t from = __shfl(r0, at) + (tile - __shfl(first, at)) * TM;
+      auto of = [&](int v) { return __builtin_amdgcn_readlane(v, at); };
+      const int from = of(r0) + (tile - of(first)) * TM;
       t.r0 = from;
-      t.n = (int)min((int64_t)TM, __shfl(r1, at) - from);
-      const int id = g0 + at < p.G ? p.adapter[g0 + at] : -1;
-      t.a = id >= 0 && id < p.adapters ? id : -1;
+      t.n = min(TM, of(r1) - from);
+      t.a = of(id);
+      if (t.a < 0 || t.a >= p.adapters) t.a = -1;
       return t;
     }
-    before += __shfl(sum, 63);
+    before = __builtin_amdgcn_readlane(to, 63);
   }
   return t;
 }
@@ -124,25 +132,41 @@ __global__ __launch_bounds__(256) void k_lora_u(LoraArgs p) {
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int i = 0; i < RT; ++i) acc[m][i] = {0.0f, 0.0f, 0.0f, 0.0f};
-  constexpr int U = MT * RT >= 8 ? 2 : LORA_STEPS;
-  for (int64_t k = k0 + wave * (32 * U); k < k1; k += 128 * U) {
-    u32x4 fa[U][RT], fx[U][MT];
+  constexpr int U = MT * RT >= 32 ? 1 : MT * RT >= 8 ? 2 : 4;  // steps of 32 along K that are loaded together
+  struct Batch {
+    u32x4 a[U][RT], x[U][MT];
+  };
+  auto load = [&](Batch& f, int64_t k) {
 #pragma unroll
     for (int s = 0; s < U; ++s) {
       const bool in = k + 32 * s + 8 * g < k1;  // (K and a split's end are multiples of 8)
 #pragma unroll
       for (int i = 0; i < RT; ++i)
-        fa[s][i] = in && a_on[i] ? *reinterpret_cast<const u32x4*>(a[i] + k + 32 * s) : u32x4{0, 0, 0, 0};
+        f.a[s][i] = in && a_on[i] ? *reinterpret_cast<const u32x4*>(a[i] + k + 32 * s) : u32x4{0, 0, 0, 0};
 #pragma unroll
       for (int m = 0; m < MT; ++m)
-        fx[s][m] = in ? *reinterpret_cast<const u32x4*>(x[m] + k + 32 * s) : u32x4{0, 0, 0, 0};
+        f.x[s][m] = in ? *reinterpret_cast<const u32x4*>(x[m] + k + 32 * s) : u32x4{0, 0, 0, 0};
     }
+  };
+  auto multiply = [&](const Batch& f) {
 #pragma unroll
     for (int s = 0; s < U; ++s)
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int i = 0; i < RT; ++i) acc[m][i] = product(fa[s][i], fx[s][m], acc[m][i]);
+        for (int i = 0; i < RT; ++i) acc[m][i] = product(f.a[s][i], f.x[s][m], acc[m][i]);
+  };
+  // the next batch on its way while one is multiplied
+  constexpr int64_t STRIDE = 128 * U;
+  Batch f0, f1;
+  int64_t k = k0 + wave * (32 * U);
+  if (k < k1) load(f0, k);
+  for (; k < k1; k += 2 * STRIDE) {
+    if (k + STRIDE < k1) load(f1, k + STRIDE);
+    multiply(f0);
+    if (k + STRIDE >= k1) break;
+    if (k + 2 * STRIDE < k1) load(f0, k + 2 * STRIDE);
+    multiply(f1);
   }
 #pragma unroll
   for (int m = 0; m < MT; ++m)
@@ -231,6 +255,34 @@ __global__ __launch_bounds__(256) void k_lora_out(LoraArgs p) {
   const LoraTile t = lora_tile<TM>(p, blockIdx.x);
   if (t.n == 0 || (t.a < 0 && p.y == p.out)) return;
   const int64_t first = (int64_t)blockIdx.y * p.iters * 256 + wave * 64;
+  const T* y = static_cast<const T*>(p.y);
+  Sixteen<T> o[MT];
+  u32x4 fb[4];
+  auto load_b = [&](int64_t n0, int s) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t n = n0 + 16 * (c >> 2) + 4 * i + (c & 3);
+      fb[i] = t.a >= 0 && n < p.N && 32 * s + 8 * g < p.rank
+                  ? *reinterpret_cast<const u32x4*>(p.b + ((int64_t)t.a * p.N + n) * p.rank + 32 * s + 8 * g)
+                  : u32x4{0, 0, 0, 0};
+    }
+  };
+  auto load = [&](int64_t n0) {  // y's part, and B's for the first ranks
+    const int64_t at = n0 + 16 * g;
+    const int left = (int)min((int64_t)16, p.N - at);  // (below 1: none of this lane's)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const int row = 16 * m + c;
+      if (y && row < t.n && left > 0) {
+        o[m].load(y + (t.r0 + row) * p.ldy + at, left);
+      } else {
+#pragma unroll
+        for (auto& w : o[m].v) w = u32x4{0, 0, 0, 0};
+      }
+    }
+    load_b(n0, 0);
+  };
+  load(first);  // (on its way while u is split)
   if (t.a >= 0) {
     // u as BF16 terms: a thread four ranks of a row
     const float s = p.scale ? p.scale[t.a] : 1.0f;
@@ -255,24 +307,11 @@ __global__ __launch_bounds__(256) void k_lora_out(LoraArgs p) {
     }
     __syncthreads();
   }
-  const T* y = static_cast<const T*>(p.y);
   T* out = static_cast<T*>(p.out);
   for (int it = 0; it < p.iters; ++it) {
     const int64_t n0 = first + it * 256;
     if (n0 >= p.N) break;
-    const int64_t at = n0 + 16 * g;
-    const int left = (int)min((int64_t)16, p.N - at);  // (below 1: none of this lane's)
-    Sixteen<T> o[MT];
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      const int row = 16 * m + c;
-      if (y && row < t.n && left > 0) {
-        o[m].load(y + (t.r0 + row) * p.ldy + at, left);
-      } else {
-#pragma unroll
-        for (auto& w : o[m].v) w = u32x4{0, 0, 0, 0};
-      }
-    }
+    if (it > 0) load(n0);
     if (t.a >= 0) {
       f32x4l acc[MT][4];
 #pragma unroll
@@ -281,14 +320,7 @@ __global__ __launch_bounds__(256) void k_lora_out(LoraArgs p) {
         for (int i = 0; i < 4; ++i) acc[m][i] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int s = 0; s < RS; ++s) {
-        u32x4 fb[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int64_t n = n0 + 16 * (c >> 2) + 4 * i + (c & 3);
-          fb[i] = n < p.N && 32 * s + 8 * g < p.rank
-                      ? *reinterpret_cast<const u32x4*>(p.b + ((int64_t)t.a * p.N + n) * p.rank + 32 * s + 8 * g)
-                      : u32x4{0, 0, 0, 0};
-        }
+        if (s > 0) load_b(n0, s);
 #pragma unroll
         for (int e = 0; e < TERMS; ++e)
 #pragma unroll
@@ -303,10 +335,11 @@ __global__ __launch_bounds__(256) void k_lora_out(LoraArgs p) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[m].add(i, acc[m][i]);
     }
+    const int left = (int)min((int64_t)16, p.N - (n0 + 16 * g));
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       const int row = 16 * m + c;
-      if (row < t.n && left > 0) o[m].store(out + (t.r0 + row) * p.ldo + at, left);
+      if (row < t.n && left > 0) o[m].store(out + (t.r0 + row) * p.ldo + n0 + 16 * g, left);
     }
   }
 }
