@@ -78,12 +78,11 @@ __device__ __forceinline__ LoraTile lora_tile(const LoraArgs& p, int tile) {
   int before = 0;
   for (int g0 = 0; g0 <= p.G; g0 += 64) {
     const int g = g0 + lane;
-    int r0 = 0, r1 = 0, id = -1;
-    if (g <= p.G) {
-      r0 = min(max(p.off[g], 0), rows);
-      r1 = g < p.G ? min(max(p.off[g + 1], r0), rows) : rows;
-      if (g < p.G) id = p.adapter[g];
-    }
+    // (loads side by side, of some request where there is none)
+    const int o0 = p.off[min(g, p.G)], o1 = p.off[min(g + 1, p.G)], o2 = p.adapter[min(g, p.G - 1)];
+    const int r0 = g <= p.G ? min(max(o0, 0), rows) : rows;
+    const int r1 = g < p.G ? min(max(o1, r0), rows) : rows;
+    const int id = g < p.G ? o2 : -1;
     const int mine = (r1 - r0 + TM - 1) / TM;
     const int to = before + sum_to_lane(mine), first = to - mine;  // of this request's tiles
     const uint64_t hit = __ballot(tile >= first && tile < to);
@@ -113,20 +112,18 @@ template <int MT, int RT>
 __global__ __launch_bounds__(256) void k_lora_u(LoraArgs p) {
   constexpr int TM = 16 * MT;
   __shared__ f32x4l s_acc[4][MT * RT][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, g = lane >> 4;
+  const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const LoraTile t = lora_tile<TM>(p, blockIdx.x);
   if (t.n == 0 || t.a < 0) return;
   const int64_t k0 = blockIdx.y * p.chunk, k1 = min(p.K, k0 + p.chunk);
+  // (of ranks and rows that are not there the last one's: what comes of them is not used)
   const uint16_t* a[RT];
   const uint16_t* x[MT];
-  bool a_on[RT];
 #pragma unroll
-  for (int i = 0; i < RT; ++i) {
-    a_on[i] = 16 * i + c < p.rank;
-    a[i] = p.a + ((int64_t)t.a * p.rank + (a_on[i] ? 16 * i + c : 0)) * p.K + 8 * g;
-  }
+  for (int i = 0; i < RT; ++i) a[i] = p.a + ((int64_t)t.a * p.rank + min(16 * i + c, p.rank - 1)) * p.K;
 #pragma unroll
-  for (int i = 0; i < MT; ++i) x[i] = p.x + (t.r0 + min(16 * i + c, t.n - 1)) * p.ldx + 8 * g;
+  for (int i = 0; i < MT; ++i) x[i] = p.x + (t.r0 + min(16 * i + c, t.n - 1)) * p.ldx;
   f32x4l acc[MT][RT];
 #pragma unroll
   for (int m = 0; m < MT; ++m)
@@ -136,19 +133,26 @@ __global__ __launch_bounds__(256) void k_lora_u(LoraArgs p) {
   struct Batch {
     u32x4 a[U][RT], x[U][MT];
   };
+  // Loads without conditions, so that none waits for another: past the split's
+  // end its first ones again, for which x counts as 0.
   auto load = [&](Batch& f, int64_t k) {
 #pragma unroll
     for (int s = 0; s < U; ++s) {
-      const bool in = k + 32 * s + 8 * g < k1;  // (K and a split's end are multiples of 8)
+      const int64_t at = k + 32 * s + 8 * g < k1 ? k + 32 * s + 8 * g : k0;  // (K and a split's end: multiples of 8)
 #pragma unroll
-      for (int i = 0; i < RT; ++i)
-        f.a[s][i] = in && a_on[i] ? *reinterpret_cast<const u32x4*>(a[i] + k + 32 * s) : u32x4{0, 0, 0, 0};
+      for (int i = 0; i < RT; ++i) f.a[s][i] = *reinterpret_cast<const u32x4*>(a[i] + at);
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
-        f.x[s][m] = in ? *reinterpret_cast<const u32x4*>(x[m] + k + 32 * s) : u32x4{0, 0, 0, 0};
+      for (int m = 0; m < MT; ++m) f.x[s][m] = *reinterpret_cast<const u32x4*>(x[m] + at);
     }
   };
-  auto multiply = [&](const Batch& f) {
+  auto multiply = [&](Batch& f, int64_t k) {
+    if (k + 32 * U > k1) {
+#pragma unroll
+      for (int s = 0; s < U; ++s)
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+          if (k + 32 * s + 8 * g >= k1) f.x[s][m] = u32x4{0, 0, 0, 0};
+    }
 #pragma unroll
     for (int s = 0; s < U; ++s)
 #pragma unroll
@@ -163,10 +167,10 @@ __global__ __launch_bounds__(256) void k_lora_u(LoraArgs p) {
   if (k < k1) load(f0, k);
   for (; k < k1; k += 2 * STRIDE) {
     if (k + STRIDE < k1) load(f1, k + STRIDE);
-    multiply(f0);
+    multiply(f0, k);
     if (k + STRIDE >= k1) break;
     if (k + 2 * STRIDE < k1) load(f0, k + 2 * STRIDE);
-    multiply(f1);
+    multiply(f1, k + STRIDE);
   }
 #pragma unroll
   for (int m = 0; m < MT; ++m)
@@ -183,165 +187,221 @@ __global__ __launch_bounds__(256) void k_lora_u(LoraArgs p) {
   }
 }
 
-// Sixteen neighbouring elements of a row of y or out, from column n0 on.
-template <typename T> struct Sixteen;
-template <> struct Sixteen<uint16_t> {
-  u32x4 v[2];
+// Sixteen bytes of a row of y or out; n: elements that the row has from p on.
+template <typename T> struct Piece;
+template <> struct Piece<uint16_t> {
+  static constexpr int N = 8;
+  u32x4 v;
   __device__ __forceinline__ void load(const uint16_t* p, int n) {
-    if (n >= 16) {
-      v[0] = *reinterpret_cast<const u32x4_2l*>(p);
-      v[1] = *reinterpret_cast<const u32x4_2l*>(p + 8);
+    if (n >= N) {
+      v = *reinterpret_cast<const u32x4_2l*>(p);
     } else {
-      v[0] = v[1] = u32x4{0, 0, 0, 0};
+      v = u32x4{0, 0, 0, 0};
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (i < n) v[i >> 3][(i >> 1) & 3] |= (uint32_t)p[i] << (16 * (i & 1));
+      for (int i = 0; i < N; ++i)
+        if (i < n) v[i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
     }
   }
   __device__ __forceinline__ void store(uint16_t* p, int n) const {
-    if (n >= 16) {
-      *reinterpret_cast<u32x4_2l*>(p) = v[0];
-      *reinterpret_cast<u32x4_2l*>(p + 8) = v[1];
+    if (n >= N) {
+      *reinterpret_cast<u32x4_2l*>(p) = v;
     } else {
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (i < n) p[i] = (uint16_t)(v[i >> 3][(i >> 1) & 3] >> (16 * (i & 1)));
+      for (int i = 0; i < N; ++i)
+        if (i < n) p[i] = (uint16_t)(v[i >> 1] >> (16 * (i & 1)));
     }
   }
   __device__ __forceinline__ void add(int i, f32x4l d) {  // elements 4i .. 4i + 3
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const uint32_t w = v[i >> 1][2 * (i & 1) + e];
+      const uint32_t w = v[2 * i + e];
       const f32x2l f = {__uint_as_float(w << 16) + d[2 * e], __uint_as_float(w & 0xFFFF0000u) + d[2 * e + 1]};
-      v[i >> 1][2 * (i & 1) + e] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f, bf16x2l));
+      v[2 * i + e] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f, bf16x2l));
     }
   }
 };
-template <> struct Sixteen<float> {
-  u32x4 v[4];
+template <> struct Piece<float> {
+  static constexpr int N = 4;
+  u32x4 v;
   __device__ __forceinline__ void load(const float* p, int n) {
-    if (n >= 16) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const u32x4_4l*>(p + 4 * i);
+    if (n >= N) {
+      v = *reinterpret_cast<const u32x4_4l*>(p);
     } else {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) v[i >> 2][i & 3] = i < n ? __float_as_uint(p[i]) : 0u;
+      for (int i = 0; i < N; ++i) v[i] = i < n ? __float_as_uint(p[i]) : 0u;
     }
   }
   __device__ __forceinline__ void store(float* p, int n) const {
-    if (n >= 16) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) *reinterpret_cast<u32x4_4l*>(p + 4 * i) = v[i];
+    if (n >= N) {
+      *reinterpret_cast<u32x4_4l*>(p) = v;
     } else {
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (i < n) p[i] = __uint_as_float(v[i >> 2][i & 3]);
+      for (int i = 0; i < N; ++i)
+        if (i < n) p[i] = __uint_as_float(v[i]);
     }
   }
-  __device__ __forceinline__ void add(int i, f32x4l d) {
+  __device__ __forceinline__ void add(int, f32x4l d) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[i][e] = __float_as_uint(__uint_as_float(v[i][e]) + d[e]);
+    for (int e = 0; e < 4; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) + d[e]);
   }
 };
 
-// out of a tile's rows, 64 columns a wave and step.  Row m of product i is column
-// 16 (m / 4) + 4 i + m % 4 of the 64, so that a lane's four products are 16
-// neighbouring columns of one row, and 16 lanes' loads of y whole lines.
-template <typename T, int MT, int RS>
+// out of a tile's rows, 64 columns a wave and step, as four products of 16
+// columns.  Which columns those are is free: row m of product i is column
+//   4 E (i / Q) + E (m / 4) + 4 (i % Q) + m % 4,  E elements of 16 bytes, Q = E / 4,
+// so that a lane's results are whole pieces of 16 bytes of one row, and the four
+// lanes that share a row load and store 64 bytes together.
+template <typename T, int MT, int RS, bool Y>
 __global__ __launch_bounds__(256) void k_lora_out(LoraArgs p) {
   constexpr int TM = 16 * MT, RP = 32 * RS, TERMS = sizeof(T) == 2 ? 2 : 3, PAD = RP + 8;
+  constexpr int E = Piece<T>::N, Q = E / 4, P = 4 / Q;  // P pieces of a lane
   __shared__ __attribute__((aligned(16))) uint16_t s_u[TERMS][TM][PAD];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, g = lane >> 4;
+  const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const LoraTile t = lora_tile<TM>(p, blockIdx.x);
-  if (t.n == 0 || (t.a < 0 && p.y == p.out)) return;
+  if (t.n == 0) return;
   const int64_t first = (int64_t)blockIdx.y * p.iters * 256 + wave * 64;
   const T* y = static_cast<const T*>(p.y);
-  Sixteen<T> o[MT];
-  u32x4 fb[4];
-  auto load_b = [&](int64_t n0, int s) {
+  T* out = static_cast<T*>(p.out);
+  if (t.a < 0) {  // no adapter: y's rows
+    if (Y && y == out) return;
+    const int64_t from = (int64_t)blockIdx.y * p.iters * 256, to = min(p.N, from + (int64_t)p.iters * 256);
+    for (int row = wave; row < t.n; row += 4)
+      for (int64_t n = from + lane * E; n < to; n += 64 * E) {
+        const int left = (int)min((int64_t)E, p.N - n);
+        Piece<T> o;
+        if (Y) o.load(y + (t.r0 + row) * p.ldy + n, left);
+        else o.v = u32x4{0, 0, 0, 0};
+        o.store(out + (t.r0 + row) * p.ldo + n, left);
+      }
+    return;
+  }
+  struct Step {
+    Piece<T> o[MT][P];
+    u32x4 b[4];
+  };
+  // Loads without conditions, so that none waits for another: of columns, ranks
+  // and rows that are not there, some that are.
+  auto load_b = [&](Step& f, int64_t n0, int s) {  // B's for ranks 32 s ..
+    const int r = 32 * s + 8 * g < p.rank ? 32 * s + 8 * g : 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int64_t n = n0 + 16 * (c >> 2) + 4 * i + (c & 3);
-      fb[i] = t.a >= 0 && n < p.N && 32 * s + 8 * g < p.rank
-                  ? *reinterpret_cast<const u32x4*>(p.b + ((int64_t)t.a * p.N + n) * p.rank + 32 * s + 8 * g)
-                  : u32x4{0, 0, 0, 0};
+      const int64_t n = min(n0 + 4 * E * (i / Q) + E * (c >> 2) + 4 * (i % Q) + (c & 3), p.N - 1);
+      f.b[i] = *reinterpret_cast<const u32x4*>(p.b + ((int64_t)t.a * p.N + n) * p.rank + r);
     }
   };
-  auto load = [&](int64_t n0) {  // y's part, and B's for the first ranks
-    const int64_t at = n0 + 16 * g;
-    const int left = (int)min((int64_t)16, p.N - at);  // (below 1: none of this lane's)
+  auto load = [&](Step& f, int64_t n0) {  // (whole steps: columns n0 .. n0 + 63 are there)
+    load_b(f, n0, 0);
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      const int row = 16 * m + c;
-      if (y && row < t.n && left > 0) {
-        o[m].load(y + (t.r0 + row) * p.ldy + at, left);
-      } else {
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (auto& w : o[m].v) w = u32x4{0, 0, 0, 0};
+      for (int j = 0; j < P; ++j) {
+        if (Y) f.o[m][j].load(y + (t.r0 + min(16 * m + c, t.n - 1)) * p.ldy + n0 + 4 * E * j + E * g, E);
+        else f.o[m][j].v = u32x4{0, 0, 0, 0};
       }
-    }
-    load_b(n0, 0);
   };
-  load(first);  // (on its way while u is split)
-  if (t.a >= 0) {
-    // u as BF16 terms: a thread four ranks of a row
-    const float s = p.scale ? p.scale[t.a] : 1.0f;
-    for (int i = threadIdx.x; i < TM * RP / 4; i += 256) {
-      const int row = i / (RP / 4), r = i % (RP / 4) * 4;
-      f32x4l v = {0.0f, 0.0f, 0.0f, 0.0f};
-      if (row < t.n && r < p.rank) {
-        const float* u = p.u + (t.r0 + row) * p.ur + r;
-        for (int k = 0; k < p.splits; ++k) v += *reinterpret_cast<const f32x4l*>(u + k * p.rows * p.ur);
-        v *= s;
+  auto add = [&](Step& f, int64_t n0) {
+    f32x4l acc[MT][4];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[m][i] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int s = 0; s < RS; ++s) {
+      if (s > 0) load_b(f, n0, s);
+      if (32 * s + 32 > p.rank) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (32 * s + 8 * g >= p.rank) f.b[i] = u32x4{0, 0, 0, 0};
       }
 #pragma unroll
-      for (int e = 0; e < TERMS; ++e) {
-        const f32x2l lo = {v[0], v[1]}, hi = {v[2], v[3]};
-        const u32x2 w = {__builtin_bit_cast(uint32_t, __builtin_convertvector(lo, bf16x2l)),
-                         __builtin_bit_cast(uint32_t, __builtin_convertvector(hi, bf16x2l))};
-        *reinterpret_cast<u32x2*>(&s_u[e][row][r]) = w;
+      for (int e = 0; e < TERMS; ++e)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          const u32x4 fu = *reinterpret_cast<const u32x4*>(&s_u[e][16 * m + c][32 * s + 8 * g]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[m][i] = product(f.b[i], fu, acc[m][i]);
+        }
+    }
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f.o[m][i / Q].add(i % Q, acc[m][i]);
+  };
+  auto finish = [&](Step& f, int64_t n0) {
+    add(f, n0);
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+      if (16 * m + c < t.n) {
+#pragma unroll
+        for (int j = 0; j < P; ++j) f.o[m][j].store(out + (t.r0 + 16 * m + c) * p.ldo + n0 + 4 * E * j + E * g, E);
+      }
+  };
+  // this wave's whole steps, and the columns after the last one
+  const int64_t end = min(p.N, first + (int64_t)p.iters * 256);
+  const int64_t whole = first + 64 <= end ? (end - 64 - first) / 256 + 1 : 0, last = first + whole * 256;
+  Step f0, f1;
+  if (whole > 0) load(f0, first);  // (on its way while u is split)
+  // u as BF16 terms: a thread four ranks of a row
+  const float s = p.scale ? p.scale[t.a] : 1.0f;
+  for (int i = threadIdx.x; i < TM * RP / 4; i += 256) {
+    const int row = i / (RP / 4), r = i % (RP / 4) * 4;
+    f32x4l v = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (row < t.n && r < p.rank) {
+      const float* u = p.u + (t.r0 + row) * p.ur + r;
+      for (int k = 0; k < p.splits; k += 4) {  // four splits' loads together
+        f32x4l w[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          v[j] -= __uint_as_float((j & 1) ? w[j >> 1] & 0xFFFF0000u : w[j >> 1] << 16);
+          w[j] = *reinterpret_cast<const f32x4l*>(u + min(k + j, p.splits - 1) * p.rows * p.ur);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (k + j < p.splits) v += w[j];
       }
+      v *= s;
     }
-    __syncthreads();
-  }
-  T* out = static_cast<T*>(p.out);
-  for (int it = 0; it < p.iters; ++it) {
-    const int64_t n0 = first + it * 256;
-    if (n0 >= p.N) break;
-    if (it > 0) load(n0);
-    if (t.a >= 0) {
-      f32x4l acc[MT][4];
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+    for (int e = 0; e < TERMS; ++e) {
+      const f32x2l lo = {v[0], v[1]}, hi = {v[2], v[3]};
+      const u32x2 w = {__builtin_bit_cast(uint32_t, __builtin_convertvector(lo, bf16x2l)),
+                       __builtin_bit_cast(uint32_t, __builtin_convertvector(hi, bf16x2l))};
+      *reinterpret_cast<u32x2*>(&s_u[e][row][r]) = w;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[m][i] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int s = 0; s < RS; ++s) {
-        if (s > 0) load_b(n0, s);
-#pragma unroll
-        for (int e = 0; e < TERMS; ++e)
-#pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            const u32x4 fu = *reinterpret_cast<const u32x4*>(&s_u[e][16 * m + c][32 * s + 8 * g]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[m][i] = product(fb[i], fu, acc[m][i]);
-          }
-      }
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[m].add(i, acc[m][i]);
-    }
-    const int left = (int)min((int64_t)16, p.N - (n0 + 16 * g));
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      const int row = 16 * m + c;
-      if (row < t.n && left > 0) o[m].store(out + (t.r0 + row) * p.ldo + n0 + 16 * g, left);
+      for (int j = 0; j < 4; ++j)
+        v[j] -= __uint_as_float((j & 1) ? w[j >> 1] & 0xFFFF0000u : w[j >> 1] << 16);
     }
   }
+  __syncthreads();
+  // a step's loads on their way while the one before is finished (after the last
+  // its own again)
+  for (int64_t i = 0; i < whole; i += 2) {
+    const int64_t n0 = first + i * 256;
+    load(f1, first + min(i + 1, whole - 1) * 256);
+    finish(f0, n0);
+    if (i + 1 >= whole) break;
+    load(f0, first + min(i + 2, whole - 1) * 256);
+    finish(f1, n0 + 256);
+  }
+  if (last >= end) return;
+  load_b(f0, last, 0);
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int j = 0; j < P; ++j) {
+      const int64_t at = last + 4 * E * j + E * g;
+      f0.o[m][j].v = u32x4{0, 0, 0, 0};
+      if (Y && 16 * m + c < t.n && at < p.N)
+        f0.o[m][j].load(y + (t.r0 + 16 * m + c) * p.ldy + at, (int)min((int64_t)E, p.N - at));
+    }
+  add(f0, last);
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int j = 0; j < P; ++j) {
+      const int64_t at = last + 4 * E * j + E * g;
+      if (16 * m + c < t.n && at < p.N)
+        f0.o[m][j].store(out + (t.r0 + 16 * m + c) * p.ldo + at, (int)min((int64_t)E, p.N - at));
+    }
 }
 
 // How a call is split, from host numbers only: rows of a tile, tiles at most
@@ -380,13 +440,24 @@ void launch_u(const LoraArgs& p, const LoraPlan& pl, hipStream_t stream) {
   else hipLaunchKernelGGL((k_lora_u<MT, 8>), grid, dim3(256), 0, stream, p);
 }
 
-template <typename T, int MT>
+template <typename T, int MT, bool Y>
 void launch_out(const LoraArgs& p, const LoraPlan& pl, hipStream_t stream) {
   const int64_t steps = (p.N + 255) / 256;
   const dim3 grid((unsigned)pl.tiles, (unsigned)((steps + pl.iters - 1) / pl.iters));
-  if (pl.rs == 1) hipLaunchKernelGGL((k_lora_out<T, MT, 1>), grid, dim3(256), 0, stream, p);
-  else if (pl.rs == 2) hipLaunchKernelGGL((k_lora_out<T, MT, 2>), grid, dim3(256), 0, stream, p);
-  else hipLaunchKernelGGL((k_lora_out<T, MT, 4>), grid, dim3(256), 0, stream, p);
+  if (pl.rs == 1) hipLaunchKernelGGL((k_lora_out<T, MT, 1, Y>), grid, dim3(256), 0, stream, p);
+  else if (pl.rs == 2) hipLaunchKernelGGL((k_lora_out<T, MT, 2, Y>), grid, dim3(256), 0, stream, p);
+  else hipLaunchKernelGGL((k_lora_out<T, MT, 4, Y>), grid, dim3(256), 0, stream, p);
+}
+
+template <typename T>
+void launch_type(const LoraArgs& p, const LoraPlan& pl, hipStream_t stream) {
+  if (pl.mt == 4) {
+    if (p.y) launch_out<T, 4, true>(p, pl, stream);
+    else launch_out<T, 4, false>(p, pl, stream);
+  } else {
+    if (p.y) launch_out<T, 1, true>(p, pl, stream);
+    else launch_out<T, 1, false>(p, pl, stream);
+  }
 }
 
 }  // namespace
@@ -404,13 +475,8 @@ void launch_lora(int f32, const uint16_t* x, int64_t ldx, const uint16_t* a, con
                       static_cast<float*>(ws), pl.rt * 16, pl.splits, pl.chunk, pl.iters};
   if (pl.mt == 4) launch_u<4>(p, pl, stream);
   else launch_u<1>(p, pl, stream);
-  if (f32) {
-    if (pl.mt == 4) launch_out<float, 4>(p, pl, stream);
-    else launch_out<float, 1>(p, pl, stream);
-  } else {
-    if (pl.mt == 4) launch_out<uint16_t, 4>(p, pl, stream);
-    else launch_out<uint16_t, 1>(p, pl, stream);
-  }
+  if (f32) launch_type<float>(p, pl, stream);
+  else launch_type<uint16_t>(p, pl, stream);
 }
 
 }  // namespace fp4q
