@@ -3,7 +3,10 @@
 //   out = y + s (x A^T) B^T   with its adapter's A [rank, K], B [N, rank].
 //
 // Bound by HBM: y is read and written once, x read once (prompts), or the
-// adapters' A and B, which a request of one token reads whole (decode).  Two
+// adapters' A and B, which a request of one token reads whole (decode).  8192 rows
+// of 11 requests, rank 32, K 4096, N 14336 (BF16, 536 MB): 22 + 109 us, 4.1 TB/s of the
+// 4.7 of a copy; 64 requests of one row with 43 adapters of rank 16 (26 MB): 4.7 + 8.5,
+// the chain of a search, three loads and the sums in each.  Two
 // kernels: u = x A^T with K split over the waves and, where there are few rows,
 // over workgroups (partial sums in F32, added in order by the second kernel);
 // then out, each workgroup some columns of a tile of rows.
@@ -26,6 +29,8 @@ typedef __bf16 bf16x8l __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x4_2l __attribute__((ext_vector_type(4), aligned(2)));
 typedef uint32_t u32x4_4l __attribute__((ext_vector_type(4), aligned(4)));
 
+constexpr int U_MT = 4, OUT_MT = 2;  // products of a tile of many rows
+
 struct LoraArgs {
   const uint16_t* x;
   int64_t ldx;
@@ -46,7 +51,7 @@ struct LoraArgs {
   int ur;
   int splits;
   int64_t chunk;       // of K, a split's
-  int iters;           // 256-column steps of a workgroup
+  int iters, parts;    // 256-column steps of a workgroup, workgroups of a tile
 };
 
 // The rows of a workgroup: `n` from row r0, of adapter `a` (-1: none).
@@ -129,7 +134,7 @@ __global__ __launch_bounds__(256) void k_lora_u(LoraArgs p) {
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int i = 0; i < RT; ++i) acc[m][i] = {0.0f, 0.0f, 0.0f, 0.0f};
-  constexpr int U = MT * RT >= 32 ? 1 : MT * RT >= 8 ? 2 : 4;  // steps of 32 along K that are loaded together
+    constexpr int U = MT * RT >= 32 ? 1 : MT * RT >= 8 ? 2 : 4;  // steps of 32 along K that are loaded together
   struct Batch {
     u32x4 a[U][RT], x[U][MT];
   };
@@ -258,14 +263,15 @@ __global__ __launch_bounds__(256) void k_lora_out(LoraArgs p) {
   __shared__ __attribute__((aligned(16))) uint16_t s_u[TERMS][TM][PAD];
   const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const LoraTile t = lora_tile<TM>(p, blockIdx.x);
+  const uint32_t tile = blockIdx.x / p.parts, part = blockIdx.x % p.parts;
+  const LoraTile t = lora_tile<TM>(p, tile);
   if (t.n == 0) return;
-  const int64_t first = (int64_t)blockIdx.y * p.iters * 256 + wave * 64;
+  const int64_t first = (int64_t)part * p.iters * 256 + wave * 64;
   const T* y = static_cast<const T*>(p.y);
   T* out = static_cast<T*>(p.out);
   if (t.a < 0) {  // no adapter: y's rows
     if (Y && y == out) return;
-    const int64_t from = (int64_t)blockIdx.y * p.iters * 256, to = min(p.N, from + (int64_t)p.iters * 256);
+    const int64_t from = (int64_t)part * p.iters * 256, to = min(p.N, from + (int64_t)p.iters * 256);
     for (int row = wave; row < t.n; row += 4)
       for (int64_t n = from + lane * E; n < to; n += 64 * E) {
         const int left = (int)min((int64_t)E, p.N - n);
@@ -404,36 +410,48 @@ __global__ __launch_bounds__(256) void k_lora_out(LoraArgs p) {
     }
 }
 
-// How a call is split, from host numbers only: rows of a tile, tiles at most
-// (every request may leave one that is not full, and so may the rows of none),
-// splits of K, columns of a workgroup.
+// How a call is split, from host numbers only (each request may leave a tile that
+// is not full, and so may the rows of none).  Its rules, with what the other choice
+// takes (us; prompt: 8192 rows of 11 requests, rank 32, K 4096, N 14336, BF16; step:
+// 64 requests of one row, rank 16, the same K and N):
+//   many    tiles of 64 rows for u and 32 for out from 32 rows a request on, else 16:
+//           prompt u 21.6, by 32 rows 24.9; out 109, by 64 rows 113
+//   splits  of K, for 512 workgroups, each 1024 of K at least: prompt 22, for 256 28
+//   parts   workgroups of a tile of out: prompt 3072, 4096, 6144 in all: 123, 109, 117;
+//           step 512, 1024, 2048: 8.4, 8.5, 10.3.  A tile's parts follow one another: by
+//           tiles first 124 (prompt, 64 rows)
 struct LoraPlan {
-  int mt, rt, rs, splits, iters;
-  int64_t tiles, chunk;
+  bool many;  // rows enough for tiles of several products
+  int rt, rs, splits, iters, parts;
+  int64_t u_tiles, out_tiles, chunk;
 };
 
 LoraPlan lora_plan(int64_t rows, int G, int rank, int64_t K, int64_t N) {
   LoraPlan p;
-  p.mt = rows >= 32 * (int64_t)G ? 4 : 1;
+  p.many = rows >= 32 * (int64_t)G;
   p.rt = rank <= 16 ? 1 : rank <= 32 ? 2 : rank <= 64 ? 4 : 8;
   p.rs = p.rt <= 2 ? 1 : p.rt / 2;
-  const int tm = 16 * p.mt;
-  const int64_t full = rows / tm + (int64_t)G + 1;
-  p.tiles = full < rows ? full : rows;
-  int64_t s = (512 + p.tiles - 1) / p.tiles;
+  auto tiles = [&](int tm) {
+    const int64_t full = rows / tm + (int64_t)G + 1;
+    return full < rows ? full : rows;
+  };
+  p.u_tiles = tiles(16 * (p.many ? U_MT : 1));
+  p.out_tiles = tiles(16 * (p.many ? OUT_MT : 1));
+  int64_t s = (512 + p.u_tiles - 1) / p.u_tiles;
   const int64_t most = (K + 1023) / 1024;
   s = s < most ? s : most;
   p.chunk = ((K + s - 1) / s + 127) / 128 * 128;
   p.splits = (int)((K + p.chunk - 1) / p.chunk);
-  const int64_t steps = (N + 255) / 256;
-  const int64_t it = (p.tiles * steps + 2047) / 2048;
+  const int64_t steps = (N + 255) / 256, want = p.many ? 4096 : 1024;
+  const int64_t it = (p.out_tiles * steps + want - 1) / want;
   p.iters = (int)(it < 1 ? 1 : it < steps ? it : steps);
+  p.parts = (int)((steps + p.iters - 1) / p.iters);
   return p;
 }
 
 template <int MT>
 void launch_u(const LoraArgs& p, const LoraPlan& pl, hipStream_t stream) {
-  const dim3 grid((unsigned)pl.tiles, (unsigned)pl.splits);
+  const dim3 grid((unsigned)pl.u_tiles, (unsigned)pl.splits);
   if (pl.rt == 1) hipLaunchKernelGGL((k_lora_u<MT, 1>), grid, dim3(256), 0, stream, p);
   else if (pl.rt == 2) hipLaunchKernelGGL((k_lora_u<MT, 2>), grid, dim3(256), 0, stream, p);
   else if (pl.rt == 4) hipLaunchKernelGGL((k_lora_u<MT, 4>), grid, dim3(256), 0, stream, p);
@@ -442,8 +460,7 @@ void launch_u(const LoraArgs& p, const LoraPlan& pl, hipStream_t stream) {
 
 template <typename T, int MT, bool Y>
 void launch_out(const LoraArgs& p, const LoraPlan& pl, hipStream_t stream) {
-  const int64_t steps = (p.N + 255) / 256;
-  const dim3 grid((unsigned)pl.tiles, (unsigned)((steps + pl.iters - 1) / pl.iters));
+  const dim3 grid((unsigned)(pl.out_tiles * pl.parts));
   if (pl.rs == 1) hipLaunchKernelGGL((k_lora_out<T, MT, 1, Y>), grid, dim3(256), 0, stream, p);
   else if (pl.rs == 2) hipLaunchKernelGGL((k_lora_out<T, MT, 2, Y>), grid, dim3(256), 0, stream, p);
   else hipLaunchKernelGGL((k_lora_out<T, MT, 4, Y>), grid, dim3(256), 0, stream, p);
@@ -451,9 +468,9 @@ void launch_out(const LoraArgs& p, const LoraPlan& pl, hipStream_t stream) {
 
 template <typename T>
 void launch_type(const LoraArgs& p, const LoraPlan& pl, hipStream_t stream) {
-  if (pl.mt == 4) {
-    if (p.y) launch_out<T, 4, true>(p, pl, stream);
-    else launch_out<T, 4, false>(p, pl, stream);
+  if (pl.many) {
+    if (p.y) launch_out<T, OUT_MT, true>(p, pl, stream);
+    else launch_out<T, OUT_MT, false>(p, pl, stream);
   } else {
     if (p.y) launch_out<T, 1, true>(p, pl, stream);
     else launch_out<T, 1, false>(p, pl, stream);
@@ -472,8 +489,8 @@ void launch_lora(int f32, const uint16_t* x, int64_t ldx, const uint16_t* a, con
                  int64_t N, const void* y, int64_t ldy, void* out, int64_t ldo, void* ws, hipStream_t stream) {
   const LoraPlan pl = lora_plan(rows, G, rank, K, N);
   const LoraArgs p = {x, ldx, a, b, scale, adapters, rank, off, adapter, G, rows, K, N, y, ldy, out, ldo,
-                      static_cast<float*>(ws), pl.rt * 16, pl.splits, pl.chunk, pl.iters};
-  if (pl.mt == 4) launch_u<4>(p, pl, stream);
+                      static_cast<float*>(ws), pl.rt * 16, pl.splits, pl.chunk, pl.iters, pl.parts};
+  if (pl.many) launch_u<U_MT>(p, pl, stream);
   else launch_u<1>(p, pl, stream);
   if (f32) launch_type<float>(p, pl, stream);
   else launch_type<uint16_t>(p, pl, stream);
