@@ -356,6 +356,14 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs p) {
 //   least   keys of a split.  8 (sequence, kv head)s over 16384 keys: 18.2, 14.0, 13.1, 16.1 for
 //           128, 256, 512, 1024; over 4096: 10.0, 10.5, 12.1, 15.4.  wide: 64 tokens over 65536
 //           keys 53.5, 38.8, 47.3 for 256, 512, 1024
+//   sinks   a window with first tokens: most sequences are longer than it and see equally
+//           many keys, so few rows take as many workgroups as run at once (one split from
+//           there on), wide ones 256.  64 sequences of 8 kv heads over 4096 + 4 keys: 72 us
+//           in one split, by want and least 93; 8, 32, 48 of them 20, 40, 54 and 23, 62, 79;
+//           dim 256 70 and 120; 1024 tokens of one sequence 163, for 512 workgroups 192.
+//           Sequences that are shorter than the window lose: 32 of 256 to 4096 keys in a
+//           window of 4000 35, for twice the workgroups 28.  Eight waves from 64 (sequence,
+//           kv head)s on: 8 of them over 1028 keys 11.8, by eight 12.4
 //   join    lane groups on a row's splits, four to eight splits each.  171 splits: 121 by one
 //           group, 115.5 by this rule and by half as many
 struct Plan {
@@ -382,12 +390,22 @@ Plan attn_plan(int D, int B, int H, int G, int64_t max_new, int64_t max_len, int
   if (groups > (1 << 30)) groups = 1 << 30;  // (keys * groups stays below 2^63)
   // eight waves on the keys of each (sequence, kv head), none to join
   p.waves = !p.wide && groups <= 256 && keys <= 2048 && p.nc == 1 && D <= 128 ? 8 : 4;
-  const int64_t want = p.wide ? 512 : 4096;
+  const int64_t want = p.wide ? (sinks > 0 && window > 0 ? 256 : 512) : 4096;
   int64_t chunk = (keys * groups + want - 1) / want;
   const int64_t least = p.wide ? 512 : p.waves == 8 ? 2048 : 256;
   chunk = chunk < least ? least : chunk;
   chunk = (chunk + p.step - 1) / p.step * p.step;
   p.chunk = (int)(chunk < (1 << 30) ? chunk : (1 << 30));
+  const bool sink = sinks > 0 && window > 0;
+  if (sink && !p.wide) {
+    p.waves = groups > 64 && groups <= 256 && keys <= 2048 && p.nc == 1 && D <= 128 ? 8 : 4;
+    const int64_t at_once = 256 * (D == 64 ? 4 : D == 128 && p.nc == 1 ? 3 : 2);
+    int64_t n = p.waves == 8 ? 1 : at_once / groups;
+    n = n < keys / 256 ? n : keys / 256;
+    n = n > 1 ? n : 1;
+    chunk = ((keys + n - 1) / n + p.step - 1) / p.step * p.step;
+    p.chunk = (int)(chunk < (1 << 30) ? chunk : (1 << 30));
+  }
   p.splits = (int)((keys + p.chunk - 1) / p.chunk);
   if (p.splits < 1) p.splits = 1;
   p.join = 1;
