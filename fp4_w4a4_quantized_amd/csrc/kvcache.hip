@@ -373,18 +373,26 @@ __device__ __forceinline__ double2 cos_sin(double a) {
   return make_double2(k == 1 || k == 2 ? -cc : cc, k >= 2 ? -ss : ss);
 }
 
-// The sequence of row r, by the whole wave: 64 offsets a step.
-__device__ __forceinline__ int wave_sequence(const int32_t* off, int B, int64_t r, int lane) {
-  int lo = 0, n = B;
-  while (n > 1) {
+// The sequence of row r by the whole wave, 64 offsets a step; the last step's lanes
+// load what the caller needs of a sequence beside them.
+struct WaveSequence {
+  int b, end, len;  // the sequence, its last row + 1, its length
+};
+
+__device__ __forceinline__ WaveSequence wave_sequence(const KvArgs& p, int64_t r, int lane) {
+  int lo = 0, n = p.B;
+  while (n > 64) {
     const int step = (n + 63) >> 6;
     const int64_t at = (int64_t)lane * step;
-    const uint64_t m = __ballot(at < n && off[lo + (at < n ? (int)at : 0)] <= r);
+    const uint64_t m = __ballot(at < n && p.off[lo + (at < n ? (int)at : 0)] <= r);
     const int k = max(__popcll(m), 1) - 1;
     lo += k * step;
     n = min(step, n - k * step);
   }
-  return lo;
+  const int mine = lo + min(lane, n - 1);
+  const int first = p.off[mine], end = p.off[mine + 1], len = p.lens[mine];
+  const int k = max(__popcll(__ballot(lane < n && first <= r)), 1) - 1;
+  return {lo + k, __builtin_amdgcn_readlane(end, k), __builtin_amdgcn_readlane(len, k)};
 }
 
 // Eight pairs: chunk a with chunk b (HALVES), or the neighbours within each.
@@ -424,53 +432,65 @@ __global__ __launch_bounds__(KV_THREADS) void k_kv_append_rotated(RotArgs p) {
   const int64_t row = (int64_t)blockIdx.x * WAVES + wave;
   if (row >= c.rows) return;
 
+  // this lane's chunks of a head; the first heads' loads are on their way while the
+  // token's place is looked up
+  const int item = lane % ITEMS, h0 = lane / ITEMS;
+  const bool pair = item < p.half / 8;
+  const int c1 = HALVES && pair ? 8 * item : 16 * item;
+  const int c2 = HALVES && pair ? p.half + 8 * item : 16 * item + 8;
+  const bool with_q = p.per == 0 || blockIdx.y > 0, with_kv = p.per == 0 || blockIdx.y == 0;
+  const int from = p.per == 0 ? 0 : ((int)blockIdx.y - 1) * p.per;
+  const int to = p.per == 0 ? p.heads : min(p.heads, from + p.per);
+  const uint16_t* const qs = p.q + row * p.ldq;
+  const uint16_t* const ks = c.k + row * c.ldk;
+  u32x4 q1, q2, k1, k2;
+  if (with_q && from + h0 < to) {
+    q1 = *reinterpret_cast<const u32x4*>(qs + (from + h0) * D + c1);
+    q2 = *reinterpret_cast<const u32x4*>(qs + (from + h0) * D + c2);
+  }
+  if (with_kv && h0 < c.H) {
+    k1 = *reinterpret_cast<const u32x4*>(ks + h0 * D + c1);
+    k2 = *reinterpret_cast<const u32x4*>(ks + h0 * D + c2);
+  }
+
   // where the token stands (of no sequence: its q is copied, nothing is stored)
   const bool on = row >= c.off[0] && row < c.off[c.B];
   uint8_t* page_of = nullptr;
   int slot = 0;
-  int64_t at = 0;
   if (on) {
-    const int b = __builtin_amdgcn_readfirstlane(wave_sequence(c.off, c.B, row, lane));
-    const int64_t pos = (int64_t)c.lens[b] - c.off[b + 1] + row;
+    const WaveSequence sq = wave_sequence(c, row, lane);
+    const int64_t pos = (int64_t)sq.len - sq.end + row;
+    const int64_t at = p.positions ? (int64_t)p.positions[row] : pos;
     const int64_t pg = pos >> c.page_shift;
-    if (pos >= 0 && pg < c.table_cols) {
-      const int64_t id = c.table[b * c.ldt + pg];
-      if (id >= 0 && id < c.n_pages) {
-        const int page = 1 << c.page_shift;
-        slot = (int)(pos & (page - 1));
-        page_of = c.cache + id * c.H * (int64_t)L::bytes(page);
-      }
-    }
-    at = p.positions ? (int64_t)p.positions[row] : pos;
-  }
-  if (on) {
+    int64_t id = -1;
+    if (with_kv && pos >= 0 && pg < c.table_cols) id = c.table[sq.b * c.ldt + pg];
     for (int i = lane; i < p.half; i += 64) s_cs[wave][i] = cos_sin((double)at * (double)p.freqs[i]);
+    if (id >= 0 && id < c.n_pages) {
+      const int page = 1 << c.page_shift;
+      slot = (int)(pos & (page - 1));
+      page_of = c.cache + id * c.H * (int64_t)L::bytes(page);
+    }
   }
   wave_fence();
 
-  // this lane's chunks of a head, and the pairs' cosines and sines
-  const int item = lane % ITEMS, h0 = lane / ITEMS;
-  const bool turns = on && item < p.half / 8;
-  const int c1 = HALVES && turns ? 8 * item : 16 * item;
-  const int c2 = HALVES && turns ? p.half + 8 * item : 16 * item + 8;
+  const bool turns = on && pair;
   double2 cs[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) cs[i] = turns ? s_cs[wave][8 * item + i] : make_double2(1.0, 0.0);
 
-  if (p.per == 0 || blockIdx.y > 0) {
-    const int from = p.per == 0 ? 0 : (blockIdx.y - 1) * p.per;
-    const int to = p.per == 0 ? p.heads : min(p.heads, from + p.per);
-    const uint16_t* src = p.q + row * p.ldq;
-    uint16_t* dst = p.qo + row * p.ldqo;
+  if (with_q) {
+    uint16_t* const dst = p.qo + row * p.ldqo;
     for (int h = from + h0; h < to; h += HEADS) {
-      u32x4 a = *reinterpret_cast<const u32x4*>(src + h * D + c1);
-      u32x4 b = *reinterpret_cast<const u32x4*>(src + h * D + c2);
-      if (turns) turn<HALVES>(a, b, cs);
-      *reinterpret_cast<u32x4*>(dst + h * D + c1) = a;
-      *reinterpret_cast<u32x4*>(dst + h * D + c2) = b;
+      if (h > from + h0) {
+        q1 = *reinterpret_cast<const u32x4*>(qs + h * D + c1);
+        q2 = *reinterpret_cast<const u32x4*>(qs + h * D + c2);
+      }
+      if (turns) turn<HALVES>(q1, q2, cs);
+      *reinterpret_cast<u32x4*>(dst + h * D + c1) = q1;
+      *reinterpret_cast<u32x4*>(dst + h * D + c2) = q2;
     }
   }
-  if ((p.per != 0 && blockIdx.y > 0) || page_of == nullptr) return;
+  if (!with_kv || page_of == nullptr) return;
 
   // keys: by HEADS heads into LDS, from there 32 elements to each of the lower
   // lanes; the upper ones quantize the same heads' values
@@ -479,12 +499,13 @@ __global__ __launch_bounds__(KV_THREADS) void k_kv_append_rotated(RotArgs p) {
   for (int hb = 0; hb < c.H; hb += HEADS) {
     const int h = hb + h0, hq = hb + run / L::J;
     if (h < c.H) {
-      const uint16_t* src = c.k + row * c.ldk + h * D;
-      u32x4 a = *reinterpret_cast<const u32x4*>(src + c1);
-      u32x4 b = *reinterpret_cast<const u32x4*>(src + c2);
-      if (turns) turn<HALVES>(a, b, cs);
-      s_k[wave][(h0 * D + c1) / 8] = a;
-      s_k[wave][(h0 * D + c2) / 8] = b;
+      if (hb > 0) {
+        k1 = *reinterpret_cast<const u32x4*>(ks + h * D + c1);
+        k2 = *reinterpret_cast<const u32x4*>(ks + h * D + c2);
+      }
+      if (turns) turn<HALVES>(k1, k2, cs);
+      s_k[wave][(h0 * D + c1) / 8] = k1;
+      s_k[wave][(h0 * D + c2) / 8] = k2;
     }
     wave_fence();
     if (hq < c.H) {
