@@ -428,7 +428,7 @@ struct LoraPlan {
 
 LoraPlan lora_plan(int64_t rows, int G, int rank, int64_t K, int64_t N) {
   LoraPlan p;
-  p.many = rows >= 32 * (int64_t)G;
+  p.many = rows >= 32 * (int64_t)G && rows >= 1024;
   p.rt = rank <= 16 ? 1 : rank <= 32 ? 2 : rank <= 64 ? 4 : 8;
   p.rs = p.rt <= 2 ? 1 : p.rt / 2;
   auto tiles = [&](int tm) {

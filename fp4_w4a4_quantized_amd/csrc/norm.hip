@@ -61,6 +61,7 @@ struct NormArgs {
 enum { EMIT_Y, EMIT_MAX, EMIT_NVFP4, EMIT_MXFP4, EMIT_MXFP8 };
 
 constexpr int CH = 8;  // elements of a lane's chunk
+constexpr int MAX_WGS = 2048;  // workgroups of a pass; further rows in turn
 
 // Eight elements as they stand in memory.
 template <typename T> struct Raw;
@@ -309,12 +310,48 @@ __global__ __launch_bounds__(WPR == 8 ? 512 : 256) void k_norm(NormArgs p) {
   uint16_t* const ys = reinterpret_cast<uint16_t*>(mine);
   uint32_t* const codes = reinterpret_cast<uint32_t*>(mine + 2 * p.cols);
   uint8_t* const scs = mine + 2 * p.cols + p.cols / 2;
+  // whole chunks where the columns are a multiple of 8
+  auto left = [&](int col) { return EMIT == EMIT_Y ? p.cols - col : CH; };
+  // a row's x (or h) and residual
+  struct In {
+    Raw<T> x[N], res[N];
+    double r;
+  };
+  const T* const xs = static_cast<const T*>(SECOND && p.h ? p.h : p.x);
+  const int64_t ldx = SECOND && p.h ? p.ldh : p.ldx;
+  auto row_of = [&](int64_t g) { return row_group(g, p.groups, 16 / ROWS, p.tiled) * ROWS + (WPR == 1 ? wave : 0); };
+  auto load = [&](In& in, int64_t row) {
+    if (WPR == 1 && row >= p.rows) return;
+#pragma unroll
+    for (int c = 0; c < N; ++c) {
+      if (c >= nc) break;
+      const int col = col0 + c * WPR * 64 * CH;
+      if (col < p.cols) in.x[c].load(xs + row * ldx + col, left(col));
+    }
+    if (SECOND) {
+      in.r = p.r64[row];
+    } else if (p.res) {
+#pragma unroll
+      for (int c = 0; c < N; ++c) {
+        if (c >= nc) break;
+        const int col = col0 + c * WPR * 64 * CH;
+        if (col < p.cols) in.res[c].load(static_cast<const T*>(p.res) + row * p.ldr + col, left(col));
+      }
+    }
+  };
+  In next;
+  load(next, row_of(blockIdx.x));  // (the first row, on its way meanwhile)
   uint32_t most = 0;
   TensorScale ts = {1.0f, 0.0f, s_rec};
   if constexpr (EMIT == EMIT_NVFP4) {
     if (SECOND) {
       uint32_t m = 0;
-      for (int i = threadIdx.x; i < p.n_max; i += WAVES * 64) m = max(m, __float_as_uint(p.maxima[i]));
+      auto maximum = [&](int i) { return __float_as_uint(p.maxima[min(i, p.n_max - 1)]); };
+      m = maximum(threadIdx.x);
+      if (p.n_max > WAVES * 64) {
+#pragma unroll
+        for (int i = 1; i < MAX_WGS / (WAVES * 64); ++i) m = max(m, maximum(i * WAVES * 64 + threadIdx.x));
+      }
       m = wave_max(m);
       if (lane == 0) s_max[wave] = m;
       __syncthreads();
@@ -349,37 +386,24 @@ __global__ __launch_bounds__(WPR == 8 ? 512 : 256) void k_norm(NormArgs p) {
     code0[c] = code_off(p.tiled, 0, col >> 1, p.cols);
     scale0[c] = scale_off<FMT>(p.tiled, 0, col / BLK, p.cols);
   }
+  // Few chunks: the next row is on its way while one is worked on (but for the
+  // second pass, which its arithmetic bounds: 29.4 us without, 31.4 with it).
+  constexpr bool AHEAD = N <= 2 && !SECOND;
   int turn = 0;
   for (int64_t gi = blockIdx.x; gi < p.groups; gi += gridDim.x, turn ^= 1) {
-    const int64_t row = row_group(gi, p.groups, 16 / ROWS, p.tiled) * ROWS + (WPR == 1 ? wave : 0);
+    const int64_t row = row_of(gi);
+    if (!AHEAD && gi != blockIdx.x) load(next, row);
+    In in = next;
+    if (AHEAD && gi + gridDim.x < p.groups) load(next, row_of(gi + gridDim.x));
     if (WPR == 1 && row >= p.rows) continue;
-    // whole chunks where the columns are a multiple of 8
-    auto left = [&](int col) { return EMIT == EMIT_Y ? p.cols - col : CH; };
-    Raw<T> h[N];
+    Raw<T>(&h)[N] = in.x;
     double r;
-    {
-      const T* x = static_cast<const T*>(SECOND && p.h ? p.h : p.x) + row * (SECOND && p.h ? p.ldh : p.ldx);
-#pragma unroll
-      for (int c = 0; c < N; ++c) {
-        if (c >= nc) break;
-        const int col = col0 + c * WPR * 64 * CH;
-        if (col < p.cols) h[c].load(x + col, left(col));
-      }
-    }
     if (SECOND) {
-      r = p.r64[row];
+      r = in.r;
     } else {
       double ss = 0.0;
       if (p.res) {
-        const T* res = static_cast<const T*>(p.res) + row * p.ldr;
         T* out = static_cast<T*>(p.h) + row * p.ldh;
-        Raw<T> a[N];
-#pragma unroll
-        for (int c = 0; c < N; ++c) {
-          if (c >= nc) break;
-          const int col = col0 + c * WPR * 64 * CH;
-          if (col < p.cols) a[c].load(res + col, left(col));
-        }
 #pragma unroll
         for (int c = 0; c < N; ++c) {
           if (c >= nc) break;
@@ -387,7 +411,7 @@ __global__ __launch_bounds__(WPR == 8 ? 512 : 256) void k_norm(NormArgs p) {
           if (col >= p.cols) continue;
           float f[CH];
 #pragma unroll
-          for (int i = 0; i < CH; ++i) f[i] = h[c].at(i) + a[c].at(i);
+          for (int i = 0; i < CH; ++i) f[i] = h[c].at(i) + in.res[c].at(i);
           h[c].set(f);
           h[c].store(out + col, left(col));
         }
@@ -523,7 +547,6 @@ __global__ __launch_bounds__(64 * WPR) void k_norm_backward(NormGradArgs p) {
     for (int i = 0; i < CH; ++i) dw[c][i] = 0.0f;
   int turn = 0;
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, turn ^= 1) {
-    const T* h = static_cast<const T*>(p.h) + row * p.ldh;
     const float r = p.rstd[row];
     Raw<T> hr[N], dh[N];
     float g[N][CH];
@@ -532,7 +555,7 @@ __global__ __launch_bounds__(64 * WPR) void k_norm_backward(NormGradArgs p) {
       if (c >= nc) break;
       const int col = col0 + c * WPR * 64 * CH, n = p.cols - col;
       if (n <= 0) continue;
-      hr[c].load(h + col, n);
+      hr[c].load(static_cast<const T*>(p.h) + row * p.ldh + col, n);
       load_any(p.dy, row * p.lddy + col, p.dy_f32, n, g[c]);
       if (p.dh) dh[c].load(static_cast<const T*>(p.dh) + row * p.lddh + col, n);
     }
@@ -659,8 +682,6 @@ __global__ __launch_bounds__(256) void k_dequantize(const uint8_t* __restrict__ 
 // The tensor scale of no rows.
 __global__ void k_scale_one(float* tscale) { *tscale = 1.0f; }
 
-constexpr int MAX_WGS = 2048;  // workgroups of a pass; further rows in turn
-
 // Waves of a row and chunks of a lane: a wave for rows of up to 1024 columns where
 // there are enough of them for all CUs, else four or eight.
 template <typename T, int WPR, int N, int EMIT, bool SECOND>
@@ -695,6 +716,7 @@ void launch_type(const NormArgs& p, int emit, bool given, hipStream_t stream) {
   if (p.rows >= 2048 && p.cols <= room(1, 2)) launch_emit<T, 1, 2>(p, emit, given, stream);
   else if (p.cols <= room(4, 2)) launch_emit<T, 4, 2>(p, emit, given, stream);
   else if (p.cols <= room(4, 4)) launch_emit<T, 4, 4>(p, emit, given, stream);
+  else if (p.cols <= room(8, 4)) launch_emit<T, 8, 4>(p, emit, given, stream);
   else launch_emit<T, 8, 8>(p, emit, given, stream);
 }
 
