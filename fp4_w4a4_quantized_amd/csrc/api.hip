@@ -915,7 +915,7 @@ int fp4q_kv_append_rotated(fp4q_format_t fmt, uint8_t* cache, int64_t n_pages, i
   if (rot % 16 != 0) return FP4Q_ERR_UNSUPPORTED;
   if (rows == 0) return FP4Q_OK;
   const int64_t cols = (int64_t)kv_heads * dim, qcols = (int64_t)heads * dim;
-  if (rows >= ((int64_t)1 << 26) || qcols >= ((int64_t)1 << 31))
+  if (rows >= ((int64_t)1 << 25) || qcols >= ((int64_t)1 << 31))
     return FP4Q_ERR_UNSUPPORTED;  // (before the packed tensors: a caller may not have made them)
   if (!packed_ok(k, ldk, cols) || !packed_ok(v, ldv, cols) || !packed_ok(q, ldq, qcols) ||
       !packed_ok(q_out, ldqo, qcols) || (rot > 0 && !freqs) || !aligned(freqs, 4))
@@ -1159,7 +1159,7 @@ int norm_forward_checks(int dtype, const void* x, int64_t ldx, const void* resid
 
 bool lora_shape_ok(int64_t rows, int32_t n_groups, int32_t rank, int64_t K, int64_t N) {
   return rank % 8 == 0 && rank <= 128 && K % 8 == 0 && K < ((int64_t)1 << 31) && N < ((int64_t)1 << 31) &&
-         rows < (1 << 24) && n_groups < (1 << 24);
+         rows < (1 << 24) && n_groups <= 65536;
 }
 
 }  // namespace

@@ -404,6 +404,7 @@ Plan attn_plan(int D, int B, int H, int G, int64_t max_new, int64_t max_len, int
     n = n < keys / 256 ? n : keys / 256;
     n = n > 1 ? n : 1;
     chunk = ((keys + n - 1) / n + p.step - 1) / p.step * p.step;
+    chunk = chunk > p.step ? chunk : p.step;  // (max_len may be 0)
     p.chunk = (int)(chunk < (1 << 30) ? chunk : (1 << 30));
   }
   p.splits = (int)((keys + p.chunk - 1) / p.chunk);

@@ -199,6 +199,15 @@ at::Tensor part(const at::Tensor& buf, at::IntArrayRef shape, int64_t at0) {
   return t;
 }
 
+// The same of another type, over buf's bytes from `byte` on (a multiple of its size).
+at::Tensor part(const at::Tensor& buf, at::IntArrayRef shape, at::ScalarType type, int64_t byte) {
+  at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(buf.storage()), buf.key_set(),
+                                                          c10::scalarTypeToTypeMeta(type));
+  t.unsafeGetTensorImpl()->set_storage_offset(byte / (int64_t)c10::elementSize(type));
+  t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
+  return t;
+}
+
 // What the cache's calls have in common: (fmt, cache, page, offsets,
 // page_table, lens, k_scale, v_scale) are arguments 1 .. 8, after the stream.
 struct Kv {
@@ -529,24 +538,37 @@ PyObject* rms_norm_quantize(PyObject* const* a) {
   const int64_t R = n.x.rows, C = n.x.cols;
   const Operand s = operand(fmt, layout, R, C);
   make_h(a, n);
-  const at::Tensor q = like(t, s.q, at::kByte), sc = like(t, s.scales, at::kByte);
-  at::Tensor mts, resid, y, rstd, ws;
-  if (fmt == FP4Q_NVFP4 && !ts) {
-    mts = like(t, {1}, at::kFloat);
+  const bool find = fmt == FP4Q_NVFP4 && !ts;
+  const size_t bytes = fp4q_rms_norm_quantize_workspace_bytes((fp4q_format_t)fmt, R, !find);
+  // one allocation for the workspace and the operand's parts, each 16-byte aligned
+  int64_t at = 0;
+  auto place = [&](int64_t n) {
+    const int64_t from = at;
+    need(n >= 0 && !__builtin_add_overflow(at, n, &at) && at <= INT64_MAX - 16, "x", "too large");
+    at = (at + 15) / 16 * 16;
+    return from;
+  };
+  auto numel = [](const c10::SmallVector<int64_t, 2>& d) { return d.size() == 1 ? d[0] : d[0] * d[1]; };
+  const int64_t at_q = place(numel(s.q)), at_s = place(numel(s.scales)), at_t = place(find ? 4 : 0),
+                at_r = place(want_r ? 4 * R : 0), at_c = place(2 * R * n_chan), at_w = place((int64_t)bytes);
+  const at::Tensor buf = like(t, {at}, at::kByte);
+  const at::Tensor q = part(buf, s.q, at::kByte, at_q), sc = part(buf, s.scales, at::kByte, at_s);
+  at::Tensor mts, resid, y, rstd;
+  if (find) {
+    mts = part(buf, {1}, at::kFloat, at_t);
     ts = mts.data_ptr<float>();
   }
-  if (n_chan > 0) resid = like(t, {R, n_chan}, at::kShort);
+  if (n_chan > 0) resid = part(buf, {R, n_chan}, at::kShort, at_c);
   if (with_y) y = like(t, {R, C}, scalar_of(type));
-  if (want_r) rstd = like(t, {R}, at::kFloat);
-  const size_t bytes = fp4q_rms_norm_quantize_workspace_bytes((fp4q_format_t)fmt, R, !mts.defined());
-  if (bytes) ws = like(t, {(int64_t)bytes}, at::kByte);
+  if (want_r) rstd = part(buf, {R}, at::kFloat, at_r);
+  uint8_t* const ws = bytes ? buf.data_ptr<uint8_t>() + at_w : nullptr;
   check("fp4q_rms_norm_quantize",
         fp4q_rms_norm_quantize((fp4q_format_t)fmt, (fp4q_layout_t)layout, n.x.type, n.x.p, n.x.ld, n.res.p, n.res.ld,
                                n.h.p, n.h.ld, n.w, n.w_type, n.eps, R, C, chan, n_chan,
-                               (uint8_t*)q.data_ptr(), (uint8_t*)sc.data_ptr(), ts, !mts.defined(),
+                               (uint8_t*)q.data_ptr(), (uint8_t*)sc.data_ptr(), ts, !find,
                                n_chan > 0 ? (uint16_t*)resid.data_ptr() : nullptr,
                                with_y ? y.data_ptr() : nullptr, type, C, want_r ? rstd.data_ptr<float>() : nullptr,
-                               bytes ? ws.data_ptr() : nullptr, bytes, stream));
+                               ws, bytes, stream));
   PyObject* pts = none();
   if (fmt == FP4Q_NVFP4) {
     Py_DECREF(pts);

@@ -29,7 +29,7 @@ typedef __bf16 bf16x8l __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x4_2l __attribute__((ext_vector_type(4), aligned(2)));
 typedef uint32_t u32x4_4l __attribute__((ext_vector_type(4), aligned(4)));
 
-constexpr int U_MT = 4, OUT_MT = 2;  // products of a tile of many rows
+constexpr int U_MT = 4, U_MT_128 = 2, OUT_MT = 2;  // products of a tile of many rows (U_MT_128: ranks above 64)
 
 struct LoraArgs {
   const uint16_t* x;
@@ -94,9 +94,10 @@ __device__ __forceinline__ LoraTile lora_tile(const LoraArgs& p, int tile) {
     if (hit) {
       const int at = __ffsll((unsigned long long)hit) - 1;
       auto of = [&](int v) { return __builtin_amdgcn_readlane(v, at); };
-      const int from = of(r0) + (tile - of(first)) * TM;
+      const int64_t from = of(r0) + (int64_t)(tile - of(first)) * TM;
+      if (from < of(r0) || from >= of(r1)) return t;  // (offsets that go down could lead here)
       t.r0 = from;
-      t.n = min(TM, of(r1) - from);
+      t.n = min(TM, of(r1) - (int)from);
       t.a = of(id);
       if (t.a < 0 || t.a >= p.adapters) t.a = -1;
       return t;
@@ -435,7 +436,7 @@ LoraPlan lora_plan(int64_t rows, int G, int rank, int64_t K, int64_t N) {
     const int64_t full = rows / tm + (int64_t)G + 1;
     return full < rows ? full : rows;
   };
-  p.u_tiles = tiles(16 * (p.many ? U_MT : 1));
+  p.u_tiles = tiles(16 * (!p.many ? 1 : p.rt == 8 ? U_MT_128 : U_MT));
   p.out_tiles = tiles(16 * (p.many ? OUT_MT : 1));
   int64_t s = (512 + p.u_tiles - 1) / p.u_tiles;
   const int64_t most = (K + 1023) / 1024;
@@ -455,7 +456,7 @@ void launch_u(const LoraArgs& p, const LoraPlan& pl, hipStream_t stream) {
   if (pl.rt == 1) hipLaunchKernelGGL((k_lora_u<MT, 1>), grid, dim3(256), 0, stream, p);
   else if (pl.rt == 2) hipLaunchKernelGGL((k_lora_u<MT, 2>), grid, dim3(256), 0, stream, p);
   else if (pl.rt == 4) hipLaunchKernelGGL((k_lora_u<MT, 4>), grid, dim3(256), 0, stream, p);
-  else hipLaunchKernelGGL((k_lora_u<MT, 8>), grid, dim3(256), 0, stream, p);
+  else hipLaunchKernelGGL((k_lora_u<(MT == U_MT ? U_MT_128 : MT), 8>), grid, dim3(256), 0, stream, p);
 }
 
 template <typename T, int MT, bool Y>

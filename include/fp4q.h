@@ -752,7 +752,7 @@ int fp4q_kv_read(fp4q_format_t fmt, const uint8_t* cache, int64_t n_pages, int32
  * Rows past offsets[batch] are copied from q to q_out.  A token whose place is
  * not in the cache (see above) is rotated too, and not stored.
  * FP4Q_ERR_UNSUPPORTED: what fp4q_kv_append does not take of dim, page,
- * kv_heads and table, rot not a multiple of 16, rows not below 2^26, heads *
+ * kv_heads and table, rot not a multiple of 16, rows not below 2^25, heads *
  * dim not below 2^31. */
 typedef enum { FP4Q_PAIRS_HALVES = 0, FP4Q_PAIRS_NEIGHBOURS = 1 } fp4q_pairs_t;
 
@@ -936,7 +936,7 @@ int fp4q_dequantize(fp4q_format_t fmt, fp4q_layout_t layout, const uint8_t* q, c
  * with F32 sums; x A^T is scaled in F32 and enters the second product as two
  * BF16 terms (three for F32 out).  Sums are taken in the same order in every call.
  * FP4Q_ERR_UNSUPPORTED: rank not a multiple of 8 or above 128, K not a multiple
- * of 8, K or N not below 2^31, rows or n_groups not below 2^24. */
+ * of 8, K or N not below 2^31, rows not below 2^24, n_groups above 65536. */
 size_t fp4q_lora_workspace_bytes(int64_t rows, int32_t n_groups, int32_t rank, int64_t K, int64_t N);
 
 int fp4q_lora(const uint16_t* x, int64_t ldx, const uint16_t* a, const uint16_t* b, const float* scale,

@@ -29,7 +29,7 @@ def test_rotated_append_refusals(L):
                           dict(rot=-16), dict(rot=144), dict(pairs=2), dict(fr=None), dict(fr=0x10002),
                           dict(pos=0x10001), dict(fmt=2)]:
         assert f(**over) == INVALID, over
-    for over in UNSUP_KV + [dict(rot=24), dict(rot=8), dict(rows=1 << 26), dict(heads=1 << 24)]:
+    for over in UNSUP_KV + [dict(rot=24), dict(rot=8), dict(rows=1 << 25), dict(heads=1 << 24)]:
         assert f(**over) == UNSUPPORTED, over
     assert f(rows=0, batch=0, cache=None, q=None, qo=None, k=None, v=None, fr=None) == 0
 
@@ -54,6 +54,8 @@ def test_sinks_refusals(L):
     # how calls with first tokens are split is a rule of their own
     assert need(4096, 4) > 0 and need(4096, 1 << 30) > 0 and need(2 ** 31 - 1, 2 ** 31 - 1) > 0
     assert need(0, 7) == need(0, 0) and need(4096, -1) == 0
+    for window, sinks in ((0, 4), (1, 1), (4096, 4), (2 ** 31 - 1, 2 ** 31 - 1)):
+        assert L.fp4q_kv_attention_sinks_workspace_bytes(0, 5, 4, 2, 128, 2, 1, 0, window, sinks) == 0
     long = dict(max_len=1 << 17, cols=1 << 13, ld=1 << 13, window=4096)
     for over in (dict(ws=None), dict(wsb=need(4096, 4) - 1), dict(ws=ODD)):
         assert f(**long, **over) == WORKSPACE, over
@@ -140,7 +142,7 @@ def test_adapter_refusals(L):
                  dict(rows=-1), dict(K=0, ldx=0), dict(N=0), dict(ldy=29), dict(out=None), dict(ldo=29),
                  dict(dt=2), dict(dt=0, out=0x10002), dict(out=A, ldo=40), dict(y=0x10001)]:
         assert f(**over) == INVALID, over
-    for over in [dict(rank=12), dict(rank=136), dict(K=60), dict(rows=1 << 24), dict(G=1 << 24)]:
+    for over in [dict(rank=12), dict(rank=136), dict(K=60), dict(rows=1 << 24), dict(G=65537)]:
         assert f(**over) == UNSUPPORTED, over
     need = L.fp4q_lora_workspace_bytes(5, 2, 16, 64, 30)
     assert need > 0 and L.fp4q_lora_workspace_bytes(5, 2, 12, 64, 30) == 0

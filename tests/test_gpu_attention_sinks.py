@@ -123,6 +123,7 @@ def test_rows_that_see_nothing(fmt):
     c["lens"][3] = 0                               # a new token before position 0
     got = check(c, 20, 3, max_len=64)
     assert torch.all(got[:2] == 0) and torch.all(got[5] == 0)
+    assert torch.all(attend(c, 20, sinks=3, max_len=0) == 0)      # every key is past max_len
 
 
 def test_captured_with_growing_lengths():

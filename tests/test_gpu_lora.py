@@ -131,6 +131,15 @@ def test_many_requests_and_long_sums():
     assert torch.equal(a, call(c)), "two runs differ"
 
 
+@pytest.mark.parametrize("rank", [16, 32, 64, 128])
+def test_tiles_of_many_rows(rank):
+    """Rows enough for the larger tiles, requests that end inside them."""
+    need_gpu()
+    for dt in (B, torch.float32):
+        c = case([1000, 3, 0, 130, 77], [2, 1, 0, -1, 3], rank, 136, 200, dt, extra=9)
+        check(c, call(c))
+
+
 def test_empty():
     need_gpu()
     c = case([0, 0], [0, 1], 16, 64, 32, B)
