@@ -5,7 +5,7 @@
 // Bound by HBM: y is read and written once, x read once (prompts), or the
 // adapters' A and B, which a request of one token reads whole (decode).  8192 rows
 // of 11 requests, rank 32, K 4096, N 14336 (BF16, 536 MB): 22 + 109 us, 4.1 TB/s of the
-// 4.7 of a copy; 64 requests of one row with 43 adapters of rank 16 (26 MB): 4.7 + 8.5,
+// 4.7 of a copy; 64 requests of one row with 37 adapters of rank 16 (26 MB): 4.7 + 8.5,
 // the chain of a search, three loads and the sums in each.  Two
 // kernels: u = x A^T with K split over the waves and, where there are few rows,
 // over workgroups (partial sums in F32, added in order by the second kernel);
@@ -415,12 +415,15 @@ __global__ __launch_bounds__(256) void k_lora_out(LoraArgs p) {
 // is not full, and so may the rows of none).  Its rules, with what the other choice
 // takes (us; prompt: 8192 rows of 11 requests, rank 32, K 4096, N 14336, BF16; step:
 // 64 requests of one row, rank 16, the same K and N):
-//   many    tiles of 64 rows for u and 32 for out from 32 rows a request on, else 16:
-//           prompt u 21.6, by 32 rows 24.9; out 109, by 64 rows 113
+//   many    tiles of 64 rows for u (32 for ranks above 64: 26, by 64 37) and 32 for out
+//           from 1024 rows and 32 a request on, else 16: prompt u 21.6, by 32 rows 24.9; out
+//           109, by 64 rows 113; 121 rows of rank 128 5.8 + 7.0, by many 10.3 + 13.0
 //   splits  of K, for 512 workgroups, each 1024 of K at least: prompt 22, for 256 28
-//   parts   workgroups of a tile of out: prompt 3072, 4096, 6144 in all: 123, 109, 117;
-//           step 512, 1024, 2048: 8.4, 8.5, 10.3.  A tile's parts follow one another: by
-//           tiles first 124 (prompt, 64 rows)
+//   iters   steps of a workgroup of out: prompt 1, 2, 3, 4, 6: 154, 123, 115, 109, 121; at
+//           2489 rows and 9186 columns of F32 57, 49, 46, 45, 44; fewer where 256
+//           workgroups would not be reached (3082 rows, 671 columns: 2 12.6, 3 18.0).  Small
+//           tiles: for 1024 workgroups (step: for 512, 1024, 2048 8.4, 8.5, 10.3).  A tile's
+//           workgroups follow one another: by tiles first 124 (prompt, 64 rows)
 struct LoraPlan {
   bool many;  // rows enough for tiles of several products
   int rt, rs, splits, iters, parts;
@@ -443,9 +446,10 @@ LoraPlan lora_plan(int64_t rows, int G, int rank, int64_t K, int64_t N) {
   s = s < most ? s : most;
   p.chunk = ((K + s - 1) / s + 127) / 128 * 128;
   p.splits = (int)((K + p.chunk - 1) / p.chunk);
-  const int64_t steps = (N + 255) / 256, want = p.many ? 4096 : 1024;
-  const int64_t it = (p.out_tiles * steps + want - 1) / want;
-  p.iters = (int)(it < 1 ? 1 : it < steps ? it : steps);
+  const int64_t steps = (N + 255) / 256, want = p.many ? 256 : 1024;
+  int64_t it = (p.out_tiles * steps + want - 1) / want;
+  if (p.many && it > 4) it = 4;
+  p.iters = (int)(it < steps ? it : steps);
   p.parts = (int)((steps + p.iters - 1) / p.iters);
   return p;
 }
