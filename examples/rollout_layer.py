@@ -4,11 +4,13 @@ then decode steps of one token a sequence.
 
     python examples/rollout_layer.py [--fmt nvfp4|mxfp4] [--steps N]
 
-Every product runs in FP4 (fp4q_gemm, fp4q_grouped_gemm), keys and values are
-stored in FP4 pages and read by the attention there, the router's order feeds
-the quantize-before-permute grouped products, and the combination brings the
-experts' outputs back.  Weights are random; torch supplies norms, the router's
-projection and the activation.
+Every product runs in FP4 (fp4q_gemm, fp4q_grouped_gemm) on operands that the
+norms before them write, with the adapters of each sequence's request beside the
+first one.  Keys are turned by their positions on the way into FP4 pages, which the
+attention reads there (a sliding window and the first tokens, in the run below),
+the router's order feeds the quantize-before-permute grouped products, and the
+combination brings the experts' outputs back.  Weights are random; torch supplies
+the router's projection and the activation.
 """
 import argparse
 import os
@@ -26,9 +28,9 @@ class Layer:
     """The layer's weights, quantized once."""
 
     def __init__(self, fmt, hidden=1024, heads=16, kv_heads=4, dim=64, experts=16, top=4,
-                 expert_hidden=512, seed=0):
+                 expert_hidden=512, seed=0, window=0, sinks=0, adapters=0, rank=8):
         self.fmt, self.heads, self.kv_heads, self.dim = fmt, heads, kv_heads, dim
-        self.experts, self.top = experts, top
+        self.experts, self.top, self.window, self.sinks = experts, top, window, sinks
         g = torch.Generator(device="cuda").manual_seed(seed)
 
         def weight(n, k):
@@ -46,6 +48,15 @@ class Layer:
         self.up = expert_weights(expert_hidden, hidden)
         self.down = expert_weights(hidden, expert_hidden)
         self.router = torch.randn(hidden, experts, generator=g, device="cuda") * hidden ** -0.5
+        self.norm1 = 1.0 + 0.1 * torch.randn(hidden, generator=g, device="cuda")
+        self.norm2 = 1.0 + 0.1 * torch.randn(hidden, generator=g, device="cuda")
+        self.freqs = 10000.0 ** (-torch.arange(dim // 2, device="cuda") / (dim // 2))
+        qkv = (heads + 2 * kv_heads) * dim
+        # the requests' adapters beside the projection to queries, keys and values
+        self.adapters = None if adapters == 0 else (
+            (torch.randn(adapters, rank, hidden, generator=g, device="cuda") * hidden ** -0.5).to(torch.bfloat16),
+            (0.3 * torch.randn(adapters, qkv, rank, generator=g, device="cuda")).to(torch.bfloat16),
+            torch.full((adapters,), 0.5, device="cuda"))
         # tensor scales of keys and values, as a calibration would leave them
         self.kv_scale = (torch.full((kv_heads,), 8.0 / 2688.0, device="cuda")
                          if fmt == fq.NVFP4 else None)
@@ -54,8 +65,10 @@ class Layer:
 class Sequences:
     """Pages, lengths and new tokens of a batch of sequences."""
 
-    def __init__(self, layer, lengths, room, page=16, seed=1):
+    def __init__(self, layer, lengths, room, page=16, seed=1, adapters=None):
         self.page, self.lengths = page, list(lengths)
+        # the adapter of each sequence (-1: none)
+        self.adapters = None if adapters is None else torch.tensor(adapters, dtype=torch.int32, device="cuda")
         need = [-(-(n + room) // page) for n in lengths]
         self.cache = fq.kv_cache(layer.fmt, sum(need), page, layer.kv_heads, layer.dim)
         ids = torch.randperm(sum(need), generator=torch.Generator().manual_seed(seed)).int()
@@ -74,7 +87,7 @@ class Sequences:
 
 
 def norm(x):
-    return (x.float() * torch.rsqrt(x.float().square().mean(-1, keepdim=True) + 1e-6)).to(x.dtype)
+    return fq.rms_norm(x, torch.ones(x.shape[1], device=x.device))["y"]
 
 
 def forward(layer, seqs, x, offsets, max_new, keep=None):
@@ -84,25 +97,36 @@ def forward(layer, seqs, x, offsets, max_new, keep=None):
     fmt, H, KV, D = layer.fmt, layer.heads, layer.kv_heads, layer.dim
     rows = x.shape[0]
     # attention
-    qkv = fq.gemm(fmt, fq.quantize(fmt, norm(x)), layer.qkv, y_dtype=fq.OUT_BF16)
+    a1 = fq.rms_norm_quantize(fmt, x, layer.norm1, y_dtype=fq.OUT_BF16)
+    shared = fq.gemm(fmt, a1, layer.qkv, y_dtype=fq.OUT_BF16)
+    qkv = shared
+    if layer.adapters is not None:
+        a, b, scale = layer.adapters
+        qkv = fq.lora(a1["y"], a, b, offsets, seqs.adapters, scale, y=shared)
     qkv = qkv.view(rows, H + 2 * KV, D)
-    q, k, v = qkv[:, :H], qkv[:, H:H + KV], qkv[:, H + KV:]
+    k, v = qkv[:, H:H + KV], qkv[:, H + KV:]
     where = (seqs.cache, seqs.page, offsets, seqs.table, seqs.lens)
-    fq.kv_append(fmt, *where, k, v, layer.kv_scale, layer.kv_scale)
-    att = fq.kv_attention(fmt, *where, q, max_new, seqs.bound, layer.kv_scale, layer.kv_scale)
-    x = x + fq.gemm(fmt, fq.quantize(fmt, att.view(rows, H * D)), layer.out, y_dtype=fq.OUT_BF16)
+    # (to show the turned keys too, they are given as queries beside these)
+    turned = fq.kv_append_rotated(fmt, *where, qkv[:, :H if keep is None else H + KV], k, v, layer.freqs,
+                                  layer.kv_scale, layer.kv_scale)
+    q = turned[:, :H]
+    att = fq.kv_attention(fmt, *where, q, max_new, seqs.bound, layer.kv_scale, layer.kv_scale,
+                          window=layer.window, sinks=layer.sinks)
+    out = fq.gemm(fmt, fq.quantize(fmt, att.view(rows, H * D)), layer.out, y_dtype=fq.OUT_BF16)
     # experts
-    h = norm(x)
+    a2 = fq.rms_norm_quantize(fmt, out, layer.norm2, residual=x, y_dtype=fq.OUT_BF16)
+    x, h = a2["h"], a2["y"]
     logits = h.float() @ layer.router
     r = fq.route(logits, layer.top)
-    a = fq.permute_quantized(fmt, h, fq.quantize(fmt, h), r["row_src"], r["offsets"])
+    a = fq.permute_quantized(fmt, h, a2, r["row_src"], r["offsets"])
     u = fq.grouped_gemm(fmt, r["offsets"], a, *layer.up, y_dtype=fq.OUT_BF16)
     u = torch.nn.functional.silu(u)
     a = fq.quantize(fmt, u, group_offsets=r["offsets"])
     y = fq.grouped_gemm(fmt, r["offsets"], a, *layer.down, y_dtype=fq.OUT_BF16)
     moe = fq.combine(y, r["row_of"], r["weights"])
     if keep is not None:
-        keep.update(q=q, k=k, v=v, att=att, logits=logits, route=r, y=y, moe=moe, offsets=offsets)
+        keep.update(a1=a1, shared=shared, qkv=qkv, q=q, k=turned[:, H:], v=v, att=att, out=out, a2=a2,
+                    logits=logits, route=r, y=y, moe=moe, offsets=offsets)
     return x + moe
 
 
@@ -112,10 +136,10 @@ def main():
     ap.add_argument("--steps", type=int, default=32)
     args = ap.parse_args()
     fmt = fq.NVFP4 if args.fmt == "nvfp4" else fq.MXFP4
-    layer = Layer(fmt)
+    layer = Layer(fmt, window=256, sinks=4, adapters=3)
     g = torch.Generator().manual_seed(2)
     prompts = torch.randint(17, 400, (24,), generator=g).tolist()
-    seqs = Sequences(layer, prompts, args.steps)
+    seqs = Sequences(layer, prompts, args.steps, adapters=[i % 4 - 1 for i in range(len(prompts))])
     x = torch.randn(sum(prompts), 1024, generator=g).to(torch.bfloat16).cuda()
     y = forward(layer, seqs, x, seqs.new(prompts), max(prompts))
     torch.cuda.synchronize()
