@@ -364,6 +364,9 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs p) {
 //           Sequences that are shorter than the window lose: 32 of 256 to 4096 keys in a
 //           window of 4000 35, for twice the workgroups 28.  Eight waves from 64 (sequence,
 //           kv head)s on: 8 of them over 1028 keys 11.8, by eight 12.4
+//           Wide: 128 rows where 256 would leave half of the CUs without work (605 tokens of
+//           2 kv heads in a window of 31 18.8, by 256 23.1), and 256 keys a split from 1024
+//           keys on (40 tokens over 3000 keys 23, by 512 30; 377 keys 25.8 and 28.3)
 //   join    lane groups on a row's splits, four to eight splits each.  171 splits: 121 by one
 //           group, 115.5 by this rule and by half as many
 struct Plan {
@@ -375,9 +378,11 @@ struct Plan {
 Plan attn_plan(int D, int B, int H, int G, int64_t max_new, int64_t max_len, int window, int sinks) {
   Plan p;
   const int64_t rows = max_new * G;
+  const bool sink = sinks > 0 && window > 0;
   p.wide = rows > 2 * ROWS;
   p.nc = rows > ROWS && D <= 128 ? 2 : 1;
   p.tile = p.wide ? (rows > 128 && D <= 128 ? 256 : 128) : ROWS * p.nc;
+  if (sink && p.tile == 256 && (rows + 255) / 256 <= 128 / (B * (int64_t)H)) p.tile = 128;
   p.step = p.wide ? 64 : KEYS;
   p.tiles = (rows + p.tile - 1) / p.tile;
   int64_t keys = max_len;
@@ -390,13 +395,12 @@ Plan attn_plan(int D, int B, int H, int G, int64_t max_new, int64_t max_len, int
   if (groups > (1 << 30)) groups = 1 << 30;  // (keys * groups stays below 2^63)
   // eight waves on the keys of each (sequence, kv head), none to join
   p.waves = !p.wide && groups <= 256 && keys <= 2048 && p.nc == 1 && D <= 128 ? 8 : 4;
-  const int64_t want = p.wide ? (sinks > 0 && window > 0 ? 256 : 512) : 4096;
+  const int64_t want = p.wide ? (sink ? 256 : 512) : 4096;
   int64_t chunk = (keys * groups + want - 1) / want;
-  const int64_t least = p.wide ? 512 : p.waves == 8 ? 2048 : 256;
+  const int64_t least = p.wide ? (sink && keys >= 1024 ? 256 : 512) : p.waves == 8 ? 2048 : 256;
   chunk = chunk < least ? least : chunk;
   chunk = (chunk + p.step - 1) / p.step * p.step;
   p.chunk = (int)(chunk < (1 << 30) ? chunk : (1 << 30));
-  const bool sink = sinks > 0 && window > 0;
   if (sink && !p.wide) {
     p.waves = groups > 64 && groups <= 256 && keys <= 2048 && p.nc == 1 && D <= 128 ? 8 : 4;
     const int64_t at_once = 256 * (D == 64 ? 4 : D == 128 && p.nc == 1 ? 3 : 2);

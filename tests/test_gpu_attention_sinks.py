@@ -152,3 +152,15 @@ def test_captured_with_growing_lengths():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D,H,n,lens", [(64, 1, [600], [600]), (128, 2, [300, 40], [2000, 40]), (128, 8, [300] * 6, [300] * 6),
+                                        (256, 1, [200], [1500])])
+def test_sizes_of_tiles(fmt, D, H, n, lens):
+    """Few and many workgroups of rows, one and several splits of the keys."""
+    need_gpu()
+    say(f"sinks tiles fmt {fmt} D {D} H {H} n {n}")
+    c = make(fmt, n, lens, G=3, H=H, D=D, page=32, seed=3)
+    for window, sinks in ((30, 70), (1200, 4)):
+        check(c, window, sinks)
