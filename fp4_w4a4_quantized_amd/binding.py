@@ -949,13 +949,11 @@ def rms_norm_quantize(fmt, x, weight, eps=1e-6, residual=None, tscale=None, chan
     tscale f32 [1]: a calibrated tensor scale (NVFP4; one pass instead of two).
     fmt may be MXFP8 (E4M3 codes u8 [rows, cols], E8M0 scales u8 [rows,
     cols/32])."""
-    rows, cols = x.shape
-    n_chan = 0 if chan_idx is None else chan_idx.numel()
     q, scales, ts, resid, y, h, r = _results(stream, _layer().rms_norm_quantize, x, weight, eps,
                                              residual, fmt, layout, tscale, chan_idx, y_dtype, h,
-                                             n_chan, rstd)
-    return {"q": q, "scales": scales, "tscale": ts, "resid": resid, "layout": layout, "rows": rows,
-            "cols": cols, "h": h, "y": y, "rstd": r}
+                                             rstd)
+    return {"q": q, "scales": scales, "tscale": ts, "resid": resid, "layout": layout,
+            "rows": h.size(0), "cols": h.size(1), "h": h, "y": y, "rstd": r}
 
 
 def rms_norm_backward_into(h, weight, rstd, d_y, d_h, d_x, d_weight, stream=None):

@@ -507,7 +507,7 @@ Operand operand(int32_t fmt, int32_t layout, int64_t rows, int64_t cols) {
 }
 
 // rms_norm_quantize(stream, x, weight, eps, residual, fmt, layout, tscale or None, chan or None,
-// y_dtype or None (no y), h or None, n_chan, rstd wanted) -> (q, scales, tscale, resid, y, h, rstd)
+// y_dtype or None (no y), h or None, rstd wanted) -> (q, scales, tscale, resid, y, h, rstd)
 PyObject* rms_norm_quantize(PyObject* const* a) {
   Norm n = norm_of(a, a[10]);
   const int32_t fmt = small(a[5], "fmt"), layout = small(a[6], "layout");
@@ -524,14 +524,16 @@ PyObject* rms_norm_quantize(PyObject* const* a) {
   const int32_t* chan = nullptr;
   int32_t n_chan = 0;
   if (a[8] != Py_None) {
-    n_chan = small(a[11], "chan_idx");
     need(fmt != FP4Q_MXFP8, "chan_idx", "not for MXFP8");
-    chan = ints(a[8], "chan_idx", n_chan);
+    const int64_t many = tensor(a[8], "chan_idx").numel();
+    need(many <= INT32_MAX, "chan_idx", "too many");
+    n_chan = (int32_t)many;
+    chan = ints(a[8], "chan_idx", many);
     if (n_chan == 0) chan = nullptr;
   }
   const bool with_y = a[9] != Py_None;
   const fp4q_dtype_t type = with_y ? dtype_of(a[9], "y_dtype") : FP4Q_OUT_BF16;
-  const int want_r = PyObject_IsTrue(a[12]);
+  const int want_r = PyObject_IsTrue(a[11]);
   if (want_r < 0) throw PythonError();
   void* const stream = stream_here(a[0]);
   const at::Tensor& t = THPVariable_Unpack(a[1]);
@@ -917,7 +919,7 @@ PyMethodDef methods[] = {FP4Q_ENTRY(append, 11),
                          FP4Q_ENTRY(attention_into, 17),
                          FP4Q_ENTRY(attention, 16),
                          FP4Q_ENTRY(rms_norm, 9),
-                         FP4Q_ENTRY(rms_norm_quantize, 13),
+                         FP4Q_ENTRY(rms_norm_quantize, 12),
                          FP4Q_ENTRY(rms_norm_backward, 8),
                          FP4Q_ENTRY(dequantize, 9),
                          FP4Q_ENTRY(lora, 10),
