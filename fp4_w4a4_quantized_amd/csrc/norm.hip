@@ -9,7 +9,10 @@
 // written once, with a row in the registers of one, four or eight waves in
 // between.  NVFP4's own tensor scale needs every row's y before the first code: a
 // first pass writes h, each row's r and the workgroups' maxima, a second reads h
-// again.
+// again.  8192 x 4096 BF16 with a residual: the first 35 us (201 MB, 5.7 TB/s), the
+// second 27.5, which its 21 vector instructions an element bound; MXFP8 in one pass 41.5
+// (236 MB, 5.7 TB/s); 4099 rows of y 24.3 and of the gradient 29 (134 MB, 5.5 and 4.6),
+// the sum of d_weight 6.5.
 //
 // The sum of squares, r and y are 64-bit: y then is the definition's F32 value
 // but in 2^-28 of the cases, and the BF16 value and code made of it with it; a y
@@ -61,7 +64,11 @@ struct NormArgs {
 enum { EMIT_Y, EMIT_MAX, EMIT_NVFP4, EMIT_MXFP4, EMIT_MXFP8 };
 
 constexpr int CH = 8;  // elements of a lane's chunk
-constexpr int MAX_WGS = 2048;  // workgroups of a pass; further rows in turn
+// Workgroups of a pass; further rows in turn: four on each CU, so that a row's loads are
+// ahead of its work.  us of NVFP4's two passes for 512, 1024, 2048:
+// 8192 x 4096 65.8, 60.3, 62.0; 16384 x 1024 40.0, 35.7, 37.2; 8192 x 2048 48.2, 36.8,
+// 38.2 (MXFP8 of 4096 x 8192 loses: 52.1, 53.5, 48.3).
+constexpr int MAX_WGS = 1024;
 
 // Eight elements as they stand in memory.
 template <typename T> struct Raw;
@@ -682,8 +689,6 @@ __global__ __launch_bounds__(256) void k_dequantize(const uint8_t* __restrict__ 
 // The tensor scale of no rows.
 __global__ void k_scale_one(float* tscale) { *tscale = 1.0f; }
 
-// Waves of a row and chunks of a lane: a wave for rows of up to 1024 columns where
-// there are enough of them for all CUs, else four or eight.
 template <typename T, int WPR, int N, int EMIT, bool SECOND>
 int launch_pass(NormArgs p, hipStream_t stream) {
   constexpr int ROWS = WPR == 1 ? 4 : 1;
@@ -711,16 +716,26 @@ void launch_emit(NormArgs p, int emit, bool given, hipStream_t stream) {
   }
 }
 
+// Waves of a row and chunks of a lane.  A wave, and no barrier, for rows of up to 1024
+// columns from 1024 rows on: 16384 x 1024 36 us (NVFP4), by four waves 54; 1024 x 1024
+// 8.4 and 8.7, x 512 7.1 and 8.4; 512 x 1024 8.2 and 8.0, 64 x 1024 8.0 and 7.3.  Longer
+// rows in a wave take its registers: 8192 x 4096 (MXFP8) 54, by four waves 43.
 template <typename T>
 void launch_type(const NormArgs& p, int emit, bool given, hipStream_t stream) {
-  if (p.rows >= 2048 && p.cols <= room(1, 2)) launch_emit<T, 1, 2>(p, emit, given, stream);
+  if (p.rows >= 1024 && p.cols <= room(1, 2)) launch_emit<T, 1, 2>(p, emit, given, stream);
   else if (p.cols <= room(4, 2)) launch_emit<T, 4, 2>(p, emit, given, stream);
   else if (p.cols <= room(4, 4)) launch_emit<T, 4, 4>(p, emit, given, stream);
   else if (p.cols <= room(8, 4)) launch_emit<T, 8, 4>(p, emit, given, stream);
   else launch_emit<T, 8, 8>(p, emit, given, stream);
 }
 
-int backward_blocks(int64_t rows) { return (int)(rows < 1024 ? rows : 1024); }
+// Workgroups, each with a row of d_weight's sums: four rows each, between 256 and 1024 of
+// them.  us for that, for 512 and for 1024 at least: 512 x 4096 13.4, 16.2, 16.2; 1024 x
+// 4096 16.6, 16.0, 20.1; 700 x 1024 8.0, 8.7, 10.0.  At most 512: 8192 x 4096 71, for 61.
+int backward_blocks(int64_t rows) {
+  const int64_t n = rows / 4 < 256 ? 256 : rows / 4 < 1024 ? rows / 4 : 1024;
+  return (int)(rows < n ? rows : n);
+}
 
 template <typename T>
 void launch_backward_type(const NormGradArgs& p, hipStream_t stream) {
