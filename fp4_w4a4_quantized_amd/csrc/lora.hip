@@ -140,7 +140,7 @@ __global__ __launch_bounds__(256) void k_lora_u(LoraArgs p) {
     u32x4 a[U][RT], x[U][MT];
   };
   // Loads without conditions, so that none waits for another: past the split's
-  // end its first ones again, for which x counts as 0.
+  // end its first ones again, which count as 0 on both sides (an infinity among them).
   auto load = [&](Batch& f, int64_t k) {
 #pragma unroll
     for (int s = 0; s < U; ++s) {
@@ -155,9 +155,12 @@ __global__ __launch_bounds__(256) void k_lora_u(LoraArgs p) {
     if (k + 32 * U > k1) {
 #pragma unroll
       for (int s = 0; s < U; ++s)
+        if (k + 32 * s + 8 * g >= k1) {
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-          if (k + 32 * s + 8 * g >= k1) f.x[s][m] = u32x4{0, 0, 0, 0};
+          for (int i = 0; i < RT; ++i) f.a[s][i] = u32x4{0, 0, 0, 0};
+#pragma unroll
+          for (int m = 0; m < MT; ++m) f.x[s][m] = u32x4{0, 0, 0, 0};
+        }
     }
 #pragma unroll
     for (int s = 0; s < U; ++s)
@@ -374,8 +377,10 @@ __global__ __launch_bounds__(256) void k_lora_out(LoraArgs p) {
                        __builtin_bit_cast(uint32_t, __builtin_convertvector(hi, bf16x2l))};
       *reinterpret_cast<u32x2*>(&s_u[e][row][r]) = w;
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        v[j] -= __uint_as_float((j & 1) ? w[j >> 1] & 0xFFFF0000u : w[j >> 1] << 16);
+      for (int j = 0; j < 4; ++j) {  // (an infinity is one term)
+        const float term = __uint_as_float((j & 1) ? w[j >> 1] & 0xFFFF0000u : w[j >> 1] << 16);
+        v[j] = fabsf(term) == INFINITY ? 0.0f : v[j] - term;
+      }
     }
   }
   __syncthreads();

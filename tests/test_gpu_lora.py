@@ -180,3 +180,29 @@ def test_captured_and_on_a_stream():
     o = fq.lora(*t1, stream=s)
     s.synchronize()
     assert torch.equal(o, w1)
+
+
+@pytest.mark.parametrize("dt", [B, torch.float32])
+@pytest.mark.parametrize("rank,K,sizes", [(8, 40, [3, 2, 4]), (40, 264, [5, 1, 2]), (32, 1032, [700, 100, 400])])
+def test_infinities(dt, rank, K, sizes):
+    """An infinite weight (in the columns that a step past the end reads again), an
+    infinite and a NaN input: each row as the formula has it, its neighbours as
+    without them."""
+    need_gpu()
+    say(f"lora infinities rank {rank} K {K} {dt}")
+    c = case(sizes, [0, 1, 2], rank, K, 72, dt)
+    c["a"][1, rank - 3, 2] = np.inf
+    row = sizes[0] + sizes[1]
+    c["a"][2, :, 5] = 0.5
+    c["x"][row, 5], c["x"][row + 1, 0] = -np.inf, np.nan
+    c["b"][2] = np.abs(c["b"][2])          # infinities of one sign
+    with np.errstate(invalid="ignore"):
+        want = layer.lora(c["x"], c["a"], c["b"], c["off"], c["ad"], c["scale"], c["y"])[0]
+    got = call(c).double().cpu().numpy()
+    finite = np.isfinite(want)
+    assert not finite[sizes[0]:row + 2].any() and finite[:sizes[0]].all() and finite[row + 2:].all()
+    assert np.isinf(want[sizes[0]:row + 1]).any() and np.isnan(want[row + 1]).all()
+    assert np.array_equal(got[~finite], want[~finite], equal_nan=True)
+    keep = [r for r in range(len(want)) if finite[r].all()]
+    clean = dict(c, a=np.where(np.isfinite(c["a"]), c["a"], 0.0), x=np.where(np.isfinite(c["x"]), c["x"], 0.0))
+    assert np.array_equal(got[keep], call(clean).double().cpu().numpy()[keep])

@@ -141,7 +141,7 @@ def same_operand(a, b, fmt, layout, rows, cols):
 
 @pytest.mark.parametrize("fmt", [fq.NVFP4, fq.MXFP4])
 @pytest.mark.parametrize("layout", [fq.ROWMAJOR, fq.TILED])
-@pytest.mark.parametrize("rows,cols", [(1, 128), (3, 256), (64, 2048), (70, 4096), (2100, 384), (5, 8320), (4, 18432)])
+@pytest.mark.parametrize("rows,cols", [(1, 128), (3, 256), (64, 2048), (70, 4096), (2100, 384), (5, 8320), (4, 18432), (2, 32768)])
 def test_operand_is_the_quantizers(fmt, layout, rows, cols):
     need_gpu()
     say(f"norm into operand fmt {fmt} layout {layout} {rows} x {cols}")
