@@ -383,13 +383,18 @@ __global__ __launch_bounds__(WPR == 8 ? 512 : 256) void k_norm(NormArgs p) {
   // chunk's codes and scale stand in row 0 of a block of rows.
   constexpr bool KEEP = N <= 2;
   constexpr int FMT = EMIT == EMIT_NVFP4 ? FP4Q_NVFP4 : FP4Q_MXFP4, BLK = FMT == FP4Q_NVFP4 ? 16 : 32;
-  float kept[KEEP ? N : 1][CH];
+  double kept[KEEP ? N : 1][CH];
   int64_t code0[N], scale0[N];
 #pragma unroll
   for (int c = 0; c < N; ++c) {
     const int col = col0 + c * WPR * 64 * CH;
     if (c >= nc || col >= p.cols) continue;
-    if (KEEP) load_any(p.w, col, p.w_f32, EMIT == EMIT_Y ? p.cols - col : CH, kept[KEEP ? c : 0]);
+    if (KEEP) {
+      float w[CH];
+      load_any(p.w, col, p.w_f32, EMIT == EMIT_Y ? p.cols - col : CH, w);
+#pragma unroll
+      for (int i = 0; i < CH; ++i) kept[KEEP ? c : 0][i] = w[i];
+    }
     code0[c] = code_off(p.tiled, 0, col >> 1, p.cols);
     scale0[c] = scale_off<FMT>(p.tiled, 0, col / BLK, p.cols);
   }
@@ -454,19 +459,10 @@ __global__ __launch_bounds__(WPR == 8 ? 512 : 256) void k_norm(NormArgs p) {
       const int col = col0 + c * WPR * 64 * CH, n = left(col);
       if (col >= p.cols) continue;
       float w[CH], f[CH];
-      if (KEEP) {
+      if (!KEEP) load_any(p.w, col, p.w_f32, n, w);
 #pragma unroll
-        for (int i = 0; i < CH; ++i) w[i] = kept[KEEP ? c : 0][i];
-      } else {
-        load_any(p.w, col, p.w_f32, n, w);
-      }
-      if (sizeof(T) == 2 && !p.w_f32) {
-#pragma unroll
-        for (int i = 0; i < CH; ++i) f[i] = (float)((double)(h[c].at(i) * w[i]) * r);  // (the first product is exact)
-      } else {
-#pragma unroll
-        for (int i = 0; i < CH; ++i) f[i] = (float)(((double)h[c].at(i) * (double)w[i]) * r);
-      }
+      for (int i = 0; i < CH; ++i)  // (the first product is exact)
+        f[i] = (float)((double)h[c].at(i) * (KEEP ? kept[KEEP ? c : 0][i] : (double)w[i]) * r);
       if (EMIT != EMIT_MAX && p.y) store_any(p.y, row * p.ldy + col, p.y_f32, n, f);
       if constexpr (EMIT != EMIT_Y) {
         Raw<uint16_t> y;

@@ -123,6 +123,22 @@ def test_rows_of_zeros_and_of_extreme_values():
             assert np.all(np.isnan(got[5]))
 
 
+@pytest.mark.parametrize("cols", [256, 2080, 9024])
+def test_products_beyond_f32(cols):
+    """h w leaves F32 on either side where y does not."""
+    need_gpu()
+    for dt, big, wbig in ((torch.bfloat16, 100, 60), (torch.bfloat16, -100, -60), (torch.float32, 100, 60)):
+        say(f"norm products beyond f32 {dt} {cols} 2^{big} 2^{wbig}")
+        x, _, w = case(4, cols, dt, False)
+        x, w = x * 2.0 ** big, w * 2.0 ** wbig
+        h, r, y = layer.rms_norm(x, w, 0.0, None)
+        assert np.abs(y).max() < 2.0 ** 70 and (np.abs(x * w).max() > 2.0 ** 128 or np.abs(x * w).max() < 2.0 ** -149)
+        f = fq.rms_norm(dev(x, dt), dev(w, dt), 0.0, y_dtype=fq.OUT_F32)
+        assert np.all(np.abs(host(f["y"]) - y) <= (E + 2.0 ** -48) * np.abs(y) + 2.0 ** -149)
+        want = fq.quantize(fq.MXFP4, dev(layer.bf16_round(y), torch.bfloat16))
+        same_operand(fq.rms_norm_quantize(fq.MXFP4, dev(x, dt), dev(w, dt), 0.0), want, fq.MXFP4, 0, 4, cols)
+
+
 # ---- quantized operands -------------------------------------------------------
 
 def same_operand(a, b, fmt, layout, rows, cols):
