@@ -27,6 +27,7 @@ namespace {
 
 typedef float f32x2n __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2n __attribute__((ext_vector_type(2)));
+typedef uint16_t u16x2n __attribute__((ext_vector_type(2)));
 // Sixteen bytes at any element's address (rows of odd strides).
 typedef uint32_t u32x4_2 __attribute__((ext_vector_type(4), aligned(2)));
 typedef uint32_t u32x4_4 __attribute__((ext_vector_type(4), aligned(4)));
@@ -164,10 +165,10 @@ __device__ __forceinline__ void store_any(void* p, int64_t at, int f32, int n, c
 }
 
 __device__ __forceinline__ uint32_t max_bits(const Raw<uint16_t>& r) {
-  uint32_t m = 0;
+  u16x2n m = {0, 0};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) m = max(m, max(r.v[i] & 0x7FFFu, (r.v[i] >> 16) & 0x7FFFu));
-  return m;
+  for (int i = 0; i < 4; ++i) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2n, r.v[i] & 0x7FFF7FFFu));
+  return max((uint32_t)m[0], (uint32_t)m[1]);
 }
 
 // The largest of v over the N (2 or 4) lanes whose chunks make up a block.
@@ -185,6 +186,13 @@ struct TensorScale {
   float t, rt;
   const float* reciprocal;  // LDS: RN(1 / (scale t)) by code, 0 for code 0
 };
+
+// quot_rn of a BF16 x: one correction is enough (it gives the IEEE quotient for each
+// of the 2^7 mantissas of x by each of the 2^23 of d).
+__device__ __forceinline__ float quot_bf16(float x, float d, float y) {
+  const float q = x * y;
+  return __builtin_fmaf(-__builtin_fmaf(q, d, -x), y, q);
+}
 
 // A chunk of y (BF16) as codes: FP4's in w[0], MXFP8's in w[0], w[1]; returns the
 // block's scale code.  FAR: a given tensor scale, whose blocks may lie far past
@@ -205,7 +213,7 @@ __device__ __forceinline__ uint32_t encode(const Raw<uint16_t>& y, uint32_t amax
       const float d = e4m3_value(sb) * ts.t, rd = ts.reciprocal[sb];
 #pragma unroll
       for (int i = 0; i < CH; ++i)
-        v[i] = quot_rn(FAR ? __builtin_amdgcn_fmed3f(y.at(i), -8.0f * d, 8.0f * d) : y.at(i), d, rd);
+        v[i] = quot_bf16(FAR ? __builtin_amdgcn_fmed3f(y.at(i), -8.0f * d, 8.0f * d) : y.at(i), d, rd);
       w[0] = e2m1_pack8(v);
       return sb;
     }
