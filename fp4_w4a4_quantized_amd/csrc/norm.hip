@@ -10,7 +10,7 @@
 // between.  NVFP4's own tensor scale needs every row's y before the first code: a
 // first pass writes h, each row's r and the workgroups' maxima, a second reads h
 // again.  8192 x 4096 BF16 with a residual: the first 35 us (201 MB, 5.7 TB/s), the
-// second 27.5, which its 21 vector instructions an element bound; MXFP8 in one pass 41.5
+// second 26.2 (17 vector instructions an element: 18 us); MXFP8 in one pass 41.5
 // (236 MB, 5.7 TB/s); 4099 rows of y 24.3 and of the gradient 29 (134 MB, 5.5 and 4.6),
 // the sum of d_weight 6.5.
 //
@@ -406,9 +406,9 @@ __global__ __launch_bounds__(WPR == 8 ? 512 : 256) void k_norm(NormArgs p) {
     code0[c] = code_off(p.tiled, 0, col >> 1, p.cols);
     scale0[c] = scale_off<FMT>(p.tiled, 0, col / BLK, p.cols);
   }
-  // Few chunks: the next row is on its way while one is worked on (but for the
-  // second pass, which its arithmetic bounds: 29.4 us without, 31.4 with it).
-  constexpr bool AHEAD = N <= 2 && !SECOND;
+  // Few chunks: the next row is on its way while one is worked on (second pass of
+  // 8192 x 4096 26.2 us, 27.6 without).
+  constexpr bool AHEAD = N <= 2;
   int turn = 0;
   for (int64_t gi = blockIdx.x; gi < p.groups; gi += gridDim.x, turn ^= 1) {
     const int64_t row = row_of(gi);
