@@ -1282,7 +1282,7 @@ int fp4q_lora(const uint16_t* x, int64_t ldx, const uint16_t* a, const uint16_t*
       !matrix_ok(out, dtype, ldo, rows, N) || (y && !matrix_ok(y, dtype, ldy, rows, N)))
     return FP4Q_ERR_INVALID;
   if (!a || !b || !offsets || !adapter || !aligned(a, 16) || !aligned(b, 16) || !aligned(scale, 4) ||
-      !aligned(offsets, 4) || !aligned(adapter, 4) || (y == out && ldy != ldo))
+      !aligned(offsets, 4) || !aligned(adapter, 4) || (y && y == out && ldy != ldo))
     return FP4Q_ERR_INVALID;
   if (rows > 0 && (!x || !aligned(x, 16) || ldx % 8 != 0)) return FP4Q_ERR_INVALID;
   if (!lora_shape_ok(rows, n_groups, rank, K, N)) return FP4Q_ERR_UNSUPPORTED;

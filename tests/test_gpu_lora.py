@@ -206,3 +206,14 @@ def test_infinities(dt, rank, K, sizes):
     keep = [r for r in range(len(want)) if finite[r].all()]
     clean = dict(c, a=np.where(np.isfinite(c["a"]), c["a"], 0.0), x=np.where(np.isfinite(c["x"]), c["x"], 0.0))
     assert np.array_equal(got[keep], call(clean).double().cpu().numpy()[keep])
+
+
+@pytest.mark.parametrize("dt", [B, torch.float32])
+def test_no_rows_without_y(dt):
+    """An empty batch's adapters alone, and into an empty result."""
+    need_gpu()
+    c = case([0, 0], [0, 1], 16, 64, 32, dt)
+    got = call(c, y=False)
+    assert got.shape == (0, 32) and got.dtype == dt
+    out = torch.empty(0, 32, device="cuda", dtype=dt)
+    fq.lora_into(dev(c["x"], B), dev(c["a"], B), dev(c["b"], B), ints(c["off"]), ints(c["ad"]), None, None, out)
