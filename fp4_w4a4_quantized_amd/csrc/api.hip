@@ -1200,8 +1200,9 @@ int fp4q_rms_norm_quantize(fp4q_format_t fmt, fp4q_layout_t layout, fp4q_dtype_t
   if ((!fmt_ok(fmt) && fmt != FP4Q_MXFP8) || !layout_ok(layout) || cols % blk_of(fmt) != 0 ||
       (layout == FP4Q_LAYOUT_TILED && (fmt == FP4Q_MXFP8 || cols % 128 != 0)))
     return FP4Q_ERR_INVALID;
-  if (n_chan < 0 || n_chan > cols || (n_chan > 0) != (chan_idx != nullptr) ||
-      (n_chan > 0) != (resid != nullptr) || (n_chan > 0 && fmt == FP4Q_MXFP8) || !aligned(chan_idx, 4) ||
+  // (an empty batch's residual has no address)
+  if (n_chan < 0 || n_chan > cols || (n_chan > 0) != (chan_idx != nullptr) || (n_chan == 0 && resid) ||
+      (rows > 0 && n_chan > 0 && !resid) || (n_chan > 0 && fmt == FP4Q_MXFP8) || !aligned(chan_idx, 4) ||
       !aligned(resid, 2))
     return FP4Q_ERR_INVALID;
   if ((fmt == FP4Q_NVFP4) != (tensor_scale != nullptr) || !aligned(tensor_scale, 4)) return FP4Q_ERR_INVALID;

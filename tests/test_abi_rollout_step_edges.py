@@ -2,6 +2,8 @@
 what they take (no GPU): empty batches, whose tensors have no address."""
 import pytest
 
+from test_abi_layer_edges import passes
+
 A, B = 0x10000, 0x20000
 INVALID = -1
 
@@ -24,3 +26,20 @@ def test_adapters_of_no_rows_without_y(L):
             for out in (None, B):
                 assert adapters(L, rows=0, x=None, y=None, ldy=ldy, out=out, dt=dt) == 0
     assert adapters(L, y=B, ldy=31) == INVALID          # out over y of another stride
+
+
+def quantized_norm(L, fmt=0, lay=0, rows=5, cols=128, x=A, res=None, h=None, ch=A, nc=4, q=A, s=A, ts=A, given=1,
+                   r=B, ws=None, wsb=0):
+    return L.fp4q_rms_norm_quantize(fmt, lay, 1, x, cols, res, cols, h, cols, A, 0, 1e-6, rows, cols, ch, nc, q, s,
+                                    ts if fmt == 0 else None, given, r, None, 1, cols, None, ws, wsb, None)
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("lay", [0, 1])
+def test_norm_into_an_operand_of_no_rows_with_channels(L, fmt, lay):
+    """(Past the checks: a launch failure that the test hook asks for.)"""
+    for given in (0, 1):
+        for r in (None, B):
+            assert passes(lambda: quantized_norm(L, fmt, lay, rows=0, x=None, q=None, s=None, r=r, given=given))
+    assert quantized_norm(L, fmt, lay, r=None) == INVALID
+    assert quantized_norm(L, fmt, lay, rows=0, ch=None, nc=0) == INVALID     # a residual of no channels
