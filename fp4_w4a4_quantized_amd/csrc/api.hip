@@ -34,6 +34,12 @@ inline int blk_of(int fmt) { return fmt == FP4Q_NVFP4 ? 16 : 32; }
 
 inline bool fmt_ok(int fmt) { return fmt == FP4Q_NVFP4 || fmt == FP4Q_MXFP4; }
 
+// The selected channels' residual (or its codes): with channels only, and an
+// empty batch's has no address.
+inline bool resid_ok(int64_t rows, int32_t n_chan, const void* resid) {
+  return n_chan > 0 ? rows == 0 || resid : !resid;
+}
+
 inline bool layout_ok(int layout) {
   return layout == FP4Q_LAYOUT_ROWMAJOR || layout == FP4Q_LAYOUT_TILED;
 }
@@ -112,8 +118,7 @@ int quantize_checks(int fmt, int layout, const uint16_t* x, int64_t rows, int64_
   if (layout == FP4Q_LAYOUT_TILED && cols % 128 != 0) return FP4Q_ERR_INVALID;
   if (num_groups < 1 || (num_groups > 1 && !group_offsets)) return FP4Q_ERR_INVALID;
   if (n_chan < 0 || n_chan > cols) return FP4Q_ERR_INVALID;
-  if ((n_chan > 0) != (chan_idx != nullptr) || (n_chan > 0) != (resid != nullptr))
-    return FP4Q_ERR_INVALID;
+  if ((n_chan > 0) != (chan_idx != nullptr) || !resid_ok(rows, n_chan, resid)) return FP4Q_ERR_INVALID;
   if (fmt == FP4Q_NVFP4 && !tensor_scale) return FP4Q_ERR_INVALID;
   if (fmt == FP4Q_MXFP4 && tensor_scale) return FP4Q_ERR_INVALID;
   if (rows > 0 && (!x || !q || !scales)) return FP4Q_ERR_INVALID;
@@ -224,8 +229,7 @@ static int validate_gemm_common(int fmt, int64_t N, int64_t K, const uint8_t* a_
   if (y_dtype != FP4Q_OUT_F32 && y_dtype != FP4Q_OUT_BF16) return FP4Q_ERR_INVALID;
   if (rows < 0 || N < 0 || K <= 0 || K % blk_of(fmt) != 0) return FP4Q_ERR_INVALID;
   if (n_chan < 0 || n_chan > K) return FP4Q_ERR_INVALID;
-  if ((n_chan > 0) != (chan_idx != nullptr) || (n_chan > 0) != (resid != nullptr))
-    return FP4Q_ERR_INVALID;
+  if ((n_chan > 0) != (chan_idx != nullptr) || !resid_ok(rows, n_chan, resid)) return FP4Q_ERR_INVALID;
   if (n_chan > 0 && !aligned(resid, 16)) return FP4Q_ERR_INVALID;
   if (fmt == FP4Q_NVFP4 && (!a_ts || !b_ts)) return FP4Q_ERR_INVALID;
   if (fmt == FP4Q_MXFP4 && (a_ts || b_ts)) return FP4Q_ERR_INVALID;
@@ -392,7 +396,7 @@ int fp4q_gemm_residual_fp4(fp4q_format_t fmt, fp4q_layout_t layout, int64_t M, i
                            const uint8_t* r_s, const float* r_ts, void* y, fp4q_dtype_t y_dtype,
                            int64_t ldy, void* workspace, size_t workspace_bytes, void* stream) {
   if (!layout_ok(layout) || !fmt_ok(fmt)) return FP4Q_ERR_INVALID;
-  if (n_chan < 0 || (n_chan > 0) != (r_q != nullptr) || (n_chan > 0) != (r_s != nullptr))
+  if (n_chan < 0 || !resid_ok(M, n_chan, r_q) || !resid_ok(M, n_chan, r_s))
     return FP4Q_ERR_INVALID;
   if (n_chan % blk_of(fmt) != 0) return FP4Q_ERR_INVALID;
   if (fmt == FP4Q_NVFP4 && (n_chan > 0) != (r_ts != nullptr)) return FP4Q_ERR_INVALID;
@@ -480,7 +484,7 @@ int fp4q_grouped_gemm_residual_fp4(fp4q_format_t fmt, fp4q_layout_t w_layout,
                                    fp4q_dtype_t y_dtype, void* workspace, size_t workspace_bytes,
                                    void* stream) {
   if (!fmt_ok(fmt)) return FP4Q_ERR_INVALID;
-  if (n_chan < 0 || (n_chan > 0) != (r_q != nullptr) || (n_chan > 0) != (r_s != nullptr))
+  if (n_chan < 0 || !resid_ok(total_rows, n_chan, r_q) || !resid_ok(total_rows, n_chan, r_s))
     return FP4Q_ERR_INVALID;
   if (n_chan % blk_of(fmt) != 0) return FP4Q_ERR_INVALID;
   if (fmt == FP4Q_NVFP4 && (n_chan > 0) != (r_ts != nullptr)) return FP4Q_ERR_INVALID;
@@ -746,8 +750,7 @@ int fp4q_permute_quantized(fp4q_format_t fmt, const uint16_t* x, int64_t tokens,
   if (rows > 0 && tokens == 0) return FP4Q_ERR_INVALID;
   if (num_groups < 1 || !group_offsets) return FP4Q_ERR_INVALID;
   if (n_chan < 0 || n_chan > cols) return FP4Q_ERR_INVALID;
-  if ((n_chan > 0) != (chan_idx != nullptr) || (n_chan > 0) != (resid_out != nullptr))
-    return FP4Q_ERR_INVALID;
+  if ((n_chan > 0) != (chan_idx != nullptr) || !resid_ok(rows, n_chan, resid_out)) return FP4Q_ERR_INVALID;
   if (fmt == FP4Q_NVFP4 && (!tensor_scale || !tensor_scale_out)) return FP4Q_ERR_INVALID;
   if (fmt == FP4Q_MXFP4 && (tensor_scale || tensor_scale_out)) return FP4Q_ERR_INVALID;
   // q_out and scales_out both NULL: the residual (and tensor scales) only,
@@ -1200,10 +1203,8 @@ int fp4q_rms_norm_quantize(fp4q_format_t fmt, fp4q_layout_t layout, fp4q_dtype_t
   if ((!fmt_ok(fmt) && fmt != FP4Q_MXFP8) || !layout_ok(layout) || cols % blk_of(fmt) != 0 ||
       (layout == FP4Q_LAYOUT_TILED && (fmt == FP4Q_MXFP8 || cols % 128 != 0)))
     return FP4Q_ERR_INVALID;
-  // (an empty batch's residual has no address)
-  if (n_chan < 0 || n_chan > cols || (n_chan > 0) != (chan_idx != nullptr) || (n_chan == 0 && resid) ||
-      (rows > 0 && n_chan > 0 && !resid) || (n_chan > 0 && fmt == FP4Q_MXFP8) || !aligned(chan_idx, 4) ||
-      !aligned(resid, 2))
+  if (n_chan < 0 || n_chan > cols || (n_chan > 0) != (chan_idx != nullptr) || !resid_ok(rows, n_chan, resid) ||
+      (n_chan > 0 && fmt == FP4Q_MXFP8) || !aligned(chan_idx, 4) || !aligned(resid, 2))
     return FP4Q_ERR_INVALID;
   if ((fmt == FP4Q_NVFP4) != (tensor_scale != nullptr) || !aligned(tensor_scale, 4)) return FP4Q_ERR_INVALID;
   if (rows > 0 && (!q || !scales || !aligned(q, 16) || !aligned(scales, 4))) return FP4Q_ERR_INVALID;

@@ -43,3 +43,37 @@ def test_norm_into_an_operand_of_no_rows_with_channels(L, fmt, lay):
             assert passes(lambda: quantized_norm(L, fmt, lay, rows=0, x=None, q=None, s=None, r=r, given=given))
     assert quantized_norm(L, fmt, lay, r=None) == INVALID
     assert quantized_norm(L, fmt, lay, rows=0, ch=None, nc=0) == INVALID     # a residual of no channels
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+def test_an_empty_batch_with_channels_through_the_layer(L, fmt):
+    """The quantizer, the products and the permutation behind such a norm: no rows'
+    residual has no address there either."""
+    ats = A if fmt == 0 else None
+
+    def quantizer(rows, r):
+        return L.fp4q_quantize(fmt, 0, A, rows, 128, 128, None, 1, A, 4, A, A, ats, r, A, 1 << 20, None)
+
+    def product(M, r):
+        return L.fp4q_gemm(fmt, 0, M, 64, 128, A, A, ats, A, A, ats, A, 4, r, A, 1, 64, A, 1 << 20, None)
+
+    def prepared(M, r):
+        return L.fp4q_gemm_prepared(fmt, 0, M, 64, 128, A, A, ats, A, A, ats, A, 4, r, A, 1 << 20, A, 1, 64, None)
+
+    def grouped(rows, r):
+        return L.fp4q_grouped_gemm(fmt, 0, rows, 64, 128, A, 2, A, A, ats, A, A, ats, A, 4, r, A, 1, A, 1 << 20, None)
+
+    def second(M, r):
+        return L.fp4q_gemm_residual_fp4(fmt, 0, M, 64, 128, A, A, ats, A, A, ats, A, 32, r, r, ats, A, 1, 64, A,
+                                        1 << 20, None)
+
+    for f in (quantizer, product, prepared, grouped, second):
+        assert f(5, None) == INVALID, f.__name__
+        for r in (None, A):
+            assert passes(lambda: f(0, r)) or f(0, r) == 0, f.__name__
+
+    def permuted(rows, r):
+        return L.fp4q_permute_quantized(fmt, A, 5, 128, 128, A, A, ats, A, rows, A, 2, A, 4, A, A, ats, r, None)
+
+    assert permuted(5, None) == INVALID
+    assert permuted(0, None) == 0 if fmt else passes(lambda: permuted(0, None))
