@@ -29,6 +29,7 @@ typedef __bf16 bf16x8l __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x4_2l __attribute__((ext_vector_type(4), aligned(2)));
 typedef uint32_t u32x4_4l __attribute__((ext_vector_type(4), aligned(4)));
 
+constexpr float BF16_MAX = 0x1.FEp127f;  // the largest finite one
 constexpr int U_MT = 4, U_MT_128 = 2, OUT_MT = 2;  // products of a tile of many rows (U_MT_128: ranks above 64)
 
 struct LoraArgs {
@@ -135,7 +136,7 @@ __global__ __launch_bounds__(256) void k_lora_u(LoraArgs p) {
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int i = 0; i < RT; ++i) acc[m][i] = {0.0f, 0.0f, 0.0f, 0.0f};
-    constexpr int U = MT * RT >= 32 ? 1 : MT * RT >= 8 ? 2 : 4;  // steps of 32 along K that are loaded together
+  constexpr int U = MT * RT >= 32 ? 1 : MT * RT >= 8 ? 2 : 4;  // steps of 32 along K that are loaded together
   struct Batch {
     u32x4 a[U][RT], x[U][MT];
   };
@@ -194,6 +195,16 @@ __global__ __launch_bounds__(256) void k_lora_u(LoraArgs p) {
     const int row = 16 * (j / RT) + c;
     if (row < t.n) *reinterpret_cast<f32x4l*>(u + (t.r0 + row) * p.ur + 16 * (j % RT) + 4 * g) = v;
   }
+}
+
+// Eight BF16 with 0 for those that are infinite or NaN.
+__device__ __forceinline__ u32x4 finite_of(u32x4 v) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if ((v[i] & 0x7F80u) == 0x7F80u) v[i] &= 0xFFFF0000u;
+    if ((v[i] & 0x7F800000u) == 0x7F800000u) v[i] &= 0xFFFFu;
+  }
+  return v;
 }
 
 // Sixteen bytes of a row of y or out; n: elements that the row has from p on.
@@ -310,28 +321,63 @@ __global__ __launch_bounds__(256) void k_lora_out(LoraArgs p) {
         else f.o[m][j].v = u32x4{0, 0, 0, 0};
       }
   };
-  auto add = [&](Step& f, int64_t n0) {
-    f32x4l acc[MT][4];
+  auto no_tail = [&](Step& f, int s) {  // ranks that are not there
+    if (32 * s + 32 > p.rank) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (32 * s + 8 * g >= p.rank) f.b[i] = u32x4{0, 0, 0, 0};
+    }
+  };
+  auto zero = [](f32x4l (&acc)[MT][4]) {
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[m][i] = {0.0f, 0.0f, 0.0f, 0.0f};
+  };
+  auto term = [&](Step& f, int s, int e, f32x4l (&acc)[MT][4]) {
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const u32x4 fu = *reinterpret_cast<const u32x4*>(&s_u[e][16 * m + c][32 * s + 8 * g]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[m][i] = product(f.b[i], fu, acc[m][i]);
+    }
+  };
+  auto add = [&](Step& f, int64_t n0) {
+    f32x4l acc[MT][4];
+    zero(acc);
 #pragma unroll
     for (int s = 0; s < RS; ++s) {
       if (s > 0) load_b(f, n0, s);
-      if (32 * s + 32 > p.rank) {
+      no_tail(f, s);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (32 * s + 8 * g >= p.rank) f.b[i] = u32x4{0, 0, 0, 0};
+      for (int e = 0; e < TERMS; ++e) term(f, s, e, acc);
+    }
+    // An infinite element of B times a lower term that is 0, or of the other sign,
+    // has made NaN of an infinite result.  Where a sum is infinite or NaN (`any` then
+    // is; two large ones make it so too, and come out again), the lower terms
+    // take B's finite elements alone.
+    float any = 0.0f;
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        any = __builtin_fmaf(acc[m][i][0], acc[m][i][1], any);
+        any = __builtin_fmaf(acc[m][i][2], acc[m][i][3], any);
       }
+    if (__any(!(fabsf(any) < INFINITY))) {
+      int64_t again = n0;  // (its own addresses: shared ones would be held in registers)
+      asm volatile("" : "+s"(again));
+      zero(acc);
+#pragma unroll 1
+      for (int s = 0; s < RS; ++s) {
+        load_b(f, again, s);
+        no_tail(f, s);
+        term(f, s, 0, acc);
 #pragma unroll
-      for (int e = 0; e < TERMS; ++e)
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          const u32x4 fu = *reinterpret_cast<const u32x4*>(&s_u[e][16 * m + c][32 * s + 8 * g]);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[m][i] = product(f.b[i], fu, acc[m][i]);
-        }
+        for (int i = 0; i < 4; ++i) f.b[i] = finite_of(f.b[i]);
+#pragma unroll 1
+        for (int e = 1; e < TERMS; ++e) term(f, s, e, acc);
+      }
     }
 #pragma unroll
     for (int m = 0; m < MT; ++m)
@@ -372,7 +418,13 @@ __global__ __launch_bounds__(256) void k_lora_out(LoraArgs p) {
     }
 #pragma unroll
     for (int e = 0; e < TERMS; ++e) {
-      const f32x2l lo = {v[0], v[1]}, hi = {v[2], v[3]};
+      f32x4l t = v;
+      if (e == 0) {  // (finite values that would be rounded to infinity: the largest BF16)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (fabsf(v[j]) < INFINITY) t[j] = __builtin_amdgcn_fmed3f(v[j], -BF16_MAX, BF16_MAX);
+      }
+      const f32x2l lo = {t[0], t[1]}, hi = {t[2], t[3]};
       const u32x2 w = {__builtin_bit_cast(uint32_t, __builtin_convertvector(lo, bf16x2l)),
                        __builtin_bit_cast(uint32_t, __builtin_convertvector(hi, bf16x2l))};
       *reinterpret_cast<u32x2*>(&s_u[e][row][r]) = w;

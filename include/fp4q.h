@@ -935,6 +935,8 @@ int fp4q_dequantize(fp4q_format_t fmt, fp4q_layout_t layout, const uint8_t* q, c
  * y's (zeros where y is NULL; untouched where out is y).  Products are BF16
  * with F32 sums; x A^T is scaled in F32 and enters the second product as two
  * BF16 terms (three for F32 out).  Sums are taken in the same order in every call.
+ * An infinite or NaN element gives what the formula gives, in the rows and columns
+ * that it enters alone.
  * FP4Q_ERR_UNSUPPORTED: rank not a multiple of 8 or above 128, K not a multiple
  * of 8, K or N not below 2^31, rows not below 2^24, n_groups above 65536. */
 size_t fp4q_lora_workspace_bytes(int64_t rows, int32_t n_groups, int32_t rank, int64_t K, int64_t N);
