@@ -921,7 +921,8 @@ int fp4q_kv_append_rotated(fp4q_format_t fmt, uint8_t* cache, int64_t n_pages, i
   if (rows >= ((int64_t)1 << 25) || qcols >= ((int64_t)1 << 31))
     return FP4Q_ERR_UNSUPPORTED;  // (before the packed tensors: a caller may not have made them)
   if (!packed_ok(k, ldk, cols) || !packed_ok(v, ldv, cols) || !packed_ok(q, ldq, qcols) ||
-      !packed_ok(q_out, ldqo, qcols) || (rot > 0 && !freqs) || !aligned(freqs, 4))
+      !packed_ok(q_out, ldqo, qcols) || (rot > 0 && !freqs) || !aligned(freqs, 4) ||
+      (q_out == q && ldqo != ldq && rows > 1))
     return FP4Q_ERR_INVALID;
   if (injected_failure()) return FP4Q_ERR_HIP;
   clear_error();
@@ -1137,6 +1138,13 @@ inline bool matrix_ok(const void* p, int dtype, int64_t ld, int64_t rows, int64_
   return ld >= cols && (rows == 0 || p) && aligned(p, dtype == FP4Q_OUT_F32 ? 4 : 2);
 }
 
+// A result over an input has its type and stride: a row would else be written over
+// others that are still to be read.
+inline bool over_ok(const void* out, int dtype, int64_t ld, const void* in, int in_dtype, int64_t in_ld,
+                    int64_t rows) {
+  return !out || out != in || (dtype == in_dtype && (ld == in_ld || rows <= 1));
+}
+
 // What the norm's calls have in common.
 int norm_checks(int dtype, const void* weight, int w_dtype, int64_t rows, int64_t cols) {
   if (!dtype_ok(dtype) || !dtype_ok(w_dtype) || rows < 0 || cols < 1) return FP4Q_ERR_INVALID;
@@ -1157,6 +1165,10 @@ int norm_forward_checks(int dtype, const void* x, int64_t ldx, const void* resid
   if (residual && (!matrix_ok(residual, dtype, ldr, rows, cols) || !matrix_ok(h, dtype, ldh, rows, cols)))
     return FP4Q_ERR_INVALID;
   if (y && !matrix_ok(y, y_dtype, ldy, rows, cols)) return FP4Q_ERR_INVALID;
+  if (!over_ok(h, dtype, ldh, x, dtype, ldx, rows) || !over_ok(h, dtype, ldh, residual, dtype, ldr, rows) ||
+      !over_ok(y, y_dtype, ldy, x, dtype, ldx, rows) || !over_ok(y, y_dtype, ldy, residual, dtype, ldr, rows) ||
+      !over_ok(y, y_dtype, ldy, h, dtype, ldh, rows))
+    return FP4Q_ERR_INVALID;
   return rc;
 }
 
@@ -1236,6 +1248,9 @@ int fp4q_rms_norm_backward(fp4q_dtype_t dtype, const void* h, int64_t ldh, const
   if (!dtype_ok(dy_dtype) || !matrix_ok(h, dtype, ldh, rows, cols) || !matrix_ok(d_y, dy_dtype, lddy, rows, cols) ||
       !matrix_ok(d_x, dtype, lddx, rows, cols) || (d_h && !matrix_ok(d_h, dtype, lddh, rows, cols)) ||
       (rows > 0 && !rstd) || !aligned(rstd, 4) || !d_weight || !aligned(d_weight, 4))
+    return FP4Q_ERR_INVALID;
+  if (!over_ok(d_x, dtype, lddx, d_h, dtype, lddh, rows) || !over_ok(d_x, dtype, lddx, d_y, dy_dtype, lddy, rows) ||
+      !over_ok(d_x, dtype, lddx, h, dtype, ldh, rows))
     return FP4Q_ERR_INVALID;
   if (rc != FP4Q_OK) return rc;
   const size_t need = fp4q_rms_norm_backward_workspace_bytes(rows, cols);

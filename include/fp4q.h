@@ -738,8 +738,8 @@ int fp4q_kv_read(fp4q_format_t fmt, const uint8_t* cache, int64_t n_pages, int32
  * are stored as they are.
  *
  *   q, q_out   bf16 [rows, heads, dim], row strides ldq, ldqo (multiples of 8,
- *              16-byte aligned); q_out may be q itself, and overlaps it in no
- *              other way
+ *              16-byte aligned); q_out may be q itself (of its stride), and
+ *              overlaps it in no other way
  *   freqs      device f32 [rot/2], finite, with angles below 2^40 (they hold
  *              whatever scaling of positions a model has)
  *   rot        a multiple of 16 up to dim; further elements pass unchanged
@@ -872,7 +872,7 @@ int fp4q_kv_attention_sinks(fp4q_format_t fmt, const uint8_t* cache, int64_t n_p
  * in F32; d_x is the gradient of x and of the residual.
  *   h, rstd     of the forward call (x where there is no residual)
  *   d_y         f32 or bf16 (dy_dtype);  d_h: of h's type, or NULL;  d_x out,
- *               of h's type (may be d_h, or d_y of the same type and stride)
+ *               of h's type (may be d_h, or d_y, of the same type and stride)
  *   d_weight    out f32 [cols] (zeros when rows is 0)
  *   workspace   fp4q_rms_norm_backward_workspace_bytes() bytes, 4-byte
  *               aligned, no initialisation

@@ -77,3 +77,40 @@ def test_an_empty_batch_with_channels_through_the_layer(L, fmt):
 
     assert permuted(5, None) == INVALID
     assert permuted(0, None) == 0 if fmt else passes(lambda: permuted(0, None))
+
+
+def test_results_over_inputs_of_another_stride_or_type(L):
+    """Each is written over rows that are still to be read; of one row the stride
+    does not count."""
+    def rotated(qo=A, ldqo=512, rows=5):
+        return L.fp4q_kv_append_rotated(0, A, 4, 16, 2, 128, A, 2, A, 3, 3, A, rows, A, 512, 4, qo, ldqo, B, 256, B,
+                                        256, A, 32, 0, None, A, A, None)
+
+    assert passes(rotated) and passes(lambda: rotated(qo=B, ldqo=520)) and passes(lambda: rotated(ldqo=520, rows=1))
+    assert rotated(ldqo=520) == INVALID
+
+    X, R, H, Y = 0x100000, 0x200000, 0x300000, 0x400000
+
+    def norm(ldx=64, res=R, ldr=64, h=H, ldh=64, y=Y, yt=1, ldy=64, rows=5):
+        return L.fp4q_rms_norm(1, X, ldx, res, ldr, h, ldh, A, 0, 1e-6, rows, 64, y, yt, ldy, A, None)
+
+    def operand(ldx=64, res=R, ldr=64, h=H, ldh=64, y=Y, yt=1, ldy=64, rows=5):
+        return L.fp4q_rms_norm_quantize(0, 0, 1, X, ldx, res, ldr, h, ldh, A, 0, 1e-6, rows, 64, None, 0, A, A, A, 1,
+                                        None, y, yt, ldy, A, None, 0, None)
+
+    for f in (norm, operand):
+        for over in (dict(h=X), dict(h=R), dict(y=X), dict(h=X, ldx=66, ldh=66), dict(h=X, ldh=66, rows=1),
+                     dict(h=R, y=X), dict(ldh=70, ldy=71, ldx=72, ldr=73)):
+            assert passes(lambda: f(**over)), (f.__name__, over)
+        for over in (dict(h=X, ldh=65), dict(h=X, ldx=65), dict(h=R, ldr=65), dict(y=X, ldy=66), dict(y=X, yt=0),
+                     dict(y=X, yt=0, rows=1), dict(res=None, h=None, y=X, ldx=80), dict(y=R, yt=0), dict(y=H, yt=0)):
+            assert f(**over) == INVALID, (f.__name__, over)
+
+    def gradient(dyt=1, lddy=64, dh=R, lddh=64, dx=Y, lddx=64, rows=5, dy=H):
+        return L.fp4q_rms_norm_backward(1, X, 64, A, 0, A, dy, dyt, lddy, dh, lddh, dx, lddx, A, rows, 64, A, 1 << 20,
+                                        None)
+
+    for over in (dict(dx=H), dict(dx=R), dict(dx=H, lddy=70, lddx=70), dict(dx=R, lddx=70, rows=1), dict(dyt=0)):
+        assert passes(lambda: gradient(**over)), over
+    for over in (dict(dx=H, lddx=70), dict(dx=H, dyt=0), dict(dx=R, lddh=70), dict(dx=X, lddx=70)):
+        assert gradient(**over) == INVALID, over
