@@ -30,9 +30,21 @@ struct PythonError {};  // a Python exception is set
 PyObject* g_fail = nullptr;     // fail(name, code): raises the package's error
 PyObject* g_device = nullptr;   // device(): the current device
 PyObject* g_current = nullptr;  // current(device): its current stream's handle
-const char* g_host = nullptr;   // a tensor of this call that is not on the GPU
-int g_gpu = -1;                 // the GPU of this call's tensors
-const char* g_apart = nullptr;  // a tensor on another one
+
+// What a call has seen of its tensors.  Its own: an argument's __index__ or __float__
+// may make other calls, here or on another thread.
+struct Seen {
+  const char* host = nullptr;   // a tensor that is not on the GPU
+  int gpu = -1;                 // the GPU of the others
+  const char* apart = nullptr;  // a tensor on another one
+};
+thread_local Seen t_seen;
+
+struct Call {
+  const Seen outer = t_seen;
+  Call() { t_seen = Seen(); }
+  ~Call() { t_seen = outer; }
+};
 
 void check(const char* fn, int rc) {
   if (rc == FP4Q_OK) return;
@@ -49,12 +61,13 @@ void need(bool ok, const char* name, const char* what) {
 const at::Tensor& tensor(PyObject* o, const char* name) {
   need(THPVariable_Check(o), name, "a tensor is needed");
   const at::Tensor& t = THPVariable_Unpack(o);
+  Seen& seen = t_seen;
   if (!t.is_cuda()) {
-    g_host = name;
-  } else if (g_gpu < 0) {
-    g_gpu = t.get_device();
-  } else if (g_gpu != t.get_device()) {
-    g_apart = name;
+    seen.host = name;
+  } else if (seen.gpu < 0) {
+    seen.gpu = t.get_device();
+  } else if (seen.gpu != t.get_device()) {
+    seen.apart = name;
   }
   return t;
 }
@@ -74,7 +87,7 @@ int32_t small(PyObject* o, const char* name) {
 // The call's stream (None: the current one), after all checks but this one:
 // every tensor is on the GPU.
 void* stream_of(PyObject* o) {
-  if (g_host) throw Refused(std::string(g_host) + ": a tensor on the GPU is needed");
+  if (t_seen.host) throw Refused(std::string(t_seen.host) + ": a tensor on the GPU is needed");
   if (o != Py_None) return reinterpret_cast<void*>(integer(o));
   PyObject* d = PyObject_CallNoArgs(g_device);
   if (!d) throw PythonError();
@@ -91,8 +104,8 @@ void* stream_of(PyObject* o) {
 // its stream that reads another device's memory may fault).
 void* stream_here(PyObject* o) {
   void* const s = stream_of(o);
-  need(!g_apart, g_apart, "on another device than the first tensor");
-  need(g_gpu == at::detail::getCUDAHooks().getCurrentDevice(), "tensors", "not on the current device");
+  need(!t_seen.apart, t_seen.apart, "on another device than the first tensor");
+  need(t_seen.gpu == at::detail::getCUDAHooks().getCurrentDevice(), "tensors", "not on the current device");
   return s;
 }
 
@@ -882,8 +895,7 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
     PyErr_Format(PyExc_TypeError, "%d arguments are needed, not %zd", N, n);
     return nullptr;
   }
-  g_host = g_apart = nullptr;
-  g_gpu = -1;
+  const Call call;
   try {
     return F(args);
   } catch (const PythonError&) {
