@@ -54,6 +54,11 @@ void check(const char* fn, int rc) {
   throw PythonError();
 }
 
+// Refuses sizes that fn would, before memory is asked for its results.
+void sizes(bool ok, const char* fn, int rc = FP4Q_ERR_UNSUPPORTED) { check(fn, ok ? FP4Q_OK : rc); }
+
+constexpr int64_t PAST_INT = (int64_t)1 << 31;
+
 void need(bool ok, const char* name, const char* what) {
   if (!ok) throw Refused(std::string(name) + ": " + what);
 }
@@ -284,8 +289,7 @@ PyObject* read(PyObject* const* a) {
   void* const stream = stream_of(a[0]);
   const at::Tensor& like_t = THPVariable_Unpack(a[2]);
   // (no memory for a call that will be refused for its size)
-  const int64_t most = (int64_t)1 << 31;
-  const bool fits = rows < most && (c.heads * dim == 0 || (rows + 3) / 4 * 4 <= most * 32 / (c.heads * dim));
+  const bool fits = rows < PAST_INT && (c.heads * dim == 0 || (rows + 3) / 4 * 4 <= PAST_INT * 32 / (c.heads * dim));
   const at::Tensor both = like(like_t, {2, fits ? rows : 0, c.heads, dim}, at::kBFloat16);
   const at::Tensor k = both.select(0, 0), v = both.select(0, 1);
   const int64_t ld = (int64_t)c.heads * dim;
@@ -335,6 +339,7 @@ PyObject* append_rotated(PyObject* const* a) {
   }
   void* const stream = stream_here(a[0]);
   if (a[15] == Py_None) {
+    sizes(q.rows < ((int64_t)1 << 25) && q.heads * q.dim < PAST_INT, "fp4q_kv_append_rotated");
     const at::Tensor& qt = THPVariable_Unpack(a[9]);
     made = like(qt, {q.rows, q.heads, q.dim}, qt.scalar_type());
     o = {made.data_ptr(), q.rows, q.heads, q.dim, q.heads * q.dim};
@@ -438,7 +443,9 @@ Norm norm_of(PyObject* const* a, PyObject* h) {
 }
 
 // The result's h, made where the caller gave none.
-void make_h(PyObject* const* a, Norm& n) {
+void make_h(PyObject* const* a, Norm& n, const char* fn) {
+  sizes(n.x.cols < 1 || n.x.rows < 1 ||
+            (n.x.rows < PAST_INT && fp4q_rms_norm_backward_workspace_bytes(1, n.x.cols) > 0), fn);
   if (a[4] == Py_None || n.h_obj != Py_None) return;
   n.made_h = like(THPVariable_Unpack(a[1]), {n.x.rows, n.x.cols}, scalar_of(n.x.type));
   n.h = {n.made_h.data_ptr(), n.x.rows, n.x.cols, n.x.cols, n.x.type};
@@ -486,7 +493,7 @@ PyObject* rms_norm(PyObject* const* a) {
   void* const stream = stream_here(a[0]);
   const at::Tensor& t = THPVariable_Unpack(a[1]);
   at::Tensor my, mr;
-  make_h(a, n);
+  make_h(a, n, "fp4q_rms_norm");
   if (a[6] == Py_None) {
     my = like(t, {n.x.rows, n.x.cols}, scalar_of(type));
     y = {my.data_ptr(), n.x.rows, n.x.cols, n.x.cols, type};
@@ -552,7 +559,8 @@ PyObject* rms_norm_quantize(PyObject* const* a) {
   const at::Tensor& t = THPVariable_Unpack(a[1]);
   const int64_t R = n.x.rows, C = n.x.cols;
   const Operand s = operand(fmt, layout, R, C);
-  make_h(a, n);
+  sizes(n_chan <= C, "fp4q_rms_norm_quantize", FP4Q_ERR_INVALID);
+  make_h(a, n, "fp4q_rms_norm_quantize");
   const bool find = fmt == FP4Q_NVFP4 && !ts;
   const size_t bytes = fp4q_rms_norm_quantize_workspace_bytes((fp4q_format_t)fmt, R, !find);
   // one allocation for the workspace and the operand's parts, each 16-byte aligned
@@ -617,6 +625,8 @@ PyObject* rms_norm_backward(PyObject* const* a) {
   }
   if (a[7] != Py_None) dw = floats(a[7], "d_weight", h.cols);
   void* const stream = stream_here(a[0]);
+  const size_t bytes = fp4q_rms_norm_backward_workspace_bytes(h.rows, h.cols);
+  sizes(h.cols < 1 || h.rows < 1 || (h.rows < PAST_INT && bytes > 0), "fp4q_rms_norm_backward");
   const at::Tensor& t = THPVariable_Unpack(a[1]);
   at::Tensor mx, mw, ws;
   if (a[6] == Py_None) {
@@ -627,7 +637,6 @@ PyObject* rms_norm_backward(PyObject* const* a) {
     mw = like(t, {h.cols}, at::kFloat);
     dw = mw.data_ptr<float>();
   }
-  const size_t bytes = fp4q_rms_norm_backward_workspace_bytes(h.rows, h.cols);
   if (bytes) ws = like(t, {(int64_t)bytes}, at::kByte);
   check("fp4q_rms_norm_backward",
         fp4q_rms_norm_backward(h.type, h.p, h.ld, w, w_type, rstd, dy.p, dy.type, dy.ld, dh.p, dh.ld, dx.p, dx.ld,
@@ -664,6 +673,7 @@ PyObject* dequantize(PyObject* const* a) {
   const float* ts = a[5] == Py_None ? nullptr : floats(a[5], "tscale", 1);
   const fp4q_dtype_t type = dtype_of(a[8], "dtype");
   void* const stream = stream_here(a[0]);
+  sizes((rows + 15) / 16 * ((cols + 511) / 512) < (1 << 24), "fp4q_dequantize");
   const at::Tensor y = like(THPVariable_Unpack(a[3]), {rows, cols}, scalar_of(type));
   check("fp4q_dequantize", fp4q_dequantize((fp4q_format_t)fmt, (fp4q_layout_t)layout, q, sc, ts, rows, cols,
                                            y.data_ptr(), type, cols, stream));
@@ -707,11 +717,12 @@ PyObject* lora(PyObject* const* a) {
   void* const stream = stream_here(a[0]);
   const at::Tensor& t = THPVariable_Unpack(a[1]);
   at::Tensor made, ws;
+  const size_t bytes = fp4q_lora_workspace_bytes(x.rows, (int32_t)ad.numel(), (int32_t)ta.size(1), x.cols, N);
   if (a[9] == Py_None) {
+    sizes(x.rows < 1 || bytes > 0 || ad.numel() < 1 || ta.size(1) < 1 || x.cols < 1 || N < 1, "fp4q_lora");
     made = like(t, {x.rows, N}, scalar_of(type));
     out = {made.data_ptr(), x.rows, N, N, type};
   }
-  const size_t bytes = fp4q_lora_workspace_bytes(x.rows, (int32_t)ad.numel(), (int32_t)ta.size(1), x.cols, N);
   if (bytes) ws = like(t, {(int64_t)bytes}, at::kByte);
   check("fp4q_lora", fp4q_lora((uint16_t*)x.p, x.ld, (uint16_t*)ta.data_ptr(), (uint16_t*)tb.data_ptr(), scale,
                                (int32_t)ta.size(0), (int32_t)ta.size(1), off, adapter, (int32_t)ad.numel(), x.rows,
