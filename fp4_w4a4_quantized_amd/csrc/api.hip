@@ -1295,10 +1295,11 @@ int fp4q_lora(const uint16_t* x, int64_t ldx, const uint16_t* a, const uint16_t*
               int32_t n_adapters, int32_t rank, const int32_t* offsets, const int32_t* adapter,
               int32_t n_groups, int64_t rows, int64_t K, int64_t N, const void* y, int64_t ldy, void* out,
               fp4q_dtype_t dtype, int64_t ldo, void* workspace, size_t workspace_bytes, void* stream) {
-  if (!dtype_ok(dtype) || n_adapters < 1 || rank < 1 || n_groups < 1 || rows < 0 || K < 1 || N < 1 || ldx < K ||
-      !matrix_ok(out, dtype, ldo, rows, N) || (y && !matrix_ok(y, dtype, ldy, rows, N)))
+  // (no requests where there are no rows: their adapters have no address)
+  if (!dtype_ok(dtype) || n_adapters < 1 || rank < 1 || n_groups < (rows == 0 ? 0 : 1) || rows < 0 || K < 1 || N < 1 ||
+      ldx < K || !matrix_ok(out, dtype, ldo, rows, N) || (y && !matrix_ok(y, dtype, ldy, rows, N)))
     return FP4Q_ERR_INVALID;
-  if (!a || !b || !offsets || !adapter || !aligned(a, 16) || !aligned(b, 16) || !aligned(scale, 4) ||
+  if (!a || !b || !offsets || (n_groups > 0 && !adapter) || !aligned(a, 16) || !aligned(b, 16) || !aligned(scale, 4) ||
       !aligned(offsets, 4) || !aligned(adapter, 4) || (y && y == out && ldy != ldo))
     return FP4Q_ERR_INVALID;
   if (rows > 0 && (!x || !aligned(x, 16) || ldx % 8 != 0)) return FP4Q_ERR_INVALID;

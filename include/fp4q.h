@@ -923,6 +923,7 @@ int fp4q_dequantize(fp4q_format_t fmt, fp4q_layout_t layout, const uint8_t* q, c
  *              aligned; adapters of lower rank are padded with zeros
  *   scale      device f32 [n_adapters], or NULL: 1
  *   offsets    device int32 [n_groups + 1], non-decreasing, offsets[0] = 0
+ *              (n_groups may be 0 where rows is)
  *   adapter    device int32 [n_groups]; outside 0 .. n_adapters - 1 (-1,
  *              say): none
  *   y, out     f32 or bf16 (dtype) [rows, N], row strides ldy, ldo of any size

@@ -28,6 +28,14 @@ def test_adapters_of_no_rows_without_y(L):
     assert adapters(L, y=B, ldy=31) == INVALID          # out over y of another stride
 
 
+def test_adapters_of_no_requests(L):
+    for y in (None, A):
+        assert adapters(L, rows=0, G=0, ad=None, x=None, y=y, out=None) == 0
+    assert adapters(L, rows=0, G=-1, ad=None) == INVALID
+    assert adapters(L, rows=0, G=1, ad=None) == INVALID
+    assert adapters(L, G=0) == INVALID                  # rows, but no request
+
+
 def quantized_norm(L, fmt=0, lay=0, rows=5, cols=128, x=A, res=None, h=None, ch=A, nc=4, q=A, s=A, ts=A, given=1,
                    r=B, ws=None, wsb=0):
     return L.fp4q_rms_norm_quantize(fmt, lay, 1, x, cols, res, cols, h, cols, A, 0, 1e-6, rows, cols, ch, nc, q, s,

@@ -287,3 +287,10 @@ def test_nan_and_infinite_y_are_copied():
         rest = np.r_[0:4, 7:12]
         assert np.array_equal(got[rest], c["y"][rest], equal_nan=True)
         assert np.isnan(got[5, 50]) and np.isfinite(np.delete(got[4:7], 50, 1)).all()
+
+
+def test_no_requests():
+    need_gpu()
+    c = case([0], [0], 16, 64, 32, B)
+    c.update(off=[0], ad=[])
+    assert call(c).shape == call(c, y=False).shape == (0, 32)
