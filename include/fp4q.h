@@ -852,7 +852,7 @@ int fp4q_kv_attention_sinks(fp4q_format_t fmt, const uint8_t* cache, int64_t n_p
  *   weight           f32 or bf16 (w_dtype) [cols]
  *   eps              >= 0
  *   y                out f32 or bf16 (y_dtype) [rows, cols], row stride ldy;
- *                    may be x of the same type and stride
+ *                    may be x or residual, of the same type and stride
  *   rstd             out f32 [rows]: r, for the gradient (or NULL)
  *
  * fp4q_rms_norm_quantize gives the operand of the product behind the norm:
