@@ -9,8 +9,8 @@ norms before them write, with the adapters of each sequence's request beside the
 first one.  Keys are turned by their positions on the way into FP4 pages, which the
 attention reads there (a sliding window and the first tokens, in the run below),
 the router's order feeds the quantize-before-permute grouped products, and the
-combination brings the experts' outputs back.  Weights are random; torch supplies
-the router's projection and the activation.
+combination brings the experts' outputs back.  Weights are random; torch supplies the router's projection,
+the activation and the addition of the experts' outputs to the residual stream.
 """
 import argparse
 import os

@@ -4,8 +4,8 @@
 //
 // Bound by HBM: y is read and written once, x read once (prompts), or the
 // adapters' A and B, which a request of one token reads whole (decode).  8192 rows
-// of 11 requests, rank 32, K 4096, N 14336 (BF16, 536 MB): 22 + 109 us, 4.1 TB/s of the
-// 4.7 of a copy; 64 requests of one row with 37 adapters of rank 16 (26 MB): 4.7 + 8.5,
+// of 11 requests, rank 32, K 4096, N 14336 (BF16, 536 MB): 22 + 114 us, 3.9 TB/s of the
+// 4.7 of a copy; 64 requests of one row with 37 adapters of rank 16 (26 MB): 4.3 + 9.6,
 // the chain of a search, three loads and the sums in each.  Two
 // kernels: u = x A^T with K split over the waves and, where there are few rows,
 // over workgroups (partial sums in F32, added in order by the second kernel);
@@ -14,6 +14,9 @@
 // Products are 16x16x32 on BF16.  x, A and B enter as they are; u enters the
 // second product as two BF16 terms (u but for 2^-17) where out is BF16, as three
 // (2^-25) where it is F32: one term, 2^-9, would be as large as out's own rounding.
+// An infinite element of B meets each term by itself, so a step's sums are looked at
+// and, where one is infinite or NaN, taken again: 64 requests of one row 13.4 to 13.7 us,
+// the 8192 rows 141.8 to 143.0 (both calls back to back, three inputs in turn).
 #include "fp4q_device.h"
 #include "fp4q_internal.h"
 
@@ -470,7 +473,7 @@ __global__ __launch_bounds__(256) void k_lora_out(LoraArgs p) {
 
 // How a call is split, from host numbers only (each request may leave a tile that
 // is not full, and so may the rows of none).  Its rules, with what the other choice
-// takes (us; prompt: 8192 rows of 11 requests, rank 32, K 4096, N 14336, BF16; step:
+// takes (us, both sides without the look at a step's sums; prompt: 8192 rows of 11 requests, rank 32, K 4096, N 14336, BF16; step:
 // 64 requests of one row, rank 16, the same K and N):
 //   many    tiles of 64 rows for u (32 for ranks above 64: 26, by 64 37) and 32 for out
 //           from 1024 rows and 32 a request on, else 16: prompt u 21.6, by 32 rows 24.9; out

@@ -33,7 +33,7 @@
  *    such that 6 * 2^e >= block_amax, stored as E8M0 code e + 127;
  *    element = e2m1(x * 2^-e).  No tensor scale.
  *  - packing: two codes per byte, even element in the low nibble.
- *  - MXFP8 (an output of the norm, for layers kept in 8 bits): elements E4M3,
+ *  - MXFP8 (an output of the norm, for products outside this library): elements E4M3,
  *    32-element blocks; scale 2^e with the smallest e in [-127, 127] such
  *    that 448 * 2^e >= block_amax, stored as E8M0 code e + 127; element =
  *    e4m3(x * 2^-e), nearest-even.  Row-major only: codes u8 [rows, cols],
