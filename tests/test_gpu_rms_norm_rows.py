@@ -39,17 +39,17 @@ def test_no_rows_through_the_product(fmt):
         assert a["resid"].shape == (0, 8) and fq.gemm(fmt, a, b, chan_idx=chan).shape == (0, 64)
 
 
-# two rounds of rows and more: a wave a row; four waves, loads of the next row ahead;
-# four and eight waves without; and the second round of one row alone
-ROUNDS = [(8201, 128), (4101, 1024), (2100, 1152), (1025, 2048), (1100, 4224), (1040, 8320), (1026, 16512)]
+# two turns of rows and more: a wave a row; four waves, loads of the next row ahead;
+# four and eight waves without; and the second turn of one row alone
+TURNS = [(8201, 128), (4101, 1024), (2100, 1152), (1025, 2048), (1100, 4224), (1040, 8320), (1026, 16512)]
 
 
 @pytest.mark.parametrize("fmt", [fq.NVFP4, fq.MXFP4])
 @pytest.mark.parametrize("layout", [fq.ROWMAJOR, fq.TILED])
-@pytest.mark.parametrize("rows,cols", ROUNDS)
-def test_several_rounds_of_rows(fmt, layout, rows, cols):
+@pytest.mark.parametrize("rows,cols", TURNS)
+def test_rows_in_several_turns(fmt, layout, rows, cols):
     need_gpu()
-    say(f"norm rounds fmt {fmt} layout {layout} {rows} x {cols}")
+    say(f"norm turns fmt {fmt} layout {layout} {rows} x {cols}")
     b = torch.bfloat16
     x, res, w = case(rows, cols, b, True)
     h, r, y = layer.rms_norm(x, w, 1e-6, res)
@@ -68,9 +68,9 @@ def test_several_rounds_of_rows(fmt, layout, rows, cols):
 
 
 @pytest.mark.parametrize("rows,cols", [(8201, 96), (2100, 1152), (1100, 4224)])
-def test_several_rounds_of_rows_mxfp8(rows, cols):
+def test_rows_in_several_turns_mxfp8(rows, cols):
     need_gpu()
-    say(f"norm rounds MXFP8 {rows} x {cols}")
+    say(f"norm turns MXFP8 {rows} x {cols}")
     x, res, w = case(rows, cols, torch.bfloat16, True)
     h, r, y = layer.rms_norm(x, w, 1e-6, res)
     codes, sc, _ = layer.mxfp8_quantize(layer.bf16_round(y))
@@ -80,8 +80,8 @@ def test_several_rounds_of_rows_mxfp8(rows, cols):
 
 
 @pytest.mark.parametrize("rows,cols", [(8201, 128), (2100, 1152), (1100, 4224)])
-def test_the_largest_value_in_any_round(rows, cols):
-    """The tensor's largest magnitude in the first row, in a later round's and in the
+def test_the_largest_value_in_any_turn(rows, cols):
+    """The tensor's largest magnitude in the first row, in a later turn's and in the
     last one: the tensor scale sees every workgroup's maximum."""
     need_gpu()
     b = torch.bfloat16

@@ -1,5 +1,5 @@
 """GPU: calls around the products that the documentation allows beside the ones of the
-operators' own tests: results over inputs in several rounds of rows, queries turned
+operators' own tests: results over inputs in several turns of rows, queries turned
 where they stand in a packed projection, F32 values beside an operand, streams."""
 import numpy as np
 import pytest
